@@ -25,6 +25,10 @@
  *                     (biased variance), the same single HBM pass:
  *                     "TorchInductor: from ATen IR to Triton kernel", section
  *                     14.12.2, and "[Inductor] Codegen Gluon", section 3.2.
+ *   kv_cache_write, kv_cache_read, kv_attention_fwd
+ *                     what follows the fused Q/K step in serving: a paged
+ *                     key/value cache in 8 or 4 bits, and causal attention
+ *                     (whole, or a sliding window with sinks) over it.
  *   add_rmsnorm_fwd   h = x + residual (written out) and y = rmsnorm(h), one
  *                     kernel: the norm / residual-add chain fused ("TorchInductor:
  *                     from ATen IR to Triton kernel", sections 14.3 and 14.27).
@@ -92,8 +96,10 @@ enum {
 enum {
     RN_STATUS_WAIT_TIMEOUT = 1u,  /* a pipeline wait ran out; that launch's
                                      output is incomplete                     */
-    RN_STATUS_BAD_POSITION = 2u   /* qk_norm_rope_fwd_checked met a position
+    RN_STATUS_BAD_POSITION = 2u,  /* qk_norm_rope_fwd_checked met a position
                                      outside [0, max_pos)                     */
+    RN_STATUS_BAD_INDEX = 4u      /* a key/value cache call met a slot, page,
+                                     token or length outside its tensors      */
 };
 
 /* Static description of a code.  Never NULL. */
@@ -500,6 +506,114 @@ int row_norm_fwd_ws(int op, int dtype, const void *x, const void *residual,
  *     them, or give each stream rmsnorm_fwd_ws and a workspace of its own. */
 int rmsnorm_fwd_noalloc(const rn_bf16 *x, const rn_bf16 *w, float eps,
                         int64_t M, int64_t N, rn_bf16 *y, rn_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Quantised key/value cache                                                  */
+/* ------------------------------------------------------------------------ */
+
+/* What follows qk_norm_rope_fwd in a serving step: the key and value heads of
+ * the packed QKV tensor go into a paged cache that holds them in 8 or 4 bits,
+ * and the queries attend over that cache.  ("[pretuned] Optimize
+ * fused_qk_norm_rope on B200", "Summary", ends at the packed tensor these
+ * calls take.)
+ *
+ * The cache of one layer is two DEVICE tensors of the caller, both 16-byte
+ * aligned, P = page_size a power of two from 16 to 256, D in {64, 128, 256}:
+ *   codes   [num_pages, 2, Hkv, P, D * bits / 8] bytes   (index 1: 0 key, 1 value)
+ *   scales  [num_pages, 2, Hkv, P, D / 32] fp16
+ * Token p of a sequence lives in row p % P of page page_table[b, p / P]; slot
+ * s names row s % P of page s / P.  32 consecutive dimensions of a head share
+ * one scale:
+ *   s = fp16(min(max|x| / Q, 65504)),  c = rne(x / s) clamped to [-Q, Q],
+ *   value = s * c,   Q = 7 in 4 bits, 127 in 8
+ * (s = 0: every value is 0).  A group that holds a NaN or an infinity reads
+ * back as NaN throughout (its scale is the NaN 0xFFFF).  Largest magnitude
+ * that is not clamped: 458528 in 4 bits, 8319008 in 8; below 7 * 2^-25 in 4
+ * bits (127 * 2^-25 in 8) the whole group is stored as zeros.
+ *
+ * Codes are stored as c + 8 or c + 128, in the order in which the attention's
+ * lanes take them: stored element e of
+ *   a key row   is dimension 32 g + 8 j + n   for e = (j * (D / 32) + g) * 8 + n,
+ *                                             j < 4, g < D / 32, n < 8;
+ *   a value row is dimension 16 b + 2 r + h   for e = (r * (D / 16) + b) * 2 + h,
+ *                                             r < 8, b < D / 16, h < 2.
+ * In 4 bits byte e / 2 holds elements e (low half; e even) and e + 1.
+ *
+ * Slots, page numbers and lengths are read on the device; what they say is
+ * checked there and never followed out of the tensors: RN_STATUS_BAD_INDEX is
+ * raised in the status word instead (each call says what the result then is). */
+enum { RN_KV_INT4 = 4, RN_KV_INT8 = 8 };
+
+/* Quantises the key and value heads of qkv [T, (Hq + 2 Hkv) D] bf16 (as
+ * qk_norm_rope_fwd leaves them; the query heads are not read) into the rows
+ * that slots [T] int64 names.  A negative slot skips its token (padding); a
+ * slot >= num_pages * page_size does too and raises RN_STATUS_BAD_INDEX.
+ * Rows that no slot names keep their content.  The slots of one call must
+ * differ: where two tokens name one row, that row's content is a mixture.
+ * T * Hkv < 2^31.  Errors: RN_ERR_NULL, RN_ERR_ALIGN, RN_ERR_SHAPE,
+ * RN_ERR_ARG (unknown format), RN_ERR_DEVICE, RN_ERR_LAUNCH. */
+int kv_cache_write(const rn_bf16 *qkv, const int64_t *slots, int64_t T, int Hq,
+                   int Hkv, int D, int format, int page_size, int64_t num_pages,
+                   uint8_t *codes, rn_f16 *scales, rn_stream_t stream);
+
+/* Reads ragged token ranges back: tokens starts[b] .. of sequence b go to rows
+ * cu_lens[b] .. cu_lens[b + 1] - 1 of k and v [total, Hkv, D] bf16, each value
+ * s * c rounded once to bf16.
+ *   page_table [B, max_pages] int32; cu_lens [B + 1] int64, nondecreasing;
+ *   starts [B] int32, or NULL for all zero.
+ * Rows outside [cu_lens[0], cu_lens[B]) are left as they were.  A token behind
+ * the table's end or on a page outside [0, num_pages) reads as zeros and
+ * raises RN_STATUS_BAD_INDEX.  k and v must not overlap each other or the
+ * cache.  total * Hkv < 2^31.  Errors as kv_cache_write; k == v is RN_ERR_ARG. */
+int kv_cache_read(const uint8_t *codes, const rn_f16 *scales, int format, int Hkv,
+                  int D, int page_size, int64_t num_pages,
+                  const int32_t *page_table, int64_t B, int64_t max_pages,
+                  const int64_t *cu_lens, const int32_t *starts, int64_t total,
+                  rn_bf16 *k, rn_bf16 *v, rn_stream_t stream);
+
+/* Causal attention of ragged queries over the cache.  Sequence b has kv_lens[b]
+ * tokens in the cache and its newest cu_q[b + 1] - cu_q[b] of them as queries:
+ * query i of n stands at position p = kv_lens[b] - n + i and sees the tokens
+ *   j <= p,  and if window > 0 only those with j > p - window or j < sinks.
+ *   out[t, h, :] = bf16( sum_j softmax_j(scale * q[t, h] . k_j) v_j )
+ *   lse[t, h]    = ln sum_j exp(scale * q[t, h] . k_j)              (fp32)
+ * with k_j and v_j the cached values s * c of head h / (Hq / Hkv).  A query
+ * that sees no token (p < 0) gets out = 0 and lse = -infinity.
+ *   q           bf16, row t at q + t * q_stride, Hq heads of D; the packed QKV
+ *               tensor itself may be passed (q_stride = (Hq + 2 Hkv) D).
+ *               q_stride a multiple of 8, at least Hq * D.
+ *   page_table  [B, max_pages] int32;  kv_lens [B] int32.
+ *   cu_q        [B + 1] int64, nondecreasing: sequence b's queries are rows
+ *               cu_q[b] .. cu_q[b + 1] - 1 of the T rows; NULL: one query for
+ *               each sequence (T == B).  Rows outside are left as they were.
+ *   max_q_len   no sequence has more queries than this (it sizes the grid).
+ *   out         [T, Hq, D] bf16, must not overlap the inputs; lse [T, Hq] or NULL.
+ *   workspace   kv_attention_workspace_bytes(...) or more bytes of DEVICE memory,
+ *               16-byte aligned.  It needs no clearing, and calls that run one
+ *               after another may share it; calls whose kernels may run at the
+ *               same time need one each.
+ * A page outside [0, num_pages) reads as zeros, a length above max_pages *
+ * page_size is cut to that, queries beyond max_q_len are left unwritten: each
+ * raises RN_STATUS_BAD_INDEX.  Entries of page_table for pages on which no
+ * query sees a token are not used.  Requirements: Hq a multiple of Hkv; T * Hq,
+ * B * Hq, max_q_len * Hq and max_pages * page_size < 2^31; scale finite,
+ * window and sinks >= 0.  Arithmetic: exact products of bf16 queries and codes,
+ * fp32 sums; the weights are rounded once to fp16 (relative error 2^-11) before
+ * they meet the values.  Errors as kv_cache_write; a workspace that is too small
+ * is RN_ERR_ARG. */
+int kv_attention_fwd(const rn_bf16 *q, int64_t q_stride, const uint8_t *codes,
+                     const rn_f16 *scales, int format, int Hq, int Hkv, int D,
+                     int page_size, int64_t num_pages, const int32_t *page_table,
+                     int64_t B, int64_t max_pages, const int32_t *kv_lens,
+                     const int64_t *cu_q, int64_t T, int64_t max_q_len, float scale,
+                     int64_t window, int64_t sinks, rn_bf16 *out, float *lse,
+                     void *workspace, int64_t workspace_bytes, rn_stream_t stream);
+
+/* Bytes of workspace a kv_attention_fwd call of these sizes needs on the
+ * current device (a negative RN_ERR_* code for sizes it refuses).  Host-only
+ * query: launches nothing. */
+int64_t kv_attention_workspace_bytes(int format, int64_t B, int Hq, int Hkv, int D,
+                                     int64_t max_q_len);
 
 /* ------------------------------------------------------------------------ */
 /* Status word                                                                */

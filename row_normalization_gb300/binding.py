@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -29,6 +30,7 @@ RN_ERR_ARG = -6
 
 RN_STATUS_WAIT_TIMEOUT = 1
 RN_STATUS_BAD_POSITION = 2
+RN_STATUS_BAD_INDEX = 4
 
 RN_SCHED_AUTO = 0
 RN_SCHED_WARP_ROW = 1
@@ -53,6 +55,10 @@ RN_OP_RMSNORM = 0
 RN_OP_L2NORM = 1
 RN_OP_ADD_RMSNORM = 2
 RN_OP_LAYERNORM = 3
+
+RN_KV_INT4 = 4
+RN_KV_INT8 = 8
+RN_KV_GROUP = 32  # elements of a key/value cache scale
 
 RN_WORKSPACE_BYTES = 256
 RN_NOALLOC_SCRATCH_BYTES = 256  # the fixed scratch array of rmsnorm_fwd_noalloc
@@ -152,6 +158,16 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.row_norm_select_schedule.restype = i32
         L.row_norm_select_schedule_ws.argtypes = [i32, i64, i64]
         L.row_norm_select_schedule_ws.restype = i32
+        L.kv_cache_write.argtypes = [vp, vp, i64, i32, i32, i32, i32, i32, i64, vp, vp, vp]
+        L.kv_cache_write.restype = i32
+        L.kv_cache_read.argtypes = [vp, vp, i32, i32, i32, i32, i64, vp, i64, i64, vp, vp, i64, vp,
+                                    vp, vp]
+        L.kv_cache_read.restype = i32
+        L.kv_attention_fwd.argtypes = [vp, i64, vp, vp, i32, i32, i32, i32, i32, i64, vp, i64, i64,
+                                       vp, vp, i64, i64, f32, i64, i64, vp, vp, vp, i64, vp]
+        L.kv_attention_fwd.restype = i32
+        L.kv_attention_workspace_bytes.argtypes = [i32, i64, i32, i32, i32, i64]
+        L.kv_attention_workspace_bytes.restype = i64
         L.rn_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), i32]
         L.rn_device_status.restype = i32
         _lib = L
@@ -589,6 +605,233 @@ def rope_cos_sin_table(theta: float, max_pos: int, rotary_dim: int,
     rc = fn(float(theta), int(max_pos), int(rotary_dim), out.data_ptr(), _stream(stream))
     _check(rc, "rope_cos_sin_table")
     return out
+
+
+# ---- quantised key/value cache --------------------------------------------------
+
+class KVCache(NamedTuple):
+    """One layer's paged key/value cache in 8 or 4 bits (include/row_norm.h has
+    the stored format).
+
+    codes   uint8 [num_pages, 2, Hkv, page_size, D * bits / 8]
+    scales  fp16  [num_pages, 2, Hkv, page_size, D / 32]
+    """
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @property
+    def num_pages(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def num_kv_heads(self) -> int:
+        return self.codes.shape[2]
+
+    @property
+    def page_size(self) -> int:
+        return self.codes.shape[3]
+
+    @property
+    def head_dim(self) -> int:
+        return self.scales.shape[4] * RN_KV_GROUP
+
+    @property
+    def format(self) -> int:
+        """RN_KV_INT4 or RN_KV_INT8 (the bits of a code)."""
+        return self.codes.shape[4] * 8 // max(1, self.head_dim)
+
+
+def new_kv_cache(num_pages: int, Hkv: int, D: int, *, page_size: int = 64,
+                 format: int = RN_KV_INT4, device=None) -> KVCache:
+    """A zeroed cache of num_pages pages of page_size tokens."""
+    if format not in (RN_KV_INT4, RN_KV_INT8):
+        raise RowNormError("new_kv_cache", RN_ERR_ARG)
+    if D not in (64, 128, 256) or page_size not in (16, 32, 64, 128, 256) or Hkv < 1 or \
+            num_pages < 1:
+        raise RowNormError("new_kv_cache", RN_ERR_SHAPE)
+    dev = device if device is not None else "cuda"
+    shape = (num_pages, 2, Hkv, page_size)
+    return KVCache(torch.zeros(*shape, D * format // 8, dtype=torch.uint8, device=dev),
+                   torch.zeros(*shape, D // RN_KV_GROUP, dtype=torch.float16, device=dev))
+
+
+def _kv_cache(cache: KVCache):
+    """Checks a cache's tensors; returns (format, Hkv, D, page_size, num_pages)."""
+    codes, scales = cache
+    _need(codes, "cache.codes", torch.uint8)
+    _need(scales, "cache.scales", torch.float16)
+    cs, ss = codes.shape, scales.shape
+    if len(cs) != 5 or len(ss) != 5 or cs[:4] != ss[:4] or cs[1] != 2:
+        raise ValueError("cache tensors must be codes [pages, 2, Hkv, page_size, D * bits / 8] "
+                         "and scales [pages, 2, Hkv, page_size, D / 32]")
+    D = ss[4] * RN_KV_GROUP
+    if cs[4] * 2 == D:
+        fmt = RN_KV_INT4
+    elif cs[4] == D:
+        fmt = RN_KV_INT8
+    else:
+        raise ValueError("cache.codes must hold D / 2 (4 bits) or D (8 bits) bytes a row")
+    return fmt, cs[2], D, cs[3], cs[0]
+
+
+def _one_device(first: torch.Tensor, *others) -> torch.device:
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    return dev
+
+
+def _kv_call(dev: torch.device, name: str, *args, stream) -> None:
+    """Calls a key/value cache entry point with the tensors' device current."""
+    fn = getattr(load(), name)
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(stream))
+    if rc != RN_OK:
+        raise RowNormError(name, rc)
+
+
+def kv_cache_write(qkv: torch.Tensor, slots: torch.Tensor, cache: KVCache, Hq: int, Hkv: int,
+                   D: int, *, stream=None) -> KVCache:
+    """Quantises the key and value heads of qkv [T, (Hq + 2*Hkv) * D] (bf16, as
+    qk_norm_rope_fwd leaves it) into the rows slots [T] (int64; page * page_size
+    + offset, negative: skip the token) names.  Returns the cache."""
+    fmt, ch, cd, P, pages = _kv_cache(cache)
+    _need(qkv, "qkv", torch.bfloat16)
+    _need(slots, "slots", torch.int64)
+    if ch != Hkv or cd != D:
+        raise ValueError(f"the cache holds {ch} heads of {cd}, not {Hkv} of {D}")
+    T = slots.numel()
+    if qkv.numel() != T * (Hq + 2 * Hkv) * D:
+        raise ValueError("qkv must be [T, (Hq + 2*Hkv) * D] with a slot for each token")
+    dev = _one_device(qkv, slots, cache.codes, cache.scales)
+    _kv_call(dev, "kv_cache_write", qkv.data_ptr(), slots.data_ptr(), T, Hq, Hkv, D, fmt, P, pages,
+             cache.codes.data_ptr(), cache.scales.data_ptr(), stream=stream)
+    return cache
+
+
+def _page_table(page_table: torch.Tensor):
+    _need(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    return page_table.shape
+
+
+def kv_cache_read(cache: KVCache, page_table: torch.Tensor, cu_lens: torch.Tensor, total: int,
+                  starts: torch.Tensor | None = None, k: torch.Tensor | None = None,
+                  v: torch.Tensor | None = None, *, stream=None):
+    """Reads tokens starts[b].. (int32, default 0) of every sequence b back into
+    rows cu_lens[b] .. cu_lens[b+1] - 1 (int64) of k and v [total, Hkv, D]
+    bf16; returns (k, v).  page_table [B, max_pages] int32."""
+    fmt, Hkv, D, P, pages = _kv_cache(cache)
+    B, width = _page_table(page_table)
+    _need(cu_lens, "cu_lens", torch.int64)
+    if cu_lens.numel() != B + 1:
+        raise ValueError("cu_lens must have B + 1 elements")
+    if starts is not None:
+        _need(starts, "starts", torch.int32)
+        if starts.numel() != B:
+            raise ValueError("starts must have B elements")
+    dev = _one_device(cache.codes, cache.scales, page_table, cu_lens, starts, k, v)
+    shape = (total, Hkv, D)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+    for name, t in (("k", k), ("v", v)):
+        _need(t, name, torch.bfloat16)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be [total, Hkv, D]")
+    _kv_call(dev, "kv_cache_read", cache.codes.data_ptr(), cache.scales.data_ptr(), fmt, Hkv, D, P,
+             pages, page_table.data_ptr(), B, width, cu_lens.data_ptr(), _ptr(starts), total,
+             k.data_ptr(), v.data_ptr(), stream=stream)
+    return k, v
+
+
+def kv_attention_workspace(cache: KVCache, B: int, Hq: int, *, max_q_len: int = 1) -> torch.Tensor:
+    """A workspace for kv_attention_fwd calls of up to these sizes.  Calls that
+    run one after another can share one; calls that may run at the same time
+    need one each."""
+    fmt, Hkv, D, _, _ = _kv_cache(cache)
+    dev = cache.codes.device
+    with torch.cuda.device(dev):
+        n = int(load().kv_attention_workspace_bytes(fmt, B, Hq, Hkv, D, max_q_len))
+    if n < 0:
+        raise RowNormError("kv_attention_workspace_bytes", n)
+    return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def kv_attention_fwd(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
+                     kv_lens: torch.Tensor, Hq: int, *, cu_q: torch.Tensor | None = None,
+                     max_q_len: int = 1, scale: float | None = None, window: int = 0,
+                     sinks: int = 0, out: torch.Tensor | None = None,
+                     lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     stream=None):
+    """Causal attention over a quantised cache: the newest tokens of every
+    sequence attend to all its cached tokens, or with window > 0 to the last
+    `window` of them and the first `sinks`.
+
+    q           bf16 [T, >= Hq * D] (rows may be strided; the packed QKV tensor
+                itself will do) or [T, Hq, D]
+    page_table  int32 [B, max_pages];  kv_lens int32 [B]: tokens in the cache
+    cu_q        int64 [B + 1]: sequence b's queries are rows cu_q[b] ..
+                cu_q[b+1] - 1; None: one query for each sequence
+    max_q_len   the largest number of queries of a sequence
+    scale       softmax scale, default D ** -0.5
+
+    Returns (out [T, Hq, D] bf16, lse [T, Hq] fp32, natural logarithms).  Rows
+    outside every sequence are left as they were."""
+    fmt, Hkv, D, P, pages = _kv_cache(cache)
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q must be {torch.bfloat16}, got {q.dtype}")
+    if q.dim() == 3:
+        if q.shape[1] != Hq or q.shape[2] != D or (q.shape[0] and q.stride()[1:] != (D, 1)):
+            raise ValueError("q must be [T, Hq, D] with contiguous rows")
+    elif q.dim() != 2 or q.shape[1] < Hq * D or (q.shape[0] and q.stride(1) != 1):
+        raise ValueError("q must be [T, >= Hq * D] with contiguous rows, or [T, Hq, D]")
+    T = q.shape[0]
+    B, width = _page_table(page_table)
+    _need(kv_lens, "kv_lens", torch.int32)
+    if kv_lens.numel() != B:
+        raise ValueError("kv_lens must have B elements")
+    if cu_q is not None:
+        _need(cu_q, "cu_q", torch.int64)
+        if cu_q.numel() != B + 1:
+            raise ValueError("cu_q must have B + 1 elements")
+    elif T != B:
+        raise ValueError("without cu_q there is one query for each sequence")
+    dev = _one_device(q, cache.codes, cache.scales, page_table, kv_lens, cu_q, out, lse, workspace)
+    if out is None:
+        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", torch.bfloat16)
+        if out.numel() != T * Hq * D:
+            raise ValueError("out must be [T, Hq, D]")
+    if lse is None:
+        lse = torch.empty(T, Hq, dtype=torch.float32, device=dev)
+    else:
+        _need(lse, "lse", torch.float32)
+        if lse.numel() != T * Hq:
+            raise ValueError("lse must be [T, Hq]")
+    if workspace is None:
+        workspace = kv_attention_workspace(cache, B, Hq, max_q_len=max_q_len)
+        if stream is not None:  # freed while `stream` may still use it
+            workspace.record_stream(
+                stream if isinstance(stream, torch.cuda.Stream)
+                else torch.cuda.ExternalStream(int(stream), device=dev))
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    row = q.stride(0) if T > 1 else Hq * D
+    _kv_call(dev, "kv_attention_fwd", q.data_ptr(), row, cache.codes.data_ptr(),
+             cache.scales.data_ptr(), fmt, Hq, Hkv, D, P, pages, page_table.data_ptr(), B, width,
+             kv_lens.data_ptr(), _ptr(cu_q), T, max_q_len,
+             D ** -0.5 if scale is None else float(scale), int(window), int(sinks), out.data_ptr(),
+             lse.data_ptr(), workspace.data_ptr(),
+             workspace.numel() * workspace.element_size(), stream=stream)
+    return out, lse
 
 
 def rmsnorm_select_schedule(M: int, N: int, *, workspace: bool = False) -> int:

@@ -161,12 +161,14 @@ int rn_device_status(unsigned int *out, int clear) {
         cudaGetLastError();
         return RN_ERR_DEVICE;
     }
-    unsigned int a = 0, b = 0, q = 0;
+    unsigned int a = 0, b = 0, q = 0, c = 0, t = 0;
     int rc = rn::rows_status_bf16(&a, clear);
     if (rc == RN_OK) rc = rn::rows_status_f16(&b, clear);
     if (rc == RN_OK) rc = rn::qk_status(&q, clear);
+    if (rc == RN_OK) rc = rn::kv_cache_status(&c, clear);
+    if (rc == RN_OK) rc = rn::kv_attention_status(&t, clear);
     if (rc != RN_OK) return rc;
-    *out = a | b | q;
+    *out = a | b | q | c | t;
     return RN_OK;
 }
 
@@ -183,6 +185,6 @@ const char *rn_error_string(int code) {
     return "unknown status code";
 }
 
-int rn_version(void) { return 101; }
+int rn_version(void) { return 102; }
 
 }  // extern "C"

@@ -1,0 +1,419 @@
+"""Attention over the quantised key/value cache (GPU) against its 64-bit definition.
+
+Tolerance of an output element (derived, nothing fitted):
+  * the result is rounded once to bf16: eps/2 * |out|;
+  * a weight p and its product with a value scale are each rounded to fp16,
+    relative 2^-12 twice: 2^-11 * sum w |v|, and what falls below fp16's normal
+    range is off by 2^-25 of the largest weight at most (weights are kept at
+    2^7 or more there): n * 2^-32 * max|v|, below 2^-12 of the scale for the
+    lengths here and only where every larger weight meets no value;
+  * a logit is an fp32 sum of exact products: at most (D + 8) * 2^-23 * sum|q k| scale,
+    which moves a weight by that fraction, its sum by the same: twice it;
+    exp2 and the running sums: 2^-20.
+lse: the logit's error plus 2^-20 plus 2^-22 |lse|.
+"""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from row_normalization_gb300 import binding
+from row_normalization_gb300.inputs import qkv_inputs
+from tests import kv_ref
+from tests.gpu_util import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+EPS = torch.finfo(torch.bfloat16).eps / 2
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+    binding.device_status()
+
+
+def to_gpu(ref):
+    return binding.KVCache(ref.codes.cuda(), ref.scales.cuda())
+
+
+def filled(bits, Hkv, D, P, lens, seed, spread=1.0, spare=2):
+    """A cache holding `lens` tokens a sequence on shuffled pages; what no token
+    wrote is NaN, and the table's unused entries are no pages."""
+    g = torch.Generator().manual_seed(seed)
+    need = [-(-n // P) for n in lens]
+    pages = sum(need) + spare
+    order = torch.randperm(pages, generator=g)
+    table = torch.full((len(lens), max(need + [1]) + 1), -1, dtype=torch.int32)
+    ref = kv_ref.Cache(pages, Hkv, D, P, bits)
+    at = 0
+    for b, n in enumerate(lens):
+        table[b, :need[b]] = order[at:at + need[b]].int()
+        at += need[b]
+        if n:
+            x = torch.randn(n, 2, Hkv, D, generator=g)
+            x *= torch.exp(math.log(spread) * torch.randn(n, 2, Hkv, 1, generator=g))
+            pos = torch.arange(n)
+            ref.write(x.to(torch.bfloat16), table[b, pos // P].long() * P + pos % P)
+    return ref, table
+
+
+def queries(T, Hq, D, seed, size=1.5):
+    g = torch.Generator().manual_seed(seed + 1000)
+    return (size * torch.randn(T, Hq, D, generator=g)).to(torch.bfloat16)
+
+
+def check(got, lse, q, ref, table, lens, cu, scale, window=0, sinks=0):
+    D = q.shape[-1]
+    for b, n in enumerate(lens):
+        lo, hi = cu[b], cu[b + 1]
+        if lo == hi:
+            continue
+        K, V = (ref.tokens(table[b], w, 0, n) for w in (0, 1))
+        # tokens no query sees may sit on pages that are gone
+        o, l, mag, big = kv_ref.attention(q[lo:hi], K, V, n, scale, window, sinks)
+        dlogit = (D + 8) * 2.0 ** -23 * big
+        tol = EPS * o.abs() + (2.0 ** -11 + 2 * dlogit + 2.0 ** -20) * 1.01 * mag + 2.0 ** -40
+        err = (got[lo:hi].double() - o).abs()
+        assert (err <= tol).all(), (b, n, float((err / tol).max()))
+        g = lse[lo:hi].double()
+        assert torch.equal(torch.isinf(g), torch.isinf(l))
+        ok = ~torch.isinf(l)
+        assert ((g - l)[ok].abs() <= dlogit + 2.0 ** -20 + 2.0 ** -22 * l[ok].abs()).all()
+
+
+def attend(ref, table, lens, q, n_q, Hq, scale=None, **kw):
+    T = sum(n_q)
+    cu = [0]
+    for n in n_q:
+        cu.append(cu[-1] + n)
+    out, lse = binding.kv_attention_fwd(
+        q.cuda(), to_gpu(ref), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), Hq,
+        cu_q=torch.tensor(cu).cuda(), max_q_len=max(n_q + [1]), scale=scale, **kw)
+    assert out.shape == (q.shape[0], Hq, ref.D) and T <= q.shape[0]
+    return out.cpu(), lse.cpu(), cu
+
+
+LAYOUTS = [(4, 1, 64, 16), (6, 2, 128, 32), (8, 8, 64, 64), (32, 8, 128, 64), (5, 1, 256, 16),
+           (16, 2, 256, 128), (9, 1, 128, 256), (48, 1, 64, 32), (20, 1, 128, 16)]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("Hq,Hkv,D,P", LAYOUTS)
+def test_one_token_ragged_lengths(bits, Hq, Hkv, D, P):
+    lens = [1, 2, 15, 16, 17, 31, 32, 33, 64, 127, 130, 257]
+    ref, table = filled(bits, Hkv, D, P, lens, seed=D + P)
+    q = queries(len(lens), Hq, D, seed=Hq)
+    out, lse = binding.kv_attention_fwd(q.cuda(), to_gpu(ref), table.cuda(),
+                                        torch.tensor(lens, dtype=torch.int32).cuda(), Hq)
+    check(out.cpu(), lse.cpu(), q, ref, table, lens, list(range(len(lens) + 1)), D ** -0.5)
+    assert binding.device_status() == 0
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("Hq,Hkv,D,P", LAYOUTS)
+def test_several_queries_a_sequence(bits, Hq, Hkv, D, P):
+    lens, n_q = [5, 40, 33, 100, 64, 7], [5, 3, 0, 17, 1, 2]
+    ref, table = filled(bits, Hkv, D, P, lens, seed=D + P + 1)
+    q = queries(sum(n_q), Hq, D, seed=Hq)
+    out, lse, cu = attend(ref, table, lens, q, n_q, Hq)
+    check(out, lse, q, ref, table, lens, cu, D ** -0.5)
+    assert binding.device_status() == 0
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 4), (33, 0), (64, 40), (100, 3),
+                                          (10 ** 6, 2)])
+@pytest.mark.parametrize("Hq,Hkv,D,P,bits", [(8, 2, 128, 16, 4), (4, 4, 64, 64, 8),
+                                             (12, 1, 256, 32, 4)])
+def test_window_and_sinks(window, sinks, Hq, Hkv, D, P, bits):
+    lens, n_q = [1, 20, 90, 200, 333], [1, 7, 1, 30, 2]
+    ref, table = filled(bits, Hkv, D, P, lens, seed=window + sinks)
+    q = queries(sum(n_q), Hq, D, seed=3)
+    out, lse, cu = attend(ref, table, lens, q, n_q, Hq, window=window, sinks=sinks)
+    check(out, lse, q, ref, table, lens, cu, D ** -0.5, window, sinks)
+    assert binding.device_status() == 0
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_tokens_behind_the_window_are_never_used(bits):
+    """Their pages hold NaN scales or are gone from the table: nothing changes."""
+    Hq, Hkv, D, P, window, sinks = 8, 2, 128, 16, 50, 3
+    lens, n_q = [300], [9]
+    ref, table = filled(bits, Hkv, D, P, lens, seed=8)
+    q = queries(9, Hq, D, seed=4)
+    out, lse, cu = attend(ref, table, lens, q, n_q, Hq, window=window, sinks=sinks)
+    check(out, lse, q, ref, table, lens, cu, D ** -0.5, window, sinks)
+    first = lens[0] - n_q[0] - window + 1                   # the first token a window reaches
+    for j in range(sinks, first):
+        pg, off = int(table[0, j // P]), j % P
+        ref.scales[pg, :, :, off] = float("nan")
+        ref.codes[pg, :, :, off] = 0xFF
+    gone = table.clone()
+    gone[0, 1:first // P] = -5
+    again, lse2, _ = attend(ref, gone, lens, q, n_q, Hq, window=window, sinks=sinks)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    assert binding.device_status() == 0
+
+
+def test_rows_that_see_nothing():
+    """More queries than cached tokens, and an empty cache: 0 and -inf."""
+    Hq, Hkv, D, P = 4, 2, 128, 16
+    lens, n_q = [0, 3, 0, 20], [1, 6, 4, 20]
+    ref, table = filled(4, Hkv, D, P, lens, seed=2)
+    q = queries(sum(n_q), Hq, D, seed=5)
+    out, lse, cu = attend(ref, table, lens, q, n_q, Hq)
+    check(out, lse, q, ref, table, lens, cu, D ** -0.5)
+    assert (out[:4] == 0).all() and torch.isneginf(lse[:4]).all()
+    assert binding.device_status() == 0
+    one, l1 = binding.kv_attention_fwd(q[:1].cuda(), to_gpu(ref), table[:1].cuda(),
+                                       torch.zeros(1, dtype=torch.int32).cuda(), Hq)
+    assert (one == 0).all() and torch.isneginf(l1).all()
+
+
+def test_rows_outside_the_sequences_keep_their_content():
+    Hq, Hkv, D, P = 8, 2, 64, 32
+    lens = [50, 7]
+    ref, table = filled(8, Hkv, D, P, lens, seed=6)
+    T = 12
+    q = queries(T, Hq, D, seed=6)
+    out = torch.full((T, Hq, D), 3.25, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, Hq), 9.0, device="cuda")
+    cu = [2, 5, 9]
+    binding.kv_attention_fwd(q.cuda(), to_gpu(ref), table.cuda(),
+                             torch.tensor(lens, dtype=torch.int32).cuda(), Hq,
+                             cu_q=torch.tensor(cu).cuda(), max_q_len=4, out=out, lse=lse)
+    out, lse = out.cpu(), lse.cpu()
+    for sl in (slice(0, 2), slice(9, 12)):
+        assert (out[sl] == 3.25).all() and (lse[sl] == 9.0).all()
+    check(out, lse, q, ref, table, lens, cu, D ** -0.5)
+
+
+def test_packed_rows_and_strides():
+    """The packed QKV tensor and a view with a wider row give the same bits."""
+    Hq, Hkv, D, P = 8, 2, 128, 32
+    lens = [40, 90, 3]
+    ref, table = filled(4, Hkv, D, P, lens, seed=12)
+    q = queries(3, Hq, D, seed=12)
+    args = (to_gpu(ref), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), Hq)
+    want, wl = binding.kv_attention_fwd(q.cuda(), *args)
+    packed = torch.full((3, (Hq + 2 * Hkv) * D), float("nan"), dtype=torch.bfloat16)
+    packed[:, :Hq * D] = q.view(3, -1)
+    wide = torch.full((3, 4000), float("inf"), dtype=torch.bfloat16)
+    wide[:, 8:8 + Hq * D] = q.view(3, -1)
+    for x in (packed.cuda(), wide.cuda()[:, 8:8 + Hq * D], wide.cuda()[:, 8:]):
+        got, gl = binding.kv_attention_fwd(x, *args)
+        assert torch.equal(got, want) and torch.equal(gl, wl)
+    heads = wide.cuda()[:, 8:8 + Hq * D].unflatten(1, (Hq, D))
+    got, gl = binding.kv_attention_fwd(heads, *args)
+    assert torch.equal(got, want) and torch.equal(gl, wl)
+
+
+@pytest.mark.parametrize("size,spread,scale", [(40.0, 1.0, None), (1e-20, 1.0, None), (1e18, 1.0, 1e-18),
+                                               (1.5, 30.0, None), (1.5, 1.0, 0.0), (1.5, 1.0, -0.2),
+                                               (0.0, 1.0, None)])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_sizes_of_queries_and_values(size, spread, scale, bits):
+    """One-hot and flat softmaxes, queries far outside fp16, values whose scales
+    span fp16's range, zero and negative softmax scales."""
+    Hq, Hkv, D, P = 4, 1, 128, 32
+    lens, n_q = [200, 77], [1, 3]
+    ref, table = filled(bits, Hkv, D, P, lens, seed=31, spread=spread)
+    if spread > 1:  # keys of plain size: the logits stay ordinary, the values do not
+        plain, _ = filled(bits, Hkv, D, P, lens, seed=31)
+        ref.codes[:, 0], ref.scales[:, 0] = plain.codes[:, 0], plain.scales[:, 0]
+        ref.vals[:, 0] = plain.vals[:, 0]
+    q = queries(4, Hq, D, seed=31, size=size)
+    out, lse, cu = attend(ref, table, lens, q, n_q, Hq, scale=scale)
+    check(out, lse, q, ref, table, lens, cu, D ** -0.5 if scale is None else scale)
+
+
+def test_nan_stays_where_the_formula_has_it():
+    Hq, Hkv, D, P = 8, 2, 128, 16
+    lens, n_q = [60, 60], [3, 1]
+    ref, table = filled(8, Hkv, D, P, lens, seed=13)
+    q = queries(4, Hq, D, seed=13)
+    q[3, 2, 5] = float("nan")                    # one head of sequence 1
+    q[3, 5, 0] = float("inf")
+    # sequence 0: a value group of the newest token, which only the last query sees
+    pg, off = int(table[0, 59 // P]), 59 % P
+    ref.scales[pg, 1, 1, off, 2] = float("nan")
+    ref.vals[pg, 1, 1, off, 64:96] = float("nan")
+    # and a key group of token 58, which queries 1 and 2 see
+    pg, off = int(table[0, 58 // P]), 58 % P
+    ref.scales[pg, 0, 0, off, 1] = float("nan")
+    out, lse, cu = attend(ref, table, lens, q, n_q, Hq)
+    bad = torch.isnan(out.float())
+    want = torch.zeros_like(bad)
+    want[1:3, :4] = True                         # the key head 0's queries from token 58 on
+    want[2, 4:, 64:96] = True                    # the value head 1's dimensions of that group
+    want[3, 2] = want[3, 5] = True
+    assert torch.equal(bad, want)
+    assert torch.equal(torch.isnan(lse), want.all(-1))
+
+
+def test_bad_pages_and_lengths_are_zeros_and_reported():
+    Hq, Hkv, D, P = 4, 2, 64, 16
+    lens, n_q = [70, 30], [2, 1]
+    ref, table = filled(4, Hkv, D, P, lens, seed=14)
+    table[0, 2] = ref.codes.shape[0]
+    table[0, 3] = -1
+    q = queries(3, Hq, D, seed=14)
+    out, lse, cu = attend(ref, table, lens, q, n_q, Hq)
+    assert binding.device_status() == binding.RN_STATUS_BAD_INDEX
+    check(out, lse, q, ref, table, lens, cu, D ** -0.5)
+    # a length above the table is cut to it
+    short = table[1:, :1].contiguous()
+    got, gl = binding.kv_attention_fwd(q[2:].cuda(), to_gpu(ref), short.cuda(),
+                                       torch.tensor([1000], dtype=torch.int32).cuda(), Hq)
+    assert binding.device_status() == binding.RN_STATUS_BAD_INDEX
+    check(got.cpu(), gl.cpu(), q[2:], ref, short, [16], [0, 1], D ** -0.5)
+    # queries beyond max_q_len stay unwritten
+    keep = torch.full((2, Hq, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    binding.kv_attention_fwd(q[:2].cuda(), to_gpu(ref), table[1:].cuda(),
+                             torch.tensor([30], dtype=torch.int32).cuda(), Hq,
+                             cu_q=torch.tensor([0, 2]).cuda(), max_q_len=1, out=keep)
+    assert binding.device_status() == binding.RN_STATUS_BAD_INDEX
+    assert (keep[1] == 5.0).all() and not (keep[0] == 5.0).all()
+
+
+@pytest.mark.parametrize("bits,Hq,Hkv,D,n", [(4, 4, 1, 128, 20000), (8, 8, 1, 64, 9000),
+                                             (4, 2, 1, 256, 6001)])
+def test_long_contexts(bits, Hq, Hkv, D, n):
+    """Many CTAs share a sequence; small sequences sit beside it."""
+    lens = [3, n, 0, 40]
+    ref, table = filled(bits, Hkv, D, 64, lens, seed=n)
+    q = queries(4, Hq, D, seed=n)
+    out, lse = binding.kv_attention_fwd(q.cuda(), to_gpu(ref), table.cuda(),
+                                        torch.tensor(lens, dtype=torch.int32).cuda(), Hq)
+    check(out.cpu(), lse.cpu(), q, ref, table, lens, [0, 1, 2, 3, 4], D ** -0.5)
+
+
+def test_many_sequences_and_a_long_chunk():
+    Hq, Hkv, D, P = 4, 2, 64, 16
+    lens = [(7 * i) % 50 for i in range(700)] + [500]
+    n_q = [1 if n else 0 for n in lens[:-1]] + [150]
+    ref, table = filled(4, Hkv, D, P, lens, seed=1)
+    q = queries(sum(n_q), Hq, D, seed=1)
+    out, lse, cu = attend(ref, table, lens, q, n_q, Hq)
+    check(out, lse, q, ref, table, lens, cu, D ** -0.5)
+
+
+def test_runs_repeat_bit_for_bit_and_share_a_workspace():
+    Hq, Hkv, D = 8, 2, 128
+    lens = [5000, 17, 900]
+    ref, table = filled(4, Hkv, D, 32, lens, seed=40)
+    cache = to_gpu(ref)
+    q = queries(3, Hq, D, seed=40).cuda()
+    args = (cache, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), Hq)
+    ws = binding.kv_attention_workspace(cache, 3, Hq)
+    ws.random_(0, 256)
+    first = binding.kv_attention_fwd(q, *args, workspace=ws)
+    other = binding.kv_attention_fwd(q.flip(0).contiguous(), *args, workspace=ws)
+    again = binding.kv_attention_fwd(q, *args, workspace=ws)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    assert not torch.equal(first[0], other[0])
+
+
+def test_captured_steps_replay_on_new_data():
+    """The whole serving step in a graph: norm + RoPE, cache write, attention;
+    lengths, slots and positions change between replays."""
+    T, Hq, Hkv, D, P, pages = 3, 8, 2, 128, 16, 40
+    cache = binding.new_kv_cache(pages, Hkv, D, page_size=P)
+    ref = kv_ref.Cache(pages, Hkv, D, P, 4)
+    ref.codes.copy_(cache.codes), ref.scales.copy_(cache.scales), ref.vals.zero_()
+    table = torch.randperm(pages)[:T * 10].view(T, 10).int()
+    static = {"qkv": torch.zeros(T, (Hq + 2 * Hkv) * D, dtype=torch.bfloat16, device="cuda"),
+              "pos": torch.zeros(T, dtype=torch.int64, device="cuda"),
+              "slots": torch.zeros(T, dtype=torch.int64, device="cuda"),
+              "lens": torch.ones(T, dtype=torch.int32, device="cuda")}
+    _, wq, wk, _ = qkv_inputs(1, Hq, Hkv, D, seed=2, device="cuda")
+    trig = binding.rope_cos_sin_table(1e6, 160, D)
+    dt = table.cuda()
+    ws = binding.kv_attention_workspace(cache, T, Hq)
+    out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(T, Hq, device="cuda")
+
+    def step():
+        binding.qk_norm_rope_fwd(static["qkv"], wq, wk, trig, static["pos"], Hq, Hkv, D, D, 1e-6)
+        binding.kv_cache_write(static["qkv"], static["slots"], cache, Hq, Hkv, D)
+        binding.kv_attention_fwd(static["qkv"], cache, dt, static["lens"], Hq, out=out, lse=lse,
+                                 workspace=ws)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        static["slots"].fill_(-1)
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(40):
+        qkv, _, _, _ = qkv_inputs(T, Hq, Hkv, D, seed=100 + i)
+        at = torch.tensor([i, i + 50, i + 119])             # sequences of different length
+        if i == 0:                                          # their first tokens
+            for b in range(T):
+                n = int(at[b])
+                pos = torch.arange(n)
+                x, _, _, _ = qkv_inputs(max(n, 1), 0, Hkv, D, seed=500 + b)
+                sl = table[b, pos // P].long() * P + pos % P
+                x = x[:n]
+                binding.kv_cache_write(x.cuda(), sl.cuda(), cache, 0, Hkv, D)
+                ref.write(x.view(n, 2, Hkv, D), sl)
+        slots = table[torch.arange(T), at // P].long() * P + at % P
+        static["qkv"].copy_(qkv), static["pos"].copy_(at), static["slots"].copy_(slots)
+        static["lens"].copy_((at + 1).int())
+        graph.replay()
+        torch.cuda.synchronize()
+        normed = static["qkv"].cpu().view(T, Hq + 2 * Hkv, D)
+        ref.write(normed[:, Hq:].unflatten(1, (2, Hkv)), slots)
+        if i % 13 == 0 or i == 39:
+            check(out.cpu(), lse.cpu(), normed[:, :Hq], ref, table, (at + 1).tolist(),
+                  list(range(T + 1)), D ** -0.5)
+    assert torch.equal(cache.codes.cpu(), ref.codes)
+    assert binding.device_status() == 0
+
+
+def test_another_stream_without_a_workspace():
+    Hq, Hkv, D = 8, 2, 128
+    lens = [3000, 90]
+    ref, table = filled(8, Hkv, D, 64, lens, seed=50)
+    q = queries(2, Hq, D, seed=50)
+    args = [q.cuda(), to_gpu(ref), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), Hq]
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    out, lse = binding.kv_attention_fwd(*args, stream=st)
+    st.synchronize()
+    check(out.cpu(), lse.cpu(), q, ref, table, lens, [0, 1, 2], D ** -0.5)
+
+
+def test_refusals_of_the_binding():
+    cache = binding.new_kv_cache(2, 2, 64, page_size=16)
+    table = torch.zeros(1, 2, dtype=torch.int32, device="cuda")
+    lens = torch.ones(1, dtype=torch.int32, device="cuda")
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(TypeError):
+        binding.kv_attention_fwd(q.half(), cache, table, lens, 4)
+    with pytest.raises(TypeError):
+        binding.kv_attention_fwd(q, cache, table.long(), lens, 4)
+    with pytest.raises(ValueError):
+        binding.kv_attention_fwd(q.expand(2, 4, 64), cache, table, lens, 4)     # T != B
+    with pytest.raises(ValueError):
+        binding.kv_attention_fwd(q.transpose(1, 2), cache, table, lens, 64)
+    with pytest.raises(ValueError):
+        binding.kv_attention_fwd(q.cpu(), cache, table, lens, 4)
+    with pytest.raises(binding.RowNormError) as e:
+        binding.kv_attention_fwd(q.view(1, 256)[:, :192].contiguous(), cache, table, lens, 3)
+    assert e.value.code == binding.RN_ERR_SHAPE                                  # 3 % 2 heads
+    with pytest.raises(binding.RowNormError) as e:
+        binding.kv_attention_fwd(q, cache, table, lens, 4,
+                                 workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        binding.kv_cache_write(torch.zeros(1, 4 * 64, dtype=torch.bfloat16, device="cuda"),
+                               torch.zeros(1, dtype=torch.int64, device="cuda"), cache, 4, 2, 64)
+    with pytest.raises(ValueError):
+        binding.kv_cache_write(torch.zeros(1, 8 * 64, dtype=torch.bfloat16, device="cuda"),
+                               torch.zeros(1, dtype=torch.int64, device="cuda"), cache, 6, 1, 64)
+    with pytest.raises(TypeError):
+        binding.kv_cache_read(cache, table, torch.zeros(2, dtype=torch.int32, device="cuda"), 1)
