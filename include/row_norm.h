@@ -598,8 +598,8 @@ int kv_cache_read(const uint8_t *codes, const rn_f16 *scales, int format, int Hk
  * query sees a token are not used.  Requirements: Hq a multiple of Hkv; T * Hq,
  * B * Hq, max_q_len * Hq and max_pages * page_size < 2^31; scale finite,
  * window and sinks >= 0.  Arithmetic: exact products of bf16 queries and codes,
- * fp32 sums; the weights are rounded once to fp16 (relative error 2^-11) before
- * they meet the values.  Errors as kv_cache_write; a workspace that is too small
+ * fp32 sums; a softmax weight and its product with a value scale are each
+ * rounded to fp16 (2^-11 relative) before they meet the codes.  Errors as kv_cache_write; a workspace that is too small
  * is RN_ERR_ARG. */
 int kv_attention_fwd(const rn_bf16 *q, int64_t q_stride, const uint8_t *codes,
                      const rn_f16 *scales, int format, int Hq, int Hkv, int D,

@@ -1,10 +1,35 @@
 // kv_attention.cu -- causal attention of ragged queries over the quantised
 // key/value cache (sm_103a).
 //
-// The simple form: one CTA for one query token and head.  Its warps take the
-// visible tokens in turn, a lane the elements it finds in its share of the
-// stored row; each warp keeps the running maximum and sum of its own tokens'
-// softmax, and the four partial results are joined at the end.
+// The mathematics.  For a query q and visible tokens t with keys s_tg c_td
+// (g = d / 32) and likewise values,
+//   x_t = scale * sum_g s_tg sum_{d in g} q_d c_td,
+//   out_d = sum_t 2^(y_t - r) s_tg c_td / sum_t 2^(y_t - r),  y = x log2(e).
+// Both sums run on the tensor cores with the codes themselves as one operand:
+// a code is an exact fp16 number, and so is the query (bf16, scaled by a power
+// of two), so x_t has no rounding but that of fp32 sums.  The scales of the
+// keys multiply fp32 partial sums of one group; the scales of the values
+// multiply the weights, in fp16, before the second product.
+//
+// Codes reach the tensor core without a conversion: a code c in the low bits
+// of a 16-bit word is the subnormal fp16 number c * 2^-24, so masking a word
+// of the stored row is all it takes (a 4-bit code four bits further up counts
+// sixteen times; the query, or the finished sum, is divided by 16 there).
+// The stored order puts the two halves of each operand register sixteen bits
+// apart.  The offset of the stored codes (8 or 128) is taken off the sums
+// where one instruction's operand serves few columns, else off the operands.
+//
+// What bounds it: a decode step reads every visible byte once (HBM).  The
+// tokens are the rows of each product (16 an instruction) and the queries its
+// columns (8, all heads of the group and all queries of the tile), so nothing
+// is padded on the long side.
+//
+// Work is cut evenly over a fixed grid: all (sequence, query tile, kv head,
+// 32-token tile) units form one line, of which every CTA takes an equal run,
+// so ragged lengths leave no CTA behind.  A run that cuts a (query tile, head)
+// leaves partial sums in the workspace, which a second kernel joins in the
+// order of the line.  Inside a CTA four warps take every fourth tile with an
+// asynchronous copy ring of their own each and join at the end.
 #include "kv_common.cuh"
 
 namespace rn {
@@ -23,136 +48,1072 @@ struct KvAttnArgs {
     int64_t T;
     int64_t max_q_len;
     int Hq;
+    int group;         // query heads of a kv head
     float scale_log2;  // softmax scale * log2(e)
-    int64_t window;
-    int64_t sinks;
+    int window;        // 0: none
+    int sinks;
     uint16_t *out;
     float *lse;
+    // workspace: the units before each item [items + 1], then the partial sums
+    int64_t *prefix;
+    float *partial;
+    int64_t q_tiles;   // query tiles of a sequence
+    int grid;          // CTAs of the attention kernel
 };
 
-constexpr int kAttnThreads = 128;
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kTile = 32;          // tokens a warp takes at once
+constexpr int kMinTiles = kAttnWarps;  // a CTA's run is no shorter: one tile a warp
 
-template <int D, int BITS>
-__global__ void __launch_bounds__(kAttnThreads) kv_attention_simple_kernel(KvAttnArgs a) {
+// Shapes of an instantiation: NT * 8 columns (queries of the tile times heads).
+template <int D, int BITS, int NT>
+struct AttnShape {
     using F = KvFormat<D, BITS>;
-    constexpr int E = D / 32;  // stored elements a lane
-    pdl_trigger();
-    pdl_wait();
-    const int64_t t = blockIdx.x;
-    const int h = blockIdx.y;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int64_t b = t, first = t, n = 1;
-    if (a.cu_q) {
-        if (t < a.cu_q[0] || t >= a.cu_q[a.B]) return;
-        int64_t lo = 0, hi = a.B - 1;
-        while (lo < hi) {
-            const int64_t mid = (lo + hi + 1) >> 1;
-            if (a.cu_q[mid] <= t)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        b = lo;
-        first = a.cu_q[b];
-        n = a.cu_q[b + 1] - first;
+    static constexpr int NQ = 8 * NT;
+    static constexpr int MT = D / 16;                 // 16-row tiles of the value product
+    static constexpr int kScaleRow = 2 * F::kGroups;  // bytes of a row's scales
+    static constexpr int kCodesBytes = kTile * F::kRow;
+    static constexpr int kScalesBytes = kTile * kScaleRow;
+    static constexpr int kStage = 2 * (kCodesBytes + kScalesBytes);
+    // queries as operand registers (else in shared memory)
+    static constexpr bool kQueryRegs = NT == 1 && D <= 128;
+    // the codes' offset comes off the sums (else off the operands)
+    static constexpr bool kOffsetSums = NT == 1;
+    // CTAs an SM is to hold: by registers (O alone is MT * NT * 4 a thread), and by
+    // shared memory for a ring of two stages or more
+    static constexpr int kQuery = kQueryRegs ? 0 : NQ * D * 2;
+    static constexpr int kRoom = 224 * 1024;
+    static constexpr int stages_at(int ctas) { return (kRoom / ctas - 2048 - kQuery) / (kAttnWarps * kStage); }
+    static constexpr int kByRegs = MT * NT * 4 >= 64 ? 2 : (D == 64 ? 4 : 3);
+    static constexpr int kCtas = stages_at(kByRegs) >= 2 ? kByRegs : 1;
+    static constexpr int kStages = stages_at(kCtas) > 4 ? 4 : stages_at(kCtas);
+    static_assert(kStages >= 2, "the ring needs two stages");
+    static constexpr int kRing = kAttnWarps * kStages * kStage;
+    static constexpr int kJoin = kAttnWarps * NQ * D * 4;  // the warps' sums, over the ring
+    static constexpr int kSmem = (kRing > kJoin ? kRing : kJoin) + kQuery;
+    static constexpr int kSlot = NQ * (D + 2);  // floats of one partial result
+};
+
+// ---- instructions ---------------------------------------------------------------
+
+// d = a b + c: a 16 x 16, b 16 x 8 (fp16), c and d 16 x 8 (fp32).
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
+                                        float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    mma_f16(d, a0, a1, a2, a3, b0, b1, d[0], d[1], d[2], d[3]);
+}
+
+// Transposes an 8 x 8 matrix of 16-bit elements held one row by four lanes.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
+    const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t hsub2_bits(uint32_t a, uint32_t b) {
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// 16 bytes global -> shared, of which `bytes` are read and the rest is zero.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int WORDS>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[WORDS], uint32_t addr) {
+    if constexpr (WORDS == 1) {
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+    } else if constexpr (WORDS == 2) {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    } else {
+        static_assert(WORDS == 4, "one, two or four words");
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(addr));
     }
+}
+
+// Byte offset of 16-byte chunk `chunk` of a tile's codes, token t at chunk
+// t * ROW / 16.  The chunks of a 128-byte line are exchanged by a mask that
+// depends on the line, so that both readers are free of bank conflicts: the
+// key operand (8 tokens, 4 runs of a row each) and the value operand (4
+// tokens, 8 runs each).  Masks found by trying all that are linear in the
+// line's number.
+template <int ROW>
+__device__ __forceinline__ int swizzle(int chunk) {
+    constexpr int m0 = ROW == 32 ? 4 : (ROW == 256 ? 1 : 2);
+    constexpr int m1 = ROW == 32 ? 0 : (ROW == 256 ? 1 : 4);
+    constexpr int m2 = ROW >= 128 ? (ROW == 256 ? 4 : 1) : 0;
+    constexpr int m3 = ROW == 256 ? 2 : 0;
+    const int line = chunk >> 3;
+    int x = chunk ^ ((line & 1) * m0) ^ ((line >> 1 & 1) * m1);
+    if (m2) x ^= (line >> 2 & 1) * m2;
+    if (m3) x ^= (line >> 3 & 1) * m3;
+    return x * 16;
+}
+
+// ---- the line of units ------------------------------------------------------------
+
+// One (sequence, query tile): its columns and the tiles of tokens they see.
+struct Item {
+    int64_t row0;    // first query row of the sequence
+    int f0, ncols;   // columns f0 .. f0 + ncols - 1 of the sequence's n_q * group
+    int pos0;        // position of the sequence's first query
+    int lo_pos, hi;  // position of the first column's query; one past the last column's
+    int win_lo;      // first token inside the first column's window (0 without one)
+    int sink_tiles;  // tiles 0 .. sink_tiles - 1, then lo_tile ..
+    int lo_tile;
+    int n;           // tiles in all
+    bool bad;        // something had to be cut to the tensors
+
+    __device__ __forceinline__ int token(int k) const {
+        return (k < sink_tiles ? k : lo_tile + (k - sink_tiles)) * kTile;
+    }
+};
+
+template <int NQ>
+__device__ __forceinline__ Item make_item(const KvAttnArgs &a, int64_t b, int64_t qt) {
+    Item it;
+    it.bad = false;
+    int64_t nq = 1;
+    it.row0 = b;
+    if (a.cu_q) {
+        it.row0 = a.cu_q[b];
+        nq = a.cu_q[b + 1] - it.row0;
+        if (nq > 0 && (it.row0 < 0 || it.row0 + nq > a.T)) {
+            it.bad = true;
+            nq = 0;
+        }
+    }
+    if (nq < 0) nq = 0;
     int64_t len = a.kv_lens[b];
     const int64_t room = a.max_pages << a.cache.log2_page;
-    if (len > room || t - first >= a.max_q_len) {
-        if (threadIdx.x == 0) atomicOr(&g_kv_attention_status, RN_STATUS_BAD_INDEX);
-        if (t - first >= a.max_q_len) return;
+    if (len > room) {
+        it.bad = true;
         len = room;
     }
-    const int64_t pos = len - n + (t - first);
-    const int kvh = h / (a.Hq / a.cache.Hkv);
-    // the lane's elements of the query in the order of the stored keys
-    float q[E], o[E], m = -INFINITY, l = 0.0f;
-    int kdim[E], vdim[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const int e = lane * E + i;
-        const int j = e / (F::kGroups * 8), g = e / 8 % F::kGroups;
-        kdim[i] = 32 * g + 8 * j + e % 8;
-        const int r = e / (D / 8), bb = e / 2 % (D / 16);
-        vdim[i] = 16 * bb + 2 * r + e % 2;
-        q[i] = bf_lo(a.q[t * a.q_stride + static_cast<int64_t>(h) * D + kdim[i]]) * a.scale_log2;
-        o[i] = 0.0f;
+    if (len < 0) len = 0;
+    it.pos0 = static_cast<int>(len - nq);
+    if (nq > a.max_q_len) {
+        it.bad = true;
+        nq = a.max_q_len;
     }
-    for (int64_t j = warp; j <= pos; j += kAttnThreads / 32) {
-        if (a.window && j <= pos - a.window && j >= a.sinks) {
-            const int64_t lo = pos - a.window + 1;  // the window's first token
-            j += (lo - j) / (kAttnThreads / 32) * (kAttnThreads / 32);
-            if (j < lo) continue;
+    const int64_t left = nq * a.group - qt * NQ;
+    it.f0 = static_cast<int>(qt * NQ);
+    it.ncols = static_cast<int>(left < 0 ? 0 : (left < NQ ? left : NQ));
+    it.lo_pos = it.pos0 + it.f0 / a.group;
+    it.hi = it.pos0 + (it.f0 + it.ncols - 1) / a.group + 1;
+    it.win_lo = it.sink_tiles = it.lo_tile = it.n = 0;
+    if (it.ncols == 0 || it.hi <= 0) return it;
+    const int tiles = (it.hi + kTile - 1) / kTile;
+    if (a.window && it.lo_pos >= a.window) {
+        it.win_lo = it.lo_pos - a.window + 1;
+        it.sink_tiles = a.sinks >= it.hi ? tiles : (a.sinks + kTile - 1) / kTile;
+        if (it.sink_tiles > tiles) it.sink_tiles = tiles;
+        it.lo_tile = it.win_lo / kTile;
+        if (it.lo_tile < it.sink_tiles) it.lo_tile = it.sink_tiles;
+    }
+    it.n = it.sink_tiles + tiles - it.lo_tile;
+    return it;
+}
+
+// CTAs that share a line of `units` units, and the first unit of CTA c.
+__host__ __device__ __forceinline__ int64_t line_ctas(int64_t units, int grid) {
+    const int64_t want = (units + kMinTiles - 1) / kMinTiles;
+    return want < grid ? (want > 0 ? want : 1) : grid;
+}
+__device__ __forceinline__ int64_t line_start(int64_t units, int64_t ctas, int64_t c) {
+    return units * c / ctas;
+}
+
+// Four dimensions of a finished column: out = sum / l (the codes' 2^-24 undone),
+// lse = (reference + log2(l)) ln 2.
+template <int D>
+__device__ __forceinline__ void store_result(const KvAttnArgs &a, const Item &it, int head0, int col, int d0,
+                                             float4 v, float ref, float l) {
+    const int f = it.f0 + col;
+    const int64_t t = it.row0 + f / a.group;
+    const int64_t row = t * a.Hq + head0 + f % a.group;
+    const float inv = l == 0.0f ? 0.0f : 0x1p24f / l;
+    const uint2 w = make_uint2(pack_bf2(v.x * inv, v.y * inv), pack_bf2(v.z * inv, v.w * inv));
+    *reinterpret_cast<uint2 *>(a.out + row * D + d0) = w;
+    if (d0 == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+}
+
+// ---- the attention kernel ---------------------------------------------------------
+
+// Sum of the item sizes before this thread's share, by a scan over the block;
+// every CTA runs it over all items, so that no launch has to come before.
+struct Line {
+    int64_t units;        // in all, over every kv head
+    int64_t item, before; // the item at a wanted unit, and the tiles of one head before it
+};
+
+template <int NQ>
+__device__ __forceinline__ Line find_unit(const KvAttnArgs &a, bool publish, int64_t *scratch) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t items = a.B * a.q_tiles;
+    const int64_t per = (items + kAttnThreads - 1) / kAttnThreads;
+    const int64_t i0 = tid * per < items ? tid * per : items;
+    const int64_t i1 = i0 + per < items ? i0 + per : items;
+    int64_t sum = 0;
+    bool bad = false;
+    for (int64_t i = i0; i < i1; ++i) {
+        const Item it = make_item<NQ>(a, i / a.q_tiles, i % a.q_tiles);
+        sum += it.n;
+        bad |= it.bad;
+    }
+    if (publish && bad) atomicOr(&g_kv_attention_status, RN_STATUS_BAD_INDEX);
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) {
+        if (w < warp) before += scratch[w];
+        total += scratch[w];
+    }
+    if (publish) {
+        int64_t run = before;
+        for (int64_t i = i0; i < i1; ++i) {
+            a.prefix[i] = run;
+            run += make_item<NQ>(a, i / a.q_tiles, i % a.q_tiles).n;
         }
-        const int64_t page = a.page_table[b * a.max_pages + (j >> a.cache.log2_page)];
-        const bool good = page >= 0 && page < a.cache.num_pages;
-        if (!good && lane == 0) atomicOr(&g_kv_attention_status, RN_STATUS_BAD_INDEX);
-        const int off = static_cast<int>(j & ((1 << a.cache.log2_page) - 1));
-        float s = 0.0f;
-        float vals[2][E];
+        if (tid == 0) a.prefix[items] = total;
+    }
+    Line line;
+    line.units = total * a.cache.Hkv;
+    const int64_t ctas = line_ctas(line.units, a.grid);
+    const int64_t u = line_start(line.units, ctas, blockIdx.x);
+    if (blockIdx.x < ctas && before * a.cache.Hkv <= u && u < (before + sum) * a.cache.Hkv) {
+        int64_t run = before;
+        for (int64_t i = i0; i < i1; ++i) {
+            const int n = make_item<NQ>(a, i / a.q_tiles, i % a.q_tiles).n;
+            if (u < (run + n) * a.cache.Hkv) {
+                scratch[kAttnWarps] = i;
+                scratch[kAttnWarps + 1] = run;
+                break;
+            }
+            run += n;
+        }
+    }
+    __syncthreads();
+    line.item = scratch[kAttnWarps];
+    line.before = scratch[kAttnWarps + 1];
+    return line;
+}
+
+// A column's query as operand registers and what goes with it.
+template <int D, int BITS>
+struct Query {
+    using F = KvFormat<D, BITS>;
+    uint32_t b[F::kGroups][2][2];  // [group][k-step][register]
+    float sum[F::kGroups];         // of the lane's elements of a group
+    float factor;                  // from a sum of codes * query to a logit in log2
+
+    // Column `col` of the item, lane j of its four.  The query is scaled so that its
+    // largest element lies in [2^13, 2^14): exact in fp16 down to 2^-28 of that.
+    __device__ __forceinline__ void load(const KvAttnArgs &a, const Item &it, int head0, int col, int j) {
+        uint32_t w[F::kGroups][4];
+        uint32_t top = 0u;
+        const bool live = col < it.ncols;
+        const int f = it.f0 + (live ? col : 0);
+        const uint16_t *src = a.q + (it.row0 + f / a.group) * a.q_stride +
+                              static_cast<int64_t>(head0 + f % a.group) * D + 8 * j;
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const int64_t r = good ? a.cache.row(page, which, kvh, off) : 0;
+        for (int g = 0; g < F::kGroups; ++g) {
+            const uint4 v = live ? ld_ro16(src + 32 * g) : make_uint4(0u, 0u, 0u, 0u);
+            w[g][0] = v.x;
+            w[g][1] = v.y;
+            w[g][2] = v.z;
+            w[g][3] = v.w;
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const int e = lane * E + i;
-                int c = 0;
-                float sc = 0.0f;
-                if (good) {
-                    c = a.cache.codes[r * F::kRow + e * BITS / 8];
-                    if (BITS == 4) c = c >> (4 * (e & 1)) & 15;
-                    sc = half_bits_to_float(
-                        a.cache.scales[r * F::kGroups + (which ? vdim[i] : kdim[i]) / 32]);
-                }
-                vals[which][i] = sc * static_cast<float>(c - F::kZero);
+            for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[g][i] & 0x7FFF7FFFu);
+        }
+        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t amax = max(top & 0xFFFFu, top >> 16);
+        const bool finite = amax < 0x7F80u;
+        int e = static_cast<int>(amax >> 7);   // biased exponent
+        e = e < 14 ? 14 : e;
+        const float up = __uint_as_float(static_cast<uint32_t>(267 - (finite ? e : 127)) << 23);  // 2^(140 - e)
+        // codes are c * 2^-24: factor = scale * 2^(e - 140 + 24), in two exact steps
+        factor = finite ? ldexpf(a.scale_log2, e - 116) : __uint_as_float(0x7FC00000u);
+        if (!live) factor = 0.0f;
+#pragma unroll
+        for (int g = 0; g < F::kGroups; ++g) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = finite ? bf_lo(w[g][i]) * up : 0.0f;
+                x[2 * i + 1] = finite ? bf_hi(w[g][i]) * up : 0.0f;
+            }
+            sum[g] = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+            if constexpr (BITS == 4) {
+                b[g][0][0] = pack_h2(x[0], x[4]);
+                b[g][0][1] = pack_h2(x[1] * 0.0625f, x[5] * 0.0625f);
+                b[g][1][0] = pack_h2(x[2], x[6]);
+                b[g][1][1] = pack_h2(x[3] * 0.0625f, x[7] * 0.0625f);
+            } else {
+                b[g][0][0] = pack_h2(x[0], x[2]);
+                b[g][0][1] = pack_h2(x[1], x[3]);
+                b[g][1][0] = pack_h2(x[4], x[6]);
+                b[g][1][1] = pack_h2(x[5], x[7]);
             }
         }
-#pragma unroll
-        for (int i = 0; i < E; ++i) s = fmaf(q[i], vals[0][i], s);
-        s = warp_sum(s);
-        const float mn = fmaxf(m, s);
-        const float base = mn == -INFINITY ? 0.0f : mn;
-        const float f = exp2f(m - base), p = exp2f(s - base);
-        l = l * f + p;
-#pragma unroll
-        for (int i = 0; i < E; ++i) o[i] = fmaf(p, vals[1][i], o[i] * f);
-        m = mn;
     }
-    __shared__ float sm_m[kAttnThreads / 32], sm_l[kAttnThreads / 32];
-    __shared__ float sm_o[kAttnThreads / 32][D];
-    if (lane == 0) {
-        sm_m[warp] = m;
-        sm_l[warp] = l;
-    }
+};
+
+// Tiles [k0, k1) of one item and kv head: all warps, joined; the result goes to
+// the output rows, or (part != null) unfinished into a slot of the workspace.
+template <int D, int BITS, int NT>
+__device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, int64_t b, int kvh,
+                                           int k0, int k1, float *part, uint8_t *smem) {
+    using S = AttnShape<D, BITS, NT>;
+    using F = KvFormat<D, BITS>;
+    constexpr int NG = F::kGroups;
+    constexpr int NQ = S::NQ;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = lane >> 2, j = lane & 3;
+    __shared__ int s_pos[NQ];
+    __shared__ float s_factor[NQ], s_ref[kAttnWarps][NQ], s_l[kAttnWarps][NQ];
+
+    // -- queries ------------------------------------------------------------------
+    const int head0 = kvh * a.group;
+    uint32_t qreg[S::kQueryRegs ? NG : 1][2][2];
+    float offset[S::kOffsetSums ? NG : 1][2];  // -zero * sum of the group's query, columns 2j, 2j+1
+    float factor[NT][2];
+    uint8_t *qsm = smem + (S::kSmem - S::kQuery);
+    if (threadIdx.x < NQ)
+        s_pos[threadIdx.x] = static_cast<int>(threadIdx.x) < it.ncols
+                                 ? it.pos0 + (it.f0 + static_cast<int>(threadIdx.x)) / a.group
+                                 : -1;
+    if constexpr (S::kOffsetSums) {
+        Query<D, BITS> q;
+        q.load(a, it, head0, r, j);
 #pragma unroll
-    for (int i = 0; i < E; ++i) sm_o[warp][vdim[i]] = o[i];
+        for (int g = 0; g < NG; ++g) {
+            float s = q.sum[g];
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            s *= -static_cast<float>(F::kZero) * 0x1p-24f;
+            offset[g][0] = __shfl_sync(0xffffffffu, s, 8 * j);
+            offset[g][1] = __shfl_sync(0xffffffffu, s, 8 * j + 4);
+            if constexpr (S::kQueryRegs) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) qreg[g][k >> 1][k & 1] = q.b[g][k >> 1][k & 1];
+            } else if (warp == 0) {
+                *reinterpret_cast<uint4 *>(qsm + (g * 32 + lane) * 16) =
+                    make_uint4(q.b[g][0][0], q.b[g][0][1], q.b[g][1][0], q.b[g][1][1]);
+            }
+        }
+        factor[0][0] = __shfl_sync(0xffffffffu, q.factor, 8 * j);
+        factor[0][1] = __shfl_sync(0xffffffffu, q.factor, 8 * j + 4);
+        __syncthreads();
+    } else {
+        for (int nt = warp; nt < NT; nt += kAttnWarps) {
+            Query<D, BITS> q;
+            q.load(a, it, head0, nt * 8 + r, j);
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                *reinterpret_cast<uint4 *>(qsm + ((nt * NG + g) * 32 + lane) * 16) =
+                    make_uint4(q.b[g][0][0], q.b[g][0][1], q.b[g][1][0], q.b[g][1][1]);
+            if (j == 0) s_factor[nt * 8 + r] = q.factor;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            factor[nt][0] = s_factor[nt * 8 + 2 * j];
+            factor[nt][1] = s_factor[nt * 8 + 2 * j + 1];
+        }
+    }
+
+    // -- the warp's copy ring --------------------------------------------------------
+    uint8_t *ring = smem + warp * (S::kStages * S::kStage);
+    const uint32_t ring_addr = smem_addr(ring);
+    const int log2_page = a.cache.log2_page;
+    const int32_t *table = a.page_table + b * a.max_pages;
+    const int64_t vrows = static_cast<int64_t>(a.cache.Hkv) << log2_page;  // key rows to value rows
+
+    struct Pages {
+        int lo, hi;  // of the tile's two halves (16 tokens each lie on one page)
+    };
+    const auto pages_of = [&](int k) {
+        Pages p = {-1, -1};
+        if (k < k1) {
+            const int t0 = it.token(k);
+            p.lo = table[t0 >> log2_page];
+            p.hi = p.lo;
+            if (log2_page == 4) p.hi = t0 + 16 < it.hi ? table[(t0 >> 4) + 1] : -1;
+        }
+        return p;
+    };
+    const auto seen = [&](int t) {  // some query sees a token of t .. t + 15
+        return t < it.hi && (it.win_lo == 0 || t < a.sinks || t + 15 >= it.win_lo);
+    };
+    const auto seen_token = [&](int t) {
+        return t < it.hi && (it.win_lo == 0 || t < a.sinks || t >= it.win_lo);
+    };
+    // Copies tile k into a stage.  Rows behind the last visible token, and rows of
+    // pages on which nothing is visible or that do not exist, arrive as zeros.
+    const auto issue = [&](int k, int stage, Pages p) {
+        const int t0 = it.token(k);
+        const bool see_lo = seen(t0), see_hi = seen(t0 + 16);
+        const bool ok_lo = p.lo >= 0 && p.lo < a.cache.num_pages;
+        const bool ok_hi = p.hi >= 0 && p.hi < a.cache.num_pages;
+        if (((see_lo && !ok_lo) || (see_hi && !ok_hi)) && lane == 0)
+            atomicOr(&g_kv_attention_status, RN_STATUS_BAD_INDEX);
+        const bool use_lo = see_lo && ok_lo, use_hi = see_hi && ok_hi;
+        const int off = t0 & ((1 << log2_page) - 1);
+        const int64_t row_lo = use_lo ? a.cache.row(p.lo, 0, kvh, off) : 0;
+        // the second half's row, less 16 so that a token's row is row + token
+        const int64_t row_hi =
+            use_hi ? (log2_page == 4 ? a.cache.row(p.hi, 0, kvh, 0) - 16 : a.cache.row(p.hi, 0, kvh, off)) : -16;
+        const int live = it.hi - t0;  // tokens that exist
+        const uint32_t dst = ring_addr + stage * S::kStage;
+        constexpr int CPR = F::kRow / 16;               // chunks of a row
+        constexpr int ITER = kTile * CPR / 32;
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            const int chunk = i * 32 + lane;
+            const int t = chunk / CPR;
+            const bool use = t < 16 ? use_lo : use_hi;
+            const int64_t row = (t < 16 ? row_lo : row_hi) + t;
+            const uint8_t *src = a.cache.codes + row * F::kRow + (chunk % CPR) * 16;
+            const int bytes = use && t < live ? 16 : 0;
+            if (bytes == 0) src = a.cache.codes;
+            const uint32_t to = dst + swizzle<F::kRow>(chunk);
+            cp_async16(to, src, bytes);
+            cp_async16(to + S::kCodesBytes, bytes ? src + vrows * F::kRow : src, bytes);
+        }
+        constexpr int SCH = S::kScalesBytes / 16;       // chunks of the scales of keys, then of values
+        constexpr int PER = 16 / S::kScaleRow;          // tokens of a chunk
+#pragma unroll
+        for (int i = 0; i < (2 * SCH + 31) / 32; ++i) {
+            const int c = i * 32 + lane;
+            if (2 * SCH >= 32 || c < 2 * SCH) {
+                const int chunk = c % SCH;
+                const int t = chunk * PER;
+                const bool use = t < 16 ? use_lo : use_hi;
+                const int64_t row = (t < 16 ? row_lo : row_hi) + t + (c >= SCH ? vrows : 0);
+                int n = live - t;
+                n = n < 0 ? 0 : (n > PER ? PER : n);
+                const uint16_t *src = a.cache.scales + row * NG;
+                if (!use || n == 0) {
+                    src = a.cache.scales;
+                    n = 0;
+                }
+                cp_async16(dst + 2 * S::kCodesBytes + c * 16, src, n * S::kScaleRow);
+            }
+        }
+    };
+
+    // -- running state: column sums, and the finished product's rows ------------------
+    float o[S::MT][NT][4], l[NT][2], m[NT][2], ref[NT][2];
+    float corr[S::kOffsetSums ? NG : 1][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            l[nt][c] = 0.0f;
+            m[nt][c] = -INFINITY;
+            ref[nt][c] = 0.0f;
+        }
+#pragma unroll
+        for (int mt = 0; mt < S::MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.0f;
+    }
+    if constexpr (S::kOffsetSums) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) corr[g][i] = 0.0f;
+    }
+    // Value scales lie below 2^(scale_exp + 1); the weights are kept below
+    // 2^(14 - scale_exp), so that their products stay inside fp16.  Weights of 2^-28
+    // of the largest are still normal numbers there.
+    int scale_exp = 0;
+
+    const auto take_off = [&]() {  // the codes' offset, collected in corr, off the sums
+        if constexpr (S::kOffsetSums) {
+            constexpr float odd = BITS == 4 ? 16.0f : 1.0f;  // odd 4-bit rows count sixteenfold
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+#pragma unroll
+                for (int mt = 2 * g; mt < 2 * g + 2; ++mt) {
+                    o[mt][0][0] += corr[g][0];
+                    o[mt][0][1] += corr[g][1];
+                    o[mt][0][2] = fmaf(odd, corr[g][2], o[mt][0][2]);
+                    o[mt][0][3] = fmaf(odd, corr[g][3], o[mt][0][3]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) corr[g][i] = 0.0f;
+            }
+        }
+    };
+    int turn = 0;  // tiles since then
+
+    int k = k0 + warp;
+    Pages next = pages_of(k);
+#pragma unroll
+    for (int s = 0; s < S::kStages - 1; ++s) {
+        const int ks = k + s * kAttnWarps;
+        if (ks < k1) issue(ks, s, next);
+        next = pages_of(ks + kAttnWarps);
+        cp_async_commit();
+    }
+
+    // lane's places in a stage
+    const int key_a = (r >> 1) + 4 * (r & 1);  // token of its first operand row
+    constexpr int KW = NG * BITS / 4;          // words of a lane's share of a key row
+    constexpr int VW = D * BITS / 256;         // and of a value row
+    constexpr int KC = KW < 4 ? KW : 4, VC = VW < 4 ? VW : 4;
+
+    int stage = 0;
+    for (; k < k1; k += kAttnWarps) {
+        cp_async_wait<S::kStages - 2>();
+        __syncwarp();
+        {
+            const int kn = k + (S::kStages - 1) * kAttnWarps;
+            int sn = stage + S::kStages - 1;
+            sn = sn >= S::kStages ? sn - S::kStages : sn;
+            if (kn < k1) issue(kn, sn, next);
+            next = pages_of(kn + kAttnWarps);
+            cp_async_commit();
+        }
+        if constexpr (S::kOffsetSums) {
+            // The sums of stored codes carry the offset, about z sum(w) beside a signal
+            // that grows like its root, and the tensor core cuts every addition to fp32:
+            // taken off every eighth tile the offset never outgrows the signal.
+            if (++turn == 8) {
+                turn = 0;
+                take_off();
+            }
+        }
+        const uint32_t base = ring_addr + stage * S::kStage;
+        const uint32_t sbase = base + 2 * S::kCodesBytes;
+        stage = stage + 1 == S::kStages ? 0 : stage + 1;
+        const int t0 = it.token(k);
+
+        // -- logits, in log2: rows are tokens, columns queries --------------------------
+        float x[2][NT][4];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            uint32_t ka[KW], kb[KW], sa[NG / 2], sb[NG / 2];
+            const int ta = 16 * mt + key_a;
+#pragma unroll
+            for (int w = 0; w < KW; w += KC) {
+                const int c0 = (j * KW + w) / 4, in = (j * KW + w) % 4 * 4;
+                uint32_t v[KC];
+                lds_words<KC>(v, base + swizzle<F::kRow>(ta * (F::kRow / 16) + c0) + in);
+#pragma unroll
+                for (int i = 0; i < KC; ++i) ka[w + i] = v[i];
+                lds_words<KC>(v, base + swizzle<F::kRow>((ta + 8) * (F::kRow / 16) + c0) + in);
+#pragma unroll
+                for (int i = 0; i < KC; ++i) kb[w + i] = v[i];
+            }
+            lds_words<NG / 2>(sa, sbase + ta * S::kScaleRow);
+            lds_words<NG / 2>(sb, sbase + (ta + 8) * S::kScaleRow);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[mt][nt][i] = 0.0f;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                uint32_t f[2][4];  // operand registers of the group's two k-steps
+                if constexpr (BITS == 4) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const uint32_t wa = ka[g] >> (8 * s), wb = kb[g] >> (8 * s);
+                        f[s][0] = wa & 0x000F000Fu;
+                        f[s][1] = wb & 0x000F000Fu;
+                        f[s][2] = wa & 0x00F000F0u;
+                        f[s][3] = wb & 0x00F000F0u;
+                    }
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        f[s][0] = ka[2 * g + s] & 0x00FF00FFu;
+                        f[s][1] = kb[2 * g + s] & 0x00FF00FFu;
+                        f[s][2] = (ka[2 * g + s] >> 8) & 0x00FF00FFu;
+                        f[s][3] = (kb[2 * g + s] >> 8) & 0x00FF00FFu;
+                    }
+                }
+                if constexpr (!S::kOffsetSums) {
+                    constexpr uint32_t z = F::kZero * 0x00010001u, z2 = BITS == 4 ? 16 * z : z;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        f[s][0] = hsub2_bits(f[s][0], z);
+                        f[s][1] = hsub2_bits(f[s][1], z);
+                        f[s][2] = hsub2_bits(f[s][2], z2);
+                        f[s][3] = hsub2_bits(f[s][3], z2);
+                    }
+                }
+                const __half2 ha = *reinterpret_cast<const __half2 *>(&sa[g / 2]);
+                const __half2 hb = *reinterpret_cast<const __half2 *>(&sb[g / 2]);
+                const float fa = g & 1 ? __high2float(ha) : __low2float(ha);
+                const float fb = g & 1 ? __high2float(hb) : __low2float(hb);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    uint32_t q0, q1, q2, q3;
+                    if constexpr (S::kQueryRegs) {
+                        q0 = qreg[g][0][0];
+                        q1 = qreg[g][0][1];
+                        q2 = qreg[g][1][0];
+                        q3 = qreg[g][1][1];
+                    } else {
+                        const uint4 v = ld_shared16(qsm + ((nt * NG + g) * 32 + lane) * 16);
+                        q0 = v.x;
+                        q1 = v.y;
+                        q2 = v.z;
+                        q3 = v.w;
+                    }
+                    float d[4];
+                    if constexpr (S::kOffsetSums)
+                        mma_f16(d, f[0][0], f[0][1], f[0][2], f[0][3], q0, q1, offset[g][0], offset[g][1],
+                                offset[g][0], offset[g][1]);
+                    else
+                        mma_f16(d, f[0][0], f[0][1], f[0][2], f[0][3], q0, q1, 0.0f, 0.0f, 0.0f, 0.0f);
+                    mma_f16(d, f[1][0], f[1][1], f[1][2], f[1][3], q2, q3);
+                    x[mt][nt][0] = fmaf(fa, d[0], x[mt][nt][0]);
+                    x[mt][nt][1] = fmaf(fa, d[1], x[mt][nt][1]);
+                    x[mt][nt][2] = fmaf(fb, d[2], x[mt][nt][2]);
+                    x[mt][nt][3] = fmaf(fb, d[3], x[mt][nt][3]);
+                }
+            }
+        }
+
+        // -- mask ------------------------------------------------------------------------
+        const bool masked = t0 + kTile - 1 > it.lo_pos ||
+                            (a.window && t0 <= it.hi - 1 - a.window && t0 + kTile > a.sinks);
+        uint32_t hidden[NT];  // bit 4 mt + i: element x[mt][nt][i] is masked
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            hidden[nt] = 0u;
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[mt][nt][i] *= factor[nt][i & 1];
+        }
+        if (masked) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int pos = s_pos[nt * 8 + 2 * j + c];
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int t = t0 + 16 * mt + 8 * h + key_a;
+                            const bool see = t <= pos && (a.window == 0 || t > pos - a.window || t < a.sinks);
+                            if (!see) {
+                                x[mt][nt][2 * h + c] = -INFINITY;
+                                hidden[nt] |= 1u << (4 * mt + 2 * h + c);
+                            }
+                        }
+                }
+            }
+        }
+
+        // -- running maximum ----------------------------------------------------------------
+        float top[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                top[nt][c] = fmaxf(fmaxf(x[0][nt][c], x[0][nt][2 + c]), fmaxf(x[1][nt][c], x[1][nt][2 + c]));
+                grow |= top[nt][c] > m[nt][c];
+            }
+        // largest value scale of the tile's visible tokens, one token a lane (the
+        // pattern of a NaN is a negative integer)
+        int vtop;
+        {
+            constexpr int W = NG / 2;
+            uint32_t v[W];
+            lds_words<W>(v, sbase + S::kScalesBytes + lane * S::kScaleRow);
+            uint32_t mx = v[0];
+#pragma unroll
+            for (int i = 1; i < W; ++i) mx = __vmaxs2(mx, v[i]);
+            vtop = max(static_cast<int>(static_cast<int16_t>(mx & 0xFFFFu)),
+                       static_cast<int>(static_cast<int16_t>(mx >> 16)));
+            if (vtop > 0x7BFF || (masked && !seen_token(t0 + lane))) vtop = -1;
+            grow |= vtop >= (scale_exp + 16) << 10;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+            const int e = (__reduce_max_sync(0xffffffffu, vtop) >> 10) - 15;
+            scale_exp = e > scale_exp ? e : scale_exp;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float f[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float t = top[nt][c];
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                    t = fmaxf(t, m[nt][c]);
+                    const float nref = t == -INFINITY ? 0.0f : t - static_cast<float>(14 - scale_exp);
+                    f[c] = m[nt][c] == -INFINITY ? 1.0f : exp2_approx(ref[nt][c] - nref);
+                    ref[nt][c] = nref;
+                    m[nt][c] = t;
+                    l[nt][c] *= f[c];
+                }
+#pragma unroll
+                for (int mt = 0; mt < S::MT; ++mt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[mt][nt][i] *= f[i & 1];
+                if constexpr (S::kOffsetSums) {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) corr[g][i] *= f[i & 1];
+                }
+            }
+        }
+
+        // -- weights: rounded once to fp16, then tokens along the operand's k --------------
+        uint32_t p[2][NT][2];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = exp2_approx(x[mt][nt][i] - ref[nt][i & 1]);
+                l[nt][0] += w[0] + w[2];
+                l[nt][1] += w[1] + w[3];
+                if (masked) {
+                    // a masked weight is -0, so that it can be told from one that underflowed
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (hidden[nt] >> (4 * mt + i) & 1u) w[i] = -0.0f;
+                }
+                p[mt][nt][0] = transpose8(pack_h2(w[0], w[1]));
+                p[mt][nt][1] = transpose8(pack_h2(w[2], w[3]));
+            }
+
+        // -- values: rows are dimensions, k tokens j, j + 4, j + 8, j + 12 -----------------
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            uint32_t v[4][VW], vs[4][NG / 2];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int t = 16 * mt + 4 * n + j;
+#pragma unroll
+                for (int w = 0; w < VW; w += VC) {
+                    const int c0 = (r * VW + w) / 4, in = (r * VW + w) % 4 * 4;
+                    uint32_t u[VC];
+                    lds_words<VC>(u, base + S::kCodesBytes + swizzle<F::kRow>(t * (F::kRow / 16) + c0) + in);
+#pragma unroll
+                    for (int i = 0; i < VC; ++i) v[n][w + i] = u[i];
+                }
+                lds_words<NG / 2>(vs[n], sbase + S::kScalesBytes + t * S::kScaleRow);
+            }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const uint32_t half = g & 1 ? 0x7632u : 0x5410u;
+                const uint32_t s0 = __byte_perm(vs[0][g / 2], vs[1][g / 2], half);
+                const uint32_t s1 = __byte_perm(vs[2][g / 2], vs[3][g / 2], half);
+                uint32_t w0[NT], w1[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    w0[nt] = hmul2_bits(p[mt][nt][0], s0);
+                    w1[nt] = hmul2_bits(p[mt][nt][1], s1);
+                    if (masked) {  // a masked token's scale may be NaN
+                        w0[nt] &= ~__vcmpeq2(p[mt][nt][0], 0x80008000u);
+                        w1[nt] &= ~__vcmpeq2(p[mt][nt][1], 0x80008000u);
+                    }
+                }
+                if constexpr (S::kOffsetSums) {
+                    constexpr uint32_t z = (0x8000u | F::kZero) * 0x00010001u;  // -zero * 2^-24
+                    mma_f16(corr[g], z, z, z, z, w0[0], w1[0]);
+                }
+#pragma unroll
+                for (int hm = 0; hm < 2; ++hm) {
+                    uint32_t f0, f1, f2, f3;
+                    if constexpr (BITS == 4) {
+                        const uint32_t u0 = __byte_perm(v[0][g / 2], v[1][g / 2], half) >> (8 * hm);
+                        const uint32_t u1 = __byte_perm(v[2][g / 2], v[3][g / 2], half) >> (8 * hm);
+                        f0 = u0 & 0x000F000Fu;
+                        f1 = u0 & 0x00F000F0u;
+                        f2 = u1 & 0x000F000Fu;
+                        f3 = u1 & 0x00F000F0u;
+                    } else {
+                        const uint32_t u0 = __byte_perm(v[0][g], v[1][g], hm ? 0x7632u : 0x5410u);
+                        const uint32_t u1 = __byte_perm(v[2][g], v[3][g], hm ? 0x7632u : 0x5410u);
+                        f0 = u0 & 0x00FF00FFu;
+                        f1 = (u0 >> 8) & 0x00FF00FFu;
+                        f2 = u1 & 0x00FF00FFu;
+                        f3 = (u1 >> 8) & 0x00FF00FFu;
+                    }
+                    if constexpr (!S::kOffsetSums) {
+                        constexpr uint32_t z = F::kZero * 0x00010001u, z2 = BITS == 4 ? 16 * z : z;
+                        f0 = hsub2_bits(f0, z);
+                        f1 = hsub2_bits(f1, z2);
+                        f2 = hsub2_bits(f2, z);
+                        f3 = hsub2_bits(f3, z2);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(o[2 * g + hm][nt], f0, f1, f2, f3, w0[nt], w1[nt]);
+                }
+            }
+        }
+    }
+
+    take_off();
+    // -- join the warps ---------------------------------------------------------------------
+    cp_async_wait<0>();
+    __syncthreads();  // every ring is idle: its space takes the sums
+    float *sums = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float t = l[nt][c];
+            t += __shfl_xor_sync(0xffffffffu, t, 4);
+            t += __shfl_xor_sync(0xffffffffu, t, 8);
+            t += __shfl_xor_sync(0xffffffffu, t, 16);
+            const int col = nt * 8 + 2 * j + c;
+            if (r == 0) {
+                s_l[warp][col] = t;
+                s_ref[warp][col] = m[nt][c] == -INFINITY ? -INFINITY : ref[nt][c];
+            }
+            if (col < it.ncols) {
+#pragma unroll
+                for (int mt = 0; mt < S::MT; ++mt) {
+                    float e = o[mt][nt][c], d = o[mt][nt][2 + c];
+                    if constexpr (BITS == 4) d *= 0.0625f;
+                    *reinterpret_cast<float2 *>(sums + (warp * NQ + col) * D + 16 * mt + 2 * r) = make_float2(e, d);
+                }
+            }
+        }
     __syncthreads();
-    float mm = -INFINITY, ll = 0.0f;
-    for (int k = 0; k < kAttnThreads / 32; ++k) mm = fmaxf(mm, sm_m[k]);
-    const float base = mm == -INFINITY ? 0.0f : mm;
-    float f[kAttnThreads / 32];
-    for (int k = 0; k < kAttnThreads / 32; ++k) {
-        f[k] = exp2f(sm_m[k] - base);
-        ll += sm_l[k] * f[k];
+    constexpr int QUADS = D / 4;  // threads of a column
+    for (int idx = threadIdx.x; idx < it.ncols * QUADS; idx += kAttnThreads) {
+        const int col = idx / QUADS, d0 = idx % QUADS * 4;
+        float top = -INFINITY, l_all = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, s_ref[w][col]);
+        const float base = top == -INFINITY ? 0.0f : top;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) {
+            const float f = exp2_approx(s_ref[w][col] - base);
+            l_all = fmaf(s_l[w][col], f, l_all);
+            const float4 v = *reinterpret_cast<const float4 *>(sums + (w * NQ + col) * D + d0);
+            acc.x = fmaf(v.x, f, acc.x);
+            acc.y = fmaf(v.y, f, acc.y);
+            acc.z = fmaf(v.z, f, acc.z);
+            acc.w = fmaf(v.w, f, acc.w);
+        }
+        if (part) {
+            *reinterpret_cast<float4 *>(part + col * D + d0) = acc;
+            if (d0 == 0) {
+                part[NQ * D + col] = top;
+                part[NQ * D + NQ + col] = l_all;
+            }
+        } else {
+            store_result<D>(a, it, head0, col, d0, acc, base, l_all);
+        }
     }
-    for (int d = threadIdx.x; d < D; d += kAttnThreads) {
-        float x = 0.0f;
-        for (int k = 0; k < kAttnThreads / 32; ++k) x = fmaf(sm_o[k][d], f[k], x);
-        x = ll == 0.0f ? 0.0f : x / ll;
-        a.out[(t * a.Hq + h) * D + d] = static_cast<uint16_t>(pack_bf2(x, 0.0f));
+    __syncthreads();  // the rings and the shared words are free again
+}
+
+template <int D, int BITS, int NT>
+__global__ void __launch_bounds__(kAttnThreads, AttnShape<D, BITS, NT>::kCtas)
+    kv_attention_kernel(const KvAttnArgs a) {
+    using S = AttnShape<D, BITS, NT>;
+    extern __shared__ __align__(128) uint8_t attn_smem[];
+    __shared__ int64_t scratch[kAttnWarps + 2];
+    pdl_trigger();
+    pdl_wait();
+    const Line line = find_unit<S::NQ>(a, blockIdx.x == 0, scratch);
+    const int64_t ctas = line_ctas(line.units, a.grid);
+    if (line.units == 0 || blockIdx.x >= ctas) return;
+    const int64_t u0 = line_start(line.units, ctas, blockIdx.x);
+    const int64_t u1 = line_start(line.units, ctas, blockIdx.x + 1);
+    int64_t item = line.item, before = line.before, u = u0;
+    while (u < u1) {
+        const int64_t b = item / a.q_tiles;
+        const Item it = make_item<S::NQ>(a, b, item % a.q_tiles);
+        if (it.n == 0) {
+            ++item;
+            continue;
+        }
+        const int64_t in = u - before * a.cache.Hkv;
+        const int head = static_cast<int>(in / it.n), k0 = static_cast<int>(in % it.n);
+        const int64_t left = u1 - u;
+        const int k1 = it.n - k0 <= left ? it.n : k0 + static_cast<int>(left);
+        float *part = nullptr;
+        if (k1 - k0 != it.n) part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1)) * S::kSlot;
+        attend_run<D, BITS, NT>(a, it, b, head, k0, k1, part, attn_smem);
+        u += k1 - k0;
+        if (k1 == it.n && head == a.cache.Hkv - 1) {
+            before += it.n;
+            ++item;
+        }
     }
-    if (threadIdx.x == 0 && a.lse)
-        a.lse[t * a.Hq + h] = ll == 0.0f ? -INFINITY : base * 0.6931471805599453f + logf(ll);
+}
+
+// ---- joining the pieces of a cut (query tile, head) -------------------------------------
+
+// One block for one item and kv head: nothing to do where one CTA held it all;
+// rows that see no token get their zeros here.
+template <int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads) kv_attention_join_kernel(const KvAttnArgs a) {
+    constexpr int NQ = 8 * NT, SLOT = NQ * (D + 2), QUADS = D / 4;
+    pdl_trigger();
+    pdl_wait();
+    const int64_t item = blockIdx.x;
+    const int kvh = blockIdx.y, Hkv = a.cache.Hkv;
+    const int64_t before = a.prefix[item], n = a.prefix[item + 1] - before;
+    const int64_t units = a.prefix[a.B * a.q_tiles] * Hkv;
+    int64_t c0 = 0, c1 = -1, first = 0, ctas = 1;
+    if (n > 0) {
+        first = before * Hkv + kvh * n;
+        ctas = line_ctas(units, a.grid);
+        // the CTAs that hold the first and the last unit
+        c0 = first * ctas / units;
+        while (line_start(units, ctas, c0 + 1) <= first) ++c0;
+        c1 = (first + n - 1) * ctas / units;
+        while (line_start(units, ctas, c1 + 1) <= first + n - 1) ++c1;
+        if (c0 == c1) return;
+    }
+    const Item it = make_item<NQ>(a, item / a.q_tiles, item % a.q_tiles);
+    for (int idx = threadIdx.x; idx < it.ncols * QUADS; idx += kAttnThreads) {
+        const int col = idx / QUADS, d0 = idx % QUADS * 4;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float l = 0.0f, top = -INFINITY;
+        for (int64_t c = c0; c <= c1; ++c) {
+            const int64_t slot = 2 * c + (c == c0 && line_start(units, ctas, c) != first ? 1 : 0);
+            const float *part = a.partial + slot * SLOT;
+            const float pr = part[NQ * D + col], pl = part[NQ * D + NQ + col];
+            const float4 v = *reinterpret_cast<const float4 *>(part + col * D + d0);
+            const float nt = fmaxf(top, pr);
+            const float base = nt == -INFINITY ? 0.0f : nt;
+            const float f = exp2_approx(top - base), g = exp2_approx(pr - base);
+            acc.x = fmaf(v.x, g, acc.x * f);
+            acc.y = fmaf(v.y, g, acc.y * f);
+            acc.z = fmaf(v.z, g, acc.z * f);
+            acc.w = fmaf(v.w, g, acc.w * f);
+            l = fmaf(pl, g, l * f);
+            top = nt;
+        }
+        store_result<D>(a, it, kvh * a.group, col, d0, acc, top == -INFINITY ? 0.0f : top, l);
+    }
 }
 
 int kv_attention_status(unsigned int *out, int clear) {
     return kv_status_word(g_kv_attention_status, out, clear);
 }
 
-template <int D, int BITS>
-static int kv_attention_launch(const KvAttnArgs &a, cudaStream_t st) {
-    return launch_pdl(kv_attention_simple_kernel<D, BITS>,
-                      dim3(static_cast<unsigned>(a.T), static_cast<unsigned>(a.Hq)),
+// ---- host -------------------------------------------------------------------------------
+
+// Columns of a query tile, in eights: the smallest that holds all queries of a
+// sequence times the heads of a group, else the largest the registers hold.
+static int attn_tiles(int D, int64_t columns) {
+    if (columns <= 8) return 1;
+    if (columns <= 16 || D == 256) return 2;
+    return 4;
+}
+
+struct AttnPlan {
+    int nt;
+    int64_t q_tiles;
+    int grid;
+    int64_t prefix_bytes;
+    int64_t bytes;
+};
+
+template <int D, int BITS, int NT>
+static AttnPlan attn_plan_of(int sm_count, int64_t B, int group, int64_t max_q_len) {
+    using S = AttnShape<D, BITS, NT>;
+    AttnPlan p;
+    p.nt = NT;
+    p.q_tiles = (max_q_len * group + S::NQ - 1) / S::NQ;
+    p.grid = sm_count * S::kCtas;
+    p.prefix_bytes = ((B * p.q_tiles + 1) * 8 + 15) / 16 * 16;
+    p.bytes = p.prefix_bytes + static_cast<int64_t>(p.grid) * 2 * S::kSlot * 4;
+    return p;
+}
+
+// Calls f with the compile-time D, BITS and NT of a checked call.
+template <typename Fn>
+static auto attn_dispatch(int D, int format, int64_t columns, Fn &&f) {
+    const int nt = attn_tiles(D, columns);
+    return kv_dispatch(D, format, [&](auto d, auto bits) {
+        if (nt == 1) return f(d, bits, std::integral_constant<int, 1>());
+        if (nt == 2) return f(d, bits, std::integral_constant<int, 2>());
+        if constexpr (d.value == 256) {
+            return f(d, bits, std::integral_constant<int, 2>());
+        } else {
+            return f(d, bits, std::integral_constant<int, 4>());
+        }
+    });
+}
+
+static AttnPlan attn_plan(int sm_count, int format, int64_t B, int Hq, int Hkv, int D, int64_t max_q_len) {
+    const int group = Hq / Hkv;
+    return attn_dispatch(D, format, max_q_len * group, [&](auto d, auto bits, auto nt) {
+        return attn_plan_of<d.value, bits.value, nt.value>(sm_count, B, group, max_q_len);
+    });
+}
+
+template <int D, int BITS, int NT>
+static int attn_launch(const KvAttnArgs &a, cudaStream_t st) {
+    using S = AttnShape<D, BITS, NT>;
+    static std::atomic<int> attr_done[kMaxDevices];
+    const int dev = current_device_index();
+    if (dev < 0 || dev >= kMaxDevices) return RN_ERR_DEVICE;
+    const auto kernel = kv_attention_kernel<D, BITS, NT>;
+    if (!attr_done[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess) {
+            cudaGetLastError();
+            return RN_ERR_DEVICE;
+        }
+        attr_done[dev].store(1, std::memory_order_release);
+    }
+    const int rc = launch_pdl(kernel, dim3(static_cast<unsigned>(a.grid)), dim3(kAttnThreads), S::kSmem, st, a);
+    if (rc != RN_OK) return rc;
+    return launch_pdl(kv_attention_join_kernel<D, NT>,
+                      dim3(static_cast<unsigned>(a.B * a.q_tiles), static_cast<unsigned>(a.cache.Hkv)),
                       dim3(kAttnThreads), 0, st, a);
 }
 
@@ -161,6 +1122,8 @@ static int kv_attention_check(int format, int64_t B, int Hq, int Hkv, int D, int
     if (rc != RN_OK) return rc;
     if (Hq < 1 || Hq > 65535 || Hq % Hkv != 0) return RN_ERR_SHAPE;
     if (B < 0 || B > INT32_MAX / Hq || max_q_len < 0 || max_q_len > INT32_MAX / Hq) return RN_ERR_SHAPE;
+    // one block of the second kernel for each sequence and query tile
+    if (B > 0 && (max_q_len * (Hq / Hkv) + 7) / 8 > INT32_MAX / B) return RN_ERR_SHAPE;
     return RN_OK;
 }
 
@@ -172,7 +1135,10 @@ int64_t kv_attention_workspace_bytes(int format, int64_t B, int Hq, int Hkv, int
                                      int64_t max_q_len) {
     const int rc = rn::kv_attention_check(format, B, Hq, Hkv, D, max_q_len);
     if (rc != RN_OK) return rc;
-    return 16;
+    const rn::DeviceInfo *dev = rn::current_device_info();
+    if (!dev) return RN_ERR_DEVICE;
+    if (B == 0 || max_q_len == 0) return 16;
+    return rn::attn_plan(dev->sm_count, format, B, Hq, Hkv, D, max_q_len).bytes;
 }
 
 int kv_attention_fwd(const rn_bf16 *q, int64_t q_stride, const uint8_t *codes,
@@ -200,9 +1166,10 @@ int kv_attention_fwd(const rn_bf16 *q, int64_t q_stride, const uint8_t *codes,
         ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(kv_lens) |
           reinterpret_cast<uintptr_t>(lse)) & 3u))
         return RN_ERR_ALIGN;
-    if (workspace_bytes < kv_attention_workspace_bytes(format, B, Hq, Hkv, D, max_q_len))
-        return RN_ERR_ARG;
-    if (!rn::current_device_info()) return RN_ERR_DEVICE;
+    const rn::DeviceInfo *dev = rn::current_device_info();
+    if (!dev) return RN_ERR_DEVICE;
+    const rn::AttnPlan plan = rn::attn_plan(dev->sm_count, format, B, Hq, Hkv, D, max_q_len);
+    if (workspace_bytes < plan.bytes) return RN_ERR_ARG;
     rn::KvAttnArgs a;
     a.q = q;
     a.q_stride = q_stride;
@@ -217,12 +1184,17 @@ int kv_attention_fwd(const rn_bf16 *q, int64_t q_stride, const uint8_t *codes,
     a.max_q_len = max_q_len;
     a.Hq = Hq;
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.window = window;
-    a.sinks = sinks;
+    a.group = Hq / Hkv;
+    a.window = static_cast<int>(window < INT32_MAX ? window : INT32_MAX);
+    a.sinks = static_cast<int>(sinks < INT32_MAX ? sinks : INT32_MAX);
     a.out = out;
     a.lse = lse;
-    return rn::kv_dispatch(D, format, [&](auto d, auto bits) {
-        return rn::kv_attention_launch<d.value, bits.value>(a, reinterpret_cast<cudaStream_t>(stream));
+    a.prefix = static_cast<int64_t *>(workspace);
+    a.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.prefix_bytes);
+    a.q_tiles = plan.q_tiles;
+    a.grid = plan.grid;
+    return rn::attn_dispatch(D, format, max_q_len * a.group, [&](auto d, auto bits, auto nt) {
+        return rn::attn_launch<d.value, bits.value, nt.value>(a, reinterpret_cast<cudaStream_t>(stream));
     });
 }
 

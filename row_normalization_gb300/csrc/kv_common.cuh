@@ -70,7 +70,7 @@ inline int kv_check_sizes(int format, int Hkv, int D, int page_size, int64_t num
 
 // Calls f with the compile-time head size and bits of a checked (D, format).
 template <typename Fn>
-inline int kv_dispatch(int D, int format, Fn &&f) {
+inline auto kv_dispatch(int D, int format, Fn &&f) {
     if (format == RN_KV_INT4) {
         if (D == 64) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 4>());
         if (D == 128) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 4>());

@@ -79,6 +79,18 @@ class Cache:
                 scale_bits(s[:, which]).view(np.float16))
             self.vals[pg, which, :, off] = values(c[:, which], s[:, which])
 
+    def token_scales(self, table_row, which: int, lo: int, hi: int) -> torch.Tensor:
+        """fp64 [hi - lo, Hkv, D]: the scale of every element, NaN as zero."""
+        out = []
+        for p in range(lo, hi):
+            pg = int(table_row[p // self.P])
+            if 0 <= pg < self.codes.shape[0]:
+                sc = torch.nan_to_num(self.scales[pg, which, :, p % self.P].double(), nan=0.0)
+                out.append(sc.repeat_interleave(32, dim=-1))
+            else:
+                out.append(torch.zeros_like(self.vals[0, which, :, 0]))
+        return torch.stack(out) if out else self.vals.new_zeros(0, *self.vals.shape[2:3], self.D)
+
     def tokens(self, table_row, which: int, lo: int, hi: int) -> torch.Tensor:
         """fp64 [hi - lo, Hkv, D]; pages outside the cache read as zeros."""
         out = []
@@ -93,25 +105,22 @@ class Cache:
 
 def attention(q, K, V, L: int, scale: float, window: int = 0, sinks: int = 0):
     """q [n, Hq, D], K and V [L, Hkv, D]: the newest n of L tokens.
-    Returns (out, lse, sum of weights * |v|, largest sum |q k| * scale) in fp64."""
+    Returns (out, lse, weights) in fp64; weights[i][h] is (token numbers, their weights)."""
     n, Hq, D = q.shape
     G = Hq // K.shape[1] if K.shape[1] else 1
     q = q.double()
     out = torch.zeros(n, Hq, D, dtype=torch.float64)
     lse = torch.full((n, Hq), -math.inf, dtype=torch.float64)
-    mag = torch.zeros(n, Hq, D, dtype=torch.float64)
-    big = 0.0
+    weights = [[None] * Hq for _ in range(n)]
     for i in range(n):
         p = L - n + i
         js = [j for j in range(0, p + 1) if window == 0 or j > p - window or j < sinks]
         if not js:
             continue
         for h in range(Hq):
-            k, v = K[js, h // G], V[js, h // G]
-            s = (k @ q[i, h]) * scale
-            big = max(big, float(torch.nan_to_num((k.abs() @ q[i, h].abs()) * abs(scale)).max()))
+            s = (K[js, h // G] @ q[i, h]) * scale
             lse[i, h] = torch.logsumexp(s, 0)
             w = torch.exp(s - lse[i, h])
-            out[i, h] = w @ v
-            mag[i, h] = w @ v.abs()
-    return out, lse, mag, big
+            out[i, h] = w @ V[js, h // G]
+            weights[i][h] = (js, w)
+    return out, lse, weights

@@ -2,14 +2,22 @@
 
 Tolerance of an output element (derived, nothing fitted):
   * the result is rounded once to bf16: eps/2 * |out|;
-  * a weight p and its product with a value scale are each rounded to fp16,
-    relative 2^-12 twice: 2^-11 * sum w |v|, and what falls below fp16's normal
-    range is off by 2^-25 of the largest weight at most (weights are kept at
-    2^7 or more there): n * 2^-32 * max|v|, below 2^-12 of the scale for the
-    lengths here and only where every larger weight meets no value;
-  * a logit is an fp32 sum of exact products: at most (D + 8) * 2^-23 * sum|q k| scale,
-    which moves a weight by that fraction, its sum by the same: twice it;
-    exp2 and the running sums: 2^-20.
+  * a weight p and its product with a value scale are each rounded to fp16, whose
+    half step is 2^-11 relative (11 significant bits): together (1 + 2^-11)^2 - 1,
+    2^-10 * sum w |v| with the factor 1.01 below.  What falls below fp16's normal
+    range, 2^-28 of the largest weight, is off by 2^-39 of it at most: n * 2^-39
+    of the value's range, nothing beside the first term for the lengths here;
+  * the second product sums stored codes 0 .. 2z (z = 8 or 128, the codes' offset),
+    whose offset is taken off at the end, so the rounding of its fp32 sums goes by
+    2z * sum w s.  One instruction adds 17 numbers, each cut to the largest one's 24
+    bits (17 * 2^-24); the caches here have fewer than 4 * 4 * 304 tiles, so a warp
+    takes two tiles of two instructions at most, and fewer than 200 partial sums are
+    joined by fused multiply-adds: together under 300 * 2^-24;
+  * a logit's group sum takes two such instructions over q * code, with z * sum q
+    taken off: 34 * 2^-24 * s * max(2z max|q|, z |sum q|) a group, then D / 32 fused
+    multiply-adds and two roundings: 10 * 2^-24 * sum |q k|, all times the scale.  A
+    logit moves a weight by that fraction and the weights' sum by the same: twice it;
+  * exp2 and the running sums: 2^-20.
 lse: the logit's error plus 2^-20 plus 2^-22 |lse|.
 """
 from __future__ import annotations
@@ -73,15 +81,32 @@ def check(got, lse, q, ref, table, lens, cu, scale, window=0, sinks=0):
             continue
         K, V = (ref.tokens(table[b], w, 0, n) for w in (0, 1))
         # tokens no query sees may sit on pages that are gone
-        o, l, mag, big = kv_ref.attention(q[lo:hi], K, V, n, scale, window, sinks)
-        dlogit = (D + 8) * 2.0 ** -23 * big
-        tol = EPS * o.abs() + (2.0 ** -11 + 2 * dlogit + 2.0 ** -20) * 1.01 * mag + 2.0 ** -40
+        o, l, weights = kv_ref.attention(q[lo:hi], K, V, n, scale, window, sinks)
+        SK, SV = (ref.token_scales(table[b], w, 0, n) for w in (0, 1))
+        z = 8 if ref.bits == 4 else 128
+        G = q.shape[1] // K.shape[1]
+        tol, dl = torch.full_like(o, 2.0 ** -40), torch.zeros_like(l)
+        for i in range(hi - lo):
+            for h in range(q.shape[1]):
+                if weights[i][h] is None:
+                    continue
+                js, w = weights[i][h]
+                x = q[lo + i, h].double()
+                k, sk = K[js, h // G], SK[js, h // G]
+                grp = x.view(-1, 32)
+                per = torch.maximum(2 * z * grp.abs().amax(1), z * grp.sum(1).abs())
+                e = 34 * (sk[:, ::32] @ per) + 10 * (k.abs() @ x.abs())
+                dlogit = float(e.max()) * 2.0 ** -24 * abs(scale)
+                dl[i, h] = dlogit
+                tol[i, h] += (2.0 ** -10 + 2 * dlogit + 2.0 ** -20) * 1.01 * (w @ V[js, h // G].abs())
+                tol[i, h] += 300 * 2.0 ** -24 * 2 * z * (w @ SV[js, h // G])
+        tol += EPS * o.abs()
         err = (got[lo:hi].double() - o).abs()
         assert (err <= tol).all(), (b, n, float((err / tol).max()))
         g = lse[lo:hi].double()
         assert torch.equal(torch.isinf(g), torch.isinf(l))
         ok = ~torch.isinf(l)
-        assert ((g - l)[ok].abs() <= dlogit + 2.0 ** -20 + 2.0 ** -22 * l[ok].abs()).all()
+        assert ((g - l)[ok].abs() <= dl[ok] + 2.0 ** -20 + 2.0 ** -22 * l[ok].abs()).all()
 
 
 def attend(ref, table, lens, q, n_q, Hq, scale=None, **kw):
