@@ -26,7 +26,8 @@
 //
 // Work is cut evenly over a fixed grid: all (sequence, query tile, kv head,
 // 32-token tile) units form one line, of which every CTA takes an equal run,
-// so ragged lengths leave no CTA behind.  A run that cuts a (query tile, head)
+// so ragged lengths leave no CTA behind.  Each (query tile, head) also has
+// kLead units without work in front, for what it costs to begin and end one.  A run that cuts a (query tile, head)
 // leaves partial sums in the workspace, which a second kernel joins in the
 // order of the line.  Inside a CTA four warps take every fourth tile with an
 // asynchronous copy ring of their own each and join at the end.
@@ -64,6 +65,12 @@ struct KvAttnArgs {
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kTile = 32;          // tokens a warp takes at once
+constexpr int kWaves = 1;          // CTAs launched for each one that fits the GPU at once
+constexpr float kSlack = 6.0f;       // powers of two a weight may grow before a rescale
+// Units without work in front of each (query tile, head): its queries, first page and
+// copies, and the joining of its warps.  64 ragged sequences of 8 heads (540k tokens):
+// 175 us with none, 158 with 8, 128 with 16, 132 with 32; 4 long ones 124-126 throughout.
+constexpr int kLead = 16;
 constexpr int kMinTiles = kAttnWarps;  // a CTA's run is no shorter: one tile a warp
 
 // Shapes of an instantiation: NT * 8 columns (queries of the tile times heads).
@@ -84,9 +91,12 @@ struct AttnShape {
     // shared memory for a ring of two stages or more
     static constexpr int kQuery = kQueryRegs ? 0 : NQ * D * 2;
     static constexpr int kRoom = 224 * 1024;
-    static constexpr int stages_at(int ctas) { return (kRoom / ctas - 2048 - kQuery) / (kAttnWarps * kStage); }
+    static constexpr int stages_at(int ctas) { return ctas < 1 ? 0 : (kRoom / ctas - 2048 - kQuery) / (kAttnWarps * kStage); }
     static constexpr int kByRegs = MT * NT * 4 >= 64 ? 2 : (D == 64 ? 4 : 3);
-    static constexpr int kCtas = stages_at(kByRegs) >= 2 ? kByRegs : 1;
+    static constexpr int kStep = 2;  // 16-token halves of a tile taken at once
+    static constexpr int kCtas = stages_at(kByRegs) >= 2         ? kByRegs
+                                 : stages_at(kByRegs - 1) >= 2 ? kByRegs - 1
+                                                               : kByRegs - 2;
     static constexpr int kStages = stages_at(kCtas) > 4 ? 4 : stages_at(kCtas);
     static_assert(kStages >= 2, "the ring needs two stages");
     static constexpr int kRing = kAttnWarps * kStages * kStage;
@@ -168,17 +178,26 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[WORDS], uint32_t addr) {
 // key operand (8 tokens, 4 runs of a row each) and the value operand (4
 // tokens, 8 runs each).  Masks found by trying all that are linear in the
 // line's number.
+// Sixteen tokens on, the mask is the same; 32 chunks on, it changes by a constant
+// (swizzle_step), so both users keep one offset a lane.
 template <int ROW>
-__device__ __forceinline__ int swizzle(int chunk) {
-    constexpr int m0 = ROW == 32 ? 4 : (ROW == 256 ? 1 : 2);
-    constexpr int m1 = ROW == 32 ? 0 : (ROW == 256 ? 1 : 4);
-    constexpr int m2 = ROW >= 128 ? (ROW == 256 ? 4 : 1) : 0;
-    constexpr int m3 = ROW == 256 ? 2 : 0;
+struct Swizzle {
+    static constexpr int m0 = ROW == 32 ? 4 : (ROW == 256 ? 1 : 2);
+    static constexpr int m1 = ROW == 32 ? 0 : (ROW == 256 ? 1 : 4);
+    static constexpr int m2 = ROW >= 128 ? (ROW == 256 ? 4 : 1) : 0;
+    static constexpr int m3 = ROW == 256 ? 2 : 0;
+};
+template <int ROW>
+__device__ __forceinline__ uint32_t swizzle(int chunk) {
+    using W = Swizzle<ROW>;
     const int line = chunk >> 3;
-    int x = chunk ^ ((line & 1) * m0) ^ ((line >> 1 & 1) * m1);
-    if (m2) x ^= (line >> 2 & 1) * m2;
-    if (m3) x ^= (line >> 3 & 1) * m3;
-    return x * 16;
+    return 16 * (chunk ^ ((line & 1) * W::m0) ^ ((line >> 1 & 1) * W::m1) ^ ((line >> 2 & 1) * W::m2) ^
+                 ((line >> 3 & 1) * W::m3));
+}
+// swizzle(32 i + lane) = 512 i + (swizzle(lane) ^ swizzle_step(i)), lane < 32.
+template <int ROW>
+constexpr uint32_t swizzle_step(int i) {
+    return 16 * (((i & 1) * Swizzle<ROW>::m2) ^ ((i >> 1 & 1) * Swizzle<ROW>::m3));
 }
 
 // ---- the line of units ------------------------------------------------------------
@@ -194,6 +213,9 @@ struct Item {
     int lo_tile;
     int n;           // tiles in all
     bool bad;        // something had to be cut to the tensors
+
+    // its units on the line, for one head
+    __device__ __forceinline__ int units() const { return n > 0 ? n + kLead : 0; }
 
     __device__ __forceinline__ int token(int k) const {
         return (k < sink_tiles ? k : lo_tile + (k - sink_tiles)) * kTile;
@@ -275,7 +297,7 @@ __device__ __forceinline__ void store_result(const KvAttnArgs &a, const Item &it
 // every CTA runs it over all items, so that no launch has to come before.
 struct Line {
     int64_t units;        // in all, over every kv head
-    int64_t item, before; // the item at a wanted unit, and the tiles of one head before it
+    int64_t item, before; // the item at a wanted unit, and the units of one head before it
 };
 
 template <int NQ>
@@ -289,7 +311,7 @@ __device__ __forceinline__ Line find_unit(const KvAttnArgs &a, bool publish, int
     bool bad = false;
     for (int64_t i = i0; i < i1; ++i) {
         const Item it = make_item<NQ>(a, i / a.q_tiles, i % a.q_tiles);
-        sum += it.n;
+        sum += it.units();
         bad |= it.bad;
     }
     if (publish && bad) atomicOr(&g_kv_attention_status, RN_STATUS_BAD_INDEX);
@@ -311,7 +333,7 @@ __device__ __forceinline__ Line find_unit(const KvAttnArgs &a, bool publish, int
         int64_t run = before;
         for (int64_t i = i0; i < i1; ++i) {
             a.prefix[i] = run;
-            run += make_item<NQ>(a, i / a.q_tiles, i % a.q_tiles).n;
+            run += make_item<NQ>(a, i / a.q_tiles, i % a.q_tiles).units();
         }
         if (tid == 0) a.prefix[items] = total;
     }
@@ -322,7 +344,7 @@ __device__ __forceinline__ Line find_unit(const KvAttnArgs &a, bool publish, int
     if (blockIdx.x < ctas && before * a.cache.Hkv <= u && u < (before + sum) * a.cache.Hkv) {
         int64_t run = before;
         for (int64_t i = i0; i < i1; ++i) {
-            const int n = make_item<NQ>(a, i / a.q_tiles, i % a.q_tiles).n;
+            const int n = make_item<NQ>(a, i / a.q_tiles, i % a.q_tiles).units();
             if (u < (run + n) * a.cache.Hkv) {
                 scratch[kAttnWarps] = i;
                 scratch[kAttnWarps + 1] = run;
@@ -370,10 +392,13 @@ struct Query {
         const bool finite = amax < 0x7F80u;
         int e = static_cast<int>(amax >> 7);   // biased exponent
         e = e < 14 ? 14 : e;
-        const float up = __uint_as_float(static_cast<uint32_t>(267 - (finite ? e : 127)) << 23);  // 2^(140 - e)
-        // codes are c * 2^-24: factor = scale * 2^(e - 140 + 24), in two exact steps
-        factor = finite ? ldexpf(a.scale_log2, e - 116) : __uint_as_float(0x7FC00000u);
-        if (!live) factor = 0.0f;
+        const float up = copysignf(__uint_as_float(static_cast<uint32_t>(267 - (finite ? e : 127)) << 23),
+                                   a.scale_log2);  // 2^(140 - e)
+        // codes are c * 2^-24: factor = |scale| * 2^(e - 140 + 24)
+        // (a negative scale turns the query's sign, and a zero one is as good as 2^-126:
+        // the factor is positive, so it can multiply a maximum, or a masked -infinity)
+        factor = fmaxf(ldexpf(fabsf(a.scale_log2), e - 116), 0x1p-126f);
+        if (!finite) factor = __uint_as_float(0x7FC00000u);
 #pragma unroll
         for (int g = 0; g < F::kGroups; ++g) {
             float x[8];
@@ -467,7 +492,15 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
     const uint32_t ring_addr = smem_addr(ring);
     const int log2_page = a.cache.log2_page;
     const int32_t *table = a.page_table + b * a.max_pages;
-    const int64_t vrows = static_cast<int64_t>(a.cache.Hkv) << log2_page;  // key rows to value rows
+    // the lane's first chunk in page 0 of this head, and the way to the next page and
+    // from a key to its value
+    constexpr int SCH = S::kScalesBytes / 16;  // chunks of a tile's key scales (then the values')
+    const uint32_t copy_off = swizzle<F::kRow>(lane);
+    const int64_t vrows = static_cast<int64_t>(a.cache.Hkv) << log2_page;
+    const int64_t head_row = static_cast<int64_t>(kvh) << log2_page;
+    const uint8_t *codes0 = a.cache.codes + head_row * F::kRow + lane * 16;
+    const uint8_t *scales0 = reinterpret_cast<const uint8_t *>(a.cache.scales) + head_row * S::kScaleRow +
+                             (lane % SCH) * 16 + (SCH < 32 && lane >= SCH ? vrows * S::kScaleRow : 0);
 
     struct Pages {
         int lo, hi;  // of the tile's two halves (16 tokens each lie on one page)
@@ -477,8 +510,7 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
         if (k < k1) {
             const int t0 = it.token(k);
             p.lo = table[t0 >> log2_page];
-            p.hi = p.lo;
-            if (log2_page == 4) p.hi = t0 + 16 < it.hi ? table[(t0 >> 4) + 1] : -1;
+            if (log2_page == 4 && t0 + 16 < it.hi) p.hi = table[(t0 >> 4) + 1];
         }
         return p;
     };
@@ -488,57 +520,52 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
     const auto seen_token = [&](int t) {
         return t < it.hi && (it.win_lo == 0 || t < a.sinks || t >= it.win_lo);
     };
-    // Copies tile k into a stage.  Rows behind the last visible token, and rows of
-    // pages on which nothing is visible or that do not exist, arrive as zeros.
-    const auto issue = [&](int k, int stage, Pages p) {
-        const int t0 = it.token(k);
-        const bool see_lo = seen(t0), see_hi = seen(t0 + 16);
-        const bool ok_lo = p.lo >= 0 && p.lo < a.cache.num_pages;
-        const bool ok_hi = p.hi >= 0 && p.hi < a.cache.num_pages;
-        if (((see_lo && !ok_lo) || (see_hi && !ok_hi)) && lane == 0)
-            atomicOr(&g_kv_attention_status, RN_STATUS_BAD_INDEX);
-        const bool use_lo = see_lo && ok_lo, use_hi = see_hi && ok_hi;
-        const int off = t0 & ((1 << log2_page) - 1);
-        const int64_t row_lo = use_lo ? a.cache.row(p.lo, 0, kvh, off) : 0;
-        // the second half's row, less 16 so that a token's row is row + token
-        const int64_t row_hi =
-            use_hi ? (log2_page == 4 ? a.cache.row(p.hi, 0, kvh, 0) - 16 : a.cache.row(p.hi, 0, kvh, off)) : -16;
-        const int live = it.hi - t0;  // tokens that exist
-        const uint32_t dst = ring_addr + stage * S::kStage;
-        constexpr int CPR = F::kRow / 16;               // chunks of a row
-        constexpr int ITER = kTile * CPR / 32;
+    // Copies rows [FROM, TO) of a tile (halves or all of it), which lie on one page
+    // starting at row `off` of it.  bytes = 0 writes zeros instead.
+    const auto copy_rows = [&](auto from, auto to, uint32_t dst, int64_t page, int off, int bytes) {
+        constexpr int FROM = decltype(from)::value, TO = decltype(to)::value;
+        constexpr int CPR = F::kRow / 16;  // chunks of a row, and copies a lane makes of a tile
+        const int64_t row = (page * 2 * a.cache.Hkv << log2_page) + off - FROM;
+        const uint8_t *src = codes0 + row * F::kRow;
+        const uint8_t *vsrc = src + vrows * F::kRow;
 #pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-            const int chunk = i * 32 + lane;
-            const int t = chunk / CPR;
-            const bool use = t < 16 ? use_lo : use_hi;
-            const int64_t row = (t < 16 ? row_lo : row_hi) + t;
-            const uint8_t *src = a.cache.codes + row * F::kRow + (chunk % CPR) * 16;
-            const int bytes = use && t < live ? 16 : 0;
-            if (bytes == 0) src = a.cache.codes;
-            const uint32_t to = dst + swizzle<F::kRow>(chunk);
-            cp_async16(to, src, bytes);
-            cp_async16(to + S::kCodesBytes, bytes ? src + vrows * F::kRow : src, bytes);
+        for (int i = CPR * FROM / kTile; i < CPR * TO / kTile; ++i) {
+            const uint32_t d = dst + 512 * i + (copy_off ^ swizzle_step<F::kRow>(i));
+            cp_async16(d, src + i * 512, bytes);
+            cp_async16(d + S::kCodesBytes, vsrc + i * 512, bytes);
         }
-        constexpr int SCH = S::kScalesBytes / 16;       // chunks of the scales of keys, then of values
-        constexpr int PER = 16 / S::kScaleRow;          // tokens of a chunk
-#pragma unroll
-        for (int i = 0; i < (2 * SCH + 31) / 32; ++i) {
-            const int c = i * 32 + lane;
-            if (2 * SCH >= 32 || c < 2 * SCH) {
-                const int chunk = c % SCH;
-                const int t = chunk * PER;
-                const bool use = t < 16 ? use_lo : use_hi;
-                const int64_t row = (t < 16 ? row_lo : row_hi) + t + (c >= SCH ? vrows : 0);
-                int n = live - t;
-                n = n < 0 ? 0 : (n > PER ? PER : n);
-                const uint16_t *src = a.cache.scales + row * NG;
-                if (!use || n == 0) {
-                    src = a.cache.scales;
-                    n = 0;
-                }
-                cp_async16(dst + 2 * S::kCodesBytes + c * 16, src, n * S::kScaleRow);
+        const uint8_t *ssrc = scales0 + row * S::kScaleRow;
+        const uint32_t d = dst + 2 * S::kCodesBytes + lane * 16;
+        if constexpr (SCH == 32) {
+            if (FROM == 0 ? (TO == kTile || lane < 16) : lane >= 16) {
+                cp_async16(d, ssrc, bytes);
+                cp_async16(d + S::kScalesBytes, ssrc + vrows * S::kScaleRow, bytes);
             }
+        } else {
+            const int c = lane % SCH;
+            if (lane < 2 * SCH && (FROM == 0 ? (TO == kTile || c < SCH / 2) : c >= SCH / 2))
+                cp_async16(d, ssrc, bytes);
+        }
+    };
+    // Copies tile k into a stage.  Rows of a page that should be there and is not
+    // arrive as zeros; what no query sees is masked, so whatever lies there will do.
+    const auto issue = [&](int k, int stage, Pages p) {
+        using I0 = std::integral_constant<int, 0>;
+        using I16 = std::integral_constant<int, 16>;
+        using I32 = std::integral_constant<int, 32>;
+        const int t0 = it.token(k);
+        const uint32_t dst = ring_addr + stage * S::kStage;
+        const bool ok = static_cast<uint32_t>(p.lo) < static_cast<uint32_t>(a.cache.num_pages);
+        if (log2_page > 4) {
+            if (!ok && lane == 0) atomicOr(&g_kv_attention_status, RN_STATUS_BAD_INDEX);
+            copy_rows(I0(), I32(), dst, ok ? p.lo : 0, ok ? t0 & ((1 << log2_page) - 1) : 0, ok ? 16 : 0);
+        } else {
+            const bool ok_hi = static_cast<uint32_t>(p.hi) < static_cast<uint32_t>(a.cache.num_pages);
+            const bool see = seen(t0), see_hi = seen(t0 + 16);
+            if (((see && !ok) || (see_hi && !ok_hi)) && lane == 0)
+                atomicOr(&g_kv_attention_status, RN_STATUS_BAD_INDEX);
+            if (see) copy_rows(I0(), I16(), dst, ok ? p.lo : 0, 0, ok ? 16 : 0);
+            if (see_hi) copy_rows(I16(), I32(), dst, ok_hi ? p.hi : 0, 0, ok_hi ? 16 : 0);
         }
     };
 
@@ -565,8 +592,10 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
             for (int i = 0; i < 4; ++i) corr[g][i] = 0.0f;
     }
     // Value scales lie below 2^(scale_exp + 1); the weights are kept below
-    // 2^(14 - scale_exp), so that their products stay inside fp16.  Weights of 2^-28
-    // of the largest are still normal numbers there.
+    // 2^(14 - scale_exp), so that their products stay inside fp16.  A new reference
+    // leaves them kSlack powers of two to grow, and is taken only when that is used
+    // up: rescaling at every new maximum took 55% of the tiles of a ragged decode batch.
+    // Weights of 2^-22 of the largest are still normal numbers.
     int scale_exp = 0;
 
     const auto take_off = [&]() {  // the codes' offset, collected in corr, off the sums
@@ -588,62 +617,55 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
     };
     int turn = 0;  // tiles since then
 
-    int k = k0 + warp;
-    Pages next = pages_of(k);
-#pragma unroll
-    for (int s = 0; s < S::kStages - 1; ++s) {
-        const int ks = k + s * kAttnWarps;
-        if (ks < k1) issue(ks, s, next);
-        next = pages_of(ks + kAttnWarps);
-        cp_async_commit();
-    }
-
     // lane's places in a stage
     const int key_a = (r >> 1) + 4 * (r & 1);  // token of its first operand row
     constexpr int KW = NG * BITS / 4;          // words of a lane's share of a key row
     constexpr int VW = D * BITS / 256;         // and of a value row
     constexpr int KC = KW < 4 ? KW : 4, VC = VW < 4 ? VW : 4;
-
-    int stage = 0;
-    for (; k < k1; k += kAttnWarps) {
-        cp_async_wait<S::kStages - 2>();
-        __syncwarp();
-        {
-            const int kn = k + (S::kStages - 1) * kAttnWarps;
-            int sn = stage + S::kStages - 1;
-            sn = sn >= S::kStages ? sn - S::kStages : sn;
-            if (kn < k1) issue(kn, sn, next);
-            next = pages_of(kn + kAttnWarps);
-            cp_async_commit();
-        }
-        if constexpr (S::kOffsetSums) {
-            // The sums of stored codes carry the offset, about z sum(w) beside a signal
-            // that grows like its root, and the tensor core cuts every addition to fp32:
-            // taken off every eighth tile the offset never outgrows the signal.
-            if (++turn == 8) {
-                turn = 0;
-                take_off();
-            }
-        }
-        const uint32_t base = ring_addr + stage * S::kStage;
-        const uint32_t sbase = base + 2 * S::kCodesBytes;
-        stage = stage + 1 == S::kStages ? 0 : stage + 1;
-        const int t0 = it.token(k);
-
-        // -- logits, in log2: rows are tokens, columns queries --------------------------
-        float x[2][NT][4];
+    // its chunk (and place in it) of token key_a and of that + 8; of tokens j + 4 n.
+    // Further chunks of its share lie a constant away before the exchange: its share
+    // starts at a multiple of its chunks, so they differ from the first in low bits only.
+    uint32_t key_off[2], val_off[4];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
+    for (int n = 0; n < 2; ++n)
+        key_off[n] = swizzle<F::kRow>((key_a + 8 * n) * (F::kRow / 16) + j * KW / 4) + j * KW % 4 * 4;
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+        val_off[n] = S::kCodesBytes + swizzle<F::kRow>((j + 4 * n) * (F::kRow / 16) + r * VW / 4) + r * VW % 4 * 4;
+
+    // One tile: MASKED where some column does not see all of it.
+    const auto do_tile = [&](auto masked_tag, uint32_t base, int t0) {
+        constexpr bool MASKED = decltype(masked_tag)::value;
+        const uint32_t sbase = base + 2 * S::kCodesBytes;
+        // largest value scale of the tile's visible tokens, one token a lane (the
+        // pattern of a NaN is a negative integer)
+        int vtop;
+        {
+            constexpr int W = NG / 2;
+            uint32_t v[W];
+            lds_words<W>(v, sbase + S::kScalesBytes + lane * S::kScaleRow);
+            uint32_t mx = v[0];
+#pragma unroll
+            for (int i = 1; i < W; ++i) mx = __vmaxs2(mx, v[i]);
+            vtop = max(static_cast<int>(static_cast<int16_t>(mx & 0xFFFFu)),
+                       static_cast<int>(static_cast<int16_t>(mx >> 16)));
+            if (vtop > 0x7BFF || (MASKED && !seen_token(t0 + lane))) vtop = -1;
+        }
+#pragma unroll 1
+        for (int m0 = 0; m0 < 2; m0 += S::kStep) {
+        // -- logits (before the factor): rows are tokens, columns queries --------------------------
+        float x[S::kStep][NT][4];
+#pragma unroll
+        for (int mt = 0; mt < S::kStep; ++mt) {
             uint32_t ka[KW], kb[KW], sa[NG / 2], sb[NG / 2];
-            const int ta = 16 * mt + key_a;
+            const int ta = 16 * (m0 + mt) + key_a;
 #pragma unroll
             for (int w = 0; w < KW; w += KC) {
-                const int c0 = (j * KW + w) / 4, in = (j * KW + w) % 4 * 4;
                 uint32_t v[KC];
-                lds_words<KC>(v, base + swizzle<F::kRow>(ta * (F::kRow / 16) + c0) + in);
+                lds_words<KC>(v, base + 16 * (m0 + mt) * F::kRow + (key_off[0] ^ 4 * w));
 #pragma unroll
                 for (int i = 0; i < KC; ++i) ka[w + i] = v[i];
-                lds_words<KC>(v, base + swizzle<F::kRow>((ta + 8) * (F::kRow / 16) + c0) + in);
+                lds_words<KC>(v, base + 16 * (m0 + mt) * F::kRow + (key_off[1] ^ 4 * w));
 #pragma unroll
                 for (int i = 0; i < KC; ++i) kb[w + i] = v[i];
             }
@@ -719,29 +741,20 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
         }
 
         // -- mask ------------------------------------------------------------------------
-        const bool masked = t0 + kTile - 1 > it.lo_pos ||
-                            (a.window && t0 <= it.hi - 1 - a.window && t0 + kTile > a.sinks);
         uint32_t hidden[NT];  // bit 4 mt + i: element x[mt][nt][i] is masked
         bool grow = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            hidden[nt] = 0u;
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[mt][nt][i] *= factor[nt][i & 1];
-        }
-        if (masked) {
+        if constexpr (MASKED) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+                hidden[nt] = 0u;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int pos = s_pos[nt * 8 + 2 * j + c];
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt)
+                    for (int mt = 0; mt < S::kStep; ++mt)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const int t = t0 + 16 * mt + 8 * h + key_a;
+                            const int t = t0 + 16 * (m0 + mt) + 8 * h + key_a;
                             const bool see = t <= pos && (a.window == 0 || t > pos - a.window || t < a.sinks);
                             if (!see) {
                                 x[mt][nt][2 * h + c] = -INFINITY;
@@ -758,24 +771,12 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                top[nt][c] = fmaxf(fmaxf(x[0][nt][c], x[0][nt][2 + c]), fmaxf(x[1][nt][c], x[1][nt][2 + c]));
-                grow |= top[nt][c] > m[nt][c];
+                float t = fmaxf(x[0][nt][c], x[0][nt][2 + c]);
+                if constexpr (S::kStep == 2) t = fmaxf(t, fmaxf(x[1][nt][c], x[1][nt][2 + c]));
+                top[nt][c] = t * factor[nt][c];
+                grow |= top[nt][c] > m[nt][c];  // m: the largest logit the reference allows
             }
-        // largest value scale of the tile's visible tokens, one token a lane (the
-        // pattern of a NaN is a negative integer)
-        int vtop;
-        {
-            constexpr int W = NG / 2;
-            uint32_t v[W];
-            lds_words<W>(v, sbase + S::kScalesBytes + lane * S::kScaleRow);
-            uint32_t mx = v[0];
-#pragma unroll
-            for (int i = 1; i < W; ++i) mx = __vmaxs2(mx, v[i]);
-            vtop = max(static_cast<int>(static_cast<int16_t>(mx & 0xFFFFu)),
-                       static_cast<int>(static_cast<int16_t>(mx >> 16)));
-            if (vtop > 0x7BFF || (masked && !seen_token(t0 + lane))) vtop = -1;
-            grow |= vtop >= (scale_exp + 16) << 10;
-        }
+        grow |= vtop >= (scale_exp + 16) << 10;
         if (__any_sync(0xffffffffu, grow)) {
             const int e = (__reduce_max_sync(0xffffffffu, vtop) >> 10) - 15;
             scale_exp = e > scale_exp ? e : scale_exp;
@@ -788,7 +789,8 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                    t = fmaxf(t, m[nt][c]);
+                    // columns that need no more room keep what they have but for scale_exp
+                    t = t > m[nt][c] ? t + kSlack : m[nt][c];
                     const float nref = t == -INFINITY ? 0.0f : t - static_cast<float>(14 - scale_exp);
                     f[c] = m[nt][c] == -INFINITY ? 1.0f : exp2_approx(ref[nt][c] - nref);
                     ref[nt][c] = nref;
@@ -809,17 +811,17 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
         }
 
         // -- weights: rounded once to fp16, then tokens along the operand's k --------------
-        uint32_t p[2][NT][2];
+        uint32_t p[S::kStep][NT][2];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < S::kStep; ++mt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = exp2_approx(x[mt][nt][i] - ref[nt][i & 1]);
+                for (int i = 0; i < 4; ++i) w[i] = exp2_approx(fmaf(x[mt][nt][i], factor[nt][i & 1], -ref[nt][i & 1]));
                 l[nt][0] += w[0] + w[2];
                 l[nt][1] += w[1] + w[3];
-                if (masked) {
+                if constexpr (MASKED) {
                     // a masked weight is -0, so that it can be told from one that underflowed
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -831,16 +833,15 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
 
         // -- values: rows are dimensions, k tokens j, j + 4, j + 8, j + 12 -----------------
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
+        for (int mt = 0; mt < S::kStep; ++mt) {
             uint32_t v[4][VW], vs[4][NG / 2];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const int t = 16 * mt + 4 * n + j;
+                const int t = 16 * (m0 + mt) + 4 * n + j;
 #pragma unroll
                 for (int w = 0; w < VW; w += VC) {
-                    const int c0 = (r * VW + w) / 4, in = (r * VW + w) % 4 * 4;
                     uint32_t u[VC];
-                    lds_words<VC>(u, base + S::kCodesBytes + swizzle<F::kRow>(t * (F::kRow / 16) + c0) + in);
+                    lds_words<VC>(u, base + 16 * (m0 + mt) * F::kRow + (val_off[n] ^ 4 * w));
 #pragma unroll
                     for (int i = 0; i < VC; ++i) v[n][w + i] = u[i];
                 }
@@ -856,7 +857,7 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
                 for (int nt = 0; nt < NT; ++nt) {
                     w0[nt] = hmul2_bits(p[mt][nt][0], s0);
                     w1[nt] = hmul2_bits(p[mt][nt][1], s1);
-                    if (masked) {  // a masked token's scale may be NaN
+                    if constexpr (MASKED) {  // a masked token's scale may be NaN
                         w0[nt] &= ~__vcmpeq2(p[mt][nt][0], 0x80008000u);
                         w1[nt] &= ~__vcmpeq2(p[mt][nt][1], 0x80008000u);
                     }
@@ -895,6 +896,51 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
                 }
             }
         }
+        }
+    };
+
+
+    int k = k0 + warp;
+    Pages next = pages_of(k);
+#pragma unroll
+    for (int s = 0; s < S::kStages - 1; ++s) {
+        const int ks = k + s * kAttnWarps;
+        if (ks < k1) issue(ks, s, next);
+        next = pages_of(ks + kAttnWarps);
+        cp_async_commit();
+    }
+
+    int stage = 0;
+    for (; k < k1; k += kAttnWarps) {
+        cp_async_wait<S::kStages - 2>();
+        __syncwarp();
+        {
+            const int kn = k + (S::kStages - 1) * kAttnWarps;
+            int sn = stage + S::kStages - 1;
+            sn = sn >= S::kStages ? sn - S::kStages : sn;
+            if (kn < k1) issue(kn, sn, next);
+            next = pages_of(kn + kAttnWarps);
+            cp_async_commit();
+        }
+        if constexpr (S::kOffsetSums) {
+            // The sums of stored codes carry the offset, about z sum(w) beside a signal
+            // that grows like its root, and the tensor core cuts every addition to fp32:
+            // taken off every eighth tile the offset never outgrows the signal.
+            if (++turn == 8) {
+                turn = 0;
+                take_off();
+            }
+        }
+        const uint32_t base = ring_addr + stage * S::kStage;
+        stage = stage + 1 == S::kStages ? 0 : stage + 1;
+        const int t0 = it.token(k);
+
+        const bool masked = t0 + kTile - 1 > it.lo_pos ||
+                            (a.window && t0 <= it.hi - 1 - a.window && t0 + kTile > a.sinks);
+        if (masked)
+            do_tile(std::true_type(), base, t0);
+        else
+            do_tile(std::false_type(), base, t0);
     }
 
     take_off();
@@ -977,16 +1023,21 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, BITS, NT>::kCtas)
             ++item;
             continue;
         }
+        const int units = it.units();
         const int64_t in = u - before * a.cache.Hkv;
-        const int head = static_cast<int>(in / it.n), k0 = static_cast<int>(in % it.n);
+        const int head = static_cast<int>(in / units), v0 = static_cast<int>(in % units);
         const int64_t left = u1 - u;
-        const int k1 = it.n - k0 <= left ? it.n : k0 + static_cast<int>(left);
-        float *part = nullptr;
-        if (k1 - k0 != it.n) part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1)) * S::kSlot;
-        attend_run<D, BITS, NT>(a, it, b, head, k0, k1, part, attn_smem);
-        u += k1 - k0;
-        if (k1 == it.n && head == a.cache.Hkv - 1) {
-            before += it.n;
+        const int v1 = units - v0 <= left ? units : v0 + static_cast<int>(left);
+        const int k0 = v0 > kLead ? v0 - kLead : 0, k1 = v1 - kLead;
+        if (k1 > k0) {
+            float *part = nullptr;
+            if (k1 - k0 != it.n)
+                part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1)) * S::kSlot;
+            attend_run<D, BITS, NT>(a, it, b, head, k0, k1, part, attn_smem);
+        }
+        u += v1 - v0;
+        if (v1 == units && head == a.cache.Hkv - 1) {
+            before += units;
             ++item;
         }
     }
@@ -1009,11 +1060,12 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_join_kernel(const K
     if (n > 0) {
         first = before * Hkv + kvh * n;
         ctas = line_ctas(units, a.grid);
-        // the CTAs that hold the first and the last unit
-        c0 = first * ctas / units;
-        while (line_start(units, ctas, c0 + 1) <= first) ++c0;
-        c1 = (first + n - 1) * ctas / units;
-        while (line_start(units, ctas, c1 + 1) <= first + n - 1) ++c1;
+        // the CTAs that hold the first and the last unit with work
+        const int64_t u0 = first + kLead, u1 = first + n - 1;
+        c0 = u0 * ctas / units;
+        while (line_start(units, ctas, c0 + 1) <= u0) ++c0;
+        c1 = u1 * ctas / units;
+        while (line_start(units, ctas, c1 + 1) <= u1) ++c1;
         if (c0 == c1) return;
     }
     const Item it = make_item<NQ>(a, item / a.q_tiles, item % a.q_tiles);
@@ -1022,7 +1074,7 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_join_kernel(const K
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         float l = 0.0f, top = -INFINITY;
         for (int64_t c = c0; c <= c1; ++c) {
-            const int64_t slot = 2 * c + (c == c0 && line_start(units, ctas, c) != first ? 1 : 0);
+            const int64_t slot = 2 * c + (line_start(units, ctas, c) < first ? 1 : 0);
             const float *part = a.partial + slot * SLOT;
             const float pr = part[NQ * D + col], pl = part[NQ * D + NQ + col];
             const float4 v = *reinterpret_cast<const float4 *>(part + col * D + d0);
@@ -1068,7 +1120,7 @@ static AttnPlan attn_plan_of(int sm_count, int64_t B, int group, int64_t max_q_l
     AttnPlan p;
     p.nt = NT;
     p.q_tiles = (max_q_len * group + S::NQ - 1) / S::NQ;
-    p.grid = sm_count * S::kCtas;
+    p.grid = sm_count * S::kCtas * kWaves;
     p.prefix_bytes = ((B * p.q_tiles + 1) * 8 + 15) / 16 * 16;
     p.bytes = p.prefix_bytes + static_cast<int64_t>(p.grid) * 2 * S::kSlot * 4;
     return p;
