@@ -11,7 +11,6 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import NamedTuple
 
 import torch
 
@@ -609,36 +608,43 @@ def rope_cos_sin_table(theta: float, max_pos: int, rotary_dim: int,
 
 # ---- quantised key/value cache --------------------------------------------------
 
-class KVCache(NamedTuple):
+class KVCache:
     """One layer's paged key/value cache in 8 or 4 bits (include/row_norm.h has
-    the stored format).
+    the stored format); checked once, here.
 
-    codes   uint8 [num_pages, 2, Hkv, page_size, D * bits / 8]
-    scales  fp16  [num_pages, 2, Hkv, page_size, D / 32]
+    codes   uint8 [num_pages, 2, num_kv_heads, page_size, head_dim * bits / 8]
+    scales  fp16  [num_pages, 2, num_kv_heads, page_size, head_dim / 32]
+    format  RN_KV_INT4 or RN_KV_INT8 (the bits of a code)
     """
-    codes: torch.Tensor
-    scales: torch.Tensor
+    __slots__ = ("codes", "scales", "format", "num_kv_heads", "head_dim", "page_size",
+                 "num_pages", "device")
 
-    @property
-    def num_pages(self) -> int:
-        return self.codes.shape[0]
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        for name, t, dtype in (("codes", codes, torch.uint8), ("scales", scales, torch.float16)):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.dtype != dtype:
+                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        cs, ss = codes.shape, scales.shape
+        if len(cs) != 5 or len(ss) != 5 or cs[:4] != ss[:4] or cs[1] != 2:
+            raise ValueError("a cache is codes [pages, 2, Hkv, page_size, D * bits / 8] and "
+                             "scales [pages, 2, Hkv, page_size, D / 32]")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales must be on one device")
+        D = ss[4] * RN_KV_GROUP
+        if D == 0 or cs[4] * 2 not in (D, 2 * D):
+            raise ValueError("codes must hold D / 2 (4 bits) or D (8 bits) bytes a row")
+        self.codes, self.scales, self.device = codes, scales, codes.device
+        self.format = RN_KV_INT4 if cs[4] * 2 == D else RN_KV_INT8
+        self.num_pages, self.num_kv_heads, self.page_size = cs[0], cs[2], cs[3]
+        self.head_dim = D
 
-    @property
-    def num_kv_heads(self) -> int:
-        return self.codes.shape[2]
-
-    @property
-    def page_size(self) -> int:
-        return self.codes.shape[3]
-
-    @property
-    def head_dim(self) -> int:
-        return self.scales.shape[4] * RN_KV_GROUP
-
-    @property
-    def format(self) -> int:
-        """RN_KV_INT4 or RN_KV_INT8 (the bits of a code)."""
-        return self.codes.shape[4] * 8 // max(1, self.head_dim)
+    def __repr__(self):
+        return (f"KVCache(pages={self.num_pages}, heads={self.num_kv_heads}, "
+                f"page_size={self.page_size}, head_dim={self.head_dim}, bits={self.format}, "
+                f"device={self.device})")
 
 
 def new_kv_cache(num_pages: int, Hkv: int, D: int, *, page_size: int = 64,
@@ -655,41 +661,33 @@ def new_kv_cache(num_pages: int, Hkv: int, D: int, *, page_size: int = 64,
                    torch.zeros(*shape, D // RN_KV_GROUP, dtype=torch.float16, device=dev))
 
 
-def _kv_cache(cache: KVCache):
-    """Checks a cache's tensors; returns (format, Hkv, D, page_size, num_pages)."""
-    codes, scales = cache
-    _need(codes, "cache.codes", torch.uint8)
-    _need(scales, "cache.scales", torch.float16)
-    cs, ss = codes.shape, scales.shape
-    if len(cs) != 5 or len(ss) != 5 or cs[:4] != ss[:4] or cs[1] != 2:
-        raise ValueError("cache tensors must be codes [pages, 2, Hkv, page_size, D * bits / 8] "
-                         "and scales [pages, 2, Hkv, page_size, D / 32]")
-    D = ss[4] * RN_KV_GROUP
-    if cs[4] * 2 == D:
-        fmt = RN_KV_INT4
-    elif cs[4] == D:
-        fmt = RN_KV_INT8
-    else:
-        raise ValueError("cache.codes must hold D / 2 (4 bits) or D (8 bits) bytes a row")
-    return fmt, cs[2], D, cs[3], cs[0]
+def _on(dev: int, t: torch.Tensor, name: str, dtype: torch.dtype, numel: int | None = None) -> int:
+    """The address of t, which must be a contiguous tensor of dtype on CUDA device dev."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or \
+            not t.is_contiguous():
+        _need(t, name, dtype)
+        raise ValueError(f"{name} must be on the cache's device")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
+    return t.data_ptr()
 
 
-def _one_device(first: torch.Tensor, *others) -> torch.device:
-    dev = first.device
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+def _kv_device(cache: KVCache) -> int:
+    dev = cache.codes.get_device()
+    if dev < 0:
+        raise ValueError("the cache must be on a CUDA device")
     return dev
 
 
-def _kv_call(dev: torch.device, name: str, *args, stream) -> None:
+def _kv_call(dev: int, name: str, *args, stream) -> None:
     """Calls a key/value cache entry point with the tensors' device current."""
-    fn = getattr(load(), name)
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, _stream(stream))
+    L = _lib if _lib is not None else load()
+    if dev == torch.cuda.current_device():
+        s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+        rc = getattr(L, name)(*args, s)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _stream(stream))
+            rc = getattr(L, name)(*args, _stream(stream))
     if rc != RN_OK:
         raise RowNormError(name, rc)
 
@@ -699,25 +697,16 @@ def kv_cache_write(qkv: torch.Tensor, slots: torch.Tensor, cache: KVCache, Hq: i
     """Quantises the key and value heads of qkv [T, (Hq + 2*Hkv) * D] (bf16, as
     qk_norm_rope_fwd leaves it) into the rows slots [T] (int64; page * page_size
     + offset, negative: skip the token) names.  Returns the cache."""
-    fmt, ch, cd, P, pages = _kv_cache(cache)
-    _need(qkv, "qkv", torch.bfloat16)
-    _need(slots, "slots", torch.int64)
-    if ch != Hkv or cd != D:
-        raise ValueError(f"the cache holds {ch} heads of {cd}, not {Hkv} of {D}")
+    dev = _kv_device(cache)
+    if cache.num_kv_heads != Hkv or cache.head_dim != D:
+        raise ValueError(f"the cache holds {cache.num_kv_heads} heads of {cache.head_dim}, "
+                         f"not {Hkv} of {D}")
+    sp = _on(dev, slots, "slots", torch.int64)
     T = slots.numel()
-    if qkv.numel() != T * (Hq + 2 * Hkv) * D:
-        raise ValueError("qkv must be [T, (Hq + 2*Hkv) * D] with a slot for each token")
-    dev = _one_device(qkv, slots, cache.codes, cache.scales)
-    _kv_call(dev, "kv_cache_write", qkv.data_ptr(), slots.data_ptr(), T, Hq, Hkv, D, fmt, P, pages,
-             cache.codes.data_ptr(), cache.scales.data_ptr(), stream=stream)
+    qp = _on(dev, qkv, "qkv", torch.bfloat16, T * (Hq + 2 * Hkv) * D)
+    _kv_call(dev, "kv_cache_write", qp, sp, T, Hq, Hkv, D, cache.format, cache.page_size,
+             cache.num_pages, cache.codes.data_ptr(), cache.scales.data_ptr(), stream=stream)
     return cache
-
-
-def _page_table(page_table: torch.Tensor):
-    _need(page_table, "page_table", torch.int32)
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages]")
-    return page_table.shape
 
 
 def kv_cache_read(cache: KVCache, page_table: torch.Tensor, cu_lens: torch.Tensor, total: int,
@@ -726,26 +715,23 @@ def kv_cache_read(cache: KVCache, page_table: torch.Tensor, cu_lens: torch.Tenso
     """Reads tokens starts[b].. (int32, default 0) of every sequence b back into
     rows cu_lens[b] .. cu_lens[b+1] - 1 (int64) of k and v [total, Hkv, D]
     bf16; returns (k, v).  page_table [B, max_pages] int32."""
-    fmt, Hkv, D, P, pages = _kv_cache(cache)
-    B, width = _page_table(page_table)
-    _need(cu_lens, "cu_lens", torch.int64)
-    if cu_lens.numel() != B + 1:
-        raise ValueError("cu_lens must have B + 1 elements")
-    if starts is not None:
-        _need(starts, "starts", torch.int32)
-        if starts.numel() != B:
-            raise ValueError("starts must have B elements")
-    dev = _one_device(cache.codes, cache.scales, page_table, cu_lens, starts, k, v)
-    shape = (total, Hkv, D)
-    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
-    for name, t in (("k", k), ("v", v)):
-        _need(t, name, torch.bfloat16)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be [total, Hkv, D]")
-    _kv_call(dev, "kv_cache_read", cache.codes.data_ptr(), cache.scales.data_ptr(), fmt, Hkv, D, P,
-             pages, page_table.data_ptr(), B, width, cu_lens.data_ptr(), _ptr(starts), total,
-             k.data_ptr(), v.data_ptr(), stream=stream)
+    dev = _kv_device(cache)
+    tp = _on(dev, page_table, "page_table", torch.int32)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, width = page_table.shape
+    cp = _on(dev, cu_lens, "cu_lens", torch.int64, B + 1)
+    sp = None if starts is None else _on(dev, starts, "starts", torch.int32, B)
+    Hkv, D = cache.num_kv_heads, cache.head_dim
+    n = total * Hkv * D
+    if k is None:
+        k = torch.empty(total, Hkv, D, dtype=torch.bfloat16, device=cache.device)
+    if v is None:
+        v = torch.empty(total, Hkv, D, dtype=torch.bfloat16, device=cache.device)
+    _kv_call(dev, "kv_cache_read", cache.codes.data_ptr(), cache.scales.data_ptr(), cache.format,
+             Hkv, D, cache.page_size, cache.num_pages, tp, B, width, cp, sp, total,
+             _on(dev, k, "k", torch.bfloat16, n), _on(dev, v, "v", torch.bfloat16, n),
+             stream=stream)
     return k, v
 
 
@@ -753,13 +739,13 @@ def kv_attention_workspace(cache: KVCache, B: int, Hq: int, *, max_q_len: int = 
     """A workspace for kv_attention_fwd calls of up to these sizes.  Calls that
     run one after another can share one; calls that may run at the same time
     need one each."""
-    fmt, Hkv, D, _, _ = _kv_cache(cache)
-    dev = cache.codes.device
+    dev = _kv_device(cache)
     with torch.cuda.device(dev):
-        n = int(load().kv_attention_workspace_bytes(fmt, B, Hq, Hkv, D, max_q_len))
+        n = int(load().kv_attention_workspace_bytes(cache.format, B, Hq, cache.num_kv_heads,
+                                                    cache.head_dim, max_q_len))
     if n < 0:
         raise RowNormError("kv_attention_workspace_bytes", n)
-    return torch.empty(n, dtype=torch.uint8, device=dev)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
 
 
 def kv_attention_fwd(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
@@ -782,55 +768,48 @@ def kv_attention_fwd(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
 
     Returns (out [T, Hq, D] bf16, lse [T, Hq] fp32, natural logarithms).  Rows
     outside every sequence are left as they were."""
-    fmt, Hkv, D, P, pages = _kv_cache(cache)
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise ValueError("q must be a CUDA tensor")
-    if q.dtype != torch.bfloat16:
+    dev = _kv_device(cache)
+    D = cache.head_dim
+    if not isinstance(q, torch.Tensor) or q.get_device() != dev:
+        raise ValueError("q must be a CUDA tensor on the cache's device")
+    if q.dtype is not torch.bfloat16:
         raise TypeError(f"q must be {torch.bfloat16}, got {q.dtype}")
-    if q.dim() == 3:
-        if q.shape[1] != Hq or q.shape[2] != D or (q.shape[0] and q.stride()[1:] != (D, 1)):
+    shape, T = q.shape, q.shape[0]
+    if len(shape) == 3:
+        if shape[1] != Hq or shape[2] != D or (T and q.stride()[1:] != (D, 1)):
             raise ValueError("q must be [T, Hq, D] with contiguous rows")
-    elif q.dim() != 2 or q.shape[1] < Hq * D or (q.shape[0] and q.stride(1) != 1):
+    elif len(shape) != 2 or shape[1] < Hq * D or (T and q.stride(1) != 1):
         raise ValueError("q must be [T, >= Hq * D] with contiguous rows, or [T, Hq, D]")
-    T = q.shape[0]
-    B, width = _page_table(page_table)
-    _need(kv_lens, "kv_lens", torch.int32)
-    if kv_lens.numel() != B:
-        raise ValueError("kv_lens must have B elements")
+    tp = _on(dev, page_table, "page_table", torch.int32)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, width = page_table.shape
+    lp = _on(dev, kv_lens, "kv_lens", torch.int32, B)
     if cu_q is not None:
-        _need(cu_q, "cu_q", torch.int64)
-        if cu_q.numel() != B + 1:
-            raise ValueError("cu_q must have B + 1 elements")
+        cp = _on(dev, cu_q, "cu_q", torch.int64, B + 1)
     elif T != B:
         raise ValueError("without cu_q there is one query for each sequence")
-    dev = _one_device(q, cache.codes, cache.scales, page_table, kv_lens, cu_q, out, lse, workspace)
+    else:
+        cp = None
     if out is None:
-        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
-    else:
-        _need(out, "out", torch.bfloat16)
-        if out.numel() != T * Hq * D:
-            raise ValueError("out must be [T, Hq, D]")
+        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=cache.device)
     if lse is None:
-        lse = torch.empty(T, Hq, dtype=torch.float32, device=dev)
-    else:
-        _need(lse, "lse", torch.float32)
-        if lse.numel() != T * Hq:
-            raise ValueError("lse must be [T, Hq]")
+        lse = torch.empty(T, Hq, dtype=torch.float32, device=cache.device)
     if workspace is None:
         workspace = kv_attention_workspace(cache, B, Hq, max_q_len=max_q_len)
         if stream is not None:  # freed while `stream` may still use it
             workspace.record_stream(
                 stream if isinstance(stream, torch.cuda.Stream)
-                else torch.cuda.ExternalStream(int(stream), device=dev))
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    row = q.stride(0) if T > 1 else Hq * D
-    _kv_call(dev, "kv_attention_fwd", q.data_ptr(), row, cache.codes.data_ptr(),
-             cache.scales.data_ptr(), fmt, Hq, Hkv, D, P, pages, page_table.data_ptr(), B, width,
-             kv_lens.data_ptr(), _ptr(cu_q), T, max_q_len,
-             D ** -0.5 if scale is None else float(scale), int(window), int(sinks), out.data_ptr(),
-             lse.data_ptr(), workspace.data_ptr(),
-             workspace.numel() * workspace.element_size(), stream=stream)
+                else torch.cuda.ExternalStream(int(stream), device=cache.device))
+    elif not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    _kv_call(dev, "kv_attention_fwd", q.data_ptr(), q.stride(0) if T > 1 else Hq * D,
+             cache.codes.data_ptr(), cache.scales.data_ptr(), cache.format, Hq, cache.num_kv_heads,
+             D, cache.page_size, cache.num_pages, tp, B, width, lp, cp, T, max_q_len,
+             D ** -0.5 if scale is None else scale, window, sinks,
+             _on(dev, out, "out", torch.bfloat16, T * Hq * D),
+             _on(dev, lse, "lse", torch.float32, T * Hq), workspace.data_ptr(), workspace.nbytes,
+             stream=stream)
     return out, lse
 
 
