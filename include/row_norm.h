@@ -518,7 +518,8 @@ int rmsnorm_fwd_noalloc(const rn_bf16 *x, const rn_bf16 *w, float eps,
  * calls take.)
  *
  * The cache of one layer is two DEVICE tensors of the caller, both 16-byte
- * aligned, P = page_size a power of two from 16 to 256, D in {64, 128, 256}:
+ * aligned, P = page_size a power of two from 16 to 256, D in {64, 128, 256},
+ * Hkv at most 16384:
  *   codes   [num_pages, 2, Hkv, P, D * bits / 8] bytes   (index 1: 0 key, 1 value)
  *   scales  [num_pages, 2, Hkv, P, D / 32] fp16
  * Token p of a sequence lives in row p % P of page page_table[b, p / P]; slot

@@ -65,12 +65,13 @@ struct KvAttnArgs {
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kTile = 32;          // tokens a warp takes at once
-constexpr int kWaves = 1;          // CTAs launched for each one that fits the GPU at once
 constexpr float kSlack = 6.0f;       // powers of two a weight may grow before a rescale
 // Units without work in front of each (query tile, head): its queries, first page and
 // copies, and the joining of its warps.  64 ragged sequences of 8 heads (540k tokens):
 // 175 us with none, 158 with 8, 128 with 16, 132 with 32; 4 long ones 124-126 throughout.
 constexpr int kLead = 16;
+constexpr int kJoinWarps = 8;
+constexpr int kFewPieces = 8;     // pieces that one warp joins by itself
 constexpr int kMinTiles = kAttnWarps;  // a CTA's run is no shorter: one tile a warp
 
 // Shapes of an instantiation: NT * 8 columns (queries of the tile times heads).
@@ -83,17 +84,16 @@ struct AttnShape {
     static constexpr int kCodesBytes = kTile * F::kRow;
     static constexpr int kScalesBytes = kTile * kScaleRow;
     static constexpr int kStage = 2 * (kCodesBytes + kScalesBytes);
-    // queries as operand registers (else in shared memory)
-    static constexpr bool kQueryRegs = NT == 1 && D <= 128;
-    // the codes' offset comes off the sums (else off the operands)
-    static constexpr bool kOffsetSums = NT == 1;
+    // the offset of the keys' codes comes off the sums, as their first addend (else off
+    // the operands, which then serve several instructions)
+    static constexpr bool kKeySums = NT == 1;
     // CTAs an SM is to hold: by registers (O alone is MT * NT * 4 a thread), and by
     // shared memory for a ring of two stages or more
-    static constexpr int kQuery = kQueryRegs ? 0 : NQ * D * 2;
+    static constexpr int kQuery = NQ * D * 2;  // the queries, as operand registers
     static constexpr int kRoom = 224 * 1024;
     static constexpr int stages_at(int ctas) { return ctas < 1 ? 0 : (kRoom / ctas - 2048 - kQuery) / (kAttnWarps * kStage); }
     static constexpr int kByRegs = MT * NT * 4 >= 64 ? 2 : (D == 64 ? 4 : 3);
-    static constexpr int kStep = 2;  // 16-token halves of a tile taken at once
+    static constexpr int kStep = D == 256 ? 1 : 2;  // 16-token halves of a tile taken at once
     static constexpr int kCtas = stages_at(kByRegs) >= 2         ? kByRegs
                                  : stages_at(kByRegs - 1) >= 2 ? kByRegs - 1
                                                                : kByRegs - 2;
@@ -204,7 +204,8 @@ constexpr uint32_t swizzle_step(int i) {
 
 // One (sequence, query tile): its columns and the tiles of tokens they see.
 struct Item {
-    int64_t row0;    // first query row of the sequence
+    int64_t seq;     // the sequence
+    int64_t row0;    // its first query row
     int f0, ncols;   // columns f0 .. f0 + ncols - 1 of the sequence's n_q * group
     int pos0;        // position of the sequence's first query
     int lo_pos, hi;  // position of the first column's query; one past the last column's
@@ -223,8 +224,14 @@ struct Item {
 };
 
 template <int NQ>
-__device__ __forceinline__ Item make_item(const KvAttnArgs &a, int64_t b, int64_t qt) {
+__device__ __forceinline__ Item make_item(const KvAttnArgs &a, int64_t item) {
     Item it;
+    uint32_t b = static_cast<uint32_t>(item), qt = 0;  // items fit 31 bits
+    if (a.q_tiles != 1) {
+        b = static_cast<uint32_t>(item) / static_cast<uint32_t>(a.q_tiles);
+        qt = static_cast<uint32_t>(item) - b * static_cast<uint32_t>(a.q_tiles);
+    }
+    it.seq = b;
     it.bad = false;
     int64_t nq = 1;
     it.row0 = b;
@@ -249,7 +256,7 @@ __device__ __forceinline__ Item make_item(const KvAttnArgs &a, int64_t b, int64_
         it.bad = true;
         nq = a.max_q_len;
     }
-    const int64_t left = nq * a.group - qt * NQ;
+    const int64_t left = nq * a.group - static_cast<int64_t>(qt) * NQ;
     it.f0 = static_cast<int>(qt * NQ);
     it.ncols = static_cast<int>(left < 0 ? 0 : (left < NQ ? left : NQ));
     it.lo_pos = it.pos0 + it.f0 / a.group;
@@ -268,14 +275,28 @@ __device__ __forceinline__ Item make_item(const KvAttnArgs &a, int64_t b, int64_
     return it;
 }
 
-// CTAs that share a line of `units` units, and the first unit of CTA c.
-__host__ __device__ __forceinline__ int64_t line_ctas(int64_t units, int grid) {
-    const int64_t want = (units + kMinTiles - 1) / kMinTiles;
-    return want < grid ? (want > 0 ? want : 1) : grid;
+// a / b, in 32 bits where both fit (they nearly always do).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
 }
-__device__ __forceinline__ int64_t line_start(int64_t units, int64_t ctas, int64_t c) {
-    return units * c / ctas;
-}
+
+// The line cut into runs for its CTAs, the first `rest` of them one unit longer.
+struct Cut {
+    int64_t ctas, run, rest;
+
+    __device__ __forceinline__ Cut(int64_t units, int grid) {
+        const int64_t want = (units + kMinTiles - 1) / kMinTiles;
+        ctas = want < grid ? (want > 0 ? want : 1) : grid;
+        run = quotient(units, ctas);
+        rest = units - run * ctas;
+    }
+    __device__ __forceinline__ int64_t start(int64_t c) const { return c * run + (c < rest ? c : rest); }
+    __device__ __forceinline__ int64_t cta_of(int64_t unit) const {
+        const int64_t longer = rest * (run + 1);
+        return unit < longer ? quotient(unit, run + 1) : rest + quotient(unit - longer, run);
+    }
+};
 
 // Four dimensions of a finished column: out = sum / l (the codes' 2^-24 undone),
 // lse = (reference + log2(l)) ln 2.
@@ -310,7 +331,7 @@ __device__ __forceinline__ Line find_unit(const KvAttnArgs &a, bool publish, int
     int64_t sum = 0;
     bool bad = false;
     for (int64_t i = i0; i < i1; ++i) {
-        const Item it = make_item<NQ>(a, i / a.q_tiles, i % a.q_tiles);
+        const Item it = make_item<NQ>(a, i);
         sum += it.units();
         bad |= it.bad;
     }
@@ -333,18 +354,18 @@ __device__ __forceinline__ Line find_unit(const KvAttnArgs &a, bool publish, int
         int64_t run = before;
         for (int64_t i = i0; i < i1; ++i) {
             a.prefix[i] = run;
-            run += make_item<NQ>(a, i / a.q_tiles, i % a.q_tiles).units();
+            run += make_item<NQ>(a, i).units();
         }
         if (tid == 0) a.prefix[items] = total;
     }
     Line line;
     line.units = total * a.cache.Hkv;
-    const int64_t ctas = line_ctas(line.units, a.grid);
-    const int64_t u = line_start(line.units, ctas, blockIdx.x);
-    if (blockIdx.x < ctas && before * a.cache.Hkv <= u && u < (before + sum) * a.cache.Hkv) {
+    const Cut cut(line.units, a.grid);
+    const int64_t u = cut.start(blockIdx.x);
+    if (blockIdx.x < cut.ctas && before * a.cache.Hkv <= u && u < (before + sum) * a.cache.Hkv) {
         int64_t run = before;
         for (int64_t i = i0; i < i1; ++i) {
-            const int n = make_item<NQ>(a, i / a.q_tiles, i % a.q_tiles).units();
+            const int n = make_item<NQ>(a, i).units();
             if (u < (run + n) * a.cache.Hkv) {
                 scratch[kAttnWarps] = i;
                 scratch[kAttnWarps + 1] = run;
@@ -426,7 +447,7 @@ struct Query {
 // Tiles [k0, k1) of one item and kv head: all warps, joined; the result goes to
 // the output rows, or (part != null) unfinished into a slot of the workspace.
 template <int D, int BITS, int NT>
-__device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, int64_t b, int kvh,
+__device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, int kvh,
                                            int k0, int k1, float *part, uint8_t *smem) {
     using S = AttnShape<D, BITS, NT>;
     using F = KvFormat<D, BITS>;
@@ -439,15 +460,14 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
 
     // -- queries ------------------------------------------------------------------
     const int head0 = kvh * a.group;
-    uint32_t qreg[S::kQueryRegs ? NG : 1][2][2];
-    float offset[S::kOffsetSums ? NG : 1][2];  // -zero * sum of the group's query, columns 2j, 2j+1
+    float offset[S::kKeySums ? NG : 1][2];  // -zero * sum of the group's query, columns 2j, 2j+1
     float factor[NT][2];
     uint8_t *qsm = smem + (S::kSmem - S::kQuery);
     if (threadIdx.x < NQ)
         s_pos[threadIdx.x] = static_cast<int>(threadIdx.x) < it.ncols
                                  ? it.pos0 + (it.f0 + static_cast<int>(threadIdx.x)) / a.group
                                  : -1;
-    if constexpr (S::kOffsetSums) {
+    if constexpr (S::kKeySums) {
         Query<D, BITS> q;
         q.load(a, it, head0, r, j);
 #pragma unroll
@@ -458,10 +478,7 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
             s *= -static_cast<float>(F::kZero) * 0x1p-24f;
             offset[g][0] = __shfl_sync(0xffffffffu, s, 8 * j);
             offset[g][1] = __shfl_sync(0xffffffffu, s, 8 * j + 4);
-            if constexpr (S::kQueryRegs) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) qreg[g][k >> 1][k & 1] = q.b[g][k >> 1][k & 1];
-            } else if (warp == 0) {
+            if (warp == 0) {
                 *reinterpret_cast<uint4 *>(qsm + (g * 32 + lane) * 16) =
                     make_uint4(q.b[g][0][0], q.b[g][0][1], q.b[g][1][0], q.b[g][1][1]);
             }
@@ -491,16 +508,18 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
     uint8_t *ring = smem + warp * (S::kStages * S::kStage);
     const uint32_t ring_addr = smem_addr(ring);
     const int log2_page = a.cache.log2_page;
-    const int32_t *table = a.page_table + b * a.max_pages;
+    const int32_t *table = a.page_table + it.seq * a.max_pages;
     // the lane's first chunk in page 0 of this head, and the way to the next page and
     // from a key to its value
     constexpr int SCH = S::kScalesBytes / 16;  // chunks of a tile's key scales (then the values')
     const uint32_t copy_off = swizzle<F::kRow>(lane);
-    const int64_t vrows = static_cast<int64_t>(a.cache.Hkv) << log2_page;
+    // bytes of a page's codes and scales (keys, then values; under 4 GB by the host's check)
+    const uint32_t page_codes = (static_cast<uint32_t>(2 * a.cache.Hkv) << log2_page) * F::kRow;
+    const uint32_t page_scales = (static_cast<uint32_t>(2 * a.cache.Hkv) << log2_page) * S::kScaleRow;
     const int64_t head_row = static_cast<int64_t>(kvh) << log2_page;
     const uint8_t *codes0 = a.cache.codes + head_row * F::kRow + lane * 16;
     const uint8_t *scales0 = reinterpret_cast<const uint8_t *>(a.cache.scales) + head_row * S::kScaleRow +
-                             (lane % SCH) * 16 + (SCH < 32 && lane >= SCH ? vrows * S::kScaleRow : 0);
+                             (lane % SCH) * 16 + (SCH < 32 && lane >= SCH ? page_scales / 2 : 0);
 
     struct Pages {
         int lo, hi;  // of the tile's two halves (16 tokens each lie on one page)
@@ -522,24 +541,23 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
     };
     // Copies rows [FROM, TO) of a tile (halves or all of it), which lie on one page
     // starting at row `off` of it.  bytes = 0 writes zeros instead.
-    const auto copy_rows = [&](auto from, auto to, uint32_t dst, int64_t page, int off, int bytes) {
+    const auto copy_rows = [&](auto from, auto to, uint32_t dst, uint32_t page, int off, int bytes) {
         constexpr int FROM = decltype(from)::value, TO = decltype(to)::value;
         constexpr int CPR = F::kRow / 16;  // chunks of a row, and copies a lane makes of a tile
-        const int64_t row = (page * 2 * a.cache.Hkv << log2_page) + off - FROM;
-        const uint8_t *src = codes0 + row * F::kRow;
-        const uint8_t *vsrc = src + vrows * F::kRow;
+        const uint8_t *src = codes0 + static_cast<uint64_t>(page) * page_codes + (off - FROM) * F::kRow;
+        const uint8_t *vsrc = src + page_codes / 2;
 #pragma unroll
         for (int i = CPR * FROM / kTile; i < CPR * TO / kTile; ++i) {
             const uint32_t d = dst + 512 * i + (copy_off ^ swizzle_step<F::kRow>(i));
             cp_async16(d, src + i * 512, bytes);
             cp_async16(d + S::kCodesBytes, vsrc + i * 512, bytes);
         }
-        const uint8_t *ssrc = scales0 + row * S::kScaleRow;
+        const uint8_t *ssrc = scales0 + static_cast<uint64_t>(page) * page_scales + (off - FROM) * S::kScaleRow;
         const uint32_t d = dst + 2 * S::kCodesBytes + lane * 16;
         if constexpr (SCH == 32) {
             if (FROM == 0 ? (TO == kTile || lane < 16) : lane >= 16) {
                 cp_async16(d, ssrc, bytes);
-                cp_async16(d + S::kScalesBytes, ssrc + vrows * S::kScaleRow, bytes);
+                cp_async16(d + S::kScalesBytes, ssrc + page_scales / 2, bytes);
             }
         } else {
             const int c = lane % SCH;
@@ -571,7 +589,6 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
 
     // -- running state: column sums, and the finished product's rows ------------------
     float o[S::MT][NT][4], l[NT][2], m[NT][2], ref[NT][2];
-    float corr[S::kOffsetSums ? NG : 1][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -585,37 +602,12 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.0f;
     }
-    if constexpr (S::kOffsetSums) {
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) corr[g][i] = 0.0f;
-    }
     // Value scales lie below 2^(scale_exp + 1); the weights are kept below
     // 2^(14 - scale_exp), so that their products stay inside fp16.  A new reference
     // leaves them kSlack powers of two to grow, and is taken only when that is used
     // up: rescaling at every new maximum took 55% of the tiles of a ragged decode batch.
     // Weights of 2^-22 of the largest are still normal numbers.
     int scale_exp = 0;
-
-    const auto take_off = [&]() {  // the codes' offset, collected in corr, off the sums
-        if constexpr (S::kOffsetSums) {
-            constexpr float odd = BITS == 4 ? 16.0f : 1.0f;  // odd 4-bit rows count sixteenfold
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-#pragma unroll
-                for (int mt = 2 * g; mt < 2 * g + 2; ++mt) {
-                    o[mt][0][0] += corr[g][0];
-                    o[mt][0][1] += corr[g][1];
-                    o[mt][0][2] = fmaf(odd, corr[g][2], o[mt][0][2]);
-                    o[mt][0][3] = fmaf(odd, corr[g][3], o[mt][0][3]);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) corr[g][i] = 0.0f;
-            }
-        }
-    };
-    int turn = 0;  // tiles since then
 
     // lane's places in a stage
     const int key_a = (r >> 1) + 4 * (r & 1);  // token of its first operand row
@@ -696,7 +688,7 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
                         f[s][3] = (kb[2 * g + s] >> 8) & 0x00FF00FFu;
                     }
                 }
-                if constexpr (!S::kOffsetSums) {
+                if constexpr (!S::kKeySums) {
                     constexpr uint32_t z = F::kZero * 0x00010001u, z2 = BITS == 4 ? 16 * z : z;
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
@@ -712,26 +704,14 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
                 const float fb = g & 1 ? __high2float(hb) : __low2float(hb);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    uint32_t q0, q1, q2, q3;
-                    if constexpr (S::kQueryRegs) {
-                        q0 = qreg[g][0][0];
-                        q1 = qreg[g][0][1];
-                        q2 = qreg[g][1][0];
-                        q3 = qreg[g][1][1];
-                    } else {
-                        const uint4 v = ld_shared16(qsm + ((nt * NG + g) * 32 + lane) * 16);
-                        q0 = v.x;
-                        q1 = v.y;
-                        q2 = v.z;
-                        q3 = v.w;
-                    }
+                    const uint4 q = ld_shared16(qsm + ((nt * NG + g) * 32 + lane) * 16);
                     float d[4];
-                    if constexpr (S::kOffsetSums)
-                        mma_f16(d, f[0][0], f[0][1], f[0][2], f[0][3], q0, q1, offset[g][0], offset[g][1],
+                    if constexpr (S::kKeySums)
+                        mma_f16(d, f[0][0], f[0][1], f[0][2], f[0][3], q.x, q.y, offset[g][0], offset[g][1],
                                 offset[g][0], offset[g][1]);
                     else
-                        mma_f16(d, f[0][0], f[0][1], f[0][2], f[0][3], q0, q1, 0.0f, 0.0f, 0.0f, 0.0f);
-                    mma_f16(d, f[1][0], f[1][1], f[1][2], f[1][3], q2, q3);
+                        mma_f16(d, f[0][0], f[0][1], f[0][2], f[0][3], q.x, q.y, 0.0f, 0.0f, 0.0f, 0.0f);
+                    mma_f16(d, f[1][0], f[1][1], f[1][2], f[1][3], q.z, q.w);
                     x[mt][nt][0] = fmaf(fa, d[0], x[mt][nt][0]);
                     x[mt][nt][1] = fmaf(fa, d[1], x[mt][nt][1]);
                     x[mt][nt][2] = fmaf(fb, d[2], x[mt][nt][2]);
@@ -801,12 +781,6 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
                 for (int mt = 0; mt < S::MT; ++mt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[mt][nt][i] *= f[i & 1];
-                if constexpr (S::kOffsetSums) {
-#pragma unroll
-                    for (int g = 0; g < NG; ++g)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) corr[g][i] *= f[i & 1];
-                }
             }
         }
 
@@ -862,10 +836,6 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
                         w1[nt] &= ~__vcmpeq2(p[mt][nt][1], 0x80008000u);
                     }
                 }
-                if constexpr (S::kOffsetSums) {
-                    constexpr uint32_t z = (0x8000u | F::kZero) * 0x00010001u;  // -zero * 2^-24
-                    mma_f16(corr[g], z, z, z, z, w0[0], w1[0]);
-                }
 #pragma unroll
                 for (int hm = 0; hm < 2; ++hm) {
                     uint32_t f0, f1, f2, f3;
@@ -884,13 +854,11 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
                         f2 = u1 & 0x00FF00FFu;
                         f3 = (u1 >> 8) & 0x00FF00FFu;
                     }
-                    if constexpr (!S::kOffsetSums) {
-                        constexpr uint32_t z = F::kZero * 0x00010001u, z2 = BITS == 4 ? 16 * z : z;
-                        f0 = hsub2_bits(f0, z);
-                        f1 = hsub2_bits(f1, z2);
-                        f2 = hsub2_bits(f2, z);
-                        f3 = hsub2_bits(f3, z2);
-                    }
+                    constexpr uint32_t z = F::kZero * 0x00010001u, z2 = BITS == 4 ? 16 * z : z;
+                    f0 = hsub2_bits(f0, z);
+                    f1 = hsub2_bits(f1, z2);
+                    f2 = hsub2_bits(f2, z);
+                    f3 = hsub2_bits(f3, z2);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) mma_f16(o[2 * g + hm][nt], f0, f1, f2, f3, w0[nt], w1[nt]);
                 }
@@ -922,15 +890,6 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
             next = pages_of(kn + kAttnWarps);
             cp_async_commit();
         }
-        if constexpr (S::kOffsetSums) {
-            // The sums of stored codes carry the offset, about z sum(w) beside a signal
-            // that grows like its root, and the tensor core cuts every addition to fp32:
-            // taken off every eighth tile the offset never outgrows the signal.
-            if (++turn == 8) {
-                turn = 0;
-                take_off();
-            }
-        }
         const uint32_t base = ring_addr + stage * S::kStage;
         stage = stage + 1 == S::kStages ? 0 : stage + 1;
         const int t0 = it.token(k);
@@ -943,7 +902,6 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, 
             do_tile(std::false_type(), base, t0);
     }
 
-    take_off();
     // -- join the warps ---------------------------------------------------------------------
     cp_async_wait<0>();
     __syncthreads();  // every ring is idle: its space takes the sums
@@ -1011,21 +969,20 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, BITS, NT>::kCtas)
     pdl_trigger();
     pdl_wait();
     const Line line = find_unit<S::NQ>(a, blockIdx.x == 0, scratch);
-    const int64_t ctas = line_ctas(line.units, a.grid);
-    if (line.units == 0 || blockIdx.x >= ctas) return;
-    const int64_t u0 = line_start(line.units, ctas, blockIdx.x);
-    const int64_t u1 = line_start(line.units, ctas, blockIdx.x + 1);
+    const Cut cut(line.units, a.grid);
+    if (line.units == 0 || blockIdx.x >= cut.ctas) return;
+    const int64_t u0 = cut.start(blockIdx.x), u1 = cut.start(blockIdx.x + 1);
     int64_t item = line.item, before = line.before, u = u0;
     while (u < u1) {
-        const int64_t b = item / a.q_tiles;
-        const Item it = make_item<S::NQ>(a, b, item % a.q_tiles);
+        const Item it = make_item<S::NQ>(a, item);
         if (it.n == 0) {
             ++item;
             continue;
         }
         const int units = it.units();
         const int64_t in = u - before * a.cache.Hkv;
-        const int head = static_cast<int>(in / units), v0 = static_cast<int>(in % units);
+        const int head = static_cast<int>(quotient(in, units));
+        const int v0 = static_cast<int>(in - static_cast<int64_t>(head) * units);
         const int64_t left = u1 - u;
         const int v1 = units - v0 <= left ? units : v0 + static_cast<int>(left);
         const int k0 = v0 > kLead ? v0 - kLead : 0, k1 = v1 - kLead;
@@ -1033,7 +990,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, BITS, NT>::kCtas)
             float *part = nullptr;
             if (k1 - k0 != it.n)
                 part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1)) * S::kSlot;
-            attend_run<D, BITS, NT>(a, it, b, head, k0, k1, part, attn_smem);
+            attend_run<D, BITS, NT>(a, it, head, k0, k1, part, attn_smem);
         }
         u += v1 - v0;
         if (v1 == units && head == a.cache.Hkv - 1) {
@@ -1045,50 +1002,94 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, BITS, NT>::kCtas)
 
 // ---- joining the pieces of a cut (query tile, head) -------------------------------------
 
-// One block for one item and kv head: nothing to do where one CTA held it all;
-// rows that see no token get their zeros here.
+// blockIdx.x: item, y: kv head, z: a share of the columns' quads of dimensions.
+// Nothing to do where one CTA held it all; rows that see no token get their zeros
+// here.  A lane owns four dimensions of a column; a warp takes all pieces of its
+// columns where they are few, else the warps share them.
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads) kv_attention_join_kernel(const KvAttnArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) kv_attention_join_kernel(const KvAttnArgs a) {
     constexpr int NQ = 8 * NT, SLOT = NQ * (D + 2), QUADS = D / 4;
+    constexpr int W = QUADS < 32 ? QUADS : 32;  // lanes of one column
+    __shared__ float4 s_acc[kJoinWarps][32];
+    __shared__ float s_ref[kJoinWarps][32], s_l[kJoinWarps][32];
     pdl_trigger();
     pdl_wait();
     const int64_t item = blockIdx.x;
     const int kvh = blockIdx.y, Hkv = a.cache.Hkv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t before = a.prefix[item], n = a.prefix[item + 1] - before;
     const int64_t units = a.prefix[a.B * a.q_tiles] * Hkv;
-    int64_t c0 = 0, c1 = -1, first = 0, ctas = 1;
+    const float *parts = nullptr, *first_part = nullptr;
+    int pieces = 0;
     if (n > 0) {
-        first = before * Hkv + kvh * n;
-        ctas = line_ctas(units, a.grid);
-        // the CTAs that hold the first and the last unit with work
-        const int64_t u0 = first + kLead, u1 = first + n - 1;
-        c0 = u0 * ctas / units;
-        while (line_start(units, ctas, c0 + 1) <= u0) ++c0;
-        c1 = u1 * ctas / units;
-        while (line_start(units, ctas, c1 + 1) <= u1) ++c1;
+        const Cut cut(units, a.grid);
+        const int64_t first = before * Hkv + kvh * n;
+        // the CTAs that hold the first and the last unit with work; all but the first
+        // of them begin with this piece
+        const int64_t c0 = cut.cta_of(first + kLead), c1 = cut.cta_of(first + n - 1);
         if (c0 == c1) return;
+        pieces = static_cast<int>(c1 - c0) + 1;
+        parts = a.partial + 2 * c0 * SLOT;
+        first_part = parts + (cut.start(c0) < first ? SLOT : 0);
     }
-    const Item it = make_item<NQ>(a, item / a.q_tiles, item % a.q_tiles);
-    for (int idx = threadIdx.x; idx < it.ncols * QUADS; idx += kAttnThreads) {
-        const int col = idx / QUADS, d0 = idx % QUADS * 4;
+    const Item it = make_item<NQ>(a, item);
+    const auto piece = [&](int p) { return p == 0 ? first_part : parts + static_cast<int64_t>(p) * 2 * SLOT; };
+    const bool share = pieces > kFewPieces;
+    const int p0 = share ? warp : 0, step = share ? kJoinWarps : 1;
+    const int chunk0 = share ? blockIdx.z : blockIdx.z * kJoinWarps + warp;
+    const int chunks = share ? gridDim.z : gridDim.z * kJoinWarps;
+    for (int base = chunk0 * 32; base < it.ncols * QUADS; base += 32 * chunks) {
+        const int col = (base + lane) / QUADS, d0 = (base + lane) % QUADS * 4;
+        const bool live = col < it.ncols;
+        // the largest reference of the warp's pieces and their sum of weights, by the
+        // column's lanes together
+        float top = -INFINITY, l = 0.0f;
+        if (live)
+            for (int p = p0 + step * (lane % W); p < pieces; p += step * W) top = fmaxf(top, piece(p)[NQ * D + col]);
+#pragma unroll
+        for (int o = W / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float ref = top == -INFINITY ? 0.0f : top;
+        if (live)
+            for (int p = p0 + step * (lane % W); p < pieces; p += step * W)
+                l = fmaf(piece(p)[NQ * D + NQ + col], exp2_approx(piece(p)[NQ * D + col] - ref), l);
+#pragma unroll
+        for (int o = W / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float l = 0.0f, top = -INFINITY;
-        for (int64_t c = c0; c <= c1; ++c) {
-            const int64_t slot = 2 * c + (line_start(units, ctas, c) < first ? 1 : 0);
-            const float *part = a.partial + slot * SLOT;
-            const float pr = part[NQ * D + col], pl = part[NQ * D + NQ + col];
-            const float4 v = *reinterpret_cast<const float4 *>(part + col * D + d0);
-            const float nt = fmaxf(top, pr);
-            const float base = nt == -INFINITY ? 0.0f : nt;
-            const float f = exp2_approx(top - base), g = exp2_approx(pr - base);
-            acc.x = fmaf(v.x, g, acc.x * f);
-            acc.y = fmaf(v.y, g, acc.y * f);
-            acc.z = fmaf(v.z, g, acc.z * f);
-            acc.w = fmaf(v.w, g, acc.w * f);
-            l = fmaf(pl, g, l * f);
-            top = nt;
+        if (live) {
+#pragma unroll 8
+            for (int p = p0; p < pieces; p += step) {
+                const float *part = piece(p);
+                const float f = exp2_approx(part[NQ * D + col] - ref);
+                const float4 v = *reinterpret_cast<const float4 *>(part + col * D + d0);
+                acc.x = fmaf(v.x, f, acc.x);
+                acc.y = fmaf(v.y, f, acc.y);
+                acc.z = fmaf(v.z, f, acc.z);
+                acc.w = fmaf(v.w, f, acc.w);
+            }
         }
-        store_result<D>(a, it, kvh * a.group, col, d0, acc, top == -INFINITY ? 0.0f : top, l);
+        if (share) {
+            s_acc[warp][lane] = acc;
+            s_ref[warp][lane] = top;
+            s_l[warp][lane] = l;
+            __syncthreads();
+            if (warp == 0) {
+                for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, s_ref[w][lane]);
+                ref = top == -INFINITY ? 0.0f : top;
+                acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                l = 0.0f;
+                for (int w = 0; w < kJoinWarps; ++w) {
+                    const float f = exp2_approx(s_ref[w][lane] - ref);
+                    const float4 v = s_acc[w][lane];
+                    l = fmaf(s_l[w][lane], f, l);
+                    acc.x = fmaf(v.x, f, acc.x);
+                    acc.y = fmaf(v.y, f, acc.y);
+                    acc.z = fmaf(v.z, f, acc.z);
+                    acc.w = fmaf(v.w, f, acc.w);
+                }
+            }
+            __syncthreads();
+        }
+        if (live && (!share || warp == 0)) store_result<D>(a, it, kvh * a.group, col, d0, acc, ref, l);
     }
 }
 
@@ -1120,7 +1121,7 @@ static AttnPlan attn_plan_of(int sm_count, int64_t B, int group, int64_t max_q_l
     AttnPlan p;
     p.nt = NT;
     p.q_tiles = (max_q_len * group + S::NQ - 1) / S::NQ;
-    p.grid = sm_count * S::kCtas * kWaves;
+    p.grid = sm_count * S::kCtas;
     p.prefix_bytes = ((B * p.q_tiles + 1) * 8 + 15) / 16 * 16;
     p.bytes = p.prefix_bytes + static_cast<int64_t>(p.grid) * 2 * S::kSlot * 4;
     return p;
@@ -1164,9 +1165,13 @@ static int attn_launch(const KvAttnArgs &a, cudaStream_t st) {
     }
     const int rc = launch_pdl(kernel, dim3(static_cast<unsigned>(a.grid)), dim3(kAttnThreads), S::kSmem, st, a);
     if (rc != RN_OK) return rc;
+    // blocks enough for two on each place of the grid, as far as there are columns
+    const int64_t heads = a.B * a.q_tiles * a.cache.Hkv, most = S::NQ * D / 4 / 32;
+    const int64_t want = (2 * static_cast<int64_t>(a.grid) + heads - 1) / heads;
+    const unsigned shares = static_cast<unsigned>(want < most ? want : most);
     return launch_pdl(kv_attention_join_kernel<D, NT>,
-                      dim3(static_cast<unsigned>(a.B * a.q_tiles), static_cast<unsigned>(a.cache.Hkv)),
-                      dim3(kAttnThreads), 0, st, a);
+                      dim3(static_cast<unsigned>(a.B * a.q_tiles), static_cast<unsigned>(a.cache.Hkv), shares),
+                      dim3(32 * kJoinWarps), 0, st, a);
 }
 
 static int kv_attention_check(int format, int64_t B, int Hq, int Hkv, int D, int64_t max_q_len) {

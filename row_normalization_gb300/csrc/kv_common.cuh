@@ -62,7 +62,7 @@ inline int kv_log2_page(int page_size) {
 inline int kv_check_sizes(int format, int Hkv, int D, int page_size, int64_t num_pages) {
     if (format != RN_KV_INT4 && format != RN_KV_INT8) return RN_ERR_ARG;
     if (D != 64 && D != 128 && D != 256) return RN_ERR_SHAPE;
-    if (Hkv < 1 || Hkv > 65535) return RN_ERR_SHAPE;
+    if (Hkv < 1 || Hkv > 16384) return RN_ERR_SHAPE;  // a page's codes stay under 4 GB
     if (kv_log2_page(page_size) < 0) return RN_ERR_SHAPE;
     if (num_pages < 1 || num_pages > INT32_MAX) return RN_ERR_SHAPE;
     return RN_OK;
