@@ -31,36 +31,9 @@
 // leaves partial sums in the workspace, which a second kernel joins in the
 // order of the line.  Inside a CTA four warps take every fourth tile with an
 // asynchronous copy ring of their own each and join at the end.
-#include "kv_common.cuh"
+#include "kv_attention.cuh"
 
 namespace rn {
-
-static __device__ unsigned int g_kv_attention_status = 0u;
-
-struct KvAttnArgs {
-    const uint16_t *q;
-    int64_t q_stride;
-    KvCache cache;
-    const int32_t *page_table;
-    int64_t B;
-    int64_t max_pages;
-    const int32_t *kv_lens;
-    const int64_t *cu_q;
-    int64_t T;
-    int64_t max_q_len;
-    int Hq;
-    int group;         // query heads of a kv head
-    float scale_log2;  // softmax scale * log2(e)
-    int window;        // 0: none
-    int sinks;
-    uint16_t *out;
-    float *lse;
-    // workspace: the units before each item [items + 1], then the partial sums
-    int64_t *prefix;
-    float *partial;
-    int64_t q_tiles;   // query tiles of a sequence
-    int grid;          // CTAs of the attention kernel
-};
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
@@ -70,8 +43,6 @@ constexpr float kSlack = 6.0f;       // powers of two a weight may grow before a
 // copies, and the joining of its warps.  64 ragged sequences of 8 heads (540k tokens):
 // 175 us with none, 158 with 8, 128 with 16, 132 with 32; 4 long ones 124-126 throughout.
 constexpr int kLead = 16;
-constexpr int kJoinWarps = 8;
-constexpr int kFewPieces = 8;     // pieces that one warp joins by itself
 constexpr int kMinTiles = kAttnWarps;  // a CTA's run is no shorter: one tile a warp
 
 // Shapes of an instantiation: NT * 8 columns (queries of the tile times heads).
@@ -79,6 +50,7 @@ template <int D, int BITS, int NT>
 struct AttnShape {
     using F = KvFormat<D, BITS>;
     static constexpr int NQ = 8 * NT;
+    using L = LineShape<NQ, kTile, kLead, kMinTiles>;
     static constexpr int MT = D / 16;                 // 16-row tiles of the value product
     static constexpr int kScaleRow = 2 * F::kGroups;  // bytes of a row's scales
     static constexpr int kCodesBytes = kTile * F::kRow;
@@ -125,12 +97,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-    return r;
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
@@ -200,185 +166,7 @@ constexpr uint32_t swizzle_step(int i) {
     return 16 * (((i & 1) * Swizzle<ROW>::m2) ^ ((i >> 1 & 1) * Swizzle<ROW>::m3));
 }
 
-// ---- the line of units ------------------------------------------------------------
-
-// One (sequence, query tile): its columns and the tiles of tokens they see.
-struct Item {
-    int64_t seq;     // the sequence
-    int64_t row0;    // its first query row
-    int f0, ncols;   // columns f0 .. f0 + ncols - 1 of the sequence's n_q * group
-    int pos0;        // position of the sequence's first query
-    int lo_pos, hi;  // position of the first column's query; one past the last column's
-    int win_lo;      // first token inside the first column's window (0 without one)
-    int sink_tiles;  // tiles 0 .. sink_tiles - 1, then lo_tile ..
-    int lo_tile;
-    int n;           // tiles in all
-    bool bad;        // something had to be cut to the tensors
-
-    // its units on the line, for one head
-    __device__ __forceinline__ int units() const { return n > 0 ? n + kLead : 0; }
-
-    __device__ __forceinline__ int token(int k) const {
-        return (k < sink_tiles ? k : lo_tile + (k - sink_tiles)) * kTile;
-    }
-};
-
-template <int NQ>
-__device__ __forceinline__ Item make_item(const KvAttnArgs &a, int64_t item) {
-    Item it;
-    uint32_t b = static_cast<uint32_t>(item), qt = 0;  // items fit 31 bits
-    if (a.q_tiles != 1) {
-        b = static_cast<uint32_t>(item) / static_cast<uint32_t>(a.q_tiles);
-        qt = static_cast<uint32_t>(item) - b * static_cast<uint32_t>(a.q_tiles);
-    }
-    it.seq = b;
-    it.bad = false;
-    int64_t nq = 1;
-    it.row0 = b;
-    if (a.cu_q) {
-        it.row0 = a.cu_q[b];
-        nq = a.cu_q[b + 1] - it.row0;
-        if (nq > 0 && (it.row0 < 0 || it.row0 + nq > a.T)) {
-            it.bad = true;
-            nq = 0;
-        }
-    }
-    if (nq < 0) nq = 0;
-    int64_t len = a.kv_lens[b];
-    const int64_t room = a.max_pages << a.cache.log2_page;
-    if (len > room) {
-        it.bad = true;
-        len = room;
-    }
-    if (len < 0) len = 0;
-    it.pos0 = static_cast<int>(len - nq);
-    if (nq > a.max_q_len) {
-        it.bad = true;
-        nq = a.max_q_len;
-    }
-    const int64_t left = nq * a.group - static_cast<int64_t>(qt) * NQ;
-    it.f0 = static_cast<int>(qt * NQ);
-    it.ncols = static_cast<int>(left < 0 ? 0 : (left < NQ ? left : NQ));
-    it.lo_pos = it.pos0 + it.f0 / a.group;
-    it.hi = it.pos0 + (it.f0 + it.ncols - 1) / a.group + 1;
-    it.win_lo = it.sink_tiles = it.lo_tile = it.n = 0;
-    if (it.ncols == 0 || it.hi <= 0) return it;
-    const int tiles = (it.hi + kTile - 1) / kTile;
-    if (a.window && it.lo_pos >= a.window) {
-        it.win_lo = it.lo_pos - a.window + 1;
-        it.sink_tiles = a.sinks >= it.hi ? tiles : (a.sinks + kTile - 1) / kTile;
-        if (it.sink_tiles > tiles) it.sink_tiles = tiles;
-        it.lo_tile = it.win_lo / kTile;
-        if (it.lo_tile < it.sink_tiles) it.lo_tile = it.sink_tiles;
-    }
-    it.n = it.sink_tiles + tiles - it.lo_tile;
-    return it;
-}
-
-// a / b, in 32 bits where both fit (they nearly always do).
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
-// The line cut into runs for its CTAs, the first `rest` of them one unit longer.
-struct Cut {
-    int64_t ctas, run, rest;
-
-    __device__ __forceinline__ Cut(int64_t units, int grid) {
-        const int64_t want = (units + kMinTiles - 1) / kMinTiles;
-        ctas = want < grid ? (want > 0 ? want : 1) : grid;
-        run = quotient(units, ctas);
-        rest = units - run * ctas;
-    }
-    __device__ __forceinline__ int64_t start(int64_t c) const { return c * run + (c < rest ? c : rest); }
-    __device__ __forceinline__ int64_t cta_of(int64_t unit) const {
-        const int64_t longer = rest * (run + 1);
-        return unit < longer ? quotient(unit, run + 1) : rest + quotient(unit - longer, run);
-    }
-};
-
-// Four dimensions of a finished column: out = sum / l (the codes' 2^-24 undone),
-// lse = (reference + log2(l)) ln 2.
-template <int D>
-__device__ __forceinline__ void store_result(const KvAttnArgs &a, const Item &it, int head0, int col, int d0,
-                                             float4 v, float ref, float l) {
-    const int f = it.f0 + col;
-    const int64_t t = it.row0 + f / a.group;
-    const int64_t row = t * a.Hq + head0 + f % a.group;
-    const float inv = l == 0.0f ? 0.0f : 0x1p24f / l;
-    const uint2 w = make_uint2(pack_bf2(v.x * inv, v.y * inv), pack_bf2(v.z * inv, v.w * inv));
-    *reinterpret_cast<uint2 *>(a.out + row * D + d0) = w;
-    if (d0 == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
-}
-
 // ---- the attention kernel ---------------------------------------------------------
-
-// Sum of the item sizes before this thread's share, by a scan over the block;
-// every CTA runs it over all items, so that no launch has to come before.
-struct Line {
-    int64_t units;        // in all, over every kv head
-    int64_t item, before; // the item at a wanted unit, and the units of one head before it
-};
-
-template <int NQ>
-__device__ __forceinline__ Line find_unit(const KvAttnArgs &a, bool publish, int64_t *scratch) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t items = a.B * a.q_tiles;
-    const int64_t per = (items + kAttnThreads - 1) / kAttnThreads;
-    const int64_t i0 = tid * per < items ? tid * per : items;
-    const int64_t i1 = i0 + per < items ? i0 + per : items;
-    int64_t sum = 0;
-    bool bad = false;
-    for (int64_t i = i0; i < i1; ++i) {
-        const Item it = make_item<NQ>(a, i);
-        sum += it.units();
-        bad |= it.bad;
-    }
-    if (publish && bad) atomicOr(&g_kv_attention_status, RN_STATUS_BAD_INDEX);
-    int64_t incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) scratch[warp] = incl;
-    __syncthreads();
-    int64_t before = incl - sum, total = 0;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) {
-        if (w < warp) before += scratch[w];
-        total += scratch[w];
-    }
-    if (publish) {
-        int64_t run = before;
-        for (int64_t i = i0; i < i1; ++i) {
-            a.prefix[i] = run;
-            run += make_item<NQ>(a, i).units();
-        }
-        if (tid == 0) a.prefix[items] = total;
-    }
-    Line line;
-    line.units = total * a.cache.Hkv;
-    const Cut cut(line.units, a.grid);
-    const int64_t u = cut.start(blockIdx.x);
-    if (blockIdx.x < cut.ctas && before * a.cache.Hkv <= u && u < (before + sum) * a.cache.Hkv) {
-        int64_t run = before;
-        for (int64_t i = i0; i < i1; ++i) {
-            const int n = make_item<NQ>(a, i).units();
-            if (u < (run + n) * a.cache.Hkv) {
-                scratch[kAttnWarps] = i;
-                scratch[kAttnWarps + 1] = run;
-                break;
-            }
-            run += n;
-        }
-    }
-    __syncthreads();
-    line.item = scratch[kAttnWarps];
-    line.before = scratch[kAttnWarps + 1];
-    return line;
-}
 
 // A column's query as operand registers and what goes with it.
 template <int D, int BITS>
@@ -390,7 +178,8 @@ struct Query {
 
     // Column `col` of the item, lane j of its four.  The query is scaled so that its
     // largest element lies in [2^13, 2^14): exact in fp16 down to 2^-28 of that.
-    __device__ __forceinline__ void load(const KvAttnArgs &a, const Item &it, int head0, int col, int j) {
+    template <class L>
+    __device__ __forceinline__ void load(const KvAttnArgs &a, const Item<L> &it, int head0, int col, int j) {
         uint32_t w[F::kGroups][4];
         uint32_t top = 0u;
         const bool live = col < it.ncols;
@@ -447,7 +236,8 @@ struct Query {
 // Tiles [k0, k1) of one item and kv head: all warps, joined; the result goes to
 // the output rows, or (part != null) unfinished into a slot of the workspace.
 template <int D, int BITS, int NT>
-__device__ __forceinline__ void attend_run(const KvAttnArgs &a, const Item &it, int kvh,
+__device__ __forceinline__ void attend_run(const KvAttnArgs &a,
+                                           const Item<typename AttnShape<D, BITS, NT>::L> &it, int kvh,
                                            int k0, int k1, float *part, uint8_t *smem) {
     using S = AttnShape<D, BITS, NT>;
     using F = KvFormat<D, BITS>;
@@ -964,17 +754,18 @@ template <int D, int BITS, int NT>
 __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, BITS, NT>::kCtas)
     kv_attention_kernel(const KvAttnArgs a) {
     using S = AttnShape<D, BITS, NT>;
+    using L = typename S::L;
     extern __shared__ __align__(128) uint8_t attn_smem[];
     __shared__ int64_t scratch[kAttnWarps + 2];
     pdl_trigger();
     pdl_wait();
-    const Line line = find_unit<S::NQ>(a, blockIdx.x == 0, scratch);
-    const Cut cut(line.units, a.grid);
+    const Line line = find_unit<L, kAttnThreads>(a, blockIdx.x == 0, scratch);
+    const Cut<L> cut(line.units, a.grid);
     if (line.units == 0 || blockIdx.x >= cut.ctas) return;
     const int64_t u0 = cut.start(blockIdx.x), u1 = cut.start(blockIdx.x + 1);
     int64_t item = line.item, before = line.before, u = u0;
     while (u < u1) {
-        const Item it = make_item<S::NQ>(a, item);
+        const Item<L> it = make_item<L>(a, item);
         if (it.n == 0) {
             ++item;
             continue;
@@ -1000,104 +791,14 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, BITS, NT>::kCtas)
     }
 }
 
-// ---- joining the pieces of a cut (query tile, head) -------------------------------------
-
-// blockIdx.x: item, y: kv head, z: a share of the columns' quads of dimensions.
-// Nothing to do where one CTA held it all; rows that see no token get their zeros
-// here.  A lane owns four dimensions of a column; a warp takes all pieces of its
-// columns where they are few, else the warps share them.
-template <int D, int NT>
-__global__ void __launch_bounds__(32 * kJoinWarps) kv_attention_join_kernel(const KvAttnArgs a) {
-    constexpr int NQ = 8 * NT, SLOT = NQ * (D + 2), QUADS = D / 4;
-    constexpr int W = QUADS < 32 ? QUADS : 32;  // lanes of one column
-    __shared__ float4 s_acc[kJoinWarps][32];
-    __shared__ float s_ref[kJoinWarps][32], s_l[kJoinWarps][32];
-    pdl_trigger();
-    pdl_wait();
-    const int64_t item = blockIdx.x;
-    const int kvh = blockIdx.y, Hkv = a.cache.Hkv;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t before = a.prefix[item], n = a.prefix[item + 1] - before;
-    const int64_t units = a.prefix[a.B * a.q_tiles] * Hkv;
-    const float *parts = nullptr, *first_part = nullptr;
-    int pieces = 0;
-    if (n > 0) {
-        const Cut cut(units, a.grid);
-        const int64_t first = before * Hkv + kvh * n;
-        // the CTAs that hold the first and the last unit with work; all but the first
-        // of them begin with this piece
-        const int64_t c0 = cut.cta_of(first + kLead), c1 = cut.cta_of(first + n - 1);
-        if (c0 == c1) return;
-        pieces = static_cast<int>(c1 - c0) + 1;
-        parts = a.partial + 2 * c0 * SLOT;
-        first_part = parts + (cut.start(c0) < first ? SLOT : 0);
-    }
-    const Item it = make_item<NQ>(a, item);
-    const auto piece = [&](int p) { return p == 0 ? first_part : parts + static_cast<int64_t>(p) * 2 * SLOT; };
-    const bool share = pieces > kFewPieces;
-    const int p0 = share ? warp : 0, step = share ? kJoinWarps : 1;
-    const int chunk0 = share ? blockIdx.z : blockIdx.z * kJoinWarps + warp;
-    const int chunks = share ? gridDim.z : gridDim.z * kJoinWarps;
-    for (int base = chunk0 * 32; base < it.ncols * QUADS; base += 32 * chunks) {
-        const int col = (base + lane) / QUADS, d0 = (base + lane) % QUADS * 4;
-        const bool live = col < it.ncols;
-        // the largest reference of the warp's pieces and their sum of weights, by the
-        // column's lanes together
-        float top = -INFINITY, l = 0.0f;
-        if (live)
-            for (int p = p0 + step * (lane % W); p < pieces; p += step * W) top = fmaxf(top, piece(p)[NQ * D + col]);
-#pragma unroll
-        for (int o = W / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float ref = top == -INFINITY ? 0.0f : top;
-        if (live)
-            for (int p = p0 + step * (lane % W); p < pieces; p += step * W)
-                l = fmaf(piece(p)[NQ * D + NQ + col], exp2_approx(piece(p)[NQ * D + col] - ref), l);
-#pragma unroll
-        for (int o = W / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (live) {
-#pragma unroll 8
-            for (int p = p0; p < pieces; p += step) {
-                const float *part = piece(p);
-                const float f = exp2_approx(part[NQ * D + col] - ref);
-                const float4 v = *reinterpret_cast<const float4 *>(part + col * D + d0);
-                acc.x = fmaf(v.x, f, acc.x);
-                acc.y = fmaf(v.y, f, acc.y);
-                acc.z = fmaf(v.z, f, acc.z);
-                acc.w = fmaf(v.w, f, acc.w);
-            }
-        }
-        if (share) {
-            s_acc[warp][lane] = acc;
-            s_ref[warp][lane] = top;
-            s_l[warp][lane] = l;
-            __syncthreads();
-            if (warp == 0) {
-                for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, s_ref[w][lane]);
-                ref = top == -INFINITY ? 0.0f : top;
-                acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                l = 0.0f;
-                for (int w = 0; w < kJoinWarps; ++w) {
-                    const float f = exp2_approx(s_ref[w][lane] - ref);
-                    const float4 v = s_acc[w][lane];
-                    l = fmaf(s_l[w][lane], f, l);
-                    acc.x = fmaf(v.x, f, acc.x);
-                    acc.y = fmaf(v.y, f, acc.y);
-                    acc.z = fmaf(v.z, f, acc.z);
-                    acc.w = fmaf(v.w, f, acc.w);
-                }
-            }
-            __syncthreads();
-        }
-        if (live && (!share || warp == 0)) store_result<D>(a, it, kvh * a.group, col, d0, acc, ref, l);
-    }
-}
-
 int kv_attention_status(unsigned int *out, int clear) {
     return kv_status_word(g_kv_attention_status, out, clear);
 }
 
 // ---- host -------------------------------------------------------------------------------
+
+// More columns than this go to the kernel that takes 128 of them at a time.
+static bool wide(int64_t columns) { return columns > 64; }
 
 // Columns of a query tile, in eights: the smallest that holds all queries of a
 // sequence times the heads of a group, else the largest the registers hold.
@@ -1107,19 +808,10 @@ static int attn_tiles(int D, int64_t columns) {
     return 4;
 }
 
-struct AttnPlan {
-    int nt;
-    int64_t q_tiles;
-    int grid;
-    int64_t prefix_bytes;
-    int64_t bytes;
-};
-
 template <int D, int BITS, int NT>
 static AttnPlan attn_plan_of(int sm_count, int64_t B, int group, int64_t max_q_len) {
     using S = AttnShape<D, BITS, NT>;
     AttnPlan p;
-    p.nt = NT;
     p.q_tiles = (max_q_len * group + S::NQ - 1) / S::NQ;
     p.grid = sm_count * S::kCtas;
     p.prefix_bytes = ((B * p.q_tiles + 1) * 8 + 15) / 16 * 16;
@@ -1144,6 +836,7 @@ static auto attn_dispatch(int D, int format, int64_t columns, Fn &&f) {
 
 static AttnPlan attn_plan(int sm_count, int format, int64_t B, int Hq, int Hkv, int D, int64_t max_q_len) {
     const int group = Hq / Hkv;
+    if (wide(max_q_len * group)) return wide_plan(sm_count, B, group, D, max_q_len);
     return attn_dispatch(D, format, max_q_len * group, [&](auto d, auto bits, auto nt) {
         return attn_plan_of<d.value, bits.value, nt.value>(sm_count, B, group, max_q_len);
     });
@@ -1165,13 +858,7 @@ static int attn_launch(const KvAttnArgs &a, cudaStream_t st) {
     }
     const int rc = launch_pdl(kernel, dim3(static_cast<unsigned>(a.grid)), dim3(kAttnThreads), S::kSmem, st, a);
     if (rc != RN_OK) return rc;
-    // blocks enough for two on each place of the grid, as far as there are columns
-    const int64_t heads = a.B * a.q_tiles * a.cache.Hkv, most = S::NQ * D / 4 / 32;
-    const int64_t want = (2 * static_cast<int64_t>(a.grid) + heads - 1) / heads;
-    const unsigned shares = static_cast<unsigned>(want < most ? want : most);
-    return launch_pdl(kv_attention_join_kernel<D, NT>,
-                      dim3(static_cast<unsigned>(a.B * a.q_tiles), static_cast<unsigned>(a.cache.Hkv), shares),
-                      dim3(32 * kJoinWarps), 0, st, a);
+    return join_launch<D, typename S::L>(a, st);
 }
 
 static int kv_attention_check(int format, int64_t B, int Hq, int Hkv, int D, int64_t max_q_len) {
@@ -1250,6 +937,7 @@ int kv_attention_fwd(const rn_bf16 *q, int64_t q_stride, const uint8_t *codes,
     a.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.prefix_bytes);
     a.q_tiles = plan.q_tiles;
     a.grid = plan.grid;
+    if (rn::wide(max_q_len * a.group)) return rn::wide_launch(D, format, a, reinterpret_cast<cudaStream_t>(stream));
     return rn::attn_dispatch(D, format, max_q_len * a.group, [&](auto d, auto bits, auto nt) {
         return rn::attn_launch<d.value, bits.value, nt.value>(a, reinterpret_cast<cudaStream_t>(stream));
     });

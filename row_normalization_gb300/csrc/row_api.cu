@@ -161,14 +161,15 @@ int rn_device_status(unsigned int *out, int clear) {
         cudaGetLastError();
         return RN_ERR_DEVICE;
     }
-    unsigned int a = 0, b = 0, q = 0, c = 0, t = 0;
+    unsigned int a = 0, b = 0, q = 0, c = 0, t = 0, w = 0;
     int rc = rn::rows_status_bf16(&a, clear);
     if (rc == RN_OK) rc = rn::rows_status_f16(&b, clear);
     if (rc == RN_OK) rc = rn::qk_status(&q, clear);
     if (rc == RN_OK) rc = rn::kv_cache_status(&c, clear);
     if (rc == RN_OK) rc = rn::kv_attention_status(&t, clear);
+    if (rc == RN_OK) rc = rn::kv_attention_wide_status(&w, clear);
     if (rc != RN_OK) return rc;
-    *out = a | b | q | c | t;
+    *out = a | b | q | c | t | w;
     return RN_OK;
 }
 
