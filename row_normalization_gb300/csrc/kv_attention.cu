@@ -760,6 +760,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, BITS, NT>::kCtas)
     pdl_trigger();
     pdl_wait();
     const Line line = find_unit<L, kAttnThreads>(a, blockIdx.x == 0, scratch);
+    store_empty<D, L, kAttnThreads>(a);
     const Cut<L> cut(line.units, a.grid);
     if (line.units == 0 || blockIdx.x >= cut.ctas) return;
     const int64_t u0 = cut.start(blockIdx.x), u1 = cut.start(blockIdx.x + 1);
@@ -777,6 +778,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, BITS, NT>::kCtas)
         const int64_t left = u1 - u;
         const int v1 = units - v0 <= left ? units : v0 + static_cast<int>(left);
         const int k0 = v0 > kLead ? v0 - kLead : 0, k1 = v1 - kLead;
+        if (threadIdx.x == 0) note_piece(a, cut, u - v0, v0, v1, units, item, head);
         if (k1 > k0) {
             float *part = nullptr;
             if (k1 - k0 != it.n)
@@ -814,8 +816,8 @@ static AttnPlan attn_plan_of(int sm_count, int64_t B, int group, int64_t max_q_l
     AttnPlan p;
     p.q_tiles = (max_q_len * group + S::NQ - 1) / S::NQ;
     p.grid = sm_count * S::kCtas;
-    p.prefix_bytes = ((B * p.q_tiles + 1) * 8 + 15) / 16 * 16;
-    p.bytes = p.prefix_bytes + static_cast<int64_t>(p.grid) * 2 * S::kSlot * 4;
+    p.head_bytes = 16 + 32 * static_cast<int64_t>(p.grid);
+    p.bytes = p.head_bytes + static_cast<int64_t>(p.grid) * 2 * S::kSlot * 4;
     return p;
 }
 
@@ -933,9 +935,11 @@ int kv_attention_fwd(const rn_bf16 *q, int64_t q_stride, const uint8_t *codes,
     a.sinks = static_cast<int>(sinks < INT32_MAX ? sinks : INT32_MAX);
     a.out = out;
     a.lse = lse;
-    a.prefix = static_cast<int64_t *>(workspace);
-    a.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.prefix_bytes);
+    a.units = static_cast<int64_t *>(workspace);
+    a.cuts = reinterpret_cast<rn::CutHead *>(static_cast<char *>(workspace) + 16);
+    a.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.head_bytes);
     a.q_tiles = plan.q_tiles;
+    a.heads = B * plan.q_tiles * Hkv;
     a.grid = plan.grid;
     if (rn::wide(max_q_len * a.group)) return rn::wide_launch(D, format, a, reinterpret_cast<cudaStream_t>(stream));
     return rn::attn_dispatch(D, format, max_q_len * a.group, [&](auto d, auto bits, auto nt) {

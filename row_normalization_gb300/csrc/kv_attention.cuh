@@ -28,11 +28,22 @@ struct KvAttnArgs {
     int sinks;
     uint16_t *out;
     float *lse;
-    // workspace: the units before each item [items + 1], then the partial sums
-    int64_t *prefix;
+    // workspace: the line's length, what each CTA's start cuts [grid], the partial sums
+    int64_t *units;
+    struct CutHead *cuts;
     float *partial;
     int64_t q_tiles;   // query tiles of a sequence
+    int64_t heads;     // (query tile, kv head)s in all
     int grid;          // CTAs of the attention kernel
+};
+
+// A (query tile, head) that the start of CTA `cta`'s run cuts, noted where the CTA
+// before holds its first piece, so that every cut one is noted once; item -1: none.
+// The notes are one for each (query tile, head) where these are fewer than the
+// CTAs, else one for each CTA.
+struct CutHead {
+    int64_t first;  // its first unit
+    int32_t item, head, cta, unused;
 };
 
 // How a kernel lays its work on the line: NQ columns (queries of the tile times
@@ -198,16 +209,9 @@ __device__ __forceinline__ Line find_unit(const KvAttnArgs &a, bool publish, int
         if (w < warp) before += scratch[w];
         total += scratch[w];
     }
-    if (publish) {
-        int64_t run = before;
-        for (int64_t i = i0; i < i1; ++i) {
-            a.prefix[i] = run;
-            run += make_item<L>(a, i).units();
-        }
-        if (tid == 0) a.prefix[items] = total;
-    }
     Line line;
     line.units = total * a.cache.Hkv;
+    if (publish && tid == 0) *a.units = line.units;
     const Cut<L> cut(line.units, a.grid);
     const int64_t u = cut.start(blockIdx.x);
     if (blockIdx.x < cut.ctas && before * a.cache.Hkv <= u && u < (before + sum) * a.cache.Hkv) {
@@ -228,15 +232,55 @@ __device__ __forceinline__ Line find_unit(const KvAttnArgs &a, bool publish, int
     return line;
 }
 
+// Zeros for the rows of items that see no token, shared out over the CTAs.
+template <int D, class L, int THREADS>
+__device__ __forceinline__ void store_empty(const KvAttnArgs &a) {
+    const int64_t items = a.B * a.q_tiles;
+    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        const Item<L> it = make_item<L>(a, i);
+        if (it.n > 0) continue;
+        if (a.heads <= a.grid && threadIdx.x < a.cache.Hkv) a.cuts[i * a.cache.Hkv + threadIdx.x].item = -1;
+        const int quads = it.ncols * (D / 4);
+        for (int idx = threadIdx.x; idx < quads * a.cache.Hkv; idx += THREADS) {
+            const int head = idx / quads, in = idx - head * quads;
+            store_result<D>(a, it, head * a.group, in / (D / 4), in % (D / 4) * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f),
+                            0.0f, 0.0f);
+        }
+    }
+}
+
+// Notes for the joining kernel on the piece [v0, v1) of `units` units of a (query
+// tile, head) whose first unit is `first`; by one thread.
+template <class L>
+__device__ __forceinline__ void note_piece(const KvAttnArgs &a, const Cut<L> &cut, int64_t first, int v0, int v1,
+                                           int units, int64_t item, int head) {
+    CutHead c;
+    c.first = first;
+    c.item = static_cast<int32_t>(item);
+    c.head = head;
+    c.cta = blockIdx.x;
+    c.unused = 0;
+    // the second piece: the CTA before holds the first unit with work
+    const bool second =
+        v0 > L::LEAD && cut.start(static_cast<int64_t>(blockIdx.x) - 1) <= first + L::LEAD;
+    if (a.heads <= a.grid) {
+        const bool whole = v0 <= L::LEAD && v1 == units;
+        if (whole) c.item = -1;
+        if (whole || second) a.cuts[item * a.cache.Hkv + head] = c;
+    } else if (first + v0 == cut.start(blockIdx.x)) {
+        if (!second) c.item = -1;
+        a.cuts[blockIdx.x] = c;
+    }
+}
+
 constexpr int kJoinWarps = 8;
+constexpr int64_t kJoinBlocks = 2432;  // about sixteen an SM
 constexpr int kFewPieces = 8;  // pieces that one warp joins by itself
 
 // ---- joining the pieces of a cut (query tile, head) -------------------------------------
 
-// blockIdx.x: item, y: kv head, z: a share of the columns' quads of dimensions.
-// Nothing to do where one CTA held it all; rows that see no token get their zeros
-// here.  A lane owns four dimensions of a column; a warp takes all pieces of its
-// columns where they are few, else the warps share them.
+// blockIdx.x: a note on a cut (query tile, head), y: a share of the columns' quads of dimensions.  A lane owns four dimensions of a column; a warp
+// takes all pieces of its columns where they are few, else the warps share them.
 template <int D, class L>
 __global__ void __launch_bounds__(32 * kJoinWarps) kv_attention_join_kernel(const KvAttnArgs a) {
     constexpr int NQ = L::NQ, SLOT = NQ * (D + 2), QUADS = D / 4;
@@ -245,30 +289,25 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_attention_join_kernel(cons
     __shared__ float s_ref[kJoinWarps][32], s_l[kJoinWarps][32];
     pdl_trigger();
     pdl_wait();
-    const int64_t item = blockIdx.x;
-    const int kvh = blockIdx.y, Hkv = a.cache.Hkv;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t before = a.prefix[item], n = a.prefix[item + 1] - before;
-    const int64_t units = a.prefix[a.B * a.q_tiles] * Hkv;
-    const float *parts = nullptr, *first_part = nullptr;
-    int pieces = 0;
-    if (n > 0) {
-        const Cut<L> cut(units, a.grid);
-        const int64_t first = before * Hkv + kvh * n;
-        // the CTAs that hold the first and the last unit with work; all but the first
-        // of them begin with this piece
-        const int64_t c0 = cut.cta_of(first + L::LEAD), c1 = cut.cta_of(first + n - 1);
-        if (c0 == c1) return;
-        pieces = static_cast<int>(c1 - c0) + 1;
-        parts = a.partial + 2 * c0 * SLOT;
-        first_part = parts + (cut.start(c0) < first ? SLOT : 0);
-    }
-    const Item<L> it = make_item<L>(a, item);
+    const int64_t units = *a.units;
+    if (units == 0) return;
+    const Cut<L> cut(units, a.grid);
+    if (a.heads > a.grid && blockIdx.x >= cut.ctas) return;
+    const CutHead cuthead = a.cuts[blockIdx.x];
+    if (cuthead.item < 0) return;
+    const Item<L> it = make_item<L>(a, cuthead.item);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kvh = cuthead.head;
+    // pieces lie with the CTA before and those up to the one that holds the last unit;
+    // all but the first of them begin with theirs
+    const int64_t c0 = cuthead.cta - 1;
+    const int pieces = static_cast<int>(cut.cta_of(cuthead.first + it.units() - 1) - c0) + 1;
+    const float *parts = a.partial + 2 * c0 * SLOT;
+    const float *first_part = parts + (cut.start(c0) < cuthead.first ? SLOT : 0);
     const auto piece = [&](int p) { return p == 0 ? first_part : parts + static_cast<int64_t>(p) * 2 * SLOT; };
     const bool share = pieces > kFewPieces;
     const int p0 = share ? warp : 0, step = share ? kJoinWarps : 1;
-    const int chunk0 = share ? blockIdx.z : blockIdx.z * kJoinWarps + warp;
-    const int chunks = share ? gridDim.z : gridDim.z * kJoinWarps;
+    const int chunk0 = share ? blockIdx.y : blockIdx.y * kJoinWarps + warp;
+    const int chunks = share ? gridDim.y : gridDim.y * kJoinWarps;
     for (int base = chunk0 * 32; base < it.ncols * QUADS; base += 32 * chunks) {
         const int col = (base + lane) / QUADS, d0 = (base + lane) % QUADS * 4;
         const bool live = col < it.ncols;
@@ -324,15 +363,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_attention_join_kernel(cons
     }
 }
 
-// Launches the joining kernel behind an attention kernel on the same stream: blocks
-// enough for two on each place of the grid, as far as there are columns.
+// Launches the joining kernel behind an attention kernel on the same stream.
 template <int D, class L>
 static int join_launch(const KvAttnArgs &a, cudaStream_t st) {
-    const int64_t heads = a.B * a.q_tiles * a.cache.Hkv, most = L::NQ * D / 4 / 32;
-    const int64_t want = (2 * static_cast<int64_t>(a.grid) + heads - 1) / heads;
-    const unsigned shares = static_cast<unsigned>(want < most ? want : most);
-    return launch_pdl(kv_attention_join_kernel<D, L>,
-                      dim3(static_cast<unsigned>(a.B * a.q_tiles), static_cast<unsigned>(a.cache.Hkv), shares),
+    // blocks for the GPU to be full of them, as far as there is work for a warp (few
+    // pieces) or a block (many) in each
+    constexpr int64_t kChunks = L::NQ * D / 4 / 32;
+    const int64_t notes = a.heads < a.grid ? a.heads : a.grid;
+    const int64_t most = a.grid > kFewPieces * a.heads ? kChunks : (kChunks + kJoinWarps - 1) / kJoinWarps;
+    int64_t shares = (kJoinBlocks + notes - 1) / notes;
+    if (shares > most) shares = most;
+    return launch_pdl(kv_attention_join_kernel<D, L>, dim3(static_cast<unsigned>(notes), static_cast<unsigned>(shares)),
                       dim3(32 * kJoinWarps), 0, st, a);
 }
 
@@ -341,7 +382,7 @@ static int join_launch(const KvAttnArgs &a, cudaStream_t st) {
 struct AttnPlan {
     int64_t q_tiles;
     int grid;
-    int64_t prefix_bytes;
+    int64_t head_bytes;  // of the workspace, before the partial sums
     int64_t bytes;
 };
 

@@ -27,25 +27,33 @@
 
 namespace rn {
 
-constexpr int kWideWarps = 13;
-constexpr int kWideThreads = 32 * kWideWarps;
 constexpr float kWideRoom = 6.0f;   // weights stay below 2^6 (2^14 where values are at 2^-8)
 constexpr float kWideSlack = 4.0f;  // powers of two a weight may grow before a rescale
-constexpr uint64_t kWideTimeout = 2000000000ull;
+constexpr long long kWideLimit = 4000000000ll;  // clocks a wait may take, about two seconds
 
-template <int D, int BITS>
+// QT query tiles of 128 columns at a time: two share the restored tiles and take
+// turns at the tensor cores, one softmax beside the other's products; one where there
+// are no more columns, or no tensor memory for two (D 256).
+template <int D, int BITS, int QT>
 struct WideShape {
     using F = KvFormat<D, BITS>;
     static constexpr int BN = D == 256 ? 64 : 128;  // tokens of a tile
-    using L = LineShape<128, BN, 4, 1>;
-    static constexpr int kQuery = 128 * D * 2;
+    static constexpr int NQ = 128 * QT;
+    using L = LineShape<NQ, BN, 4, 1>;
+    static constexpr int kWarps = 4 * QT + 9;        // softmax, keys, values, products
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kQuery = 128 * D * 2;       // a query tile
     static constexpr int kStage = BN * D * 2;        // a tile's keys, or values
-    static constexpr int kUsed = 1024 + kQuery + 4 * kStage;
+    static constexpr int kUsed = 1024 + QT * kQuery + 4 * kStage;
     // more than half of an SM's shared memory: the tensor memory of an SM has one owner
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
-    static constexpr int kSlot = 128 * (D + 2);
-    static constexpr uint32_t kO = 2 * BN;           // tensor memory columns: S0, S1, O
-    static_assert(kO + D <= 512, "tensor memory");
+    static constexpr int kSlot = NQ * (D + 2);
+    // tensor memory columns: two S (one query tile: by turns, two: one each), then O
+    static constexpr uint32_t kO = 2 * BN;
+    static_assert(kO + QT * D <= 512, "tensor memory");
+    // S buffer and barrier phase of a query tile's c-th tile of tokens
+    __device__ static __forceinline__ uint32_t buf(uint32_t qt, uint32_t c) { return QT == 1 ? c & 1 : qt; }
+    __device__ static __forceinline__ uint32_t phase(uint32_t c) { return QT == 1 ? c >> 1 & 1 : c & 1; }
 };
 
 // ---- tensor memory and tcgen05 ------------------------------------------------------
@@ -79,20 +87,39 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
         : "memory");
 }
-// 32 columns of the warp's 32 rows, one row a thread; complete on return.
-__device__ __forceinline__ void tmem_load32(float (&r)[32], uint32_t addr) {
-    uint32_t u[32];
+// 32 columns of the warp's 32 rows, one row a thread; the registers hold them after
+// the next tmem_wait_load on them.
+__device__ __forceinline__ void tmem_load32(uint32_t (&u)[32], uint32_t addr) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
           "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
           "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
           "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
         : "r"(addr)
         : "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(u[i]);
+}
+// Waits for every load of the thread; u takes part so that no use of it comes before.
+__device__ __forceinline__ void tmem_wait_load(uint32_t (&u)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]), "+r"(u[6]), "+r"(u[7]),
+                   "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]), "+r"(u[12]), "+r"(u[13]), "+r"(u[14]),
+                   "+r"(u[15]), "+r"(u[16]), "+r"(u[17]), "+r"(u[18]), "+r"(u[19]), "+r"(u[20]), "+r"(u[21]),
+                   "+r"(u[22]), "+r"(u[23]), "+r"(u[24]), "+r"(u[25]), "+r"(u[26]), "+r"(u[27]), "+r"(u[28]),
+                   "+r"(u[29]), "+r"(u[30]), "+r"(u[31])
+                 :
+                 : "memory");
+}
+// 16 columns, complete on return.
+__device__ __forceinline__ void tmem_load16(uint32_t (&u)[16], uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(addr)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&u)[16]) {
     asm volatile(
@@ -108,6 +135,21 @@ __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::
 
 // Generic writes to shared memory become visible to the tensor core's reads.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// s0 += x0, s1 += x1 in one instruction.
+__device__ __forceinline__ void add_pairs(float &s0, float &s1, float x0, float x1) {
+    asm("{\n\t.reg .b64 s, x;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 x, {%2, %3};\n\tadd.rn.f32x2 s, s, x;\n\t"
+        "mov.b64 {%0, %1}, s;\n\t}"
+        : "+f"(s0), "+f"(s1) : "f"(x0), "f"(x1));
+}
+
+// The bits below bit n (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
 
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
@@ -156,18 +198,31 @@ __device__ __forceinline__ void load_global(uint32_t (&w)[WORDS], const void *sr
 constexpr uint32_t kScale255 = 0x5BF8u;  // fp16 255: larger scales (and NaN) take the slow way
 
 struct WideShared {
-    uint64_t q_full, k_full[2], v_full[2], s_full[2], p_full[2], pv_done[2], drained;
+    uint64_t q_full[2];                            // by query tile
+    uint64_t k_full[2], v_full[2], k_free[2], v_free[2];  // by stage
+    uint64_t s_full[2], p_full[2], pv_done[2];     // by S buffer
+    uint64_t drained;
     uint32_t tmem;
     int abort;
     // powers of two taken off, by restoring warp: keys of four tiles (their producer runs
     // ahead of the softmax by up to three), values of two
     int key_exp[4][4], val_exp[2][4], val_nan[2][4];
-    int64_t scratch[kWideWarps + 2];
+    int64_t scratch[17 + 2];
 };
 
-// A wait with a limit; gives up for the whole CTA when it runs out.
+// A wait with a limit; gives up for the whole CTA when it runs out.  (The limit is
+// counted in SM clocks: reading the global timer in every wait costs more than the
+// wait.)
 __device__ __forceinline__ bool wide_wait(WideShared &sh, uint64_t *bar, uint32_t parity) {
-    if (mbar_wait_bounded(bar, parity, kWideTimeout, &sh.abort)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 63u) == 0) {
+            if (*const_cast<volatile int *>(&sh.abort)) return false;
+            if (clock64() - t0 > kWideLimit) break;
+        }
+    }
     if (atomicExch(&sh.abort, 1) == 0) atomicOr(&g_kv_attention_status, RN_STATUS_WAIT_TIMEOUT);
     return false;
 }
@@ -186,12 +241,15 @@ struct TokenRows {
     __device__ __forceinline__ bool seen(int t) const {
         return t < it.hi && (it.win_lo == 0 || t < a.sinks || t >= it.win_lo);
     }
-    // The row of token t's key (which 0) or value, or -1: nothing of t .. t + n - 1 is
-    // seen (n tokens of one page), or its page does not exist.
-    __device__ __forceinline__ int64_t row(int t, int n, int which) const {
-        bool any = false;
-        for (int i = 0; i < n; ++i) any |= seen(t + i);
-        if (!any) return -1;
+    // Every (some) token of t .. t + 7 is seen.
+    __device__ __forceinline__ bool all_seen(int t) const {
+        return t + 7 < it.hi && (it.win_lo == 0 || t >= it.win_lo || t + 7 < a.sinks);
+    }
+    __device__ __forceinline__ bool some_seen(int t) const {
+        return t < it.hi && (it.win_lo == 0 || t < a.sinks || t + 7 >= it.win_lo);
+    }
+    // The row of token t's key (which 0) or value, or -1 where its page does not exist.
+    __device__ __forceinline__ int64_t row(int t, int which) const {
         const int page = a.page_table[it.seq * a.max_pages + (t >> a.cache.log2_page)];
         if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.cache.num_pages)) {
             atomicOr(&g_kv_attention_status, RN_STATUS_BAD_INDEX);
@@ -206,7 +264,7 @@ struct TokenRows {
 // quarter of the stored row.  A group's eight elements are one chunk of the operand.
 template <int D, int BITS>
 struct KeyTile {
-    using S = WideShape<D, BITS>;
+    using S = WideShape<D, BITS, 1>;
     using F = KvFormat<D, BITS>;
     static constexpr int ITER = S::BN / 32, KW = F::kGroups * BITS / 4, SW = F::kGroups / 2;
     uint32_t w[ITER][KW], s[ITER][SW];
@@ -215,7 +273,8 @@ struct KeyTile {
     __device__ __forceinline__ void load(const Rows &rows, int t0, int warp, int lane) {
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
-            const int64_t r = rows.row(t0 + warp * (S::BN / 4) + 8 * i + (lane & 7), 1, 0);
+            const int t = t0 + warp * (S::BN / 4) + 8 * i + (lane & 7);
+            const int64_t r = rows.seen(t) ? rows.row(t, 0) : -1;
             if (r >= 0) {
                 load_global<KW>(w[i], rows.a.cache.codes + r * F::kRow + (lane >> 3) * KW * 4);
                 load_global<SW>(s[i], rows.a.cache.scales + r * F::kGroups);
@@ -235,15 +294,20 @@ struct KeyTile {
             for (int k = 0; k < SW; ++k) m = __vmaxu2(m, s[i][k]);
         return max(m & 0xFFFFu, m >> 16) > kScale255;
     }
-    __device__ __forceinline__ void store(uint8_t *stage, int warp, int lane, bool small) const {
-        const __half2 down = __float2half2_rn(small ? 0.00390625f : 1.0f);
+    __device__ __forceinline__ void scale_down() {  // to 2^-8
+#pragma unroll
+        for (int i = 0; i < ITER; ++i)
+#pragma unroll
+            for (int k = 0; k < SW; ++k) s[i][k] = h2_bits(__hmul2(as_h2(s[i][k]), __float2half2_rn(0.00390625f)));
+    }
+    __device__ __forceinline__ void store(uint8_t *stage, int warp, int lane) const {
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             const int row = warp * (S::BN / 4) + 8 * i + (lane & 7);
 #pragma unroll
             for (int g = 0; g < F::kGroups; ++g) {
                 const __half2 pair = as_h2(s[i][g / 2]);
-                const __half2 sc = __hmul2(g & 1 ? __high2half2(pair) : __low2half2(pair), down);
+                const __half2 sc = g & 1 ? __high2half2(pair) : __low2half2(pair);
                 __half2 h[4];
                 if constexpr (BITS == 4)
                     codes_of(w[i][g], h);
@@ -266,7 +330,7 @@ struct KeyTile {
 // neighbours write eight different banks' chunks.
 template <int D, int BITS>
 struct ValueTile {
-    using S = WideShape<D, BITS>;
+    using S = WideShape<D, BITS, 1>;
     using F = KvFormat<D, BITS>;
     static constexpr int SPLIT = D == 256 ? 2 : 1;
     static constexpr int VW = D * BITS / 256 / SPLIT, SW = BITS == 4 ? VW : (VW + 1) / 2;
@@ -287,11 +351,12 @@ struct ValueTile {
     template <class Rows>
     __device__ __forceinline__ void load(const Rows &rows, int t0, const Place &p) {
         const int t = t0 + 8 * p.chunk;
-        const int64_t r = rows.row(t, 8, 1);
+        const int64_t r = rows.some_seen(t) ? rows.row(t, 1) : -1;
+        const bool all = rows.all_seen(t);
         other = 0u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (r >= 0 && rows.seen(t + i)) {
+            if (r >= 0 && (all || rows.seen(t + i))) {
                 load_global<VW>(w[i], rows.a.cache.codes + (r + i) * F::kRow + (p.r * SPLIT + p.part) * VW * 4);
                 load_global<SW>(s[i], rows.a.cache.scales + (r + i) * F::kGroups + p.part * SW * 2);
                 if constexpr (SPLIT == 2) {
@@ -382,30 +447,32 @@ struct ValueTile {
 
 // ---- the kernel ------------------------------------------------------------------------------
 
-template <int D, int BITS>
-__global__ void __launch_bounds__(kWideThreads, 1) kv_attention_wide_kernel(const KvAttnArgs a) {
-    using S = WideShape<D, BITS>;
-    using F = KvFormat<D, BITS>;
+template <int D, int BITS, int QT>
+__global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attention_wide_kernel(const KvAttnArgs a) {
+    using S = WideShape<D, BITS, QT>;
     using L = typename S::L;
-    constexpr int BN = S::BN;
+    constexpr int BN = S::BN, NQ = S::NQ;
     extern __shared__ uint8_t wide_raw[];
     __shared__ WideShared sh;
     __shared__ uint8_t nan_groups[2][2 * BN];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *qs = wide_raw + ((1024u - (smem_addr(wide_raw) & 1023u)) & 1023u);
-    uint8_t *ks = qs + S::kQuery, *vs = ks + 2 * S::kStage;
+    uint8_t *ks = qs + QT * S::kQuery, *vs = ks + 2 * S::kStage;
 
     pdl_trigger();
     pdl_wait();
-    const Line line = find_unit<L, kWideThreads>(a, blockIdx.x == 0, sh.scratch);
+    const Line line = find_unit<L, S::kThreads>(a, blockIdx.x == 0, sh.scratch);
+    store_empty<D, L, S::kThreads>(a);
     const Cut<L> cut(line.units, a.grid);
     if (line.units == 0 || blockIdx.x >= cut.ctas) return;
     if (threadIdx.x == 0) {
-        mbar_init(&sh.q_full, 128);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.q_full[i], 128);
             mbar_init(&sh.k_full[i], 128);
             mbar_init(&sh.v_full[i], 128);
             mbar_init(&sh.p_full[i], 128);
+            mbar_init(&sh.k_free[i], 1);
+            mbar_init(&sh.v_free[i], 1);
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.pv_done[i], 1);
         }
@@ -413,7 +480,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv_attention_wide_kernel(cons
         sh.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 12) {
+    if (warp == S::kWarps - 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -440,6 +507,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv_attention_wide_kernel(cons
             const int64_t left = u1 - u;
             const int v1 = units - v0 <= left ? units : v0 + static_cast<int>(left);
             const int k0 = v0 > L::LEAD ? v0 - L::LEAD : 0, k1 = v1 - L::LEAD;
+            if (threadIdx.x == 0) note_piece(a, cut, u - v0, v0, v1, units, item, head);
             if (k1 > k0) {
                 float *part = nullptr;
                 if (k1 - k0 != it.n)
@@ -454,14 +522,22 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv_attention_wide_kernel(cons
         }
     };
 
-    uint32_t n = 0;  // tiles so far
-    if (warp < 4) {
+    if (warp < 4 * QT) {
         // -- softmax: one accumulator row a thread -------------------------------------------
-        const int row = threadIdx.x;
-        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+        const uint32_t qt = warp >> 2;
+        const int row = threadIdx.x & 127;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t obase = tmem + lanes + S::kO + qt * D;
+        uint8_t *const qtile = qs + qt * S::kQuery;
+        uint32_t n = 0, c = 0;  // tiles so far: of the CTA, and those this query tile took
         each_run([&](const Item<L> &it, int head, int k0, int k1, float *part) {
-            const bool live = row < it.ncols;
-            const int f = it.f0 + (live ? row : 0);
+            const int col = static_cast<int>(qt) * 128 + row;
+            if (static_cast<int>(qt) * 128 >= it.ncols) {  // no columns for this query tile
+                n += k1 - k0;
+                return true;
+            }
+            const bool live = col < it.ncols;
+            const int f = it.f0 + (live ? col : 0);
             const int pos = live ? it.pos0 + f / a.group : -1;
             float factor;
             {
@@ -470,12 +546,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv_attention_wide_kernel(cons
                 const uint16_t *src = a.q + (it.row0 + f / a.group) * a.q_stride +
                                       (static_cast<int64_t>(head) * a.group + f % a.group) * D;
                 uint32_t top = 0u;
-                if (live)
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 v = ld_ro16(src + 8 * c);
+                if (live) {
+#pragma unroll 4
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint4 v = ld_ro16(src + 8 * i);
                         top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
                                                      __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
                     }
+                }
                 const uint32_t amax = max(top & 0xFFFFu, top >> 16);
                 const bool finite = amax < 0x7F80u;
                 int e = static_cast<int>(amax >> 7);
@@ -484,8 +562,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv_attention_wide_kernel(cons
                                            a.scale_log2);
                 factor = fmaxf(ldexpf(fabsf(a.scale_log2), e - 140), 0x1p-126f);
                 if (!finite) factor = __uint_as_float(0x7FC00000u);
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 v = live && finite ? ld_ro16(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 2
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 v = live && finite ? ld_ro16(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
                     const float x[8] = {bf_lo(v.x) * up, bf_hi(v.x) * up, bf_lo(v.y) * up, bf_hi(v.y) * up,
                                         bf_lo(v.z) * up, bf_hi(v.z) * up, bf_lo(v.w) * up, bf_hi(v.w) * up};
                     uint4 o;
@@ -495,219 +574,259 @@ __global__ void __launch_bounds__(kWideThreads, 1) kv_attention_wide_kernel(cons
                     else
                         o = make_uint4(h2_bits(__floats2half2_rn(x[0], x[1])), h2_bits(__floats2half2_rn(x[2], x[3])),
                                        h2_bits(__floats2half2_rn(x[4], x[5])), h2_bits(__floats2half2_rn(x[6], x[7])));
-                    *reinterpret_cast<uint4 *>(qs + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = o;
+                    *reinterpret_cast<uint4 *>(qtile + (i >> 3) * (128 * 128) + row * 128 +
+                                               (((i & 7) ^ (row & 7)) << 4)) = o;
                 }
             }
             fence_async_shared();
-            mbar_arrive(&sh.q_full);
+            mbar_arrive(&sh.q_full[qt]);
 
             float m = -INFINITY, ref = 0.0f, l = 0.0f;
             uint32_t nan_mask = 0u;  // groups of which a visible value is NaN
-            for (int k = k0; k < k1; ++k, ++n) {
-                const uint32_t s = n & 1, par = (n >> 1) & 1;
+            // first visible token of the window (sinks apart), for the masked tiles
+            const int lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
+            // Multiplies O and the weights of the tile's first `chunks` quarters by scale.
+            const auto rescale = [&](bool sums, int chunks, float scale, uint32_t sbase) {
+                if (sums) {
+                    if (!wide_wait_warp(sh, &sh.pv_done[S::buf(qt, c - 1)], S::phase(c - 1))) return false;
+                    tc_fence_after();
+                }
+                tmem_wait_store();
+                const __half2 hs = __float2half2_rn(scale);
+#pragma unroll 1
+                for (int i = 0; i < chunks + (sums ? D / 16 : 0); ++i) {
+                    const bool weight = i < chunks;
+                    const uint32_t at = weight ? sbase + 16 * i : obase + 16 * (i - chunks);
+                    uint32_t x[16];
+                    tmem_load16(x, at);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        x[j] = weight ? h2_bits(__hmul2(as_h2(x[j]), hs))
+                                      : __float_as_uint(__uint_as_float(x[j]) * scale);
+                    tmem_store16(at, x);
+                }
+                tmem_wait_store();
+                return true;
+            };
+            for (int k = k0; k < k1; ++k, ++n, ++c) {
+                const uint32_t b = S::buf(qt, c), vstage = n & 1;
                 const int t0 = it.token(k);
-                if (!wide_wait_warp(sh, &sh.s_full[s], par) || !wide_wait_warp(sh, &sh.v_full[s], par)) return false;
+                if (!wide_wait_warp(sh, &sh.s_full[b], S::phase(c))) return false;
                 tc_fence_after();
-                const uint32_t sbase = tmem + lanes + s * BN;
-                // the factor of columns 32c + 16h ..
-                const auto factor_of = [&](int c, int h) {
-                    return factor * static_cast<float>(1 << sh.key_exp[n & 3][(32 * c + 16 * h) / (BN / 4)]);
+                const uint32_t sbase = tmem + lanes + b * BN;
+                // the factor of columns 32i + 16h ..
+                const auto factor_of = [&](int i, int h) {
+                    return factor * static_cast<float>(1 << sh.key_exp[n & 3][(32 * i + 16 * h) / (BN / 4)]);
                 };
                 const bool masked = t0 + BN - 1 > it.lo_pos ||
                                     (a.window && t0 <= it.hi - 1 - a.window && t0 + BN > a.sinks);
-                // first visible token of the window (sinks apart), for the masked tiles
-                const int lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
-                const auto hidden = [&](int t) { return t > pos || (t < lo && t >= a.sinks); };
-                float x[32];
-                float top = -INFINITY;
-                for (int c = 0; c < BN / 32; ++c) {
-                    tmem_load32(x, sbase + 32 * c);
+                // bit j: the row does not see token t0 + 32i + j
+                const auto hidden = [&](int i) {
+                    const int t = t0 + 32 * i;
+                    return ~below(pos + 1 - t) | (below(lo - t) & ~below(a.sinks - t));
+                };
+                // (the values' exponents are there once their stage is)
+                if (!wide_wait_warp(sh, &sh.v_full[vstage], (n >> 1) & 1)) return false;
+#pragma unroll 1
+                for (int i = 0; i < BN / 32; ++i) {
+                    uint32_t v[32];
+                    tmem_load32(v, sbase + 32 * i);
+                    const float fk[2] = {factor_of(i, 0), factor_of(i, 1)};
+                    const uint32_t mask = masked ? hidden(i) : 0u;
+                    const int ve = sh.val_exp[vstage][i];
+                    tmem_wait_load(v);
                     if (masked) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (hidden(t0 + 32 * c + i)) x[i] = -INFINITY;
+                        for (int j = 0; j < 32; ++j)
+                            if (mask >> j & 1u) v[j] = 0xFF800000u;
                     }
-                    float most[2] = {-INFINITY, -INFINITY};
+                    float most[2];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) most[i / 16] = fmaxf(most[i / 16], x[i]);
-                    top = fmaxf(top, fmaxf(most[0] * factor_of(c, 0), most[1] * factor_of(c, 1)));
-                }
-                if (__any_sync(0xffffffffu, top > m)) {
-                    float scale = 1.0f;
-                    if (top > m) {
-                        const float nref = top + (kWideSlack - kWideRoom);
-                        if (m != -INFINITY) scale = exp2_approx(ref - nref);
-                        ref = nref;
-                        m = top + kWideSlack;
-                        l *= scale;
+                    for (int h = 0; h < 2; ++h) {
+                        most[h] = __uint_as_float(v[16 * h]);
+#pragma unroll
+                        for (int j = 1; j < 15; j += 2)
+                            most[h] = max3(most[h], __uint_as_float(v[16 * h + j]), __uint_as_float(v[16 * h + j + 1]));
+                        most[h] = fmaxf(most[h], __uint_as_float(v[16 * h + 15]));
                     }
-                    if (k > k0) {
-                        if (!wide_wait_warp(sh, &sh.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) return false;
-                        tc_fence_after();
-                        for (int c = 0; c < D / 32; ++c) {
-                            const uint32_t at = tmem + lanes + S::kO + 32 * c;
-                            tmem_load32(x, at);
-                            uint32_t y[16];
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[16 * h + i] * scale);
-                                tmem_store16(at + 16 * h, y);
-                            }
+                    const float top = fmaxf(most[0] * fk[0], most[1] * fk[1]);
+                    if (__any_sync(0xffffffffu, top > m)) {
+                        // References are whole numbers, so a rescale is exact: of O, and of
+                        // this tile's weights already stored.
+                        float scale = 1.0f;
+                        if (top > m) {
+                            const float nref = ceilf(top) + (kWideSlack - kWideRoom);
+                            if (m != -INFINITY) scale = exp2_approx(ref - nref);
+                            ref = nref;
+                            m = nref + kWideRoom;
+                            l *= scale;
                         }
-                        tmem_wait_store();
+                        if (!rescale(k > k0, i, scale, sbase)) return false;
                     }
-                }
-                for (int c = 0; c < BN / 32; ++c) {
-                    tmem_load32(x, sbase + 32 * c);
-                    uint32_t y[16];
-                    const float fk[2] = {factor_of(c, 0), factor_of(c, 1)};
-                    const int ve = sh.val_exp[s][c];
                     const float shift = static_cast<float>(ve) - ref;
-                    float sum = 0.0f;
+                    uint32_t y[16];
+                    float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = exp2_approx(fmaf(x[i], fk[i / 16], shift));
-                    if (masked) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (hidden(t0 + 32 * c + i)) x[i] = 0.0f;
+                    for (int j = 0; j < 16; ++j) {
+                        float p0, p1;
+                        fma2(p0, p1, __uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), fk[j / 8], shift);
+                        p0 = exp2_approx(p0);
+                        p1 = exp2_approx(p1);
+                        add_pairs(sum[0], sum[1], p0, p1);
+                        y[j] = h2_bits(__floats2half2_rn(p0, p1));
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        sum += x[2 * i] + x[2 * i + 1];
-                        y[i] = h2_bits(__floats2half2_rn(x[2 * i], x[2 * i + 1]));
-                    }
-                    tmem_store16(sbase + 16 * c, y);  // over columns already read
-                    l = fmaf(sum, ve ? 0.00390625f : 1.0f, l);
+                    tmem_store16(sbase + 16 * i, y);  // over columns already read
+                    l = fmaf(sum[0] + sum[1], ve ? 0.00390625f : 1.0f, l);
                 }
                 for (int w = 0; w < 4; ++w)
-                    if (sh.val_nan[s][w]) {
+                    if (sh.val_nan[vstage][w]) {
                         const int first = D == 256 ? 32 * (w & 1) : 32 * w, part_of = D == 256 ? BN * (w >> 1) : 0;
-                        for (int t = first; t < first + 32; ++t)
-                            if (!hidden(t0 + t)) nan_mask |= nan_groups[s][part_of + t];
+                        const uint32_t mask = hidden(first / 32);
+                        for (int j = 0; j < 32; ++j)
+                            if (!(mask >> j & 1u)) nan_mask |= nan_groups[vstage][part_of + first + j];
                     }
                 tmem_wait_store();
                 tc_fence_before();
-                mbar_arrive(&sh.p_full[s]);
+                mbar_arrive(&sh.p_full[b]);
             }
             // -- the run's sums: finished, or a piece ---------------------------------------
-            if (!wide_wait_warp(sh, &sh.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1)) return false;
+            if (!wide_wait_warp(sh, &sh.pv_done[S::buf(qt, c - 1)], S::phase(c - 1))) return false;
             tc_fence_after();
             const float top = m == -INFINITY ? -INFINITY : ref;
-            for (int c = 0; c < D / 32; ++c) {
-                float x[32];
-                tmem_load32(x, tmem + lanes + S::kO + 32 * c);
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+                uint32_t x[32];
+                tmem_load32(x, obase + 32 * i);
+                tmem_wait_load(x);
                 // store_result undoes 2^-24, which the other kernel's sums carry
-                const float unit = nan_mask >> c & 1u ? __uint_as_float(0x7FC00000u) : 0x1p-24f;
+                const float unit = nan_mask >> i & 1u ? __uint_as_float(0x7FC00000u) : 0x1p-24f;
                 if (live) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 v = make_float4(x[i] * unit, x[i + 1] * unit, x[i + 2] * unit, x[i + 3] * unit);
-                        const int d = 32 * c + i;
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 v = make_float4(__uint_as_float(x[j]) * unit, __uint_as_float(x[j + 1]) * unit,
+                                                     __uint_as_float(x[j + 2]) * unit, __uint_as_float(x[j + 3]) * unit);
+                        const int d = 32 * i + j;
                         if (part)
-                            *reinterpret_cast<float4 *>(part + row * D + d) = v;
+                            *reinterpret_cast<float4 *>(part + col * D + d) = v;
                         else
-                            store_result<D>(a, it, head * a.group, row, d, v, ref, l);
+                            store_result<D>(a, it, head * a.group, col, d, v, ref, l);
                     }
                 }
             }
             if (part && live) {
-                part[128 * D + row] = top;
-                part[128 * D + 128 + row] = l;
+                part[NQ * D + col] = top;
+                part[NQ * D + NQ + col] = l;
             }
             tc_fence_before();  // O is read before the next run's products
             return true;
         });
-    } else if (warp < 8) {
+    } else if (warp < 4 * QT + 4) {
         // -- keys -----------------------------------------------------------------------------
-        const int w = warp - 4;
+        const int w = warp - 4 * QT;
+        uint32_t n = 0;
         each_run([&](const Item<L> &it, int head, int k0, int k1, float *) {
             const TokenRows<D, BITS, L> rows{a, it, head};
-            KeyTile<D, BITS> cur, next;
-            cur.load(rows, it.token(k0), w, lane);
+            KeyTile<D, BITS> tile;
+            tile.load(rows, it.token(k0), w, lane);
             for (int k = k0; k < k1; ++k, ++n) {
                 const uint32_t s = n & 1, par = (n >> 1) & 1;
-                if (k + 1 < k1) next.load(rows, it.token(k + 1), w, lane);
-                // the product that read this stage before is over
-                if (!wide_wait_warp(sh, &sh.s_full[s], par ^ 1)) return false;
-                const bool small = __any_sync(0xffffffffu, cur.special());
+                // the products that read this stage before are over
+                if (!wide_wait_warp(sh, &sh.k_free[s], par ^ 1)) return false;
+                const bool small = __any_sync(0xffffffffu, tile.special());
+                if (small) tile.scale_down();
                 if (lane == 0) sh.key_exp[n & 3][w] = small ? 8 : 0;
-                cur.store(ks + s * S::kStage, w, lane, small);
+                tile.store(ks + s * S::kStage, w, lane);
                 fence_async_shared();
                 mbar_arrive(&sh.k_full[s]);
-                cur = next;
+                // the next tile's bytes come while this one is used
+                if (k + 1 < k1) tile.load(rows, it.token(k + 1), w, lane);
             }
             return true;
         });
-    } else if (warp < 12) {
+    } else if (warp < 4 * QT + 8) {
         // -- values ---------------------------------------------------------------------------
-        const int w = warp - 8;
+        const int w = warp - 4 * QT - 4;
         const auto place = ValueTile<D, BITS>::place(w, lane);
+        uint32_t n = 0;
         each_run([&](const Item<L> &it, int head, int k0, int k1, float *) {
             const TokenRows<D, BITS, L> rows{a, it, head};
-            ValueTile<D, BITS> cur, next;
-            cur.load(rows, it.token(k0), place);
+            ValueTile<D, BITS> tile;
+            tile.load(rows, it.token(k0), place);
             for (int k = k0; k < k1; ++k, ++n) {
                 const uint32_t s = n & 1, par = (n >> 1) & 1;
-                if (k + 1 < k1) next.load(rows, it.token(k + 1), place);
-                if (!wide_wait_warp(sh, &sh.pv_done[s], par ^ 1)) return false;
-                const bool slow = __any_sync(0xffffffffu, cur.special());
+                if (!wide_wait_warp(sh, &sh.v_free[s], par ^ 1)) return false;
+                const bool slow = __any_sync(0xffffffffu, tile.special());
                 bool nan = false;
-                if (slow) nan = __any_sync(0xffffffffu, cur.tame(nan_groups[s], place));
+                if (slow) nan = __any_sync(0xffffffffu, tile.tame(nan_groups[s], place));
                 if (lane == 0) {
                     sh.val_exp[s][w] = slow ? 8 : 0;
                     sh.val_nan[s][w] = nan;
                 }
-                cur.store(vs + s * S::kStage, place);
+                tile.store(vs + s * S::kStage, place);
                 fence_async_shared();
                 mbar_arrive(&sh.v_full[s]);
-                cur = next;
+                if (k + 1 < k1) tile.load(rows, it.token(k + 1), place);
             }
             return true;
         });
     } else if (lane == 0) {
         // -- products ---------------------------------------------------------------------------
         const uint32_t qa = smem_addr(qs), ka = smem_addr(ks), va = smem_addr(vs);
-        uint32_t run = 0;
-        const auto value_product = [&](uint32_t i, bool first) {
-            const uint32_t s = i & 1, par = (i >> 1) & 1;
-            if (!wide_wait(sh, &sh.p_full[s], par) || !wide_wait(sh, &sh.v_full[s], par)) return false;
+        uint32_t n = 0, runs[2] = {0, 0}, s_done[2] = {0, 0}, pv_count[2] = {0, 0};
+        // S of query tile qt with the keys of the CTA's tile i, into the buffer of the
+        // query tile's next tile: its weights of before have been used up
+        const auto logits = [&](uint32_t qt, uint32_t i, bool last) {
+            const uint32_t c = s_done[qt]++, b = S::buf(qt, c), s = i & 1;
+            constexpr uint32_t kBack = QT == 1 ? 2 : 1;
+            if (c >= kBack && !wide_wait(sh, &sh.pv_done[b], S::phase(c - kBack))) return false;
+            if (!wide_wait(sh, &sh.k_full[s], (i >> 1) & 1)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < D / 16; ++q)
+                mma_ss(tmem + b * BN, operand_desc(qa + qt * S::kQuery + (q >> 2) * (128 * 128) + (q & 3) * 32),
+                       operand_desc(ka + s * S::kStage + (q >> 2) * (BN * 128) + (q & 3) * 32), wide_idesc(BN), q != 0);
+            tc_commit(&sh.s_full[b]);
+            if (last) tc_commit(&sh.k_free[s]);
+            return true;
+        };
+        const auto outputs = [&](uint32_t qt, uint32_t i, bool first, bool last) {
+            const uint32_t c = pv_count[qt]++, b = S::buf(qt, c), s = i & 1;
+            if (!wide_wait(sh, &sh.p_full[b], S::phase(c)) || !wide_wait(sh, &sh.v_full[s], (i >> 1) & 1)) return false;
             tc_fence_after();
 #pragma unroll
             for (int q = 0; q < BN / 16; ++q)
-                mma_ts(tmem + S::kO, tmem + s * BN + 8 * q,
+                mma_ts(tmem + S::kO + qt * D, tmem + b * BN + 8 * q,
                        operand_desc(va + s * S::kStage + (q >> 2) * (D * 128) + (q & 3) * 32), wide_idesc(D),
                        !(first && q == 0));
-            tc_commit(&sh.pv_done[s]);
+            tc_commit(&sh.pv_done[b]);
+            if (last) tc_commit(&sh.v_free[s]);
             return true;
         };
-        each_run([&](const Item<L> &, int, int k0, int k1, float *) {
-            if (!wide_wait(sh, &sh.q_full, run & 1)) return false;
-            ++run;
-            for (int k = k0; k < k1; ++k, ++n) {
-                const uint32_t s = n & 1, par = (n >> 1) & 1;
-                // the weights of tile n - 2, which this S replaces, have been used up
-                if (n >= 2 && !wide_wait(sh, &sh.pv_done[s], par ^ 1)) return false;
-                if (!wide_wait(sh, &sh.k_full[s], par)) return false;
-                tc_fence_after();
-#pragma unroll
-                for (int q = 0; q < D / 16; ++q)
-                    mma_ss(tmem + s * BN, operand_desc(qa + (q >> 2) * (128 * 128) + (q & 3) * 32),
-                           operand_desc(ka + s * S::kStage + (q >> 2) * (BN * 128) + (q & 3) * 32), wide_idesc(BN),
-                           q != 0);
-                tc_commit(&sh.s_full[s]);
-                if (k > k0 && !value_product(n - 1, k - 1 == k0)) return false;
+        each_run([&](const Item<L> &it, int, int k0, int k1, float *) {
+            const uint32_t tiles = it.ncols > 128 ? 2 : 1, end = n + (k1 - k0), start = n;
+            for (uint32_t qt = 0; qt < tiles; ++qt) {
+                if (!wide_wait(sh, &sh.q_full[qt], runs[qt] & 1)) return false;
+                ++runs[qt];
             }
-            return value_product(n - 1, k1 - k0 == 1);
+            for (uint32_t qt = 0; qt < tiles; ++qt)
+                if (!logits(qt, n, qt + 1 == tiles)) return false;
+            for (; n < end; ++n) {
+                if (QT == 1 && n + 1 < end && !logits(0, n + 1, true)) return false;
+                for (uint32_t qt = 0; qt < tiles; ++qt) {
+                    if (!outputs(qt, n, n == start, qt + 1 == tiles)) return false;
+                    if (QT == 2 && n + 1 < end && !logits(qt, n + 1, qt + 1 == tiles)) return false;
+                }
+            }
+            return true;
         });
         // nothing of this CTA is under way any more when its tensor memory goes back
         tc_commit(&sh.drained);
-        mbar_wait_bounded(&sh.drained, 0, kWideTimeout, nullptr);
+        mbar_wait_bounded(&sh.drained, 0, 2000000000ull, nullptr);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == S::kWarps - 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
@@ -719,13 +838,13 @@ int kv_attention_wide_status(unsigned int *out, int clear) {
 
 // ---- host --------------------------------------------------------------------------------------
 
-template <int D, int BITS>
+template <int D, int BITS, int QT>
 static int wide_launch_of(const KvAttnArgs &a, cudaStream_t st) {
-    using S = WideShape<D, BITS>;
+    using S = WideShape<D, BITS, QT>;
     static std::atomic<int> attr_done[kMaxDevices];
     const int dev = current_device_index();
     if (dev < 0 || dev >= kMaxDevices) return RN_ERR_DEVICE;
-    const auto kernel = kv_attention_wide_kernel<D, BITS>;
+    const auto kernel = kv_attention_wide_kernel<D, BITS, QT>;
     if (!attr_done[dev].load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess) {
             cudaGetLastError();
@@ -733,22 +852,30 @@ static int wide_launch_of(const KvAttnArgs &a, cudaStream_t st) {
         }
         attr_done[dev].store(1, std::memory_order_release);
     }
-    const int rc = launch_pdl(kernel, dim3(static_cast<unsigned>(a.grid)), dim3(kWideThreads), S::kSmem, st, a);
+    const int rc = launch_pdl(kernel, dim3(static_cast<unsigned>(a.grid)), dim3(S::kThreads), S::kSmem, st, a);
     if (rc != RN_OK) return rc;
     return join_launch<D, typename S::L>(a, st);
 }
 
+static int query_tiles(int D, int64_t columns) { return D <= 128 && columns > 128 ? 2 : 1; }
+
 AttnPlan wide_plan(int sm_count, int64_t B, int group, int D, int64_t max_q_len) {
+    const int64_t nq = 128 * query_tiles(D, max_q_len * group);
     AttnPlan p;
-    p.q_tiles = (max_q_len * group + 127) / 128;
+    p.q_tiles = (max_q_len * group + nq - 1) / nq;
     p.grid = sm_count;
-    p.prefix_bytes = ((B * p.q_tiles + 1) * 8 + 15) / 16 * 16;
-    p.bytes = p.prefix_bytes + static_cast<int64_t>(p.grid) * 2 * 128 * (D + 2) * 4;
+    p.head_bytes = 16 + 32 * static_cast<int64_t>(p.grid);
+    p.bytes = p.head_bytes + static_cast<int64_t>(p.grid) * 2 * nq * (D + 2) * 4;
     return p;
 }
 
 int wide_launch(int D, int format, const KvAttnArgs &a, cudaStream_t st) {
-    return kv_dispatch(D, format, [&](auto d, auto bits) { return wide_launch_of<d.value, bits.value>(a, st); });
+    const int tiles = query_tiles(D, a.max_q_len * a.group);
+    return kv_dispatch(D, format, [&](auto d, auto bits) {
+        if constexpr (d.value <= 128)
+            if (tiles == 2) return wide_launch_of<d.value, bits.value, 2>(a, st);
+        return wide_launch_of<d.value, bits.value, 1>(a, st);
+    });
 }
 
 }  // namespace rn

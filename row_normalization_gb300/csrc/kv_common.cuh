@@ -50,6 +50,28 @@ __device__ __forceinline__ float half_bits_to_float(uint16_t h) {
     return __half2float(__ushort_as_half(h));
 }
 
+// Two fp32 operations an instruction: r = x * b + c and r = x + c, each rounded once.
+__device__ __forceinline__ void fma2(float &r0, float &r1, float x0, float x1, float b, float c) {
+    asm("{\n\t.reg .b64 x, b, c, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %5};\n\t"
+        "fma.rn.f32x2 r, x, b, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r0), "=f"(r1) : "f"(x0), "f"(x1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float &r0, float &r1, float x0, float x1, float c) {
+    asm("{\n\t.reg .b64 x, c, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 c, {%4, %4};\n\t"
+        "add.rn.f32x2 r, x, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r0), "=f"(r1) : "f"(x0), "f"(x1), "f"(c));
+}
+
+struct KvWriteArgs {
+    const uint16_t *kv;    // first key element of token 0
+    int64_t stride;        // elements from one token to the next
+    const int64_t *slots;
+    uint32_t tokens;       // T
+    uint32_t parts;        // groups of kHeads heads of a token
+    int64_t num_slots;
+    KvCache cache;
+};
+
 // log2 of a page size the cache takes (16, 32, 64, 128 or 256), else -1.
 inline int kv_log2_page(int page_size) {
     for (int l = 4; l <= 8; ++l)
