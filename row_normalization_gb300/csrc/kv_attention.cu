@@ -59,12 +59,14 @@ struct AttnShape {
     // the offset of the keys' codes comes off the sums, as their first addend (else off
     // the operands, which then serve several instructions)
     static constexpr bool kKeySums = NT == 1;
-    // CTAs an SM is to hold: by registers (O alone is MT * NT * 4 a thread), and by
-    // shared memory for a ring of two stages or more
+    // CTAs an SM is to hold: by registers (O alone is MT * NT * 4 a thread), fewer with
+    // deeper rings in 8 bits, where the bytes bound (heads of 128, 64 sequences: 185 us
+    // with two, 230 with three; heads of 64, 96 sequences: 104 with three, 115 with four;
+    // in 4 bits 112 with three, 119 with two), and by shared memory for two stages
     static constexpr int kQuery = NQ * D * 2;  // the queries, as operand registers
     static constexpr int kRoom = 224 * 1024;
     static constexpr int stages_at(int ctas) { return ctas < 1 ? 0 : (kRoom / ctas - 2048 - kQuery) / (kAttnWarps * kStage); }
-    static constexpr int kByRegs = MT * NT * 4 >= 64 ? 2 : (D == 64 ? 4 : 3);
+    static constexpr int kByRegs = MT * NT * 4 >= 64 ? 2 : (D == 64 ? 4 : 3) - (BITS == 8 ? 1 : 0);
     static constexpr int kStep = D == 256 ? 1 : 2;  // 16-token halves of a tile taken at once
     static constexpr int kCtas = stages_at(kByRegs) >= 2         ? kByRegs
                                  : stages_at(kByRegs - 1) >= 2 ? kByRegs - 1
