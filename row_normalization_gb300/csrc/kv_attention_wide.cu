@@ -37,23 +37,31 @@ constexpr long long kWideLimit = 4000000000ll;  // clocks a wait may take, about
 template <int D, int BITS, int QT>
 struct WideShape {
     using F = KvFormat<D, BITS>;
-    static constexpr int BN = D == 256 ? 64 : 128;  // tokens of a tile
+    // Tokens of a tile.  (D 128 with two query tiles: tiles of 64 would leave tensor
+    // memory for two S each, but what a tile costs beside its tokens outweighs that: 64
+    // queries over 131072 tokens of 8 heads 289 against 257 us.)
+    static constexpr int BN = D == 256 ? 64 : 128;
+    static constexpr int kBufs = QT * (2 * BN + D) <= 512 ? 2 : 1;  // S of a query tile
+    static constexpr int kStages = 2;
     static constexpr int NQ = 128 * QT;
     using L = LineShape<NQ, BN, 4, 1>;
     static constexpr int kWarps = 4 * QT + 9;        // softmax, keys, values, products
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kQuery = 128 * D * 2;       // a query tile
     static constexpr int kStage = BN * D * 2;        // a tile's keys, or values
-    static constexpr int kUsed = 1024 + QT * kQuery + 4 * kStage;
+    static constexpr int kUsed = 1024 + QT * kQuery + 2 * kStages * kStage;
     // more than half of an SM's shared memory: the tensor memory of an SM has one owner
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
     static constexpr int kSlot = NQ * (D + 2);
-    // tensor memory columns: two S (one query tile: by turns, two: one each), then O
-    static constexpr uint32_t kO = 2 * BN;
-    static_assert(kO + QT * D <= 512, "tensor memory");
+    // tensor memory columns: the S buffers, then O
+    static constexpr uint32_t kO = QT * kBufs * BN;
+    static_assert(kO + QT * D <= 512 && kUsed <= 227 * 1024, "tensor and shared memory");
     // S buffer and barrier phase of a query tile's c-th tile of tokens
-    __device__ static __forceinline__ uint32_t buf(uint32_t qt, uint32_t c) { return QT == 1 ? c & 1 : qt; }
-    __device__ static __forceinline__ uint32_t phase(uint32_t c) { return QT == 1 ? c >> 1 & 1 : c & 1; }
+    __device__ static __forceinline__ uint32_t buf(uint32_t qt, uint32_t c) { return qt * kBufs + c % kBufs; }
+    __device__ static __forceinline__ uint32_t phase(uint32_t c) { return c / kBufs & 1; }
+    // stage and barrier phase of the CTA's n-th tile
+    __device__ static __forceinline__ uint32_t stage(uint32_t n) { return n % kStages; }
+    __device__ static __forceinline__ uint32_t round(uint32_t n) { return n / kStages & 1; }
 };
 
 // ---- tensor memory and tcgen05 ------------------------------------------------------
@@ -200,13 +208,15 @@ constexpr uint32_t kScale255 = 0x5BF8u;  // fp16 255: larger scales (and NaN) ta
 struct WideShared {
     uint64_t q_full[2];                            // by query tile
     uint64_t k_full[2], v_full[2], k_free[2], v_free[2];  // by stage
-    uint64_t s_full[2], p_full[2], pv_done[2];     // by S buffer
+    uint64_t s_full[2], p_full[2], pv_done[2];            // by S buffer
     uint64_t drained;
     uint32_t tmem;
     int abort;
-    // powers of two taken off, by restoring warp: keys of four tiles (their producer runs
-    // ahead of the softmax by up to three), values of two
-    int key_exp[4][4], val_exp[2][4], val_nan[2][4];
+    // What restoring a tile met, a byte for each of the four warps: 1 where it is at 2^-8
+    // of its size, 2 where a value is NaN.  Keys: their producers wait for the products of
+    // two tiles before, which wait for the softmax of two tiles before that, so eight
+    // tiles' are kept.  Values: by stage.
+    uint32_t key_flags[8], val_flags[2];
     int64_t scratch[17 + 2];
 };
 
@@ -262,18 +272,17 @@ struct TokenRows {
 // ---- restoring keys ---------------------------------------------------------------------
 // Four warps, BN / 4 tokens each (each with a power of two of its own), eight at a time: lane = token % 8 + 8 j with j the
 // quarter of the stored row.  A group's eight elements are one chunk of the operand.
-template <int D, int BITS>
+template <int D, int BITS, int BN>
 struct KeyTile {
-    using S = WideShape<D, BITS, 1>;
     using F = KvFormat<D, BITS>;
-    static constexpr int ITER = S::BN / 32, KW = F::kGroups * BITS / 4, SW = F::kGroups / 2;
+    static constexpr int ITER = BN / 32, KW = F::kGroups * BITS / 4, SW = F::kGroups / 2;
     uint32_t w[ITER][KW], s[ITER][SW];
 
     template <class Rows>
     __device__ __forceinline__ void load(const Rows &rows, int t0, int warp, int lane) {
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
-            const int t = t0 + warp * (S::BN / 4) + 8 * i + (lane & 7);
+            const int t = t0 + warp * (BN / 4) + 8 * i + (lane & 7);
             const int64_t r = rows.seen(t) ? rows.row(t, 0) : -1;
             if (r >= 0) {
                 load_global<KW>(w[i], rows.a.cache.codes + r * F::kRow + (lane >> 3) * KW * 4);
@@ -303,7 +312,7 @@ struct KeyTile {
     __device__ __forceinline__ void store(uint8_t *stage, int warp, int lane) const {
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
-            const int row = warp * (S::BN / 4) + 8 * i + (lane & 7);
+            const int row = warp * (BN / 4) + 8 * i + (lane & 7);
 #pragma unroll
             for (int g = 0; g < F::kGroups; ++g) {
                 const __half2 pair = as_h2(s[i][g / 2]);
@@ -314,7 +323,7 @@ struct KeyTile {
                 else
                     codes_of(w[i][2 * g], w[i][2 * g + 1], h);
                 const int chunk = 4 * g + (lane >> 3);
-                *reinterpret_cast<uint4 *>(stage + (chunk >> 3) * (S::BN * 128) + row * 128 +
+                *reinterpret_cast<uint4 *>(stage + (chunk >> 3) * (BN * 128) + row * 128 +
                                            (((chunk & 7) ^ (row & 7)) << 4)) =
                     make_uint4(h2_bits(__hmul2(h[0], sc)), h2_bits(__hmul2(h[1], sc)), h2_bits(__hmul2(h[2], sc)),
                                h2_bits(__hmul2(h[3], sc)));
@@ -324,18 +333,17 @@ struct KeyTile {
 };
 
 // ---- restoring values, transposed --------------------------------------------------------
-// A thread takes eight tokens of the stored rows' r-th run (or half of it, D 256) and
+// A thread takes eight tokens of the stored rows' r-th run (or half of it, 64 tokens) and
 // writes, for each of its dimensions, the eight tokens as one chunk of that
 // dimension's row.  r and the tokens are mixed over the lanes so that eight
 // neighbours write eight different banks' chunks.
-template <int D, int BITS>
+template <int D, int BITS, int BN>
 struct ValueTile {
-    using S = WideShape<D, BITS, 1>;
     using F = KvFormat<D, BITS>;
-    static constexpr int SPLIT = D == 256 ? 2 : 1;
+    static constexpr int SPLIT = BN == 64 ? 2 : 1;
     static constexpr int VW = D * BITS / 256 / SPLIT, SW = BITS == 4 ? VW : (VW + 1) / 2;
     uint32_t w[8][VW], s[8][SW];
-    uint32_t other;  // D 256: the largest scales of the row's other part
+    uint32_t other;  // the largest scales of the row's other part
 
     struct Place {
         int r, chunk, part;
@@ -403,7 +411,7 @@ struct ValueTile {
             }
             any |= groups != 0u;
             // every run of a row notes the same groups; the parts of a row their own
-            if (p.r == 0) nan_groups[(p.part * S::BN) + 8 * p.chunk + i] = static_cast<uint8_t>(groups << (p.part * 2 * SW));
+            if (p.r == 0) nan_groups[(p.part * BN) + 8 * p.chunk + i] = static_cast<uint8_t>(groups << (p.part * 2 * SW));
         }
         return any;
     }
@@ -457,7 +465,7 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
     __shared__ uint8_t nan_groups[2][2 * BN];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *qs = wide_raw + ((1024u - (smem_addr(wide_raw) & 1023u)) & 1023u);
-    uint8_t *ks = qs + QT * S::kQuery, *vs = ks + 2 * S::kStage;
+    uint8_t *ks = qs + QT * S::kQuery, *vs = ks + S::kStages * S::kStage;
 
     pdl_trigger();
     pdl_wait();
@@ -609,14 +617,15 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
                 return true;
             };
             for (int k = k0; k < k1; ++k, ++n, ++c) {
-                const uint32_t b = S::buf(qt, c), vstage = n & 1;
+                const uint32_t b = S::buf(qt, c), vstage = S::stage(n);
                 const int t0 = it.token(k);
                 if (!wide_wait_warp(sh, &sh.s_full[b], S::phase(c))) return false;
                 tc_fence_after();
                 const uint32_t sbase = tmem + lanes + b * BN;
+                const uint32_t kflags = sh.key_flags[n & 7];
                 // the factor of columns 32i + 16h ..
                 const auto factor_of = [&](int i, int h) {
-                    return factor * static_cast<float>(1 << sh.key_exp[n & 3][(32 * i + 16 * h) / (BN / 4)]);
+                    return kflags >> (8 * ((32 * i + 16 * h) / (BN / 4))) & 1u ? factor * 256.0f : factor;
                 };
                 const bool masked = t0 + BN - 1 > it.lo_pos ||
                                     (a.window && t0 <= it.hi - 1 - a.window && t0 + BN > a.sinks);
@@ -625,15 +634,20 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
                     const int t = t0 + 32 * i;
                     return ~below(pos + 1 - t) | (below(lo - t) & ~below(a.sinks - t));
                 };
-                // (the values' exponents are there once their stage is)
-                if (!wide_wait_warp(sh, &sh.v_full[vstage], (n >> 1) & 1)) return false;
+                // (the values' flags are there once their stage is)
+                if (!wide_wait_warp(sh, &sh.v_full[vstage], S::round(n))) return false;
+                const uint32_t vflags = sh.val_flags[vstage];
 #pragma unroll 1
                 for (int i = 0; i < BN / 32; ++i) {
                     uint32_t v[32];
                     tmem_load32(v, sbase + 32 * i);
-                    const float fk[2] = {factor_of(i, 0), factor_of(i, 1)};
+                    float fk[2] = {factor, factor};
+                    if (kflags) {
+                        fk[0] = factor_of(i, 0);
+                        fk[1] = factor_of(i, 1);
+                    }
                     const uint32_t mask = masked ? hidden(i) : 0u;
-                    const int ve = sh.val_exp[vstage][i];
+                    const bool ve = vflags >> (8 * i) & 1u;  // chunk i: warp i (and i + 2) restored it
                     tmem_wait_load(v);
                     if (masked) {
 #pragma unroll
@@ -663,7 +677,7 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
                         }
                         if (!rescale(k > k0, i, scale, sbase)) return false;
                     }
-                    const float shift = static_cast<float>(ve) - ref;
+                    const float shift = (ve ? 8.0f : 0.0f) - ref;
                     uint32_t y[16];
                     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -678,13 +692,15 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
                     tmem_store16(sbase + 16 * i, y);  // over columns already read
                     l = fmaf(sum[0] + sum[1], ve ? 0.00390625f : 1.0f, l);
                 }
-                for (int w = 0; w < 4; ++w)
-                    if (sh.val_nan[vstage][w]) {
-                        const int first = D == 256 ? 32 * (w & 1) : 32 * w, part_of = D == 256 ? BN * (w >> 1) : 0;
+                if (vflags & 0x02020202u) {
+                    for (int w = 0; w < 4; ++w) {
+                        if (!(vflags >> (8 * w) & 2u)) continue;
+                        const int first = BN == 64 ? 32 * (w & 1) : 32 * w, part_of = BN == 64 ? BN * (w >> 1) : 0;
                         const uint32_t mask = hidden(first / 32);
                         for (int j = 0; j < 32; ++j)
                             if (!(mask >> j & 1u)) nan_mask |= nan_groups[vstage][part_of + first + j];
                     }
+                }
                 tmem_wait_store();
                 tc_fence_before();
                 mbar_arrive(&sh.p_full[b]);
@@ -726,15 +742,15 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
         uint32_t n = 0;
         each_run([&](const Item<L> &it, int head, int k0, int k1, float *) {
             const TokenRows<D, BITS, L> rows{a, it, head};
-            KeyTile<D, BITS> tile;
+            KeyTile<D, BITS, BN> tile;
             tile.load(rows, it.token(k0), w, lane);
             for (int k = k0; k < k1; ++k, ++n) {
-                const uint32_t s = n & 1, par = (n >> 1) & 1;
+                const uint32_t s = S::stage(n), par = S::round(n);
                 // the products that read this stage before are over
                 if (!wide_wait_warp(sh, &sh.k_free[s], par ^ 1)) return false;
                 const bool small = __any_sync(0xffffffffu, tile.special());
                 if (small) tile.scale_down();
-                if (lane == 0) sh.key_exp[n & 3][w] = small ? 8 : 0;
+                if (lane == 0) reinterpret_cast<uint8_t *>(&sh.key_flags[n & 7])[w] = small ? 1 : 0;
                 tile.store(ks + s * S::kStage, w, lane);
                 fence_async_shared();
                 mbar_arrive(&sh.k_full[s]);
@@ -746,22 +762,19 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
     } else if (warp < 4 * QT + 8) {
         // -- values ---------------------------------------------------------------------------
         const int w = warp - 4 * QT - 4;
-        const auto place = ValueTile<D, BITS>::place(w, lane);
+        const auto place = ValueTile<D, BITS, BN>::place(w, lane);
         uint32_t n = 0;
         each_run([&](const Item<L> &it, int head, int k0, int k1, float *) {
             const TokenRows<D, BITS, L> rows{a, it, head};
-            ValueTile<D, BITS> tile;
+            ValueTile<D, BITS, BN> tile;
             tile.load(rows, it.token(k0), place);
             for (int k = k0; k < k1; ++k, ++n) {
-                const uint32_t s = n & 1, par = (n >> 1) & 1;
+                const uint32_t s = S::stage(n), par = S::round(n);
                 if (!wide_wait_warp(sh, &sh.v_free[s], par ^ 1)) return false;
                 const bool slow = __any_sync(0xffffffffu, tile.special());
                 bool nan = false;
                 if (slow) nan = __any_sync(0xffffffffu, tile.tame(nan_groups[s], place));
-                if (lane == 0) {
-                    sh.val_exp[s][w] = slow ? 8 : 0;
-                    sh.val_nan[s][w] = nan;
-                }
+                if (lane == 0) reinterpret_cast<uint8_t *>(&sh.val_flags[s])[w] = (slow ? 1 : 0) | (nan ? 2 : 0);
                 tile.store(vs + s * S::kStage, place);
                 fence_async_shared();
                 mbar_arrive(&sh.v_full[s]);
@@ -776,10 +789,10 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
         // S of query tile qt with the keys of the CTA's tile i, into the buffer of the
         // query tile's next tile: its weights of before have been used up
         const auto logits = [&](uint32_t qt, uint32_t i, bool last) {
-            const uint32_t c = s_done[qt]++, b = S::buf(qt, c), s = i & 1;
-            constexpr uint32_t kBack = QT == 1 ? 2 : 1;
+            const uint32_t c = s_done[qt]++, b = S::buf(qt, c), s = S::stage(i);
+            constexpr uint32_t kBack = S::kBufs;
             if (c >= kBack && !wide_wait(sh, &sh.pv_done[b], S::phase(c - kBack))) return false;
-            if (!wide_wait(sh, &sh.k_full[s], (i >> 1) & 1)) return false;
+            if (!wide_wait(sh, &sh.k_full[s], S::round(i))) return false;
             tc_fence_after();
 #pragma unroll
             for (int q = 0; q < D / 16; ++q)
@@ -790,8 +803,8 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
             return true;
         };
         const auto outputs = [&](uint32_t qt, uint32_t i, bool first, bool last) {
-            const uint32_t c = pv_count[qt]++, b = S::buf(qt, c), s = i & 1;
-            if (!wide_wait(sh, &sh.p_full[b], S::phase(c)) || !wide_wait(sh, &sh.v_full[s], (i >> 1) & 1)) return false;
+            const uint32_t c = pv_count[qt]++, b = S::buf(qt, c), s = S::stage(i);
+            if (!wide_wait(sh, &sh.p_full[b], S::phase(c)) || !wide_wait(sh, &sh.v_full[s], S::round(i))) return false;
             tc_fence_after();
 #pragma unroll
             for (int q = 0; q < BN / 16; ++q)
@@ -811,10 +824,11 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
             for (uint32_t qt = 0; qt < tiles; ++qt)
                 if (!logits(qt, n, qt + 1 == tiles)) return false;
             for (; n < end; ++n) {
-                if (QT == 1 && n + 1 < end && !logits(0, n + 1, true)) return false;
                 for (uint32_t qt = 0; qt < tiles; ++qt) {
+                    // with a second buffer the next logits come first, beside this softmax
+                    if (S::kBufs == 2 && n + 1 < end && !logits(qt, n + 1, qt + 1 == tiles)) return false;
                     if (!outputs(qt, n, n == start, qt + 1 == tiles)) return false;
-                    if (QT == 2 && n + 1 < end && !logits(qt, n + 1, qt + 1 == tiles)) return false;
+                    if (S::kBufs == 1 && n + 1 < end && !logits(qt, n + 1, qt + 1 == tiles)) return false;
                 }
             }
             return true;
