@@ -250,52 +250,6 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
     __shared__ int s_pos[NQ];
     __shared__ float s_factor[NQ], s_ref[kAttnWarps][NQ], s_l[kAttnWarps][NQ];
 
-    // -- queries ------------------------------------------------------------------
-    const int head0 = kvh * a.group;
-    float offset[S::kKeySums ? NG : 1][2];  // -zero * sum of the group's query, columns 2j, 2j+1
-    float factor[NT][2];
-    uint8_t *qsm = smem + (S::kSmem - S::kQuery);
-    if (threadIdx.x < NQ)
-        s_pos[threadIdx.x] = static_cast<int>(threadIdx.x) < it.ncols
-                                 ? it.pos0 + (it.f0 + static_cast<int>(threadIdx.x)) / a.group
-                                 : -1;
-    if constexpr (S::kKeySums) {
-        Query<D, BITS> q;
-        q.load(a, it, head0, r, j);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            float s = q.sum[g];
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            s += __shfl_xor_sync(0xffffffffu, s, 2);
-            s *= -static_cast<float>(F::kZero) * 0x1p-24f;
-            offset[g][0] = __shfl_sync(0xffffffffu, s, 8 * j);
-            offset[g][1] = __shfl_sync(0xffffffffu, s, 8 * j + 4);
-            if (warp == 0) {
-                *reinterpret_cast<uint4 *>(qsm + (g * 32 + lane) * 16) =
-                    make_uint4(q.b[g][0][0], q.b[g][0][1], q.b[g][1][0], q.b[g][1][1]);
-            }
-        }
-        factor[0][0] = __shfl_sync(0xffffffffu, q.factor, 8 * j);
-        factor[0][1] = __shfl_sync(0xffffffffu, q.factor, 8 * j + 4);
-        __syncthreads();
-    } else {
-        for (int nt = warp; nt < NT; nt += kAttnWarps) {
-            Query<D, BITS> q;
-            q.load(a, it, head0, nt * 8 + r, j);
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-                *reinterpret_cast<uint4 *>(qsm + ((nt * NG + g) * 32 + lane) * 16) =
-                    make_uint4(q.b[g][0][0], q.b[g][0][1], q.b[g][1][0], q.b[g][1][1]);
-            if (j == 0) s_factor[nt * 8 + r] = q.factor;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            factor[nt][0] = s_factor[nt * 8 + 2 * j];
-            factor[nt][1] = s_factor[nt * 8 + 2 * j + 1];
-        }
-    }
-
     // -- the warp's copy ring --------------------------------------------------------
     uint8_t *ring = smem + warp * (S::kStages * S::kStage);
     const uint32_t ring_addr = smem_addr(ring);
@@ -378,6 +332,62 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
             if (see_hi) copy_rows(I16(), I32(), dst, ok_hi ? p.hi : 0, 0, ok_hi ? 16 : 0);
         }
     };
+
+    int k = k0 + warp;
+    Pages next = pages_of(k);
+#pragma unroll
+    for (int s = 0; s < S::kStages - 1; ++s) {
+        const int ks = k + s * kAttnWarps;
+        if (ks < k1) issue(ks, s, next);
+        next = pages_of(ks + kAttnWarps);
+        cp_async_commit();
+    }
+
+    // -- queries ------------------------------------------------------------------
+    const int head0 = kvh * a.group;
+    float offset[S::kKeySums ? NG : 1][2];  // -zero * sum of the group's query, columns 2j, 2j+1
+    float factor[NT][2];
+    uint8_t *qsm = smem + (S::kSmem - S::kQuery);
+    if (threadIdx.x < NQ)
+        s_pos[threadIdx.x] = static_cast<int>(threadIdx.x) < it.ncols
+                                 ? it.pos0 + (it.f0 + static_cast<int>(threadIdx.x)) / a.group
+                                 : -1;
+    if constexpr (S::kKeySums) {
+        Query<D, BITS> q;
+        q.load(a, it, head0, r, j);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            float s = q.sum[g];
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            s *= -static_cast<float>(F::kZero) * 0x1p-24f;
+            offset[g][0] = __shfl_sync(0xffffffffu, s, 8 * j);
+            offset[g][1] = __shfl_sync(0xffffffffu, s, 8 * j + 4);
+            if (warp == 0) {
+                *reinterpret_cast<uint4 *>(qsm + (g * 32 + lane) * 16) =
+                    make_uint4(q.b[g][0][0], q.b[g][0][1], q.b[g][1][0], q.b[g][1][1]);
+            }
+        }
+        factor[0][0] = __shfl_sync(0xffffffffu, q.factor, 8 * j);
+        factor[0][1] = __shfl_sync(0xffffffffu, q.factor, 8 * j + 4);
+        __syncthreads();
+    } else {
+        for (int nt = warp; nt < NT; nt += kAttnWarps) {
+            Query<D, BITS> q;
+            q.load(a, it, head0, nt * 8 + r, j);
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                *reinterpret_cast<uint4 *>(qsm + ((nt * NG + g) * 32 + lane) * 16) =
+                    make_uint4(q.b[g][0][0], q.b[g][0][1], q.b[g][1][0], q.b[g][1][1]);
+            if (j == 0) s_factor[nt * 8 + r] = q.factor;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            factor[nt][0] = s_factor[nt * 8 + 2 * j];
+            factor[nt][1] = s_factor[nt * 8 + 2 * j + 1];
+        }
+    }
 
     // -- running state: column sums, and the finished product's rows ------------------
     float o[S::MT][NT][4], l[NT][2], m[NT][2], ref[NT][2];
@@ -660,16 +670,6 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
     };
 
 
-    int k = k0 + warp;
-    Pages next = pages_of(k);
-#pragma unroll
-    for (int s = 0; s < S::kStages - 1; ++s) {
-        const int ks = k + s * kAttnWarps;
-        if (ks < k1) issue(ks, s, next);
-        next = pages_of(ks + kAttnWarps);
-        cp_async_commit();
-    }
-
     int stage = 0;
     for (; k < k1; k += kAttnWarps) {
         cp_async_wait<S::kStages - 2>();
@@ -780,13 +780,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, BITS, NT>::kCtas)
         const int64_t left = u1 - u;
         const int v1 = units - v0 <= left ? units : v0 + static_cast<int>(left);
         const int k0 = v0 > kLead ? v0 - kLead : 0, k1 = v1 - kLead;
-        if (threadIdx.x == 0) note_piece(a, cut, u - v0, v0, v1, units, item, head);
         if (k1 > k0) {
             float *part = nullptr;
             if (k1 - k0 != it.n)
                 part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1)) * S::kSlot;
             attend_run<D, BITS, NT>(a, it, head, k0, k1, part, attn_smem);
         }
+        if (threadIdx.x == 0) note_piece(a, cut, u - v0, v0, v1, units, it, item, head);
         u += v1 - v0;
         if (v1 == units && head == a.cache.Hkv - 1) {
             before += units;
@@ -938,7 +938,7 @@ int kv_attention_fwd(const rn_bf16 *q, int64_t q_stride, const uint8_t *codes,
     a.out = out;
     a.lse = lse;
     a.units = static_cast<int64_t *>(workspace);
-    a.cuts = reinterpret_cast<rn::CutHead *>(static_cast<char *>(workspace) + 16);
+    a.cuts = reinterpret_cast<rn::CutNote *>(static_cast<char *>(workspace) + 16);
     a.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.head_bytes);
     a.q_tiles = plan.q_tiles;
     a.heads = B * plan.q_tiles * Hkv;

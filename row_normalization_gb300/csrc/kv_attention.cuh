@@ -30,20 +30,23 @@ struct KvAttnArgs {
     float *lse;
     // workspace: the line's length, what each CTA's start cuts [grid], the partial sums
     int64_t *units;
-    struct CutHead *cuts;
+    struct CutNote *cuts;
     float *partial;
     int64_t q_tiles;   // query tiles of a sequence
     int64_t heads;     // (query tile, kv head)s in all
     int grid;          // CTAs of the attention kernel
 };
 
-// A (query tile, head) that the start of CTA `cta`'s run cuts, noted where the CTA
-// before holds its first piece, so that every cut one is noted once; item -1: none.
-// The notes are one for each (query tile, head) where these are fewer than the
-// CTAs, else one for each CTA.
-struct CutHead {
-    int64_t first;  // its first unit
-    int32_t item, head, cta, unused;
+// A (query tile, head) cut into pieces, with all the joining kernel needs of it; noted
+// by the CTA of its second piece, so once.  The notes are one for each (query tile,
+// head) where these are fewer than the CTAs, else one for each CTA; pieces 0: none.
+struct CutNote {
+    int64_t row0;       // as Item
+    int32_t f0, ncols;
+    int32_t head0;      // first query head
+    int32_t pieces;
+    int32_t first_slot; // of the first piece; the others lie two on from an even slot each
+    int32_t unused;
 };
 
 // How a kernel lays its work on the line: NQ columns (queries of the tile times
@@ -215,16 +218,14 @@ __device__ __forceinline__ Line find_unit(const KvAttnArgs &a, bool publish, int
     const Cut<L> cut(line.units, a.grid);
     const int64_t u = cut.start(blockIdx.x);
     if (blockIdx.x < cut.ctas && before * a.cache.Hkv <= u && u < (before + sum) * a.cache.Hkv) {
-        int64_t run = before;
-        for (int64_t i = i0; i < i1; ++i) {
+        int64_t run = before, i = i0;
+        for (; i + 1 < i1; ++i) {
             const int n = make_item<L>(a, i).units();
-            if (u < (run + n) * a.cache.Hkv) {
-                scratch[THREADS / 32] = i;
-                scratch[THREADS / 32 + 1] = run;
-                break;
-            }
+            if (u < (run + n) * a.cache.Hkv) break;
             run += n;
         }
+        scratch[THREADS / 32] = i;
+        scratch[THREADS / 32 + 1] = run;
     }
     __syncthreads();
     line.item = scratch[THREADS / 32];
@@ -239,7 +240,8 @@ __device__ __forceinline__ void store_empty(const KvAttnArgs &a) {
     for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
         const Item<L> it = make_item<L>(a, i);
         if (it.n > 0) continue;
-        if (a.heads <= a.grid && threadIdx.x < a.cache.Hkv) a.cuts[i * a.cache.Hkv + threadIdx.x].item = -1;
+        if (a.heads <= a.grid)
+            for (int h = threadIdx.x; h < a.cache.Hkv; h += THREADS) a.cuts[i * a.cache.Hkv + h].pieces = 0;
         const int quads = it.ncols * (D / 4);
         for (int idx = threadIdx.x; idx < quads * a.cache.Hkv; idx += THREADS) {
             const int head = idx / quads, in = idx - head * quads;
@@ -253,28 +255,27 @@ __device__ __forceinline__ void store_empty(const KvAttnArgs &a) {
 // tile, head) whose first unit is `first`; by one thread.
 template <class L>
 __device__ __forceinline__ void note_piece(const KvAttnArgs &a, const Cut<L> &cut, int64_t first, int v0, int v1,
-                                           int units, int64_t item, int head) {
-    CutHead c;
-    c.first = first;
-    c.item = static_cast<int32_t>(item);
-    c.head = head;
-    c.cta = blockIdx.x;
-    c.unused = 0;
+                                           int units, const Item<L> &it, int64_t item, int head) {
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) - 1;
     // the second piece: the CTA before holds the first unit with work
-    const bool second =
-        v0 > L::LEAD && cut.start(static_cast<int64_t>(blockIdx.x) - 1) <= first + L::LEAD;
-    if (a.heads <= a.grid) {
-        const bool whole = v0 <= L::LEAD && v1 == units;
-        if (whole) c.item = -1;
-        if (whole || second) a.cuts[item * a.cache.Hkv + head] = c;
-    } else if (first + v0 == cut.start(blockIdx.x)) {
-        if (!second) c.item = -1;
-        a.cuts[blockIdx.x] = c;
-    }
+    const bool second = v0 > L::LEAD && cut.start(c0) <= first + L::LEAD;
+    const bool by_head = a.heads <= a.grid;
+    const bool none = by_head ? v0 <= L::LEAD && v1 == units : !second && first + v0 == cut.start(blockIdx.x);
+    if (!second && !none) return;
+    CutNote n;
+    n.row0 = it.row0;
+    n.f0 = it.f0;
+    n.ncols = it.ncols;
+    n.head0 = head * a.group;
+    n.pieces = second ? static_cast<int>(cut.cta_of(first + units - 1) - c0) + 1 : 0;
+    n.first_slot = static_cast<int>(2 * c0 + (cut.start(c0) < first ? 1 : 0));
+    n.unused = 0;
+    a.cuts[by_head ? item * a.cache.Hkv + head : blockIdx.x] = n;
 }
 
 constexpr int kJoinWarps = 8;
 constexpr int64_t kJoinBlocks = 2432;  // about sixteen an SM
+constexpr int kEarly = 4;      // pieces a warp loads ahead
 constexpr int kFewPieces = 8;  // pieces that one warp joins by itself
 
 // ---- joining the pieces of a cut (query tile, head) -------------------------------------
@@ -290,19 +291,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_attention_join_kernel(cons
     pdl_trigger();
     pdl_wait();
     const int64_t units = *a.units;
-    if (units == 0) return;
-    const Cut<L> cut(units, a.grid);
-    if (a.heads > a.grid && blockIdx.x >= cut.ctas) return;
-    const CutHead cuthead = a.cuts[blockIdx.x];
-    if (cuthead.item < 0) return;
-    const Item<L> it = make_item<L>(a, cuthead.item);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kvh = cuthead.head;
-    // pieces lie with the CTA before and those up to the one that holds the last unit;
-    // all but the first of them begin with theirs
-    const int64_t c0 = cuthead.cta - 1;
-    const int pieces = static_cast<int>(cut.cta_of(cuthead.first + it.units() - 1) - c0) + 1;
-    const float *parts = a.partial + 2 * c0 * SLOT;
-    const float *first_part = parts + (cut.start(c0) < cuthead.first ? SLOT : 0);
+    const CutNote note = a.cuts[blockIdx.x];
+    if (units == 0 || (a.heads > a.grid && blockIdx.x >= Cut<L>(units, a.grid).ctas)) return;
+    const int pieces = note.pieces;
+    if (pieces == 0) return;
+    Item<L> it;
+    it.row0 = note.row0;
+    it.f0 = note.f0;
+    it.ncols = note.ncols;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // all pieces but the first are the first of their CTAs
+    const float *first_part = a.partial + static_cast<int64_t>(note.first_slot) * SLOT;
+    const float *parts = a.partial + static_cast<int64_t>(note.first_slot & ~1) * SLOT;
     const auto piece = [&](int p) { return p == 0 ? first_part : parts + static_cast<int64_t>(p) * 2 * SLOT; };
     const bool share = pieces > kFewPieces;
     const int p0 = share ? warp : 0, step = share ? kJoinWarps : 1;
@@ -314,6 +314,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_attention_join_kernel(cons
         // the largest reference of the warp's pieces and their sum of weights, by the
         // column's lanes together
         float top = -INFINITY, l = 0.0f;
+        // (the first pieces' sums come while their references are looked at)
+        float4 early[kEarly];
+        if (live)
+#pragma unroll
+            for (int i = 0; i < kEarly; ++i)
+                if (p0 + i * step < pieces)
+                    early[i] = *reinterpret_cast<const float4 *>(piece(p0 + i * step) + col * D + d0);
         if (live)
             for (int p = p0 + step * (lane % W); p < pieces; p += step * W) top = fmaxf(top, piece(p)[NQ * D + col]);
 #pragma unroll
@@ -325,17 +332,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_attention_join_kernel(cons
 #pragma unroll
         for (int o = W / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const auto add = [&](const float *part, float4 v) {
+            const float f = exp2_approx(part[NQ * D + col] - ref);
+            acc.x = fmaf(v.x, f, acc.x);
+            acc.y = fmaf(v.y, f, acc.y);
+            acc.z = fmaf(v.z, f, acc.z);
+            acc.w = fmaf(v.w, f, acc.w);
+        };
         if (live) {
+#pragma unroll
+            for (int i = 0; i < kEarly; ++i)
+                if (p0 + i * step < pieces) add(piece(p0 + i * step), early[i]);
 #pragma unroll 8
-            for (int p = p0; p < pieces; p += step) {
-                const float *part = piece(p);
-                const float f = exp2_approx(part[NQ * D + col] - ref);
-                const float4 v = *reinterpret_cast<const float4 *>(part + col * D + d0);
-                acc.x = fmaf(v.x, f, acc.x);
-                acc.y = fmaf(v.y, f, acc.y);
-                acc.z = fmaf(v.z, f, acc.z);
-                acc.w = fmaf(v.w, f, acc.w);
-            }
+            for (int p = p0 + kEarly * step; p < pieces; p += step)
+                add(piece(p), *reinterpret_cast<const float4 *>(piece(p) + col * D + d0));
         }
         if (share) {
             s_acc[warp][lane] = acc;
@@ -359,7 +369,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_attention_join_kernel(cons
             }
             __syncthreads();
         }
-        if (live && (!share || warp == 0)) store_result<D, L>(a, it, kvh * a.group, col, d0, acc, ref, l);
+        if (live && (!share || warp == 0)) store_result<D, L>(a, it, note.head0, col, d0, acc, ref, l);
     }
 }
 

@@ -515,13 +515,13 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
             const int64_t left = u1 - u;
             const int v1 = units - v0 <= left ? units : v0 + static_cast<int>(left);
             const int k0 = v0 > L::LEAD ? v0 - L::LEAD : 0, k1 = v1 - L::LEAD;
-            if (threadIdx.x == 0) note_piece(a, cut, u - v0, v0, v1, units, item, head);
             if (k1 > k0) {
                 float *part = nullptr;
                 if (k1 - k0 != it.n)
                     part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1)) * S::kSlot;
                 if (!body(it, head, k0, k1, part)) return;
             }
+            if (threadIdx.x == 0) note_piece(a, cut, u - v0, v0, v1, units, it, item, head);
             u += v1 - v0;
             if (v1 == units && head == a.cache.Hkv - 1) {
                 before += units;
