@@ -323,6 +323,182 @@ def test_long_contexts(bits, Hq, Hkv, D, n):
     check(out.cpu(), lse.cpu(), q, ref, table, lens, [0, 1, 2, 3, 4], D ** -0.5)
 
 
+# ---- more than 64 columns: 128 at a time, one or two such tiles side by side -------------
+
+CHUNKS = [(4, 1, 64, 16), (8, 2, 128, 16), (6, 2, 128, 64), (3, 1, 256, 32), (70, 1, 128, 128),
+          (5, 1, 64, 64), (8, 1, 256, 16)]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("Hq,Hkv,D,P", CHUNKS)
+def test_chunks_of_ragged_length(bits, Hq, Hkv, D, P):
+    """Tiles of 128 columns that are full, partly full and empty, tiles of tokens that
+    end anywhere, beside sequences of one query and of none."""
+    lens, n_q = [140, 33, 257, 1, 96, 400], [33, 20, 70, 1, 0, 2]
+    ref, table = filled(bits, Hkv, D, P, lens, seed=D + P + 2)
+    q = queries(sum(n_q), Hq, D, seed=Hq)
+    out, lse, cu = attend(ref, table, lens, q, n_q, Hq)
+    check(out, lse, q, ref, table, lens, cu, D ** -0.5)
+    again, lse2, _ = attend(ref, table, lens, q, n_q, Hq)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    assert binding.device_status() == 0
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (40, 3), (129, 130), (300, 1)])
+@pytest.mark.parametrize("Hq,Hkv,D,P,bits", [(8, 2, 128, 16, 4), (4, 1, 64, 32, 8), (4, 2, 256, 64, 4)])
+def test_chunks_with_window_and_sinks(window, sinks, Hq, Hkv, D, P, bits):
+    lens, n_q = [500, 70], [60, 70]
+    ref, table = filled(bits, Hkv, D, P, lens, seed=window)
+    first = lens[0] - n_q[0] - window + 1                   # nothing between the sinks and here
+    for j in range(sinks, max(first, 0)):
+        ref.scales[int(table[0, j // P]), :, :, j % P] = float("nan")
+    gone = table.clone()
+    for pg in range(-(-sinks // P), max(first, 0) // P):
+        gone[0, pg] = -3
+    q = queries(sum(n_q), Hq, D, seed=9)
+    out, lse, cu = attend(ref, gone, lens, q, n_q, Hq, window=window, sinks=sinks)
+    check(out, lse, q, ref, table, lens, cu, D ** -0.5, window, sinks)
+    assert binding.device_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_chunk_rows_that_see_nothing_and_rows_outside(D):
+    Hq, Hkv, P = 4, 1, 16
+    lens, n_q = [0, 25, 40], [40, 60, 40]
+    ref, table = filled(8, Hkv, D, P, lens, seed=3)
+    T = sum(n_q) + 5
+    q = queries(T, Hq, D, seed=5)
+    keep = torch.full((T, Hq, D), 2.5, dtype=torch.bfloat16, device="cuda")
+    out, lse, cu = attend(ref, table, lens, q, n_q, Hq, out=keep)
+    check(out, lse, q, ref, table, lens, cu, D ** -0.5)
+    assert (out[:40] == 0).all() and (out[40:75] == 0).all() and torch.isneginf(lse[:75]).all()
+    assert (out[140:] == 2.5).all()
+    assert binding.device_status() == 0
+
+
+@pytest.mark.parametrize("D,bits", [(64, 4), (128, 8), (256, 4), (256, 8)])
+def test_chunk_nan_and_infinite_queries_stay_in_their_place(D, bits):
+    Hq, Hkv, P, n, L = 4, 2, 16, 50, 120
+    ref, table = filled(bits, Hkv, D, P, [L], seed=17)
+    q = queries(n, Hq, D, seed=17)
+    q[7, 1, 3] = float("inf")
+    g = D // 32 - 1
+    spots = [(1, 0, 100, g), (1, 1, 60, 0), (0, 1, 110, 1)]  # value, value, key
+    for which, h, t, grp in spots:
+        pg, off = int(table[0, t // P]), t % P
+        ref.scales[pg, which, h, off, grp] = float("nan")
+        ref.vals[pg, which, h, off, 32 * grp:32 * grp + 32] = float("nan")
+    out, lse, cu = attend(ref, table, [L], q, [n], Hq)
+    want = torch.zeros(n, Hq, D, dtype=torch.bool)
+    want[7, 1] = True
+    want[100 - (L - n):, :2, 32 * g:32 * g + 32] = True     # queries from token 100 on
+    want[:, 2:, :32] = True                                  # token 60 is before them all
+    want[110 - (L - n):, 2:] = True
+    assert torch.equal(torch.isnan(out.float()), want)
+    assert torch.equal(torch.isnan(lse), want.all(-1))
+
+
+@pytest.mark.parametrize("D,bits", [(64, 8), (128, 4), (256, 8)])
+def test_chunk_scales_above_255(D, bits):
+    """Values (and, with small queries, keys) far above the rest: restored at 2^-8."""
+    Hq, Hkv, P = 4, 1, 32
+    lens, n_q = [300, 150], [40, 35]
+    ref, table = filled(bits, Hkv, D, P, lens, seed=23)
+    g = torch.Generator().manual_seed(1)
+    for b, n in enumerate(lens):
+        pos = torch.arange(n)
+        x = torch.randn(n, 2, Hkv, D, generator=g)
+        x[40:50, 1] *= 4000.0
+        x[120, 0] *= 20000.0
+        ref.write(x.to(torch.bfloat16), table[b, pos // P].long() * P + pos % P)
+    q = queries(sum(n_q), Hq, D, seed=2, size=1e-4)
+    out, lse, cu = attend(ref, table, lens, q, n_q, Hq)
+    check(out, lse, q, ref, table, lens, cu, D ** -0.5)
+
+
+def test_chunk_bad_pages_are_zeros_and_reported():
+    Hq, Hkv, D, P = 8, 2, 128, 16
+    lens, n_q = [200], [30]
+    ref, table = filled(4, Hkv, D, P, lens, seed=14)
+    table[0, 2], table[0, 7] = ref.codes.shape[0], -1
+    q = queries(30, Hq, D, seed=14)
+    out, lse, cu = attend(ref, table, lens, q, n_q, Hq)
+    assert binding.device_status() == binding.RN_STATUS_BAD_INDEX
+    check(out, lse, q, ref, table, lens, cu, D ** -0.5)
+
+
+def test_chunk_sizes_of_queries():
+    Hq, Hkv, D, P = 4, 1, 128, 32
+    lens, n_q = [200], [40]
+    ref, table = filled(8, Hkv, D, P, lens, seed=33)
+    for size, scale in ((40.0, None), (1e-20, None), (1e18, 1e-18), (1.5, 0.0), (1.5, -0.2)):
+        q = queries(40, Hq, D, seed=33, size=size)
+        out, lse, cu = attend(ref, table, lens, q, n_q, Hq, scale=scale)
+        check(out, lse, q, ref, table, lens, cu, D ** -0.5 if scale is None else scale)
+
+
+def test_chunk_captured_beside_another_on_a_second_stream():
+    """A captured chunk call replays on new lengths; two calls run at the same time with
+    a workspace each."""
+    Hq, Hkv, D, P = 8, 2, 128, 16
+    ref, table = filled(4, Hkv, D, P, [300, 180], seed=44)
+    cache, dt = to_gpu(ref), table.cuda()
+    T = 70
+    q = queries(T, Hq, D, seed=44).cuda()
+    lens = torch.tensor([300, 180], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 40, 70], device="cuda")
+    ws = [binding.kv_attention_workspace(cache, 2, Hq, max_q_len=60) for _ in range(2)]
+    outs = [torch.empty(T, Hq, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    lses = [torch.empty(T, Hq, device="cuda") for _ in range(2)]
+
+    def call(i):
+        binding.kv_attention_fwd(q, cache, dt, lens, Hq, cu_q=cu, max_q_len=60, out=outs[i],
+                                 lse=lses[i], workspace=ws[i])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(0)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(0)
+    for a, b, c in ((300, 180, 40), (41, 177, 12), (259, 64, 58)):
+        lens.copy_(torch.tensor([a, b], dtype=torch.int32))
+        cu.copy_(torch.tensor([0, c, 70]))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            call(1)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], outs[1]) and torch.equal(lses[0], lses[1])
+        check(outs[0].cpu(), lses[0].cpu(), q.cpu(), ref, table, [a, b], [0, c, 70], D ** -0.5)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,bits,n_q", [(4, 1, 128, 4, 64), (4, 1, 64, 8, 64), (2, 1, 256, 4, 40)])
+def test_chunk_over_a_long_context(Hq, Hkv, D, bits, n_q):
+    """Many CTAs share a chunk's tiles of tokens; the pieces are joined."""
+    lens = [6000]
+    ref, table = filled(bits, Hkv, D, 64, lens, seed=71)
+    q = queries(n_q, Hq, D, seed=71)
+    out, lse, cu = attend(ref, table, lens, q, [n_q], Hq)
+    check(out, lse, q, ref, table, lens, cu, D ** -0.5)
+
+
+def test_more_heads_than_ctas_of_every_length():
+    """Notes by CTA instead of by head, pieces of every kind."""
+    Hq, Hkv, D, P = 40, 20, 64, 16
+    lens = [(37 * i) % 400 for i in range(40)]
+    ref, table = filled(8, Hkv, D, P, lens, seed=5)
+    q = queries(len(lens), Hq, D, seed=5)
+    ws = binding.kv_attention_workspace(to_gpu(ref), len(lens), Hq)
+    ws.fill_(0xFF)
+    out, lse = binding.kv_attention_fwd(q.cuda(), to_gpu(ref), table.cuda(),
+                                        torch.tensor(lens, dtype=torch.int32).cuda(), Hq,
+                                        workspace=ws)
+    check(out.cpu(), lse.cpu(), q, ref, table, lens, list(range(len(lens) + 1)), D ** -0.5)
+
+
 def test_many_sequences_and_a_long_chunk():
     Hq, Hkv, D, P = 4, 2, 64, 16
     lens = [(7 * i) % 50 for i in range(700)] + [500]
@@ -341,7 +517,7 @@ def test_runs_repeat_bit_for_bit_and_share_a_workspace():
     q = queries(3, Hq, D, seed=40).cuda()
     args = (cache, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), Hq)
     ws = binding.kv_attention_workspace(cache, 3, Hq)
-    ws.random_(0, 256)
+    ws.fill_(0x7F)                                          # it needs no clearing
     first = binding.kv_attention_fwd(q, *args, workspace=ws)
     other = binding.kv_attention_fwd(q.flip(0).contiguous(), *args, workspace=ws)
     again = binding.kv_attention_fwd(q, *args, workspace=ws)
