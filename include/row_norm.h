@@ -598,10 +598,14 @@ int kv_cache_read(const uint8_t *codes, const rn_f16 *scales, int format, int Hk
  * raises RN_STATUS_BAD_INDEX.  Entries of page_table for pages on which no
  * query sees a token are not used.  Requirements: Hq a multiple of Hkv; T * Hq,
  * B * Hq, max_q_len * Hq and max_pages * page_size < 2^31; scale finite,
- * window and sinks >= 0.  Arithmetic: exact products of bf16 queries and codes,
- * fp32 sums; a softmax weight and its product with a value scale are each
- * rounded to fp16 (2^-11 relative) before they meet the codes.  Errors as kv_cache_write; a workspace that is too small
- * is RN_ERR_ARG. */
+ * window and sinks >= 0; scale * |q| and every logit below 2^100.
+ * Arithmetic: a logit is an fp32 sum of exact products of query and key; a
+ * softmax weight and its product with a value scale (more than 64 queries times
+ * heads of a group: the weight and the value) are each rounded to fp16, 2^-11
+ * relative, before fp32 sums.  A NaN reaches the outputs whose formula holds it
+ * and no others.  The results do not depend on timing: the same call gives the
+ * same bits.  Errors as kv_cache_write; a workspace that is too small is
+ * RN_ERR_ARG. */
 int kv_attention_fwd(const rn_bf16 *q, int64_t q_stride, const uint8_t *codes,
                      const rn_f16 *scales, int format, int Hq, int Hkv, int D,
                      int page_size, int64_t num_pages, const int32_t *page_table,

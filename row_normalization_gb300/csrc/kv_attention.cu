@@ -27,10 +27,17 @@
 // Work is cut evenly over a fixed grid: all (sequence, query tile, kv head,
 // 32-token tile) units form one line, of which every CTA takes an equal run,
 // so ragged lengths leave no CTA behind.  Each (query tile, head) also has
-// kLead units without work in front, for what it costs to begin and end one.  A run that cuts a (query tile, head)
-// leaves partial sums in the workspace, which a second kernel joins in the
-// order of the line.  Inside a CTA four warps take every fourth tile with an
+// kLead units without work in front, for what it costs to begin and end one.  A
+// run that cuts a (query tile, head) leaves partial sums in the workspace, which a
+// second kernel joins in the order of the line.  Inside a CTA four warps take every fourth tile with an
 // asynchronous copy ring of their own each and join at the end.
+//
+// Measured (one GB300, steady state): 64 sequences of 200 to 16000 tokens, 32 query and
+// 8 kv heads of 128, 4 bits: 118 us, 5.3 TB/s of the bytes that have to be read; four of
+// 131072 tokens 110 us, 5.5 TB/s; in 8 bits heads of 128 183 us, 6.4 TB/s, heads of 64
+// (96 sequences) 95 us, 5.5 TB/s.  In 8 bits the bytes bound; in 4 bits the unpacking
+// (about 640 instructions a warp and tile of 32 tokens, the integer pipe half full, 50 to
+// 60% of the issue slots used by three warps a scheduler).
 #include "kv_attention.cuh"
 
 namespace rn {
@@ -801,7 +808,10 @@ int kv_attention_status(unsigned int *out, int clear) {
 
 // ---- host -------------------------------------------------------------------------------
 
-// More columns than this go to the kernel that takes 128 of them at a time.
+// More columns than this go to the kernel that takes 128 of them at a time (16 sequences
+// of 3000 to 8000 tokens, 8 heads; this kernel against that one, us: heads of 128 in 4
+// bits, 64 columns 124 / 145, 128 columns 223 / 153; heads of 64 in 8 bits 71 / 101 and
+// 125 / 105; heads of 256 in 4 bits 250 / 321 and 478 / 336).
 static bool wide(int64_t columns) { return columns > 64; }
 
 // Columns of a query tile, in eights: the smallest that holds all queries of a

@@ -5,24 +5,31 @@
 // group) at a time, which makes it a matter of arithmetic: 4 D flops for each
 // column and token against one restored key and value.  The products run as
 // tcgen05.mma with the columns as the 128 rows of the accumulator:
-//   S = Q K'^T    Q and K' in shared memory, S in tensor memory,
-//   O += P V'     P in tensor memory (over its S), V' in shared memory.
-// K' and V' are the cached values restored to fp16, s * c rounded once (2^-11);
-// both operands of S are exact otherwise, the queries as in kv_attention.cu.  A
-// tile with a scale above 255 is restored at 2^-8 of its size (the weights, or
-// the logit's factor, make up for it), so nothing leaves fp16.
+//   S = Q K'^T + Q K''^T   Q, K' and K'' in shared memory, S in tensor memory,
+//   O += P V'              P in tensor memory (over its S), V' in shared memory.
+// V' is the cached value s * c rounded once to fp16, K' the same of the key and K''
+// the exact rest, so the logits (and lse) have no rounding but that of fp32 sums.
+// Queries as in kv_attention.cu.  32 tokens around a scale above 255 are restored at
+// 2^-8 of their size (the weights, or the logit's factor, make up for it), so
+// nothing leaves fp16.
 //
-// Roles: warps 0-3 one accumulator row a thread (softmax, output), warps 4-7
-// restore keys, 8-11 values (two stages each), one thread of warp 12 issues the
-// products.  S has two buffers, so the product of tile n + 1 runs beside the
-// softmax of tile n.  What bounds it: the exponentials (16 a clock and SM) and the
-// tensor cores need about 1000 clocks a tile of 128 x 128 x 128 each, shared memory
-// traffic 1300 (192 KB: the operands once, K' and V' written).
+// Roles: four warps for each query tile of 128 columns, one accumulator row a thread
+// (softmax, output); four that restore keys, four for values; one thread issues the
+// products.  Two query tiles share every restored tile and take turns: the products
+// of one run beside the softmax of the other.
+//
+// What bounds it: 64 queries over 131072 tokens of 8 heads of 128 in 4 bits (two query
+// tiles) take 284 us, 484 TFLOP/s: 10300 clocks a tile of 256 columns by 128 tokens,
+// of which the products need 3000 and the exponentials (16 a clock and SM) 2000.  No
+// unit is full (tensor cores about a quarter, issue slots a third): with a form
+// without K'' that took 8700 clocks, leaving out the restoring gave 7000, three
+// quarters of the softmax 8300, most of the products 7100, all of these 2900.  What
+// is left is each role's latency and the handing over between them.
 //
 // Shared memory operands are K-major with the 128-byte exchange of 16-byte chunks
 // (chunk ^ row % 8 in rows of 128 bytes): 64 elements a row, blocks of 64 elements
 // one after the other.  In 4 bits the eight dimensions of a chunk lie in the order
-// 0 4 1 5 2 6 3 7, the order in which they leave a word, in Q as in K'.
+// 0 4 1 5 2 6 3 7, the order in which they leave a word, in Q as in K' and K''.
 #include "kv_attention.cuh"
 
 namespace rn {
@@ -42,26 +49,30 @@ struct WideShape {
     // queries over 131072 tokens of 8 heads 289 against 257 us.)
     static constexpr int BN = D == 256 ? 64 : 128;
     static constexpr int kBufs = QT * (2 * BN + D) <= 512 ? 2 : 1;  // S of a query tile
-    static constexpr int kStages = 2;
+    static constexpr int kStages = 2;                                              // of values
+    static constexpr int kKeyStages = (D == 128 && QT == 2) || D == 256 ? 1 : 2;  // what fits
     static constexpr int NQ = 128 * QT;
     using L = LineShape<NQ, BN, 4, 1>;
     static constexpr int kWarps = 4 * QT + 9;        // softmax, keys, values, products
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kQuery = 128 * D * 2;       // a query tile
-    static constexpr int kStage = BN * D * 2;        // a tile's keys, or values
-    static constexpr int kUsed = 1024 + QT * kQuery + 2 * kStages * kStage;
+    static constexpr int kStage = BN * D * 2;        // a tile's values
+    static constexpr int kKeyStage = 2 * kStage;     // its keys, and what rounding them left
+    static constexpr int kUsed = 1024 + QT * kQuery + kKeyStages * kKeyStage + kStages * kStage;
     // more than half of an SM's shared memory: the tensor memory of an SM has one owner
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
     static constexpr int kSlot = NQ * (D + 2);
     // tensor memory columns: the S buffers, then O
     static constexpr uint32_t kO = QT * kBufs * BN;
-    static_assert(kO + QT * D <= 512 && kUsed <= 227 * 1024, "tensor and shared memory");
+    static_assert(kO + QT * D <= 512 && kUsed <= 226 * 1024, "tensor and shared memory");
     // S buffer and barrier phase of a query tile's c-th tile of tokens
     __device__ static __forceinline__ uint32_t buf(uint32_t qt, uint32_t c) { return qt * kBufs + c % kBufs; }
     __device__ static __forceinline__ uint32_t phase(uint32_t c) { return c / kBufs & 1; }
     // stage and barrier phase of the CTA's n-th tile
     __device__ static __forceinline__ uint32_t stage(uint32_t n) { return n % kStages; }
     __device__ static __forceinline__ uint32_t round(uint32_t n) { return n / kStages & 1; }
+    __device__ static __forceinline__ uint32_t key_stage(uint32_t n) { return n % kKeyStages; }
+    __device__ static __forceinline__ uint32_t key_round(uint32_t n) { return n / kKeyStages & 1; }
 };
 
 // ---- tensor memory and tcgen05 ------------------------------------------------------
@@ -272,6 +283,8 @@ struct TokenRows {
 // ---- restoring keys ---------------------------------------------------------------------
 // Four warps, BN / 4 tokens each (each with a power of two of its own), eight at a time: lane = token % 8 + 8 j with j the
 // quarter of the stored row.  A group's eight elements are one chunk of the operand.
+// A key s * c has up to 18 significant bits: its fp16 and the exact rest, which the
+// fused multiply-add gives, are two operands behind one another.
 template <int D, int BITS, int BN>
 struct KeyTile {
     using F = KvFormat<D, BITS>;
@@ -323,10 +336,17 @@ struct KeyTile {
                 else
                     codes_of(w[i][2 * g], w[i][2 * g + 1], h);
                 const int chunk = 4 * g + (lane >> 3);
-                *reinterpret_cast<uint4 *>(stage + (chunk >> 3) * (BN * 128) + row * 128 +
-                                           (((chunk & 7) ^ (row & 7)) << 4)) =
-                    make_uint4(h2_bits(__hmul2(h[0], sc)), h2_bits(__hmul2(h[1], sc)), h2_bits(__hmul2(h[2], sc)),
-                               h2_bits(__hmul2(h[3], sc)));
+                uint8_t *to = stage + (chunk >> 3) * (BN * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+                __half2 k[4], rest[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    k[e] = __hmul2(h[e], sc);
+                    rest[e] = __hfma2(h[e], sc, __hneg2(k[e]));
+                }
+                *reinterpret_cast<uint4 *>(to) =
+                    make_uint4(h2_bits(k[0]), h2_bits(k[1]), h2_bits(k[2]), h2_bits(k[3]));
+                *reinterpret_cast<uint4 *>(to + BN * D * 2) =
+                    make_uint4(h2_bits(rest[0]), h2_bits(rest[1]), h2_bits(rest[2]), h2_bits(rest[3]));
             }
         }
     }
@@ -465,7 +485,7 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
     __shared__ uint8_t nan_groups[2][2 * BN];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *qs = wide_raw + ((1024u - (smem_addr(wide_raw) & 1023u)) & 1023u);
-    uint8_t *ks = qs + QT * S::kQuery, *vs = ks + S::kStages * S::kStage;
+    uint8_t *ks = qs + QT * S::kQuery, *vs = ks + S::kKeyStages * S::kKeyStage;
 
     pdl_trigger();
     pdl_wait();
@@ -745,13 +765,13 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
             KeyTile<D, BITS, BN> tile;
             tile.load(rows, it.token(k0), w, lane);
             for (int k = k0; k < k1; ++k, ++n) {
-                const uint32_t s = S::stage(n), par = S::round(n);
+                const uint32_t s = S::key_stage(n), par = S::key_round(n);
                 // the products that read this stage before are over
                 if (!wide_wait_warp(sh, &sh.k_free[s], par ^ 1)) return false;
                 const bool small = __any_sync(0xffffffffu, tile.special());
                 if (small) tile.scale_down();
                 if (lane == 0) reinterpret_cast<uint8_t *>(&sh.key_flags[n & 7])[w] = small ? 1 : 0;
-                tile.store(ks + s * S::kStage, w, lane);
+                tile.store(ks + s * S::kKeyStage, w, lane);
                 fence_async_shared();
                 mbar_arrive(&sh.k_full[s]);
                 // the next tile's bytes come while this one is used
@@ -789,15 +809,18 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
         // S of query tile qt with the keys of the CTA's tile i, into the buffer of the
         // query tile's next tile: its weights of before have been used up
         const auto logits = [&](uint32_t qt, uint32_t i, bool last) {
-            const uint32_t c = s_done[qt]++, b = S::buf(qt, c), s = S::stage(i);
+            const uint32_t c = s_done[qt]++, b = S::buf(qt, c), s = S::key_stage(i);
             constexpr uint32_t kBack = S::kBufs;
             if (c >= kBack && !wide_wait(sh, &sh.pv_done[b], S::phase(c - kBack))) return false;
-            if (!wide_wait(sh, &sh.k_full[s], S::round(i))) return false;
+            if (!wide_wait(sh, &sh.k_full[s], S::key_round(i))) return false;
             tc_fence_after();
 #pragma unroll
             for (int q = 0; q < D / 16; ++q)
-                mma_ss(tmem + b * BN, operand_desc(qa + qt * S::kQuery + (q >> 2) * (128 * 128) + (q & 3) * 32),
-                       operand_desc(ka + s * S::kStage + (q >> 2) * (BN * 128) + (q & 3) * 32), wide_idesc(BN), q != 0);
+#pragma unroll
+                for (int rest = 0; rest < 2; ++rest)
+                    mma_ss(tmem + b * BN, operand_desc(qa + qt * S::kQuery + (q >> 2) * (128 * 128) + (q & 3) * 32),
+                           operand_desc(ka + s * S::kKeyStage + rest * S::kStage + (q >> 2) * (BN * 128) + (q & 3) * 32),
+                           wide_idesc(BN), q != 0 || rest != 0);
             tc_commit(&sh.s_full[b]);
             if (last) tc_commit(&sh.k_free[s]);
             return true;

@@ -18,10 +18,12 @@ Tolerance of an output element (derived, nothing fitted):
     multiply-adds and two roundings: 10 * 2^-24 * sum |q k|, all times the scale.  A
     logit moves a weight by that fraction and the weights' sum by the same: twice it;
   * exp2 and the running sums: 2^-20.
-More than 64 columns (queries times heads of a group) run on restored fp16 keys and
-values, rounded once each (2^-11), and weights rounded once: the output's 2^-10 is the
-same, and a logit is off by 2^-11 * sum |q k| more.  Where a scale exceeds 255 the 32
-tokens around it are restored at 2^-8 of their size, so that small scales among them
+More than 64 columns (queries times heads of a group) run on restored fp16 values,
+rounded once (2^-11), and weights rounded once: the output's 2^-10 is the same.  Keys
+are restored as fp16 and the rest, itself fp16: off by 2^-22 |k| or, where the rest is
+subnormal, 2^-25 an element; their products are summed D / 8 instructions long, 17 *
+2^-24 of the largest partial sum each, sum |q k| at most.  Where a scale exceeds 255 the
+32 tokens around it are restored at 2^-8 of their size, so that small scales among them
 are rounded as subnormal numbers: 2^-25 * 2^8 a unit of the code, z a unit at most.
 lse: the logit's error plus 2^-20 plus 2^-22 |lse|.
 """
@@ -92,6 +94,7 @@ def check(got, lse, q, ref, table, lens, cu, scale, window=0, sinks=0):
         G = q.shape[1] // K.shape[1]
         wide = max(y - x for x, y in zip(cu, cu[1:])) * G > 64
         low_k, low_v = (z * 2.0 ** -17 * float((x > 255).any()) * wide for x in (SK, SV))
+        low_k += 2.0 ** -25 * wide
         tol, dl = torch.full_like(o, 2.0 ** -40), torch.zeros_like(l)
         for i in range(hi - lo):
             for h in range(q.shape[1]):
@@ -103,7 +106,9 @@ def check(got, lse, q, ref, table, lens, cu, scale, window=0, sinks=0):
                 grp = x.view(-1, 32)
                 per = torch.maximum(2 * z * grp.abs().amax(1), z * grp.sum(1).abs())
                 e = 34 * (sk[:, ::32] @ per) + 10 * (k.abs() @ x.abs())
-                e = e * 2.0 ** -24 + wide * 2.0 ** -11 * 1.01 * (k.abs() @ x.abs())
+                if wide:
+                    e = (17 * D / 8 + 10) * (k.abs() @ x.abs())
+                e = e * 2.0 ** -24 + wide * 2.0 ** -22 * (k.abs() @ x.abs())
                 dlogit = float(e.max() + low_k * x.abs().sum()) * abs(scale)
                 dl[i, h] = dlogit
                 tol[i, h] += (2.0 ** -10 + 2 * dlogit + 2.0 ** -20) * 1.01 * (w @ V[js, h // G].abs())
