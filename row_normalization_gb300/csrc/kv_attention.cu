@@ -36,7 +36,7 @@
 // 8 kv heads of 128, 4 bits: 118 us, 5.3 TB/s of the bytes that have to be read; four of
 // 131072 tokens 110 us, 5.5 TB/s; in 8 bits heads of 128 183 us, 6.4 TB/s, heads of 64
 // (96 sequences) 95 us, 5.5 TB/s.  In 8 bits the bytes bound; in 4 bits the unpacking
-// (about 640 instructions a warp and tile of 32 tokens, the integer pipe half full, 50 to
+// (about 620 instructions a warp and tile of 32 tokens, the integer pipe half full, 50 to
 // 60% of the issue slots used by three warps a scheduler).
 #include "kv_attention.cuh"
 
