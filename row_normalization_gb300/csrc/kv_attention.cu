@@ -29,7 +29,8 @@
 // so ragged lengths leave no CTA behind.  Each (query tile, head) also has
 // kLead units without work in front, for what it costs to begin and end one.  A
 // run that cuts a (query tile, head) leaves partial sums in the workspace, which a
-// second kernel joins in the order of the line.  Inside a CTA four warps take every fourth tile with an
+// second kernel joins in the order of the line.  Short contexts go without: a CTA
+// for each (query tile, head), one launch (attn_direct).  Inside a CTA four warps take every fourth tile with an
 // asynchronous copy ring of their own each and join at the end.
 //
 // Measured (one GB300, steady state): 64 sequences of 200 to 16000 tokens, 32 query and
@@ -768,32 +769,48 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, BITS, NT>::kCtas)
     __shared__ int64_t scratch[kAttnWarps + 2];
     pdl_trigger();
     pdl_wait();
-    const Line line = find_unit<L, kAttnThreads>(a, blockIdx.x == 0, scratch);
-    store_empty<D, L, kAttnThreads>(a);
-    const Cut<L> cut(line.units, a.grid);
-    if (line.units == 0 || blockIdx.x >= cut.ctas) return;
-    const int64_t u0 = cut.start(blockIdx.x), u1 = cut.start(blockIdx.x + 1);
-    int64_t item = line.item, before = line.before, u = u0;
+    int64_t item, before = 0, u = 0, u0 = 0, u1 = 1;
+    Cut<L> cut(1, 1);
+    if (a.direct) {
+        item = blockIdx.x / static_cast<uint32_t>(a.cache.Hkv);
+    } else {
+        const Line line = find_unit<L, kAttnThreads>(a, blockIdx.x == 0, scratch);
+        store_empty<D, L, kAttnThreads>(a);
+        cut = Cut<L>(line.units, a.grid);
+        if (line.units == 0 || blockIdx.x >= cut.ctas) return;
+        u = u0 = cut.start(blockIdx.x);
+        u1 = cut.start(blockIdx.x + 1);
+        item = line.item;
+        before = line.before;
+    }
     while (u < u1) {
         const Item<L> it = make_item<L>(a, item);
-        if (it.n == 0) {
-            ++item;
-            continue;
-        }
-        const int units = it.units();
-        const int64_t in = u - before * a.cache.Hkv;
-        const int head = static_cast<int>(quotient(in, units));
-        const int v0 = static_cast<int>(in - static_cast<int64_t>(head) * units);
-        const int64_t left = u1 - u;
-        const int v1 = units - v0 <= left ? units : v0 + static_cast<int>(left);
-        const int k0 = v0 > kLead ? v0 - kLead : 0, k1 = v1 - kLead;
-        if (k1 > k0) {
-            float *part = nullptr;
+        int head, k0, k1, v0 = 0, v1 = 1, units = 1;
+        float *part = nullptr;
+        if (a.direct) {
+            head = static_cast<int>(blockIdx.x - static_cast<uint32_t>(item) * static_cast<uint32_t>(a.cache.Hkv));
+            k0 = 0;
+            k1 = it.n;
+            if (it.bad && head == 0 && threadIdx.x == 0) atomicOr(&g_kv_attention_status, RN_STATUS_BAD_INDEX);
+            if (it.n == 0) store_zeros<D, L, kAttnThreads>(a, it, head);
+        } else {
+            if (it.n == 0) {
+                ++item;
+                continue;
+            }
+            units = it.units();
+            const int64_t in = u - before * a.cache.Hkv;
+            head = static_cast<int>(quotient(in, units));
+            v0 = static_cast<int>(in - static_cast<int64_t>(head) * units);
+            const int64_t left = u1 - u;
+            v1 = units - v0 <= left ? units : v0 + static_cast<int>(left);
+            k0 = v0 > kLead ? v0 - kLead : 0;
+            k1 = v1 - kLead;
             if (k1 - k0 != it.n)
                 part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1)) * S::kSlot;
-            attend_run<D, BITS, NT>(a, it, head, k0, k1, part, attn_smem);
         }
-        if (threadIdx.x == 0) note_piece(a, cut, u - v0, v0, v1, units, it, item, head);
+        if (k1 > k0) attend_run<D, BITS, NT>(a, it, head, k0, k1, part, attn_smem);
+        if (!a.direct && threadIdx.x == 0) note_piece(a, cut, u - v0, v0, v1, units, it, item, head);
         u += v1 - v0;
         if (v1 == units && head == a.cache.Hkv - 1) {
             before += units;
@@ -856,9 +873,28 @@ static AttnPlan attn_plan(int sm_count, int format, int64_t B, int Hq, int Hkv, 
     });
 }
 
+// Whether each (query tile, head) gets a CTA of its own: no line, no joining.  Where no
+// CTA can meet more than 1024 tokens, or 2048 and there are heads to fill the GPU (one
+// token a sequence, 4 bits, 8 heads of 128, us on the line / directly: 4 sequences of up
+// to 700 tokens 10.1 / 7.3, 256 of up to 900 59 / 50; of 300 to 1900 tokens 16
+// sequences 15.8 / 17.4, 64 of them 30.1 / 29.1; of 1000 to 4000, 16: 24 / 33).
+static bool attn_direct(const KvAttnArgs &a, int columns) {
+    // the most tiles a CTA can meet: the table's, or the window's and the sinks'
+    const int64_t room = a.max_pages << a.cache.log2_page;
+    int64_t tiles = (room + kTile - 1) / kTile;
+    if (a.window) {
+        const int64_t span = static_cast<int64_t>(a.window) + columns / a.group + 1;
+        const int64_t sinks = a.sinks < room ? a.sinks : room;
+        const int64_t few = span / kTile + 2 + (sinks + kTile - 1) / kTile;
+        tiles = few < tiles ? few : tiles;
+    }
+    return tiles <= 32 || (tiles <= 64 && 3 * a.heads >= 2 * static_cast<int64_t>(a.grid));
+}
+
 template <int D, int BITS, int NT>
-static int attn_launch(const KvAttnArgs &a, cudaStream_t st) {
+static int attn_launch(KvAttnArgs &a, cudaStream_t st) {
     using S = AttnShape<D, BITS, NT>;
+    a.direct = attn_direct(a, S::NQ);
     static std::atomic<int> attr_done[kMaxDevices];
     const int dev = current_device_index();
     if (dev < 0 || dev >= kMaxDevices) return RN_ERR_DEVICE;
@@ -870,8 +906,9 @@ static int attn_launch(const KvAttnArgs &a, cudaStream_t st) {
         }
         attr_done[dev].store(1, std::memory_order_release);
     }
-    const int rc = launch_pdl(kernel, dim3(static_cast<unsigned>(a.grid)), dim3(kAttnThreads), S::kSmem, st, a);
-    if (rc != RN_OK) return rc;
+    const unsigned ctas = static_cast<unsigned>(a.direct ? a.heads : a.grid);
+    const int rc = launch_pdl(kernel, dim3(ctas), dim3(kAttnThreads), S::kSmem, st, a);
+    if (rc != RN_OK || a.direct) return rc;
     return join_launch<D, typename S::L>(a, st);
 }
 

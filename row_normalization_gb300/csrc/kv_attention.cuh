@@ -35,6 +35,7 @@ struct KvAttnArgs {
     int64_t q_tiles;   // query tiles of a sequence
     int64_t heads;     // (query tile, kv head)s in all
     int grid;          // CTAs of the attention kernel
+    bool direct;       // one for each (query tile, kv head) instead
 };
 
 // A (query tile, head) cut into pieces, with all the joining kernel needs of it; noted
@@ -233,7 +234,15 @@ __device__ __forceinline__ Line find_unit(const KvAttnArgs &a, bool publish, int
     return line;
 }
 
-// Zeros for the rows of items that see no token, shared out over the CTAs.
+// Zeros for the rows of an item that sees no token, of one kv head.
+template <int D, class L, int THREADS>
+__device__ __forceinline__ void store_zeros(const KvAttnArgs &a, const Item<L> &it, int head) {
+    for (int idx = threadIdx.x; idx < it.ncols * (D / 4); idx += THREADS)
+        store_result<D>(a, it, head * a.group, idx / (D / 4), idx % (D / 4) * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f),
+                        0.0f, 0.0f);
+}
+
+// The same of every such item, shared out over the CTAs.
 template <int D, class L, int THREADS>
 __device__ __forceinline__ void store_empty(const KvAttnArgs &a) {
     const int64_t items = a.B * a.q_tiles;
@@ -242,12 +251,7 @@ __device__ __forceinline__ void store_empty(const KvAttnArgs &a) {
         if (it.n > 0) continue;
         if (a.heads <= a.grid)
             for (int h = threadIdx.x; h < a.cache.Hkv; h += THREADS) a.cuts[i * a.cache.Hkv + h].pieces = 0;
-        const int quads = it.ncols * (D / 4);
-        for (int idx = threadIdx.x; idx < quads * a.cache.Hkv; idx += THREADS) {
-            const int head = idx / quads, in = idx - head * quads;
-            store_result<D>(a, it, head * a.group, in / (D / 4), in % (D / 4) * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f),
-                            0.0f, 0.0f);
-        }
+        for (int head = 0; head < a.cache.Hkv; ++head) store_zeros<D, L, THREADS>(a, it, head);
     }
 }
 

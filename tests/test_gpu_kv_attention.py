@@ -42,6 +42,15 @@ from tests.gpu_util import require_gpu
 pytestmark = pytest.mark.gpu
 
 EPS = torch.finfo(torch.bfloat16).eps / 2
+EXTRA_TOKENS = 0  # room in the page tables behind the longest sequence
+
+
+@pytest.fixture(params=["direct", "line"])
+def both_layouts(request, monkeypatch):
+    """Short page tables give every head a CTA of its own; longer ones (here by entries
+    that are no pages) the line of units and the joining kernel."""
+    monkeypatch.setattr("tests.test_gpu_kv_attention.EXTRA_TOKENS",
+                        2560 if request.param == "line" else 0)
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -61,7 +70,7 @@ def filled(bits, Hkv, D, P, lens, seed, spread=1.0, spare=2):
     need = [-(-n // P) for n in lens]
     pages = sum(need) + spare
     order = torch.randperm(pages, generator=g)
-    table = torch.full((len(lens), max(need + [1]) + 1), -1, dtype=torch.int32)
+    table = torch.full((len(lens), max(need + [1]) + 1 + EXTRA_TOKENS // P), -1, dtype=torch.int32)
     ref = kv_ref.Cache(pages, Hkv, D, P, bits)
     at = 0
     for b, n in enumerate(lens):
@@ -140,6 +149,7 @@ LAYOUTS = [(4, 1, 64, 16), (6, 2, 128, 32), (8, 8, 64, 64), (32, 8, 128, 64), (5
 
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("Hq,Hkv,D,P", LAYOUTS)
+@pytest.mark.usefixtures("both_layouts")
 def test_one_token_ragged_lengths(bits, Hq, Hkv, D, P):
     lens = [1, 2, 15, 16, 17, 31, 32, 33, 64, 127, 130, 257]
     ref, table = filled(bits, Hkv, D, P, lens, seed=D + P)
@@ -152,6 +162,7 @@ def test_one_token_ragged_lengths(bits, Hq, Hkv, D, P):
 
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("Hq,Hkv,D,P", LAYOUTS)
+@pytest.mark.usefixtures("both_layouts")
 def test_several_queries_a_sequence(bits, Hq, Hkv, D, P):
     lens, n_q = [5, 40, 33, 100, 64, 7], [5, 3, 0, 17, 1, 2]
     ref, table = filled(bits, Hkv, D, P, lens, seed=D + P + 1)
@@ -165,6 +176,7 @@ def test_several_queries_a_sequence(bits, Hq, Hkv, D, P):
                                           (10 ** 6, 2)])
 @pytest.mark.parametrize("Hq,Hkv,D,P,bits", [(8, 2, 128, 16, 4), (4, 4, 64, 64, 8),
                                              (12, 1, 256, 32, 4)])
+@pytest.mark.usefixtures("both_layouts")
 def test_window_and_sinks(window, sinks, Hq, Hkv, D, P, bits):
     lens, n_q = [1, 20, 90, 200, 333], [1, 7, 1, 30, 2]
     ref, table = filled(bits, Hkv, D, P, lens, seed=window + sinks)
@@ -175,6 +187,7 @@ def test_window_and_sinks(window, sinks, Hq, Hkv, D, P, bits):
 
 
 @pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.usefixtures("both_layouts")
 def test_tokens_behind_the_window_are_never_used(bits):
     """Their pages hold NaN scales or are gone from the table: nothing changes."""
     Hq, Hkv, D, P, window, sinks = 8, 2, 128, 16, 50, 3
@@ -195,6 +208,7 @@ def test_tokens_behind_the_window_are_never_used(bits):
     assert binding.device_status() == 0
 
 
+@pytest.mark.usefixtures("both_layouts")
 def test_rows_that_see_nothing():
     """More queries than cached tokens, and an empty cache: 0 and -inf."""
     Hq, Hkv, D, P = 4, 2, 128, 16
@@ -210,6 +224,7 @@ def test_rows_that_see_nothing():
     assert (one == 0).all() and torch.isneginf(l1).all()
 
 
+@pytest.mark.usefixtures("both_layouts")
 def test_rows_outside_the_sequences_keep_their_content():
     Hq, Hkv, D, P = 8, 2, 64, 32
     lens = [50, 7]
@@ -228,6 +243,7 @@ def test_rows_outside_the_sequences_keep_their_content():
     check(out, lse, q, ref, table, lens, cu, D ** -0.5)
 
 
+@pytest.mark.usefixtures("both_layouts")
 def test_packed_rows_and_strides():
     """The packed QKV tensor and a view with a wider row give the same bits."""
     Hq, Hkv, D, P = 8, 2, 128, 32
@@ -252,6 +268,7 @@ def test_packed_rows_and_strides():
                                                (1.5, 30.0, None), (1.5, 1.0, 0.0), (1.5, 1.0, -0.2),
                                                (0.0, 1.0, None)])
 @pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.usefixtures("both_layouts")
 def test_sizes_of_queries_and_values(size, spread, scale, bits):
     """One-hot and flat softmaxes, queries far outside fp16, values whose scales
     span fp16's range, zero and negative softmax scales."""
@@ -267,6 +284,7 @@ def test_sizes_of_queries_and_values(size, spread, scale, bits):
     check(out, lse, q, ref, table, lens, cu, D ** -0.5 if scale is None else scale)
 
 
+@pytest.mark.usefixtures("both_layouts")
 def test_nan_stays_where_the_formula_has_it():
     Hq, Hkv, D, P = 8, 2, 128, 16
     lens, n_q = [60, 60], [3, 1]
@@ -291,6 +309,7 @@ def test_nan_stays_where_the_formula_has_it():
     assert torch.equal(torch.isnan(lse), want.all(-1))
 
 
+@pytest.mark.usefixtures("both_layouts")
 def test_bad_pages_and_lengths_are_zeros_and_reported():
     Hq, Hkv, D, P = 4, 2, 64, 16
     lens, n_q = [70, 30], [2, 1]
@@ -490,11 +509,36 @@ def test_chunk_over_a_long_context(Hq, Hkv, D, bits, n_q):
     check(out, lse, q, ref, table, lens, cu, D ** -0.5)
 
 
+@pytest.mark.parametrize("width", [0, 1, 70])
+def test_short_and_long_tables_agree_with_the_formula(width):
+    """The table's width decides between a CTA for each head and the line of units; rows
+    that see nothing, a bad length and bad pages are the same on both."""
+    Hq, Hkv, D, P = 8, 2, 128, 32
+    lens, n_q = [0, 5, 90, 200, 31], [1, 3, 0, 2, 1]
+    ref, table = filled(4, Hkv, D, P, lens, seed=61)
+    table = torch.cat((table, torch.full((5, 100 * width), -1, dtype=torch.int32)), dim=1)
+    q = queries(sum(n_q) + 1, Hq, D, seed=61)
+    keep = torch.full((sum(n_q) + 1, Hq, D), 1.5, dtype=torch.bfloat16, device="cuda")
+    out, lse, cu = attend(ref, table, lens, q, n_q, Hq, out=keep)
+    check(out, lse, q, ref, table, lens, cu, D ** -0.5)
+    assert (out[0] == 0).all() and (out[-1] == 1.5).all()
+    assert binding.device_status() == 0
+    table[3, 1] = -1
+    out, lse, cu = attend(ref, table, lens, q, n_q, Hq)
+    assert binding.device_status() == binding.RN_STATUS_BAD_INDEX
+    check(out, lse, q, ref, table, lens, cu, D ** -0.5)
+    if width == 0:
+        binding.kv_attention_fwd(q[:5].cuda(), to_gpu(ref), table.cuda(),
+                                 torch.tensor([0, 5, 90, 40000, 31], dtype=torch.int32).cuda(), Hq)
+        assert binding.device_status() == binding.RN_STATUS_BAD_INDEX
+
+
 def test_more_heads_than_ctas_of_every_length():
     """Notes by CTA instead of by head, pieces of every kind."""
     Hq, Hkv, D, P = 40, 20, 64, 16
     lens = [(37 * i) % 400 for i in range(40)]
     ref, table = filled(8, Hkv, D, P, lens, seed=5)
+    table = torch.cat((table, torch.full((40, 200), -1, dtype=torch.int32)), dim=1)
     q = queries(len(lens), Hq, D, seed=5)
     ws = binding.kv_attention_workspace(to_gpu(ref), len(lens), Hq)
     ws.fill_(0xFF)
