@@ -45,20 +45,22 @@ namespace rn {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kTile = 32;          // tokens a warp takes at once
 constexpr float kSlack = 6.0f;       // powers of two a weight may grow before a rescale
 // Units without work in front of each (query tile, head): its queries, first page and
 // copies, and the joining of its warps.  64 ragged sequences of 8 heads (540k tokens):
 // 175 us with none, 158 with 8, 128 with 16, 132 with 32; 4 long ones 124-126 throughout.
-constexpr int kLead = 16;
-constexpr int kMinTiles = kAttnWarps;  // a CTA's run is no shorter: one tile a warp
+constexpr int kLead = 16 * 32;  // in tokens
+constexpr int kMinTokens = 32 * kAttnWarps;  // a CTA's run is no shorter
 
 // Shapes of an instantiation: NT * 8 columns (queries of the tile times heads).
 template <int D, int BITS, int NT>
 struct AttnShape {
     using F = KvFormat<D, BITS>;
     static constexpr int NQ = 8 * NT;
-    using L = LineShape<NQ, kTile, kLead, kMinTiles>;
+    // tokens a warp takes at once: 16 where 32 would leave room for one CTA an SM (17
+    // sequences, drafts of 3 to 5 tokens, heads of 256 in 8 bits: 47 against 57 us)
+    static constexpr int kTile = D == 256 && BITS == 8 ? 16 : 32;
+    using L = LineShape<NQ, kTile, kLead / kTile, kMinTokens / kTile>;
     static constexpr int MT = D / 16;                 // 16-row tiles of the value product
     static constexpr int kScaleRow = 2 * F::kGroups;  // bytes of a row's scales
     static constexpr int kCodesBytes = kTile * F::kRow;
@@ -283,7 +285,7 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
         if (k < k1) {
             const int t0 = it.token(k);
             p.lo = table[t0 >> log2_page];
-            if (log2_page == 4 && t0 + 16 < it.hi) p.hi = table[(t0 >> 4) + 1];
+            if (S::kTile == 32 && log2_page == 4 && t0 + 16 < it.hi) p.hi = table[(t0 >> 4) + 1];
         }
         return p;
     };
@@ -301,7 +303,7 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
         const uint8_t *src = codes0 + static_cast<uint64_t>(page) * page_codes + (off - FROM) * F::kRow;
         const uint8_t *vsrc = src + page_codes / 2;
 #pragma unroll
-        for (int i = CPR * FROM / kTile; i < CPR * TO / kTile; ++i) {
+        for (int i = CPR * FROM / 32; i < CPR * TO / 32; ++i) {
             const uint32_t d = dst + 512 * i + (copy_off ^ swizzle_step<F::kRow>(i));
             cp_async16(d, src + i * 512, bytes);
             cp_async16(d + S::kCodesBytes, vsrc + i * 512, bytes);
@@ -309,13 +311,13 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
         const uint8_t *ssrc = scales0 + static_cast<uint64_t>(page) * page_scales + (off - FROM) * S::kScaleRow;
         const uint32_t d = dst + 2 * S::kCodesBytes + lane * 16;
         if constexpr (SCH == 32) {
-            if (FROM == 0 ? (TO == kTile || lane < 16) : lane >= 16) {
+            if (FROM == 0 ? (TO == S::kTile || lane < 16) : lane >= 16) {
                 cp_async16(d, ssrc, bytes);
                 cp_async16(d + S::kScalesBytes, ssrc + page_scales / 2, bytes);
             }
         } else {
             const int c = lane % SCH;
-            if (lane < 2 * SCH && (FROM == 0 ? (TO == kTile || c < SCH / 2) : c >= SCH / 2))
+            if (lane < 2 * SCH && (FROM == 0 ? (TO == S::kTile || c < SCH / 2) : c >= SCH / 2))
                 cp_async16(d, ssrc, bytes);
         }
     };
@@ -328,7 +330,10 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
         const int t0 = it.token(k);
         const uint32_t dst = ring_addr + stage * S::kStage;
         const bool ok = static_cast<uint32_t>(p.lo) < static_cast<uint32_t>(a.cache.num_pages);
-        if (log2_page > 4) {
+        if constexpr (S::kTile == 16) {
+            if (!ok && lane == 0) atomicOr(&g_kv_attention_status, RN_STATUS_BAD_INDEX);
+            copy_rows(I0(), I16(), dst, ok ? p.lo : 0, ok ? t0 & ((1 << log2_page) - 1) : 0, ok ? 16 : 0);
+        } else if (log2_page > 4) {
             if (!ok && lane == 0) atomicOr(&g_kv_attention_status, RN_STATUS_BAD_INDEX);
             copy_rows(I0(), I32(), dst, ok ? p.lo : 0, ok ? t0 & ((1 << log2_page) - 1) : 0, ok ? 16 : 0);
         } else {
@@ -445,16 +450,16 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
         {
             constexpr int W = NG / 2;
             uint32_t v[W];
-            lds_words<W>(v, sbase + S::kScalesBytes + lane * S::kScaleRow);
+            lds_words<W>(v, sbase + S::kScalesBytes + lane % S::kTile * S::kScaleRow);
             uint32_t mx = v[0];
 #pragma unroll
             for (int i = 1; i < W; ++i) mx = __vmaxs2(mx, v[i]);
             vtop = max(static_cast<int>(static_cast<int16_t>(mx & 0xFFFFu)),
                        static_cast<int>(static_cast<int16_t>(mx >> 16)));
-            if (vtop > 0x7BFF || (MASKED && !seen_token(t0 + lane))) vtop = -1;
+            if (vtop > 0x7BFF || (MASKED && !seen_token(t0 + lane % S::kTile))) vtop = -1;
         }
 #pragma unroll 1
-        for (int m0 = 0; m0 < 2; m0 += S::kStep) {
+        for (int m0 = 0; m0 < S::kTile / 16; m0 += S::kStep) {
         // -- logits (before the factor): rows are tokens, columns queries --------------------------
         float x[S::kStep][NT][4];
 #pragma unroll
@@ -694,8 +699,8 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
         stage = stage + 1 == S::kStages ? 0 : stage + 1;
         const int t0 = it.token(k);
 
-        const bool masked = t0 + kTile - 1 > it.lo_pos ||
-                            (a.window && t0 <= it.hi - 1 - a.window && t0 + kTile > a.sinks);
+        const bool masked = t0 + S::kTile - 1 > it.lo_pos ||
+                            (a.window && t0 <= it.hi - 1 - a.window && t0 + S::kTile > a.sinks);
         if (masked)
             do_tile(std::true_type(), base, t0);
         else
@@ -804,8 +809,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, BITS, NT>::kCtas)
             v0 = static_cast<int>(in - static_cast<int64_t>(head) * units);
             const int64_t left = u1 - u;
             v1 = units - v0 <= left ? units : v0 + static_cast<int>(left);
-            k0 = v0 > kLead ? v0 - kLead : 0;
-            k1 = v1 - kLead;
+            k0 = v0 > L::LEAD ? v0 - L::LEAD : 0;
+            k1 = v1 - L::LEAD;
             if (k1 - k0 != it.n)
                 part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1)) * S::kSlot;
         }
@@ -879,13 +884,13 @@ static AttnPlan attn_plan(int sm_count, int format, int64_t B, int Hq, int Hkv, 
 // to 700 tokens 10.1 / 7.3, 256 of up to 900 59 / 50; of 300 to 1900 tokens 16
 // sequences 15.8 / 17.4, 64 of them 30.1 / 29.1; of 1000 to 4000, 16: 24 / 33).
 static bool attn_direct(const KvAttnArgs &a, int columns) {
-    // the most tiles a CTA can meet: the table's, or the window's and the sinks'
+    // the most tokens a CTA can meet, in 32s: the table's, or the window's and the sinks'
     const int64_t room = a.max_pages << a.cache.log2_page;
-    int64_t tiles = (room + kTile - 1) / kTile;
+    int64_t tiles = (room + 31) / 32;
     if (a.window) {
         const int64_t span = static_cast<int64_t>(a.window) + columns / a.group + 1;
         const int64_t sinks = a.sinks < room ? a.sinks : room;
-        const int64_t few = span / kTile + 2 + (sinks + kTile - 1) / kTile;
+        const int64_t few = span / 32 + 2 + (sinks + 31) / 32;
         tiles = few < tiles ? few : tiles;
     }
     return tiles <= 32 || (tiles <= 64 && 3 * a.heads >= 2 * static_cast<int64_t>(a.grid));
