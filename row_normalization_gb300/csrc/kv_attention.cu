@@ -884,16 +884,8 @@ static AttnPlan attn_plan(int sm_count, int format, int64_t B, int Hq, int Hkv, 
 // to 700 tokens 10.1 / 7.3, 256 of up to 900 59 / 50; of 300 to 1900 tokens 16
 // sequences 15.8 / 17.4, 64 of them 30.1 / 29.1; of 1000 to 4000, 16: 24 / 33).
 static bool attn_direct(const KvAttnArgs &a, int columns) {
-    // the most tokens a CTA can meet, in 32s: the table's, or the window's and the sinks'
-    const int64_t room = a.max_pages << a.cache.log2_page;
-    int64_t tiles = (room + 31) / 32;
-    if (a.window) {
-        const int64_t span = static_cast<int64_t>(a.window) + columns / a.group + 1;
-        const int64_t sinks = a.sinks < room ? a.sinks : room;
-        const int64_t few = span / 32 + 2 + (sinks + 31) / 32;
-        tiles = few < tiles ? few : tiles;
-    }
-    return tiles <= 32 || (tiles <= 64 && 3 * a.heads >= 2 * static_cast<int64_t>(a.grid));
+    const int64_t most = attn_most_tokens(a, columns);
+    return most <= 1024 || (most <= 2048 && 3 * a.heads >= 2 * static_cast<int64_t>(a.grid));
 }
 
 template <int D, int BITS, int NT>

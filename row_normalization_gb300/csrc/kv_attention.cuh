@@ -400,8 +400,17 @@ struct AttnPlan {
     int64_t bytes;
 };
 
+// The most tokens a query tile of `columns` can see: the table's, or the window's (and
+// the ends of tiles) and the sinks'.
+inline int64_t attn_most_tokens(const KvAttnArgs &a, int columns) {
+    const int64_t room = a.max_pages << a.cache.log2_page;
+    if (!a.window) return room;
+    const int64_t few = static_cast<int64_t>(a.window) + columns / a.group + 64 + (a.sinks < room ? a.sinks : room);
+    return few < room ? few : room;
+}
+
 // kv_attention_wide.cu: 128 columns at a time.
 AttnPlan wide_plan(int sm_count, int64_t B, int group, int D, int64_t max_q_len);
-int wide_launch(int D, int format, const KvAttnArgs &a, cudaStream_t st);
+int wide_launch(int D, int format, KvAttnArgs &a, cudaStream_t st);
 
 }  // namespace rn

@@ -489,10 +489,24 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
 
     pdl_trigger();
     pdl_wait();
-    const Line line = find_unit<L, S::kThreads>(a, blockIdx.x == 0, sh.scratch);
-    store_empty<D, L, S::kThreads>(a);
-    const Cut<L> cut(line.units, a.grid);
-    if (line.units == 0 || blockIdx.x >= cut.ctas) return;
+    Line line = {};
+    Cut<L> cut(1, 1);
+    int own_head = 0;  // of the CTA's only (query tile, head), where it has just one
+    if (a.direct) {
+        line.item = blockIdx.x / static_cast<uint32_t>(a.cache.Hkv);
+        own_head = static_cast<int>(blockIdx.x - static_cast<uint32_t>(line.item) * static_cast<uint32_t>(a.cache.Hkv));
+        const Item<L> it = make_item<L>(a, line.item);
+        if (it.bad && own_head == 0 && threadIdx.x == 0) atomicOr(&g_kv_attention_status, RN_STATUS_BAD_INDEX);
+        if (it.n == 0) {
+            store_zeros<D, L, S::kThreads>(a, it, own_head);
+            return;
+        }
+    } else {
+        line = find_unit<L, S::kThreads>(a, blockIdx.x == 0, sh.scratch);
+        store_empty<D, L, S::kThreads>(a);
+        cut = Cut<L>(line.units, a.grid);
+        if (line.units == 0 || blockIdx.x >= cut.ctas) return;
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.q_full[i], 128);
@@ -519,7 +533,7 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
     const uint32_t tmem = sh.tmem;
 
     // Every role walks the CTA's runs in the same order; n counts its tiles over all.
-    const int64_t u0 = cut.start(blockIdx.x), u1 = cut.start(blockIdx.x + 1);
+    const int64_t u0 = a.direct ? 0 : cut.start(blockIdx.x), u1 = a.direct ? 1 : cut.start(blockIdx.x + 1);
     const auto each_run = [&](auto &&body) {
         int64_t item = line.item, before = line.before, u = u0;
         while (u < u1) {
@@ -528,20 +542,24 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
                 ++item;
                 continue;
             }
-            const int units = it.units();
-            const int64_t in = u - before * a.cache.Hkv;
-            const int head = static_cast<int>(quotient(in, units));
-            const int v0 = static_cast<int>(in - static_cast<int64_t>(head) * units);
-            const int64_t left = u1 - u;
-            const int v1 = units - v0 <= left ? units : v0 + static_cast<int>(left);
-            const int k0 = v0 > L::LEAD ? v0 - L::LEAD : 0, k1 = v1 - L::LEAD;
+            int units = 1, head = own_head, v0 = 0, v1 = 1, k0 = 0, k1 = it.n;
+            if (!a.direct) {
+                units = it.units();
+                const int64_t in = u - before * a.cache.Hkv;
+                head = static_cast<int>(quotient(in, units));
+                v0 = static_cast<int>(in - static_cast<int64_t>(head) * units);
+                const int64_t left = u1 - u;
+                v1 = units - v0 <= left ? units : v0 + static_cast<int>(left);
+                k0 = v0 > L::LEAD ? v0 - L::LEAD : 0;
+                k1 = v1 - L::LEAD;
+            }
             if (k1 > k0) {
                 float *part = nullptr;
                 if (k1 - k0 != it.n)
                     part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1)) * S::kSlot;
                 if (!body(it, head, k0, k1, part)) return;
             }
-            if (threadIdx.x == 0) note_piece(a, cut, u - v0, v0, v1, units, it, item, head);
+            if (!a.direct && threadIdx.x == 0) note_piece(a, cut, u - v0, v0, v1, units, it, item, head);
             u += v1 - v0;
             if (v1 == units && head == a.cache.Hkv - 1) {
                 before += units;
@@ -876,8 +894,16 @@ int kv_attention_wide_status(unsigned int *out, int clear) {
 // ---- host --------------------------------------------------------------------------------------
 
 template <int D, int BITS, int QT>
-static int wide_launch_of(const KvAttnArgs &a, cudaStream_t st) {
+static int wide_launch_of(KvAttnArgs &a, cudaStream_t st) {
     using S = WideShape<D, BITS, QT>;
+    // A CTA for each (query tile, head), without line and joining, where there are few
+    // tiles of tokens, or heads to fill the GPU with them, or so many that the last round
+    // does not matter (chunks of a quarter of their context, 8 heads of 128, us on the
+    // line / directly: contexts of 600, 1 sequence 32 / 29, 32 of them 163 / 141; 2000, 1
+    // sequence 50 / 56, 8 of them 224 / 208; 3000, 16 of them 718 / 679).
+    const int64_t most = attn_most_tokens(a, S::NQ);
+    a.direct = most <= 640 || (most <= 2048 && 5 * a.heads >= 3 * static_cast<int64_t>(a.grid)) ||
+               a.heads >= 4 * static_cast<int64_t>(a.grid);
     static std::atomic<int> attr_done[kMaxDevices];
     const int dev = current_device_index();
     if (dev < 0 || dev >= kMaxDevices) return RN_ERR_DEVICE;
@@ -889,8 +915,9 @@ static int wide_launch_of(const KvAttnArgs &a, cudaStream_t st) {
         }
         attr_done[dev].store(1, std::memory_order_release);
     }
-    const int rc = launch_pdl(kernel, dim3(static_cast<unsigned>(a.grid)), dim3(S::kThreads), S::kSmem, st, a);
-    if (rc != RN_OK) return rc;
+    const unsigned ctas = static_cast<unsigned>(a.direct ? a.heads : a.grid);
+    const int rc = launch_pdl(kernel, dim3(ctas), dim3(S::kThreads), S::kSmem, st, a);
+    if (rc != RN_OK || a.direct) return rc;
     return join_launch<D, typename S::L>(a, st);
 }
 
@@ -906,7 +933,7 @@ AttnPlan wide_plan(int sm_count, int64_t B, int group, int D, int64_t max_q_len)
     return p;
 }
 
-int wide_launch(int D, int format, const KvAttnArgs &a, cudaStream_t st) {
+int wide_launch(int D, int format, KvAttnArgs &a, cudaStream_t st) {
     const int tiles = query_tiles(D, a.max_q_len * a.group);
     return kv_dispatch(D, format, [&](auto d, auto bits) {
         if constexpr (d.value <= 128)

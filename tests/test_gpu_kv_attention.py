@@ -355,6 +355,7 @@ CHUNKS = [(4, 1, 64, 16), (8, 2, 128, 16), (6, 2, 128, 64), (3, 1, 256, 32), (70
 
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("Hq,Hkv,D,P", CHUNKS)
+@pytest.mark.usefixtures("both_layouts")
 def test_chunks_of_ragged_length(bits, Hq, Hkv, D, P):
     """Tiles of 128 columns that are full, partly full and empty, tiles of tokens that
     end anywhere, beside sequences of one query and of none."""
@@ -370,6 +371,7 @@ def test_chunks_of_ragged_length(bits, Hq, Hkv, D, P):
 
 @pytest.mark.parametrize("window,sinks", [(1, 0), (40, 3), (129, 130), (300, 1)])
 @pytest.mark.parametrize("Hq,Hkv,D,P,bits", [(8, 2, 128, 16, 4), (4, 1, 64, 32, 8), (4, 2, 256, 64, 4)])
+@pytest.mark.usefixtures("both_layouts")
 def test_chunks_with_window_and_sinks(window, sinks, Hq, Hkv, D, P, bits):
     lens, n_q = [500, 70], [60, 70]
     ref, table = filled(bits, Hkv, D, P, lens, seed=window)
@@ -386,6 +388,7 @@ def test_chunks_with_window_and_sinks(window, sinks, Hq, Hkv, D, P, bits):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.usefixtures("both_layouts")
 def test_chunk_rows_that_see_nothing_and_rows_outside(D):
     Hq, Hkv, P = 4, 1, 16
     lens, n_q = [0, 25, 40], [40, 60, 40]
@@ -401,6 +404,7 @@ def test_chunk_rows_that_see_nothing_and_rows_outside(D):
 
 
 @pytest.mark.parametrize("D,bits", [(64, 4), (128, 8), (256, 4), (256, 8)])
+@pytest.mark.usefixtures("both_layouts")
 def test_chunk_nan_and_infinite_queries_stay_in_their_place(D, bits):
     Hq, Hkv, P, n, L = 4, 2, 16, 50, 120
     ref, table = filled(bits, Hkv, D, P, [L], seed=17)
@@ -423,6 +427,7 @@ def test_chunk_nan_and_infinite_queries_stay_in_their_place(D, bits):
 
 
 @pytest.mark.parametrize("D,bits", [(64, 8), (128, 4), (256, 8)])
+@pytest.mark.usefixtures("both_layouts")
 def test_chunk_scales_above_255(D, bits):
     """Values (and, with small queries, keys) far above the rest: restored at 2^-8."""
     Hq, Hkv, P = 4, 1, 32
@@ -440,6 +445,7 @@ def test_chunk_scales_above_255(D, bits):
     check(out, lse, q, ref, table, lens, cu, D ** -0.5)
 
 
+@pytest.mark.usefixtures("both_layouts")
 def test_chunk_bad_pages_are_zeros_and_reported():
     Hq, Hkv, D, P = 8, 2, 128, 16
     lens, n_q = [200], [30]
