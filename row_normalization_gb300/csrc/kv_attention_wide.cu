@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
                                       (static_cast<int64_t>(head) * a.group + f % a.group) * D;
                 uint32_t top = 0u;
                 if (live) {
-#pragma unroll 4
+#pragma unroll 8
                     for (int i = 0; i < D / 8; ++i) {
                         const uint4 v = ld_ro16(src + 8 * i);
                         top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
                                            a.scale_log2);
                 factor = fmaxf(ldexpf(fabsf(a.scale_log2), e - 140), 0x1p-126f);
                 if (!finite) factor = __uint_as_float(0x7FC00000u);
-#pragma unroll 2
+#pragma unroll 4
                 for (int i = 0; i < D / 8; ++i) {
                     const uint4 v = live && finite ? ld_ro16(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
                     const float x[8] = {bf_lo(v.x) * up, bf_hi(v.x) * up, bf_lo(v.y) * up, bf_hi(v.y) * up,
@@ -746,30 +746,37 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
             // -- the run's sums: finished, or a piece ---------------------------------------
             if (!wide_wait_warp(sh, &sh.pv_done[S::buf(qt, c - 1)], S::phase(c - 1))) return false;
             tc_fence_after();
-            const float top = m == -INFINITY ? -INFINITY : ref;
+            const int64_t out_row = (it.row0 + f / a.group) * a.Hq + static_cast<int64_t>(head) * a.group + f % a.group;
+            // (a piece carries the 2^-24 that the other kernel's sums have)
+            const float scale = part ? 0x1p-24f : (l == 0.0f ? 0.0f : 1.0f / l);
 #pragma unroll 1
             for (int i = 0; i < D / 32; ++i) {
                 uint32_t x[32];
                 tmem_load32(x, obase + 32 * i);
                 tmem_wait_load(x);
-                // store_result undoes 2^-24, which the other kernel's sums carry
-                const float unit = nan_mask >> i & 1u ? __uint_as_float(0x7FC00000u) : 0x1p-24f;
-                if (live) {
+                const float unit = nan_mask >> i & 1u ? __uint_as_float(0x7FC00000u) : scale;
+                if (!live) continue;
+                float y[32];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 v = make_float4(__uint_as_float(x[j]) * unit, __uint_as_float(x[j + 1]) * unit,
-                                                     __uint_as_float(x[j + 2]) * unit, __uint_as_float(x[j + 3]) * unit);
-                        const int d = 32 * i + j;
-                        if (part)
-                            *reinterpret_cast<float4 *>(part + col * D + d) = v;
-                        else
-                            store_result<D>(a, it, head * a.group, col, d, v, ref, l);
-                    }
+                for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(x[j]) * unit;
+                if (part) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        *reinterpret_cast<float4 *>(part + col * D + 32 * i + j) =
+                            make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8)
+                        st16(a.out + out_row * D + 32 * i + j,
+                             make_uint4(pack_bf2(y[j], y[j + 1]), pack_bf2(y[j + 2], y[j + 3]),
+                                        pack_bf2(y[j + 4], y[j + 5]), pack_bf2(y[j + 6], y[j + 7])));
                 }
             }
-            if (part && live) {
-                part[NQ * D + col] = top;
+            if (live && part) {
+                part[NQ * D + col] = m == -INFINITY ? -INFINITY : ref;
                 part[NQ * D + NQ + col] = l;
+            } else if (live && a.lse) {
+                a.lse[out_row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
             }
             tc_fence_before();  // O is read before the next run's products
             return true;
