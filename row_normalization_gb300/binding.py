@@ -679,6 +679,15 @@ def _kv_device(cache: KVCache) -> int:
     return dev
 
 
+def _held(stream, t: torch.Tensor) -> torch.Tensor:
+    """t, allocated here for a call on `stream`: its memory is not used again before
+    that stream is done with it, even where the caller drops t at once."""
+    if stream is not None:
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                        else torch.cuda.ExternalStream(int(stream), device=t.device))
+    return t
+
+
 def _kv_call(dev: int, name: str, *args, stream) -> None:
     """Calls a key/value cache entry point with the tensors' device current."""
     L = _lib if _lib is not None else load()
@@ -725,9 +734,9 @@ def kv_cache_read(cache: KVCache, page_table: torch.Tensor, cu_lens: torch.Tenso
     Hkv, D = cache.num_kv_heads, cache.head_dim
     n = total * Hkv * D
     if k is None:
-        k = torch.empty(total, Hkv, D, dtype=torch.bfloat16, device=cache.device)
+        k = _held(stream, torch.empty(total, Hkv, D, dtype=torch.bfloat16, device=cache.device))
     if v is None:
-        v = torch.empty(total, Hkv, D, dtype=torch.bfloat16, device=cache.device)
+        v = _held(stream, torch.empty(total, Hkv, D, dtype=torch.bfloat16, device=cache.device))
     _kv_call(dev, "kv_cache_read", cache.codes.data_ptr(), cache.scales.data_ptr(), cache.format,
              Hkv, D, cache.page_size, cache.num_pages, tp, B, width, cp, sp, total,
              _on(dev, k, "k", torch.bfloat16, n), _on(dev, v, "v", torch.bfloat16, n),
@@ -792,15 +801,11 @@ def kv_attention_fwd(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
     else:
         cp = None
     if out is None:
-        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=cache.device)
+        out = _held(stream, torch.empty(T, Hq, D, dtype=torch.bfloat16, device=cache.device))
     if lse is None:
-        lse = torch.empty(T, Hq, dtype=torch.float32, device=cache.device)
+        lse = _held(stream, torch.empty(T, Hq, dtype=torch.float32, device=cache.device))
     if workspace is None:
-        workspace = kv_attention_workspace(cache, B, Hq, max_q_len=max_q_len)
-        if stream is not None:  # freed while `stream` may still use it
-            workspace.record_stream(
-                stream if isinstance(stream, torch.cuda.Stream)
-                else torch.cuda.ExternalStream(int(stream), device=cache.device))
+        workspace = _held(stream, kv_attention_workspace(cache, B, Hq, max_q_len=max_q_len))
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     _kv_call(dev, "kv_attention_fwd", q.data_ptr(), q.stride(0) if T > 1 else Hq * D,

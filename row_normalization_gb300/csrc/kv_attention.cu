@@ -194,7 +194,8 @@ struct Query {
     __device__ __forceinline__ void load(const KvAttnArgs &a, const Item<L> &it, int head0, int col, int j) {
         uint32_t w[F::kGroups][4];
         uint32_t top = 0u;
-        const bool live = col < it.ncols;
+        // (a query that sees no token counts as zeros, whatever it holds)
+        const bool live = col < it.ncols && it.pos0 + (it.f0 + col) / a.group >= 0;
         const int f = it.f0 + (live ? col : 0);
         const uint16_t *src = a.q + (it.row0 + f / a.group) * a.q_stride +
                               static_cast<int64_t>(head0 + f % a.group) * D + 8 * j;
@@ -885,7 +886,8 @@ static AttnPlan attn_plan(int sm_count, int format, int64_t B, int Hq, int Hkv, 
 // sequences 15.8 / 17.4, 64 of them 30.1 / 29.1; of 1000 to 4000, 16: 24 / 33).
 static bool attn_direct(const KvAttnArgs &a, int columns) {
     const int64_t most = attn_most_tokens(a, columns);
-    return most <= 1024 || (most <= 2048 && 3 * a.heads >= 2 * static_cast<int64_t>(a.grid));
+    return attn_few_idle(a, columns) &&
+           (most <= 1024 || (most <= 2048 && 3 * a.heads >= 2 * static_cast<int64_t>(a.grid)));
 }
 
 template <int D, int BITS, int NT>

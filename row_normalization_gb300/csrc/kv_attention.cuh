@@ -101,13 +101,10 @@ __device__ __forceinline__ Item<L> make_item(const KvAttnArgs &a, int64_t item) 
     it.row0 = b;
     if (a.cu_q) {
         it.row0 = a.cu_q[b];
-        nq = a.cu_q[b + 1] - it.row0;
-        if (nq > 0 && (it.row0 < 0 || it.row0 + nq > a.T)) {
-            it.bad = true;
-            nq = 0;
-        }
+        const int64_t end = a.cu_q[b + 1];
+        it.bad = end > it.row0 && (it.row0 < 0 || end > a.T);
+        nq = end > it.row0 && !it.bad ? end - it.row0 : 0;  // (no difference of wild numbers)
     }
-    if (nq < 0) nq = 0;
     int64_t len = a.kv_lens[b];
     const int64_t room = a.max_pages << a.cache.log2_page;
     if (len > room) {
@@ -407,6 +404,13 @@ inline int64_t attn_most_tokens(const KvAttnArgs &a, int columns) {
     if (!a.window) return room;
     const int64_t few = static_cast<int64_t>(a.window) + columns / a.group + 64 + (a.sinks < room ? a.sinks : room);
     return few < room ? few : room;
+}
+
+// Whether the grid of a CTA for each (query tile, kv head) is mostly CTAs with work: the
+// queries there are make at least half of the query tiles that max_q_len allows for.
+inline bool attn_few_idle(const KvAttnArgs &a, int columns) {
+    const int64_t busy = (a.T * a.group / columns + a.B) * a.cache.Hkv;
+    return a.heads <= 2 * busy && a.heads <= INT32_MAX;
 }
 
 // kv_attention_wide.cu: 128 columns at a time.

@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
                 const uint16_t *src = a.q + (it.row0 + f / a.group) * a.q_stride +
                                       (static_cast<int64_t>(head) * a.group + f % a.group) * D;
                 uint32_t top = 0u;
-                if (live) {
+                if (pos >= 0) {  // (a query that sees no token counts as zeros)
 #pragma unroll 8
                     for (int i = 0; i < D / 8; ++i) {
                         const uint4 v = ld_ro16(src + 8 * i);
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
                 if (!finite) factor = __uint_as_float(0x7FC00000u);
 #pragma unroll 4
                 for (int i = 0; i < D / 8; ++i) {
-                    const uint4 v = live && finite ? ld_ro16(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 v = pos >= 0 && finite ? ld_ro16(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
                     const float x[8] = {bf_lo(v.x) * up, bf_hi(v.x) * up, bf_lo(v.y) * up, bf_hi(v.y) * up,
                                         bf_lo(v.z) * up, bf_hi(v.z) * up, bf_lo(v.w) * up, bf_hi(v.w) * up};
                     uint4 o;
@@ -909,8 +909,9 @@ static int wide_launch_of(KvAttnArgs &a, cudaStream_t st) {
     // line / directly: contexts of 600, 1 sequence 32 / 29, 32 of them 163 / 141; 2000, 1
     // sequence 50 / 56, 8 of them 224 / 208; 3000, 16 of them 718 / 679).
     const int64_t most = attn_most_tokens(a, S::NQ);
-    a.direct = most <= 640 || (most <= 2048 && 5 * a.heads >= 3 * static_cast<int64_t>(a.grid)) ||
-               a.heads >= 4 * static_cast<int64_t>(a.grid);
+    a.direct = attn_few_idle(a, S::NQ) &&
+               (most <= 640 || (most <= 2048 && 5 * a.heads >= 3 * static_cast<int64_t>(a.grid)) ||
+                a.heads >= 4 * static_cast<int64_t>(a.grid));
     static std::atomic<int> attr_done[kMaxDevices];
     const int dev = current_device_index();
     if (dev < 0 || dev >= kMaxDevices) return RN_ERR_DEVICE;

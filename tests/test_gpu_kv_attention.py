@@ -29,6 +29,7 @@ lse: the logit's error plus 2^-20 plus 2^-22 |lse|.
 """
 from __future__ import annotations
 
+import copy
 import math
 
 import pytest
@@ -650,6 +651,83 @@ def test_another_stream_without_a_workspace():
     out, lse = binding.kv_attention_fwd(*args, stream=st)
     st.synchronize()
     check(out.cpu(), lse.cpu(), q, ref, table, lens, [0, 1, 2], D ** -0.5)
+
+
+def test_results_dropped_at_once_are_not_reused_while_their_stream_writes():
+    Hq, D, lens = 8, 128, [700] * 3
+    ref, table = filled(4, 2, D, 64, lens, seed=1)
+    q, cache, t = queries(3, Hq, D, seed=1).cuda(), to_gpu(ref), table.cuda()
+    n = torch.tensor(lens, dtype=torch.int32).cuda()
+    ws = binding.kv_attention_workspace(cache, 3, Hq)
+    cu = torch.tensor([0, 700, 1400, 2100]).cuda()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)          # the calls below start later than what follows
+    binding.kv_attention_fwd(q, cache, t, n, Hq, workspace=ws, stream=side)
+    binding.kv_cache_read(cache, t, cu, 2100, stream=side.cuda_stream)
+    mine = [torch.full(shape, 7.0, dtype=dtype, device="cuda")
+            for shape, dtype in (((3, Hq, D), torch.bfloat16), ((3, Hq), torch.float32),
+                                 ((2100, 2, D), torch.bfloat16), ((2100, 2, D), torch.bfloat16))]
+    torch.cuda.synchronize()
+    assert all((x == 7).all() for x in mine)
+
+
+@pytest.mark.parametrize("n_q,len_", [(5, 3), (40, 25), (200, 130)])
+@pytest.mark.usefixtures("both_layouts")
+def test_nan_queries_that_see_nothing_are_zeros(n_q, len_):
+    Hq, Hkv, D = 8, 2, 128
+    ref, table = filled(8, Hkv, D, 32, [len_], seed=n_q)
+    q = queries(n_q, Hq, D, seed=n_q)
+    blind = n_q - len_
+    q[:blind] = float("nan")
+    q[blind - 1] = float("inf")
+    out, lse, cu = attend(ref, table, [len_], q, [n_q], Hq)
+    assert (out[:blind] == 0).all() and (lse[:blind] == -math.inf).all()
+    plain = q.clone()
+    plain[:blind] = 0
+    want, want_lse, _ = attend(ref, table, [len_], plain, [n_q], Hq)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_wild_row_offsets_are_no_queries():
+    """Offsets whose difference leaves 64 bits; they are looked at one by one."""
+    Hq, D = 4, 64
+    ref, table = filled(4, 1, D, 16, [20, 20], seed=2)
+    q, t = queries(4, Hq, D, seed=2).cuda(), table.cuda()
+    n = torch.tensor([20, 20], dtype=torch.int32).cuda()
+    for cu, bad in (([2 ** 62, -2 ** 63 + 1, -2 ** 63], False), ([2 ** 63 - 1, -2 ** 63, -2 ** 63 + 2], True),
+                    ([-2 ** 63, 2 ** 62, 2 ** 62 + 1], True), ([3, 5, 4], True), ([-1, 1, 1], True)):
+        for max_q_len in (2, 40):
+            out = torch.full((4, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+            lse = torch.full((4, Hq), 7.0, device="cuda")
+            binding.kv_attention_fwd(q, to_gpu(ref), t, n, Hq, cu_q=torch.tensor(cu).cuda(),
+                                     max_q_len=max_q_len, out=out, lse=lse)
+            assert (out == 7).all() and (lse == 7).all()
+            assert binding.device_status() == (binding.RN_STATUS_BAD_INDEX if bad else 0)
+
+
+def heads_of(ref, n):
+    """The cache's first n heads, for the plain form."""
+    few = copy.copy(ref)
+    few.vals, few.scales = ref.vals[:, :, :n], ref.scales[:, :, :n]
+    return few
+
+
+def test_more_query_tiles_and_heads_than_a_grid_holds():
+    """A million sequences that might have 8192 queries each, of which two have some."""
+    Hq = Hkv = D = 64
+    B, n_q = 2 ** 20, [130, 2]
+    ref, table = filled(4, Hkv, D, 256, [200, 40], seed=3)
+    q = queries(sum(n_q), Hq, D, seed=3)
+    t = torch.full((B, table.shape[1]), -1, dtype=torch.int32)
+    lens, cu = torch.zeros(B, dtype=torch.int32), torch.full((B + 1,), 130)
+    t[0], t[-1], lens[0], lens[-1], cu[0], cu[-1] = table[0], table[1], 200, 40, 0, 132
+    out, lse = binding.kv_attention_fwd(q.cuda(), to_gpu(ref), t.cuda(), lens.cuda(), Hq,
+                                        cu_q=cu.cuda(), max_q_len=8192)
+    check(out[:, :4].cpu(), lse[:, :4].cpu(), q[:, :4], heads_of(ref, 4), table, [200, 40],
+          [0, 130, 132], D ** -0.5)
+    assert binding.device_status() == 0
 
 
 def test_refusals_of_the_binding():
