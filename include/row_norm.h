@@ -600,9 +600,10 @@ int kv_cache_read(const uint8_t *codes, const rn_f16 *scales, int format, int Hk
  * B * Hq, max_q_len * Hq and max_pages * page_size < 2^31; scale finite,
  * window and sinks >= 0; scale * |q| and every logit below 2^100.
  * Arithmetic: a logit is an fp32 sum of exact products of query and key; a
- * softmax weight and its product with a value scale (more than 64 queries times
- * heads of a group: the weight and the value) are each rounded to fp16, 2^-11
- * relative, before fp32 sums.  A NaN reaches the outputs whose formula holds it
+ * softmax weight and its product with a value scale (where max_q_len * Hq / Hkv is
+ * above 64: the weight and the value, or as before for sequences of few queries
+ * that such a call launches apart) are each rounded to fp16, 2^-11 relative, before
+ * fp32 sums.  A NaN reaches the outputs whose formula holds it
  * and no others.  The results do not depend on timing: the same call gives the
  * same bits.  Errors as kv_cache_write; a workspace that is too small is
  * RN_ERR_ARG. */

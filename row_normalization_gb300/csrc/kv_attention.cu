@@ -30,8 +30,10 @@
 // kLead units without work in front, for what it costs to begin and end one.  A
 // run that cuts a (query tile, head) leaves partial sums in the workspace, which a
 // second kernel joins in the order of the line.  Short contexts go without: a CTA
-// for each (query tile, head), one launch (attn_direct).  Inside a CTA four warps take every fourth tile with an
-// asynchronous copy ring of their own each and join at the end.
+// for each (query tile, head), one launch (attn_direct).  Inside a CTA four warps
+// take every fourth tile with an asynchronous copy ring of their own each and join at
+// the end.  Calls that mix chunks with single tokens take two launches, each with the
+// tile that fits its sequences (attn_mixed).
 //
 // Measured (one GB300, steady state): 64 sequences of 200 to 16000 tokens, 32 query and
 // 8 kv heads of 128, 4 bits: 118 us, 5.3 TB/s of the bytes that have to be read; four of
@@ -871,12 +873,20 @@ static auto attn_dispatch(int D, int format, int64_t columns, Fn &&f) {
     });
 }
 
-static AttnPlan attn_plan(int sm_count, int format, int64_t B, int Hq, int Hkv, int D, int64_t max_q_len) {
-    const int group = Hq / Hkv;
+// The plan of one launch for sequences of up to max_q_len queries.
+static AttnPlan attn_plan(int sm_count, int format, int64_t B, int group, int D, int64_t max_q_len) {
     if (wide(max_q_len * group)) return wide_plan(sm_count, B, group, D, max_q_len);
     return attn_dispatch(D, format, max_q_len * group, [&](auto d, auto bits, auto nt) {
         return attn_plan_of<d.value, bits.value, nt.value>(sm_count, B, group, max_q_len);
     });
+}
+
+// Up to how many queries a sequence may go to a launch of its own: eight columns, or one
+// token; 0 where max_q_len's kernel is the same, or takes 16 columns and is as good.
+static int64_t attn_few(int D, int group, int64_t max_q_len) {
+    const int64_t few = group < 8 ? 8 / group : 1, columns = few * group, most = max_q_len * group;
+    if (wide(columns) || max_q_len <= few) return 0;
+    return wide(most) || (attn_tiles(D, most) == 4 && attn_tiles(D, columns) != 4) ? few : 0;
 }
 
 // Whether each (query tile, head) gets a CTA of its own: no line, no joining.  Where no
@@ -885,9 +895,9 @@ static AttnPlan attn_plan(int sm_count, int format, int64_t B, int Hq, int Hkv, 
 // to 700 tokens 10.1 / 7.3, 256 of up to 900 59 / 50; of 300 to 1900 tokens 16
 // sequences 15.8 / 17.4, 64 of them 30.1 / 29.1; of 1000 to 4000, 16: 24 / 33).
 static bool attn_direct(const KvAttnArgs &a, int columns) {
-    const int64_t most = attn_most_tokens(a, columns);
-    return attn_few_idle(a, columns) &&
-           (most <= 1024 || (most <= 2048 && 3 * a.heads >= 2 * static_cast<int64_t>(a.grid)));
+    const int64_t most = attn_most_tokens(a, columns), busy = attn_busy_heads(a, columns);
+    if (a.heads > 2 * busy || a.heads > INT32_MAX) return false;  // a grid of CTAs without work
+    return most <= 1024 || (most <= 2048 && 3 * busy >= 2 * static_cast<int64_t>(a.grid));
 }
 
 template <int D, int BITS, int NT>
@@ -911,6 +921,47 @@ static int attn_launch(KvAttnArgs &a, cudaStream_t st) {
     return join_launch<D, typename S::L>(a, st);
 }
 
+// Workspace of a call, whichever launches it takes.
+static int64_t attn_bytes(int sm_count, int format, int64_t B, int group, int D, int64_t max_q_len) {
+    const int64_t all = attn_plan(sm_count, format, B, group, D, max_q_len).bytes;
+    const int64_t few = attn_few(D, group, max_q_len);
+    if (few == 0) return all;
+    const int64_t part = attn_plan(sm_count, format, B, group, D, few).bytes;
+    return part > all ? part : all;
+}
+
+// Whether sequences of few queries get a launch of their own, before the others': where
+// there are at most half as many queries as max_q_len allows (some sequences then have
+// far fewer than others), and sequences enough to pay for the second launch.  One chunk
+// of n queries among sequences of one (32 and 8 heads of 128 in 4 bits, contexts of up
+// to 2000 tokens, us in one / in two): 64 sequences, n 4 49 / 61, 12 88 / 72, 60 226 / 95,
+// 500 284 / 107; 16, n 12 32 / 46, 60 71 / 63, 500 113 / 81; 4, n 60 37 / 51, 500 76 / 76.
+static bool attn_mixed(const KvAttnArgs &a, int64_t few, int sm_count) {
+    if (few == 0 || !a.cu_q || 2 * a.T > a.B * a.max_q_len) return false;
+    const int64_t heads = (a.T < a.B ? a.T : a.B) * a.cache.Hkv;  // that may have a query
+    return wide(a.max_q_len * a.group) ? 4 * heads >= 3 * static_cast<int64_t>(sm_count)
+                                       : heads >= 2 * static_cast<int64_t>(sm_count);
+}
+
+// The launches for the sequences of min_q to most_q queries.
+static int attn_pass(KvAttnArgs a, int sm_count, int D, int format, int64_t min_q, int64_t most_q, int64_t max_q_len,
+                     void *workspace, cudaStream_t st) {
+    const AttnPlan plan = attn_plan(sm_count, format, a.B, a.group, D, max_q_len);
+    a.min_q = min_q;
+    a.most_q = most_q;
+    a.max_q_len = max_q_len;
+    a.units = static_cast<int64_t *>(workspace);
+    a.cuts = reinterpret_cast<CutNote *>(static_cast<char *>(workspace) + 16);
+    a.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.head_bytes);
+    a.q_tiles = plan.q_tiles;
+    a.heads = a.B * plan.q_tiles * a.cache.Hkv;
+    a.grid = plan.grid;
+    if (wide(max_q_len * a.group)) return wide_launch(D, format, a, st);
+    return attn_dispatch(D, format, max_q_len * a.group, [&](auto d, auto bits, auto nt) {
+        return attn_launch<d.value, bits.value, nt.value>(a, st);
+    });
+}
+
 static int kv_attention_check(int format, int64_t B, int Hq, int Hkv, int D, int64_t max_q_len) {
     const int rc = kv_check_sizes(format, Hkv, D, 16, 1);
     if (rc != RN_OK) return rc;
@@ -932,7 +983,7 @@ int64_t kv_attention_workspace_bytes(int format, int64_t B, int Hq, int Hkv, int
     const rn::DeviceInfo *dev = rn::current_device_info();
     if (!dev) return RN_ERR_DEVICE;
     if (B == 0 || max_q_len == 0) return 16;
-    return rn::attn_plan(dev->sm_count, format, B, Hq, Hkv, D, max_q_len).bytes;
+    return rn::attn_bytes(dev->sm_count, format, B, Hq / Hkv, D, max_q_len);
 }
 
 int kv_attention_fwd(const rn_bf16 *q, int64_t q_stride, const uint8_t *codes,
@@ -962,8 +1013,7 @@ int kv_attention_fwd(const rn_bf16 *q, int64_t q_stride, const uint8_t *codes,
         return RN_ERR_ALIGN;
     const rn::DeviceInfo *dev = rn::current_device_info();
     if (!dev) return RN_ERR_DEVICE;
-    const rn::AttnPlan plan = rn::attn_plan(dev->sm_count, format, B, Hq, Hkv, D, max_q_len);
-    if (workspace_bytes < plan.bytes) return RN_ERR_ARG;
+    if (workspace_bytes < rn::attn_bytes(dev->sm_count, format, B, Hq / Hkv, D, max_q_len)) return RN_ERR_ARG;
     rn::KvAttnArgs a;
     a.q = q;
     a.q_stride = q_stride;
@@ -983,16 +1033,13 @@ int kv_attention_fwd(const rn_bf16 *q, int64_t q_stride, const uint8_t *codes,
     a.sinks = static_cast<int>(sinks < INT32_MAX ? sinks : INT32_MAX);
     a.out = out;
     a.lse = lse;
-    a.units = static_cast<int64_t *>(workspace);
-    a.cuts = reinterpret_cast<rn::CutNote *>(static_cast<char *>(workspace) + 16);
-    a.partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.head_bytes);
-    a.q_tiles = plan.q_tiles;
-    a.heads = B * plan.q_tiles * Hkv;
-    a.grid = plan.grid;
-    if (rn::wide(max_q_len * a.group)) return rn::wide_launch(D, format, a, reinterpret_cast<cudaStream_t>(stream));
-    return rn::attn_dispatch(D, format, max_q_len * a.group, [&](auto d, auto bits, auto nt) {
-        return rn::attn_launch<d.value, bits.value, nt.value>(a, reinterpret_cast<cudaStream_t>(stream));
-    });
+    const auto st = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t few = rn::attn_few(D, a.group, max_q_len);
+    if (!rn::attn_mixed(a, few, dev->sm_count))
+        return rn::attn_pass(a, dev->sm_count, D, format, 0, INT64_MAX, max_q_len, workspace, st);
+    rc = rn::attn_pass(a, dev->sm_count, D, format, 0, few, few, workspace, st);
+    if (rc != RN_OK) return rc;
+    return rn::attn_pass(a, dev->sm_count, D, format, few + 1, INT64_MAX, max_q_len, workspace, st);
 }
 
 }  // extern "C"

@@ -21,6 +21,7 @@ struct KvAttnArgs {
     const int64_t *cu_q;
     int64_t T;
     int64_t max_q_len;
+    int64_t min_q, most_q;  // sequences with fewer or more queries are another launch's
     int Hq;
     int group;         // query heads of a kv head
     float scale_log2;  // softmax scale * log2(e)
@@ -104,6 +105,7 @@ __device__ __forceinline__ Item<L> make_item(const KvAttnArgs &a, int64_t item) 
         const int64_t end = a.cu_q[b + 1];
         it.bad = end > it.row0 && (it.row0 < 0 || end > a.T);
         nq = end > it.row0 && !it.bad ? end - it.row0 : 0;  // (no difference of wild numbers)
+        if (nq < a.min_q || nq > a.most_q) nq = 0;
     }
     int64_t len = a.kv_lens[b];
     const int64_t room = a.max_pages << a.cache.log2_page;
@@ -406,11 +408,12 @@ inline int64_t attn_most_tokens(const KvAttnArgs &a, int columns) {
     return few < room ? few : room;
 }
 
-// Whether the grid of a CTA for each (query tile, kv head) is mostly CTAs with work: the
-// queries there are make at least half of the query tiles that max_q_len allows for.
-inline bool attn_few_idle(const KvAttnArgs &a, int columns) {
-    const int64_t busy = (a.T * a.group / columns + a.B) * a.cache.Hkv;
-    return a.heads <= 2 * busy && a.heads <= INT32_MAX;
+// About how many (query tile, kv head)s have work: by the queries there are, not those that
+// max_q_len allows for.  (The second launch of a mixed call counts on few sequences: of 16
+// one with 60 queries over 2000 tokens took 50 us with a CTA for each head, 32 on the line.)
+inline int64_t attn_busy_heads(const KvAttnArgs &a, int columns) {
+    const int64_t busy = (a.T * a.group / columns + (a.min_q > 1 ? 1 : a.B)) * a.cache.Hkv;
+    return busy < a.heads ? busy : a.heads;
 }
 
 // kv_attention_wide.cu: 128 columns at a time.

@@ -908,10 +908,10 @@ static int wide_launch_of(KvAttnArgs &a, cudaStream_t st) {
     // does not matter (chunks of a quarter of their context, 8 heads of 128, us on the
     // line / directly: contexts of 600, 1 sequence 32 / 29, 32 of them 163 / 141; 2000, 1
     // sequence 50 / 56, 8 of them 224 / 208; 3000, 16 of them 718 / 679).
-    const int64_t most = attn_most_tokens(a, S::NQ);
-    a.direct = attn_few_idle(a, S::NQ) &&
-               (most <= 640 || (most <= 2048 && 5 * a.heads >= 3 * static_cast<int64_t>(a.grid)) ||
-                a.heads >= 4 * static_cast<int64_t>(a.grid));
+    const int64_t most = attn_most_tokens(a, S::NQ), busy = attn_busy_heads(a, S::NQ);
+    a.direct = a.heads <= 2 * busy && a.heads <= INT32_MAX &&  // few CTAs without work
+               (most <= 640 || (most <= 2048 && 5 * busy >= 3 * static_cast<int64_t>(a.grid)) ||
+                busy >= 4 * static_cast<int64_t>(a.grid));
     static std::atomic<int> attr_done[kMaxDevices];
     const int dev = current_device_index();
     if (dev < 0 || dev >= kMaxDevices) return RN_ERR_DEVICE;

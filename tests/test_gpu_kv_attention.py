@@ -90,7 +90,7 @@ def queries(T, Hq, D, seed, size=1.5):
     return (size * torch.randn(T, Hq, D, generator=g)).to(torch.bfloat16)
 
 
-def check(got, lse, q, ref, table, lens, cu, scale, window=0, sinks=0):
+def check(got, lse, q, ref, table, lens, cu, scale, window=0, sinks=0, wide=None):
     D = q.shape[-1]
     for b, n in enumerate(lens):
         lo, hi = cu[b], cu[b + 1]
@@ -102,7 +102,8 @@ def check(got, lse, q, ref, table, lens, cu, scale, window=0, sinks=0):
         SK, SV = (ref.token_scales(table[b], w, 0, n) for w in (0, 1))
         z = 8 if ref.bits == 4 else 128
         G = q.shape[1] // K.shape[1]
-        wide = max(y - x for x, y in zip(cu, cu[1:])) * G > 64
+        if wide is None:  # the arithmetic of more than 64 columns
+            wide = max(y - x for x, y in zip(cu, cu[1:])) * G > 64
         low_k, low_v = (z * 2.0 ** -17 * float((x > 255).any()) * wide for x in (SK, SV))
         low_k += 2.0 ** -25 * wide
         tol, dl = torch.full_like(o, 2.0 ** -40), torch.zeros_like(l)
@@ -563,6 +564,69 @@ def test_many_sequences_and_a_long_chunk():
     q = queries(sum(n_q), Hq, D, seed=1)
     out, lse, cu = attend(ref, table, lens, q, n_q, Hq)
     check(out, lse, q, ref, table, lens, cu, D ** -0.5)
+
+
+@pytest.mark.parametrize("long,Hq,Hkv,D,P,bits", [(30, 24, 24, 64, 16, 8), (14, 48, 24, 64, 32, 4),
+                                                  (90, 12, 12, 128, 16, 4), (40, 20, 10, 256, 32, 8),
+                                                  (14, 40, 2, 64, 32, 8)])
+@pytest.mark.usefixtures("both_layouts")
+def test_one_chunk_among_single_tokens(long, Hq, Hkv, D, P, bits):
+    """With heads enough (ten or more here) sequences of few queries are a launch of their
+    own; each row has the arithmetic of its launch, and rows of neither keep their content."""
+    G = Hq // Hkv
+    split = Hkv >= (10 if long * G > 64 else 24)
+    lens = [1, 0, 300, 64, 20, long + 33, 5, 2, 129, 31, 0, 90, 150, 17]
+    n_q = [1, 0, 1, 2, 0, long, 1, 3, 1, 1, 1, 9, 8 // G + 1, max(8 // G, 1)]
+    assert 2 * sum(n_q) <= len(n_q) * long
+    ref, table = filled(bits, Hkv, D, P, lens, seed=long + D)
+    q = queries(sum(n_q) + 3, Hq, D, seed=long)
+    T = sum(n_q)
+    out = torch.full((T + 3, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T + 3, Hq), 7.0, device="cuda")
+    ws = binding.kv_attention_workspace(to_gpu(ref), len(lens), Hq, max_q_len=long)
+    ws.fill_(0xFF)
+    got, got_lse, cu = attend(ref, table, lens, q, n_q, Hq, out=out, lse=lse, workspace=ws)
+    for b, n in enumerate(lens):
+        few = split and n_q[b] <= max(8 // G, 1)
+        check(got, got_lse, q, ref, table[b:b + 1], [n], cu[b:b + 2], D ** -0.5,
+              wide=long * G > 64 and not few)
+    assert (got[T:] == 7).all() and (got_lse[T:] == 7).all()
+    assert binding.device_status() == 0
+
+
+def test_a_mixed_step_captured_and_replayed():
+    """Both launches of a mixed call read lengths and offsets at replay."""
+    Hq, Hkv, D, P, B = 40, 20, 64, 32, 6
+    lens = [200, 130, 90, 300, 64, 33]
+    ref, table = filled(4, Hkv, D, P, lens, seed=12)
+    q = queries(70, Hq, D, seed=12)
+    cache, t, qd = to_gpu(ref), table.cuda(), q.cuda()
+    n = torch.tensor(lens, dtype=torch.int32).cuda()
+    cu = torch.zeros(B + 1, dtype=torch.int64).cuda()
+    ws = binding.kv_attention_workspace(cache, B, Hq, max_q_len=60)
+    out = torch.empty(70, Hq, D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(70, Hq, device="cuda")
+
+    def step():
+        binding.kv_attention_fwd(qd, cache, t, n, Hq, cu_q=cu, max_q_len=60, out=out, lse=lse,
+                                 workspace=ws)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for n_q in ([60, 1, 1, 1, 1, 1], [1, 2, 1, 40, 0, 20], [1] * 6, [2, 3, 2, 3, 2, 3]):
+        offsets = [0]
+        for x in n_q:
+            offsets.append(offsets[-1] + x)
+        cu.copy_(torch.tensor(offsets))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for b in range(B):
+            check(out.cpu(), lse.cpu(), q, ref, table[b:b + 1], [lens[b]], offsets[b:b + 2], D ** -0.5,
+                  wide=n_q[b] > 4)
+        assert (out[offsets[-1]:] == 7).all()
 
 
 def test_runs_repeat_bit_for_bit_and_share_a_workspace():
