@@ -9,6 +9,7 @@ library is not built, the first call raises ``RuntimeError``.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -679,13 +680,21 @@ def _kv_device(cache: KVCache) -> int:
     return dev
 
 
-def _held(stream, t: torch.Tensor) -> torch.Tensor:
-    """t, allocated here for a call on `stream`: its memory is not used again before
-    that stream is done with it, even where the caller drops t at once."""
+def _result(dev: int, t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple,
+            device: torch.device, stream):
+    """(t, its address): the caller's tensor, checked, or a new one.  A new one's memory
+    is not used again before `stream` is done with it, even if it is dropped at once."""
+    if t is not None:
+        return t, _on(dev, t, name, dtype, math.prod(shape))
+    t = torch.empty(shape, dtype=dtype, device=device)
+    _hold(t, stream)
+    return t, t.data_ptr()
+
+
+def _hold(t: torch.Tensor, stream) -> None:
     if stream is not None:
         t.record_stream(stream if isinstance(stream, torch.cuda.Stream)
                         else torch.cuda.ExternalStream(int(stream), device=t.device))
-    return t
 
 
 def _kv_call(dev: int, name: str, *args, stream) -> None:
@@ -732,14 +741,11 @@ def kv_cache_read(cache: KVCache, page_table: torch.Tensor, cu_lens: torch.Tenso
     cp = _on(dev, cu_lens, "cu_lens", torch.int64, B + 1)
     sp = None if starts is None else _on(dev, starts, "starts", torch.int32, B)
     Hkv, D = cache.num_kv_heads, cache.head_dim
-    n = total * Hkv * D
-    if k is None:
-        k = _held(stream, torch.empty(total, Hkv, D, dtype=torch.bfloat16, device=cache.device))
-    if v is None:
-        v = _held(stream, torch.empty(total, Hkv, D, dtype=torch.bfloat16, device=cache.device))
+    shape = (total, Hkv, D)
+    k, kp = _result(dev, k, "k", torch.bfloat16, shape, cache.device, stream)
+    v, vp = _result(dev, v, "v", torch.bfloat16, shape, cache.device, stream)
     _kv_call(dev, "kv_cache_read", cache.codes.data_ptr(), cache.scales.data_ptr(), cache.format,
-             Hkv, D, cache.page_size, cache.num_pages, tp, B, width, cp, sp, total,
-             _on(dev, k, "k", torch.bfloat16, n), _on(dev, v, "v", torch.bfloat16, n),
+             Hkv, D, cache.page_size, cache.num_pages, tp, B, width, cp, sp, total, kp, vp,
              stream=stream)
     return k, v
 
@@ -800,21 +806,18 @@ def kv_attention_fwd(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
         raise ValueError("without cu_q there is one query for each sequence")
     else:
         cp = None
-    if out is None:
-        out = _held(stream, torch.empty(T, Hq, D, dtype=torch.bfloat16, device=cache.device))
-    if lse is None:
-        lse = _held(stream, torch.empty(T, Hq, dtype=torch.float32, device=cache.device))
+    out, op = _result(dev, out, "out", torch.bfloat16, (T, Hq, D), cache.device, stream)
+    lse, sp = _result(dev, lse, "lse", torch.float32, (T, Hq), cache.device, stream)
     if workspace is None:
-        workspace = _held(stream, kv_attention_workspace(cache, B, Hq, max_q_len=max_q_len))
+        workspace = kv_attention_workspace(cache, B, Hq, max_q_len=max_q_len)
+        _hold(workspace, stream)
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     _kv_call(dev, "kv_attention_fwd", q.data_ptr(), q.stride(0) if T > 1 else Hq * D,
              cache.codes.data_ptr(), cache.scales.data_ptr(), cache.format, Hq, cache.num_kv_heads,
              D, cache.page_size, cache.num_pages, tp, B, width, lp, cp, T, max_q_len,
-             D ** -0.5 if scale is None else scale, window, sinks,
-             _on(dev, out, "out", torch.bfloat16, T * Hq * D),
-             _on(dev, lse, "lse", torch.float32, T * Hq), workspace.data_ptr(), workspace.nbytes,
-             stream=stream)
+             D ** -0.5 if scale is None else scale, window, sinks, op, sp, workspace.data_ptr(),
+             workspace.nbytes, stream=stream)
     return out, lse
 
 
