@@ -283,8 +283,9 @@ constexpr int kFewPieces = 8;  // pieces that one warp joins by itself
 
 // ---- joining the pieces of a cut (query tile, head) -------------------------------------
 
-// blockIdx.x: a note on a cut (query tile, head), y: a share of the columns' quads of dimensions.  A lane owns four dimensions of a column; a warp
-// takes all pieces of its columns where they are few, else the warps share them.
+// blockIdx.x: a note on a cut (query tile, head), y: a share of the columns' quads of
+// dimensions.  A lane owns four dimensions of a column; a warp takes all pieces of its
+// columns where they are few, else the warps share them.
 template <int D, class L>
 __global__ void __launch_bounds__(32 * kJoinWarps) kv_attention_join_kernel(const KvAttnArgs a) {
     constexpr int NQ = L::NQ, SLOT = NQ * (D + 2), QUADS = D / 4;

@@ -281,8 +281,9 @@ struct TokenRows {
 };
 
 // ---- restoring keys ---------------------------------------------------------------------
-// Four warps, BN / 4 tokens each (each with a power of two of its own), eight at a time: lane = token % 8 + 8 j with j the
-// quarter of the stored row.  A group's eight elements are one chunk of the operand.
+// Four warps, BN / 4 tokens each (each with a power of two of its own), eight at a time:
+// lane = token % 8 + 8 j with j the quarter of the stored row.  A group's eight elements
+// are one chunk of the operand.
 // A key s * c has up to 18 significant bits: its fp16 and the exact rest, which the
 // fused multiply-add gives, are two operands behind one another.
 template <int D, int BITS, int BN>
