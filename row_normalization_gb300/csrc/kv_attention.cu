@@ -818,7 +818,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, BITS, NT>::kCtas)
                 part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1)) * S::kSlot;
         }
         if (k1 > k0) attend_run<D, BITS, NT>(a, it, head, k0, k1, part, attn_smem);
-        if (!a.direct && threadIdx.x == 0) note_piece(a, cut, u - v0, v0, v1, units, it, item, head);
+        if (!a.direct && threadIdx.x == 0) note_piece(a, cut, blockIdx.x, u - v0, v0, v1, units, it, item, head);
         u += v1 - v0;
         if (v1 == units && head == a.cache.Hkv - 1) {
             before += units;

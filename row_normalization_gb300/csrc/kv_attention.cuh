@@ -81,15 +81,15 @@ struct Item {
     bool bad;        // something had to be cut to the tensors
 
     // its units on the line, for one head
-    __device__ __forceinline__ int units() const { return n > 0 ? n + L::LEAD : 0; }
+    __host__ __device__ __forceinline__ int units() const { return n > 0 ? n + L::LEAD : 0; }
 
-    __device__ __forceinline__ int token(int k) const {
+    __host__ __device__ __forceinline__ int token(int k) const {
         return (k < sink_tiles ? k : lo_tile + (k - sink_tiles)) * L::TILE;
     }
 };
 
 template <class L>
-__device__ __forceinline__ Item<L> make_item(const KvAttnArgs &a, int64_t item) {
+__host__ __device__ __forceinline__ Item<L> make_item(const KvAttnArgs &a, int64_t item) {
     Item<L> it;
     uint32_t b = static_cast<uint32_t>(item), qt = 0;  // items fit 31 bits
     if (a.q_tiles != 1) {
@@ -139,7 +139,7 @@ __device__ __forceinline__ Item<L> make_item(const KvAttnArgs &a, int64_t item) 
 }
 
 // a / b, in 32 bits where both fit (they nearly always do).
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+__host__ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
     return a / b;
 }
@@ -149,14 +149,14 @@ template <class L>
 struct Cut {
     int64_t ctas, run, rest;
 
-    __device__ __forceinline__ Cut(int64_t units, int grid) {
+    __host__ __device__ __forceinline__ Cut(int64_t units, int grid) {
         const int64_t want = (units + L::MIN - 1) / L::MIN;
         ctas = want < grid ? (want > 0 ? want : 1) : grid;
         run = quotient(units, ctas);
         rest = units - run * ctas;
     }
-    __device__ __forceinline__ int64_t start(int64_t c) const { return c * run + (c < rest ? c : rest); }
-    __device__ __forceinline__ int64_t cta_of(int64_t unit) const {
+    __host__ __device__ __forceinline__ int64_t start(int64_t c) const { return c * run + (c < rest ? c : rest); }
+    __host__ __device__ __forceinline__ int64_t cta_of(int64_t unit) const {
         const int64_t longer = rest * (run + 1);
         return unit < longer ? quotient(unit, run + 1) : rest + quotient(unit - longer, run);
     }
@@ -255,15 +255,16 @@ __device__ __forceinline__ void store_empty(const KvAttnArgs &a) {
 }
 
 // Notes for the joining kernel on the piece [v0, v1) of `units` units of a (query
-// tile, head) whose first unit is `first`; by one thread.
+// tile, head) whose first unit is `first`; by one thread of CTA `cta`.
 template <class L>
-__device__ __forceinline__ void note_piece(const KvAttnArgs &a, const Cut<L> &cut, int64_t first, int v0, int v1,
-                                           int units, const Item<L> &it, int64_t item, int head) {
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x) - 1;
+__host__ __device__ __forceinline__ void note_piece(const KvAttnArgs &a, const Cut<L> &cut, int64_t cta, int64_t first,
+                                                    int v0, int v1, int units, const Item<L> &it, int64_t item,
+                                                    int head) {
+    const int64_t c0 = cta - 1;
     // the second piece: the CTA before holds the first unit with work
     const bool second = v0 > L::LEAD && cut.start(c0) <= first + L::LEAD;
     const bool by_head = a.heads <= a.grid;
-    const bool none = by_head ? v0 <= L::LEAD && v1 == units : !second && first + v0 == cut.start(blockIdx.x);
+    const bool none = by_head ? v0 <= L::LEAD && v1 == units : !second && first + v0 == cut.start(cta);
     if (!second && !none) return;
     CutNote n;
     n.row0 = it.row0;
@@ -273,7 +274,51 @@ __device__ __forceinline__ void note_piece(const KvAttnArgs &a, const Cut<L> &cu
     n.pieces = second ? static_cast<int>(cut.cta_of(first + units - 1) - c0) + 1 : 0;
     n.first_slot = static_cast<int>(2 * c0 + (cut.start(c0) < first ? 1 : 0));
     n.unused = 0;
-    a.cuts[by_head ? item * a.cache.Hkv + head : blockIdx.x] = n;
+    a.cuts[by_head ? item * a.cache.Hkv + head : cta] = n;
+}
+
+// Calls body(item, head, first tile, end, slot for a piece or null) for each run of CTA
+// `cta` of the line, which begins at `item` with `before` units of one head in front of
+// it, or for its only (query tile, head) where a.direct.  A body that returns false (its
+// wait ran out) is the thread's last; but the thread that notes walks on and notes every
+// piece, for the joining kernel follows the notes whatever became of the sums.
+#pragma nv_exec_check_disable
+template <int SLOT, class L, class Body>
+__host__ __device__ __forceinline__ void walk_runs(const KvAttnArgs &a, const Cut<L> &cut, int64_t cta, int64_t item,
+                                                   int64_t before, int own_head, bool notes, Body &&body) {
+    const int64_t u0 = a.direct ? 0 : cut.start(cta), u1 = a.direct ? 1 : cut.start(cta + 1);
+    int64_t u = u0;
+    bool ok = true;
+    while (u < u1) {
+        const Item<L> it = make_item<L>(a, item);
+        if (it.n == 0) {
+            ++item;
+            continue;
+        }
+        int units = 1, head = own_head, v0 = 0, v1 = 1, k0 = 0, k1 = it.n;
+        if (!a.direct) {
+            units = it.units();
+            const int64_t in = u - before * a.cache.Hkv;
+            head = static_cast<int>(quotient(in, units));
+            v0 = static_cast<int>(in - static_cast<int64_t>(head) * units);
+            const int64_t left = u1 - u;
+            v1 = units - v0 <= left ? units : v0 + static_cast<int>(left);
+            k0 = v0 > L::LEAD ? v0 - L::LEAD : 0;
+            k1 = v1 - L::LEAD;
+        }
+        if (ok && k1 > k0) {
+            float *part = nullptr;
+            if (k1 - k0 != it.n) part = a.partial + (2 * cta + (u == u0 ? 0 : 1)) * SLOT;
+            ok = body(it, head, k0, k1, part);
+        }
+        if (!a.direct && notes) note_piece(a, cut, cta, u - v0, v0, v1, units, it, item, head);
+        if (!ok && !notes) return;
+        u += v1 - v0;
+        if (v1 == units && head == a.cache.Hkv - 1) {
+            before += units;
+            ++item;
+        }
+    }
 }
 
 constexpr int kJoinWarps = 8;

@@ -534,39 +534,8 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
     const uint32_t tmem = sh.tmem;
 
     // Every role walks the CTA's runs in the same order; n counts its tiles over all.
-    const int64_t u0 = a.direct ? 0 : cut.start(blockIdx.x), u1 = a.direct ? 1 : cut.start(blockIdx.x + 1);
     const auto each_run = [&](auto &&body) {
-        int64_t item = line.item, before = line.before, u = u0;
-        while (u < u1) {
-            const Item<L> it = make_item<L>(a, item);
-            if (it.n == 0) {
-                ++item;
-                continue;
-            }
-            int units = 1, head = own_head, v0 = 0, v1 = 1, k0 = 0, k1 = it.n;
-            if (!a.direct) {
-                units = it.units();
-                const int64_t in = u - before * a.cache.Hkv;
-                head = static_cast<int>(quotient(in, units));
-                v0 = static_cast<int>(in - static_cast<int64_t>(head) * units);
-                const int64_t left = u1 - u;
-                v1 = units - v0 <= left ? units : v0 + static_cast<int>(left);
-                k0 = v0 > L::LEAD ? v0 - L::LEAD : 0;
-                k1 = v1 - L::LEAD;
-            }
-            if (k1 > k0) {
-                float *part = nullptr;
-                if (k1 - k0 != it.n)
-                    part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1)) * S::kSlot;
-                if (!body(it, head, k0, k1, part)) return;
-            }
-            if (!a.direct && threadIdx.x == 0) note_piece(a, cut, u - v0, v0, v1, units, it, item, head);
-            u += v1 - v0;
-            if (v1 == units && head == a.cache.Hkv - 1) {
-                before += units;
-                ++item;
-            }
-        }
+        walk_runs<S::kSlot>(a, cut, blockIdx.x, line.item, line.before, own_head, threadIdx.x == 0, body);
     };
 
     if (warp < 4 * QT) {
@@ -884,7 +853,8 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
         });
         // nothing of this CTA is under way any more when its tensor memory goes back
         tc_commit(&sh.drained);
-        mbar_wait_bounded(&sh.drained, 0, 2000000000ull, nullptr);
+        if (!mbar_wait_bounded(&sh.drained, 0, 2000000000ull, nullptr))
+            atomicOr(&g_kv_attention_status, RN_STATUS_WAIT_TIMEOUT);
     }
     __syncwarp();
     tc_fence_before();
