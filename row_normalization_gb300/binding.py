@@ -682,19 +682,26 @@ def _kv_device(cache: KVCache) -> int:
 
 def _result(dev: int, t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple,
             device: torch.device, stream):
-    """(t, its address): the caller's tensor, checked, or a new one.  A new one's memory
-    is not used again before `stream` is done with it, even if it is dropped at once."""
+    """(t, its address): the caller's tensor, checked, or a new one."""
     if t is not None:
         return t, _on(dev, t, name, dtype, math.prod(shape))
-    t = torch.empty(shape, dtype=dtype, device=device)
-    _hold(t, stream)
+    t = _new(shape, dtype, device, stream)
     return t, t.data_ptr()
 
 
-def _hold(t: torch.Tensor, stream) -> None:
-    if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                        else torch.cuda.ExternalStream(int(stream), device=t.device))
+def _new(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """A new tensor that `stream` may write at once: its memory is that stream's, not a
+    block whose last use may still wait on the caller's stream.  It is not used again
+    before either stream is done with it, even if it is dropped at once."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
+            torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _kv_call(dev: int, name: str, *args, stream) -> None:
@@ -754,13 +761,16 @@ def kv_attention_workspace(cache: KVCache, B: int, Hq: int, *, max_q_len: int = 
     """A workspace for kv_attention_fwd calls of up to these sizes.  Calls that
     run one after another can share one; calls that may run at the same time
     need one each."""
-    dev = _kv_device(cache)
-    with torch.cuda.device(dev):
+    return _new(_workspace_bytes(cache, B, Hq, max_q_len), torch.uint8, cache.device, None)
+
+
+def _workspace_bytes(cache: KVCache, B: int, Hq: int, max_q_len: int) -> int:
+    with torch.cuda.device(_kv_device(cache)):
         n = int(load().kv_attention_workspace_bytes(cache.format, B, Hq, cache.num_kv_heads,
                                                     cache.head_dim, max_q_len))
     if n < 0:
         raise RowNormError("kv_attention_workspace_bytes", n)
-    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+    return n
 
 
 def kv_attention_fwd(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
@@ -809,8 +819,7 @@ def kv_attention_fwd(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
     out, op = _result(dev, out, "out", torch.bfloat16, (T, Hq, D), cache.device, stream)
     lse, sp = _result(dev, lse, "lse", torch.float32, (T, Hq), cache.device, stream)
     if workspace is None:
-        workspace = kv_attention_workspace(cache, B, Hq, max_q_len=max_q_len)
-        _hold(workspace, stream)
+        workspace = _new(_workspace_bytes(cache, B, Hq, max_q_len), torch.uint8, cache.device, stream)
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     _kv_call(dev, "kv_attention_fwd", q.data_ptr(), q.stride(0) if T > 1 else Hq * D,
