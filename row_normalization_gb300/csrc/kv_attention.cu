@@ -9,7 +9,10 @@
 // a code is an exact fp16 number, and so is the query (bf16, scaled by a power
 // of two), so x_t has no rounding but that of fp32 sums.  The scales of the
 // keys multiply fp32 partial sums of one group; the scales of the values
-// multiply the weights, in fp16, before the second product.
+// multiply the weights before the second product.  Weight and product are fp16,
+// which the tensor core takes at twice tf32's rate and half its registers: 2^-11
+// relative each, within a range that attend_run keeps wide (64 sequences of 200 to 16000
+// tokens, 4 bits: 4% of the time).
 //
 // Codes reach the tensor core without a conversion: a code c in the low bits
 // of a 16-bit word is the subnormal fp16 number c * 2^-24, so masking a word
@@ -36,10 +39,10 @@
 // tile that fits its sequences (attn_mixed).
 //
 // Measured (one GB300, steady state): 64 sequences of 200 to 16000 tokens, 32 query and
-// 8 kv heads of 128, 4 bits: 118 us, 5.3 TB/s of the bytes that have to be read; four of
-// 131072 tokens 110 us, 5.5 TB/s; in 8 bits heads of 128 183 us, 6.4 TB/s, heads of 64
-// (96 sequences) 95 us, 5.5 TB/s.  In 8 bits the bytes bound; in 4 bits the unpacking
-// (about 620 instructions a warp and tile of 32 tokens, the integer pipe half full, 50 to
+// 8 kv heads of 128, 4 bits: 125 us, 5.0 TB/s of the bytes that have to be read; four of
+// 131072 tokens 116 us, 5.2 TB/s; in 8 bits heads of 128 184 us, 6.4 TB/s, heads of 64
+// (96 sequences) 98 us, 5.3 TB/s.  In 8 bits the bytes bound; in 4 bits the unpacking
+// (about 640 instructions a warp and tile of 32 tokens, the integer pipe half full, 50 to
 // 60% of the issue slots used by three warps a scheduler).
 #include "kv_attention.cuh"
 
@@ -47,7 +50,8 @@ namespace rn {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr float kSlack = 6.0f;       // powers of two a weight may grow before a rescale
+constexpr float kTop = 15.0f;        // weights stay below 2^kTop
+constexpr float kSlack = 4.0f;       // powers of two a weight may grow before a rescale
 // Units without work in front of each (query tile, head): its queries, first page and
 // copies, and the joining of its warps.  64 ragged sequences of 8 heads (540k tokens):
 // 175 us with none, 158 with 8, 128 with 16, 132 with 32; 4 long ones 124-126 throughout.
@@ -79,7 +83,10 @@ struct AttnShape {
     static constexpr int kRoom = 224 * 1024;
     static constexpr int stages_at(int ctas) { return ctas < 1 ? 0 : (kRoom / ctas - 2048 - kQuery) / (kAttnWarps * kStage); }
     static constexpr int kByRegs = MT * NT * 4 >= 64 ? 2 : (D == 64 ? 4 : 3) - (BITS == 8 ? 1 : 0);
-    static constexpr int kStep = D == 256 ? 1 : 2;  // 16-token halves of a tile taken at once
+    // 16-token halves of a tile taken at once: one where the registers hold no more (32
+    // sequences, drafts of 3 to 8 tokens, heads of 128: in 4 bits 95 against 103 us, in 8
+    // bits 104 against 149; one token a sequence 139 against 128)
+    static constexpr int kStep = MT * NT >= 32 || D == 256 ? 1 : 2;
     static constexpr int kCtas = stages_at(kByRegs) >= 2         ? kByRegs
                                  : stages_at(kByRegs - 1) >= 2 ? kByRegs - 1
                                                                : kByRegs - 2;
@@ -149,6 +156,20 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[WORDS], uint32_t addr) {
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                      : "r"(addr));
+    }
+}
+
+template <int WORDS>
+__device__ __forceinline__ void sts_words(uint32_t addr, const uint32_t (&w)[WORDS]) {
+    if constexpr (WORDS == 1) {
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(w[0]) : "memory");
+    } else if constexpr (WORDS == 2) {
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(w[0]), "r"(w[1]) : "memory");
+    } else {
+        static_assert(WORDS == 4, "one, two or four words");
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3])
+                     : "memory");
     }
 }
 
@@ -262,6 +283,7 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
     const int r = lane >> 2, j = lane & 3;
     __shared__ int s_pos[NQ];
     __shared__ float s_factor[NQ], s_ref[kAttnWarps][NQ], s_l[kAttnWarps][NQ];
+    __shared__ float2 s_unit[kAttnWarps][S::kTile];  // of the tile's tokens: e, 2^-e
 
     // -- the warp's copy ring --------------------------------------------------------
     uint8_t *ring = smem + warp * (S::kStages * S::kStage);
@@ -294,9 +316,6 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
     };
     const auto seen = [&](int t) {  // some query sees a token of t .. t + 15
         return t < it.hi && (it.win_lo == 0 || t < a.sinks || t + 15 >= it.win_lo);
-    };
-    const auto seen_token = [&](int t) {
-        return t < it.hi && (it.win_lo == 0 || t < a.sinks || t >= it.win_lo);
     };
     // Copies rows [FROM, TO) of a tile (halves or all of it), which lie on one page
     // starting at row `off` of it.  bytes = 0 writes zeros instead.
@@ -420,12 +439,15 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.0f;
     }
-    // Value scales lie below 2^(scale_exp + 1); the weights are kept below
-    // 2^(14 - scale_exp), so that their products stay inside fp16.  A new reference
-    // leaves them kSlack powers of two to grow, and is taken only when that is used
-    // up: rescaling at every new maximum took 55% of the tiles of a ragged decode batch.
-    // Weights of 2^-22 of the largest are still normal numbers.
-    int scale_exp = 0;
+    // A token's weight counts 2^e and its values' scales 2^-e, with 2^e the power of two
+    // above its largest scale in this head (2^-14 at least): scales lie below 1, and what
+    // the weights are kept below, 2^kTop, bounds their products too.  m, ref and the fp16
+    // weights are about weight * 2^e, so a token matters by what it adds to the result: one
+    // of large weight and no value (a sink), or of huge values and no weight, takes no
+    // bits from the others.
+    // A new reference leaves the weights kSlack powers of two to grow, and is taken only when
+    // that is used up: rescaling at every new maximum took 55% of the tiles of a ragged
+    // decode batch.  So the largest is 2^11 at least, and 2^-25 of it is a normal number.
 
     // lane's places in a stage
     const int key_a = (r >> 1) + 4 * (r & 1);  // token of its first operand row
@@ -447,20 +469,25 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
     const auto do_tile = [&](auto masked_tag, uint32_t base, int t0) {
         constexpr bool MASKED = decltype(masked_tag)::value;
         const uint32_t sbase = base + 2 * S::kCodesBytes;
-        // largest value scale of the tile's visible tokens, one token a lane (the
-        // pattern of a NaN is a negative integer)
-        int vtop;
-        {
+        // one token a lane: e and 2^-e for the warp, and its value scales times 2^-e in place
+        if (S::kTile == 32 || lane < S::kTile) {
             constexpr int W = NG / 2;
-            uint32_t v[W];
-            lds_words<W>(v, sbase + S::kScalesBytes + lane % S::kTile * S::kScaleRow);
-            uint32_t mx = v[0];
+            const uint32_t at = sbase + S::kScalesBytes + lane * S::kScaleRow;
+            uint32_t v[W], mx = 0x04000400u;
+            lds_words<W>(v, at);
+            // (shifted by an exponent, so that infinity and NaN are negative integers)
 #pragma unroll
-            for (int i = 1; i < W; ++i) mx = __vmaxs2(mx, v[i]);
-            vtop = max(static_cast<int>(static_cast<int16_t>(mx & 0xFFFFu)),
-                       static_cast<int>(static_cast<int16_t>(mx >> 16)));
-            if (vtop > 0x7BFF || (MASKED && !seen_token(t0 + lane % S::kTile))) vtop = -1;
+            for (int i = 0; i < W; ++i) mx = __vmaxs2(mx, (v[i] & 0x7FFF7FFFu) + 0x04000400u);
+            mx = __vmaxs2(mx, __byte_perm(mx, mx, 0x1032));
+            const int e = static_cast<int>(mx >> 26) - 15;
+            const float unit = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            const __half2 h = __float2half2_rn(unit);
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] = hmul2_bits(v[i], *reinterpret_cast<const uint32_t *>(&h));
+            sts_words<W>(at, v);
+            s_unit[warp][lane] = make_float2(static_cast<float>(e), unit);
         }
+        __syncwarp();
 #pragma unroll 1
         for (int m0 = 0; m0 < S::kTile / 16; m0 += S::kStep) {
         // -- logits (before the factor): rows are tokens, columns queries --------------------------
@@ -563,7 +590,20 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
             }
         }
 
-        // -- running maximum ----------------------------------------------------------------
+        // -- running maximum, of the logits plus e ----------------------------------------
+        float back[S::kStep][2];  // 2^-e of the lane's two tokens
+#pragma unroll
+        for (int mt = 0; mt < S::kStep; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 unit = s_unit[warp][16 * (m0 + mt) + 8 * h + key_a];
+                back[mt][h] = unit.y;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        x[mt][nt][2 * h + c] = fmaf(x[mt][nt][2 * h + c], factor[nt][c], unit.x);
+            }
         float top[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -571,13 +611,10 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
             for (int c = 0; c < 2; ++c) {
                 float t = fmaxf(x[0][nt][c], x[0][nt][2 + c]);
                 if constexpr (S::kStep == 2) t = fmaxf(t, fmaxf(x[1][nt][c], x[1][nt][2 + c]));
-                top[nt][c] = t * factor[nt][c];
-                grow |= top[nt][c] > m[nt][c];  // m: the largest logit the reference allows
+                top[nt][c] = t;
+                grow |= t > m[nt][c];  // m: the largest the reference allows
             }
-        grow |= vtop >= (scale_exp + 16) << 10;
         if (__any_sync(0xffffffffu, grow)) {
-            const int e = (__reduce_max_sync(0xffffffffu, vtop) >> 10) - 15;
-            scale_exp = e > scale_exp ? e : scale_exp;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float f[2];
@@ -587,9 +624,9 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                    // columns that need no more room keep what they have but for scale_exp
+                    // columns that need no more room keep what they have
                     t = t > m[nt][c] ? t + kSlack : m[nt][c];
-                    const float nref = t == -INFINITY ? 0.0f : t - static_cast<float>(14 - scale_exp);
+                    const float nref = t == -INFINITY ? 0.0f : t - kTop;
                     f[c] = m[nt][c] == -INFINITY ? 1.0f : exp2_approx(ref[nt][c] - nref);
                     ref[nt][c] = nref;
                     m[nt][c] = t;
@@ -610,9 +647,9 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
             for (int nt = 0; nt < NT; ++nt) {
                 float w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = exp2_approx(fmaf(x[mt][nt][i], factor[nt][i & 1], -ref[nt][i & 1]));
-                l[nt][0] += w[0] + w[2];
-                l[nt][1] += w[1] + w[3];
+                for (int i = 0; i < 4; ++i) w[i] = exp2_approx(x[mt][nt][i] - ref[nt][i & 1]);
+                l[nt][0] = fmaf(w[0], back[mt][0], fmaf(w[2], back[mt][1], l[nt][0]));
+                l[nt][1] = fmaf(w[1], back[mt][0], fmaf(w[3], back[mt][1], l[nt][1]));
                 if constexpr (MASKED) {
                     // a masked weight is -0, so that it can be told from one that underflowed
 #pragma unroll
@@ -658,19 +695,19 @@ __device__ __forceinline__ void attend_run(const KvAttnArgs &a,
                 for (int hm = 0; hm < 2; ++hm) {
                     uint32_t f0, f1, f2, f3;
                     if constexpr (BITS == 4) {
-                        const uint32_t u0 = __byte_perm(v[0][g / 2], v[1][g / 2], half) >> (8 * hm);
-                        const uint32_t u1 = __byte_perm(v[2][g / 2], v[3][g / 2], half) >> (8 * hm);
-                        f0 = u0 & 0x000F000Fu;
-                        f1 = u0 & 0x00F000F0u;
-                        f2 = u1 & 0x000F000Fu;
-                        f3 = u1 & 0x00F000F0u;
+                        const uint32_t c0 = __byte_perm(v[0][g / 2], v[1][g / 2], half) >> (8 * hm);
+                        const uint32_t c1 = __byte_perm(v[2][g / 2], v[3][g / 2], half) >> (8 * hm);
+                        f0 = c0 & 0x000F000Fu;
+                        f1 = c0 & 0x00F000F0u;
+                        f2 = c1 & 0x000F000Fu;
+                        f3 = c1 & 0x00F000F0u;
                     } else {
-                        const uint32_t u0 = __byte_perm(v[0][g], v[1][g], hm ? 0x7632u : 0x5410u);
-                        const uint32_t u1 = __byte_perm(v[2][g], v[3][g], hm ? 0x7632u : 0x5410u);
-                        f0 = u0 & 0x00FF00FFu;
-                        f1 = (u0 >> 8) & 0x00FF00FFu;
-                        f2 = u1 & 0x00FF00FFu;
-                        f3 = (u1 >> 8) & 0x00FF00FFu;
+                        const uint32_t c0 = __byte_perm(v[0][g], v[1][g], hm ? 0x7632u : 0x5410u);
+                        const uint32_t c1 = __byte_perm(v[2][g], v[3][g], hm ? 0x7632u : 0x5410u);
+                        f0 = c0 & 0x00FF00FFu;
+                        f1 = (c0 >> 8) & 0x00FF00FFu;
+                        f2 = c1 & 0x00FF00FFu;
+                        f3 = (c1 >> 8) & 0x00FF00FFu;
                     }
                     constexpr uint32_t z = F::kZero * 0x00010001u, z2 = BITS == 4 ? 16 * z : z;
                     f0 = hsub2_bits(f0, z);
