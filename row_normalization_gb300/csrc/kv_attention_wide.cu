@@ -9,9 +9,9 @@
 //   O += P V'              P in tensor memory (over its S), V' in shared memory.
 // V' is the cached value s * c rounded once to fp16, K' the same of the key and K''
 // the exact rest, so the logits (and lse) have no rounding but that of fp32 sums.
-// Queries as in kv_attention.cu.  32 tokens around a scale above 255 are restored at
-// 2^-8 of their size (the weights, or the logit's factor, make up for it), so
-// nothing leaves fp16.
+// Queries as in kv_attention.cu.  A token with a scale so large that s * c would leave
+// fp16 is restored at 2^-3 of its size (2^-7 in 8 bits), and its logit, or its weight,
+// makes up for it; what it has beside that in scales 2^-11 (2^-7) and below loses bits.
 //
 // Roles: four warps for each query tile of 128 columns, one accumulator row a thread
 // (softmax, output); four that restore keys, four for values; one thread issues the
@@ -30,11 +30,13 @@
 // (chunk ^ row % 8 in rows of 128 bytes): 64 elements a row, blocks of 64 elements
 // one after the other.  In 4 bits the eight dimensions of a chunk lie in the order
 // 0 4 1 5 2 6 3 7, the order in which they leave a word, in Q as in K' and K''.
+#include <float.h>
+
 #include "kv_attention.cuh"
 
 namespace rn {
 
-constexpr float kWideRoom = 6.0f;   // weights stay below 2^6 (2^14 where values are at 2^-8)
+constexpr float kWideRoom = 6.0f;   // weights (times 2^kDown of a large token) stay below 2^6
 constexpr float kWideSlack = 4.0f;  // powers of two a weight may grow before a rescale
 constexpr long long kWideLimit = 4000000000ll;  // clocks a wait may take, about two seconds
 
@@ -214,7 +216,80 @@ __device__ __forceinline__ void load_global(uint32_t (&w)[WORDS], const void *sr
     }
 }
 
-constexpr uint32_t kScale255 = 0x5BF8u;  // fp16 255: larger scales (and NaN) take the slow way
+// Scales above kBig (the largest s with s * Q inside fp16: 9352, 515.5), and NaN, take the
+// slow way: the token counts at 2^-kDown.
+template <int BITS>
+struct Big {
+    static constexpr uint32_t kBig = BITS == 4 ? 0x7091u : 0x6007u;
+    static constexpr int kDown = BITS == 4 ? 3 : 7;
+    static constexpr float kUp = static_cast<float>(1 << kDown);
+    // Scales of a token, two a word: whether one is that large.  (Shifted by an exponent, so
+    // that infinity and NaN are negative integers.)
+    template <int N>
+    __device__ static __forceinline__ bool some(const uint32_t (&s)[N]) {
+        constexpr uint32_t kMost = (kBig + 0x0400u) * 0x00010001u;
+        uint32_t m = kMost;
+#pragma unroll
+        for (int k = 0; k < N; ++k) m = __vmaxs2(m, (s[k] & 0x7FFF7FFFu) + 0x04000400u);
+        return m != kMost;
+    }
+    template <int N>
+    __device__ static __forceinline__ void down(uint32_t (&s)[N]) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) s[k] = h2_bits(__hmul2(as_h2(s[k]), __float2half2_rn(1.0f / kUp)));
+    }
+};
+
+// Tokens t .. t + 31 that a row does not see, a bit each: behind its position pos, or
+// before its window's first token lo and no sink.
+__device__ __forceinline__ uint32_t hidden_tokens(int pos, int lo, int sinks, int t) {
+    return ~below(pos + 1 - t) | (below(lo - t) & ~below(sinks - t));
+}
+
+// Large tokens are rare.  What the softmax does about them is two calls, by tensor memory:
+// inlined into the loop over 32 tokens it cost every tile its place in the instruction
+// caches (3 chunks of 500 to 1300 queries 426 us, as calls 359).
+//
+// In front of a tile's softmax: the products with large keys come up to their size.  Returns
+// the row's largest logit with a large value, whose weight counts 2^DOWN.
+template <int BN, int DOWN>
+__device__ __noinline__ float large_logits(uint32_t sbase, const uint32_t *key_big, const uint32_t *val_big,
+                                           float factor, int pos, int lo, int sinks, int t0) {
+    float most = -INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < BN; i += 16) {
+        const uint32_t up = key_big[i / 32] >> (i & 31);
+        const uint32_t bound = (val_big[i / 32] & ~hidden_tokens(pos, lo, sinks, t0 + (i & ~31))) >> (i & 31);
+        uint32_t x[16];
+        tmem_load16(x, sbase + i);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float y = __uint_as_float(x[j]) * (up >> j & 1u ? static_cast<float>(1 << DOWN) : 1.0f);
+            x[j] = __float_as_uint(y);
+            if (bound >> j & 1u) most = fmaxf(most, fmaf(y, factor, DOWN));
+        }
+        tmem_store16(sbase + i, x);
+    }
+    tmem_wait_store();
+    return most;
+}
+// Behind it: the weights of large values come up.
+template <int BN, int DOWN>
+__device__ __noinline__ void large_weights(uint32_t sbase, const uint32_t *val_big) {
+    tmem_wait_store();
+#pragma unroll 1
+    for (int i = 0; i < BN / 32; ++i) {
+        const uint32_t up = val_big[i];
+        uint32_t x[16];
+        tmem_load16(x, sbase + 16 * i);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const uint32_t two = up >> (2 * j);
+            x[j] = h2_bits(__hmul2(as_h2(x[j]), as_h2(0x3C003C00u + ((two & 1u) | (two & 2u) << 15) * (DOWN << 10))));
+        }
+        tmem_store16(sbase + 16 * i, x);
+    }
+}
 
 struct WideShared {
     uint64_t q_full[2];                            // by query tile
@@ -223,11 +298,13 @@ struct WideShared {
     uint64_t drained;
     uint32_t tmem;
     int abort;
-    // What restoring a tile met, a byte for each of the four warps: 1 where it is at 2^-8
-    // of its size, 2 where a value is NaN.  Keys: their producers wait for the products of
-    // two tiles before, which wait for the softmax of two tiles before that, so eight
-    // tiles' are kept.  Values: by stage.
+    // What restoring a tile met, a byte for each of the four warps: 1 where a token counts
+    // at 2^-kDown, 2 where a value is NaN; and those tokens, a bit each, 32 a word.  Keys:
+    // their producers wait for the products of two tiles before, which wait for the softmax
+    // of two tiles before that, so eight tiles' are kept.  Values: by stage.
     uint32_t key_flags[8], val_flags[2];
+    uint32_t key_big[8][4], val_big[2][4];
+    float large[256];  // by row: its largest logit with a large value of the tile, and kDown
     int64_t scratch[17 + 2];
 };
 
@@ -253,37 +330,39 @@ __device__ __forceinline__ bool wide_wait_warp(WideShared &sh, uint64_t *bar, ui
 }
 
 // What a thread needs to find a token's rows.
-template <int D, int BITS, class L>
 struct TokenRows {
-    const KvAttnArgs &a;
-    const Item<L> &it;
-    int kvh;
+    KvCache cache;
+    const int32_t *table;  // of the sequence
+    int kvh, hi, win_lo, sinks;
 
+    template <class L>
+    __device__ __forceinline__ TokenRows(const KvAttnArgs &a, const Item<L> &it, int head)
+        : cache(a.cache), table(a.page_table + it.seq * a.max_pages), kvh(head), hi(it.hi), win_lo(it.win_lo),
+          sinks(a.sinks) {}
     __device__ __forceinline__ bool seen(int t) const {
-        return t < it.hi && (it.win_lo == 0 || t < a.sinks || t >= it.win_lo);
+        return t < hi && (win_lo == 0 || t < sinks || t >= win_lo);
     }
     // Every (some) token of t .. t + 7 is seen.
     __device__ __forceinline__ bool all_seen(int t) const {
-        return t + 7 < it.hi && (it.win_lo == 0 || t >= it.win_lo || t + 7 < a.sinks);
+        return t + 7 < hi && (win_lo == 0 || t >= win_lo || t + 7 < sinks);
     }
     __device__ __forceinline__ bool some_seen(int t) const {
-        return t < it.hi && (it.win_lo == 0 || t < a.sinks || t + 7 >= it.win_lo);
+        return t < hi && (win_lo == 0 || t < sinks || t + 7 >= win_lo);
     }
     // The row of token t's key (which 0) or value, or -1 where its page does not exist.
     __device__ __forceinline__ int64_t row(int t, int which) const {
-        const int page = a.page_table[it.seq * a.max_pages + (t >> a.cache.log2_page)];
-        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.cache.num_pages)) {
+        const int page = table[t >> cache.log2_page];
+        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(cache.num_pages)) {
             atomicOr(&g_kv_attention_status, RN_STATUS_BAD_INDEX);
             return -1;
         }
-        return a.cache.row(page, which, kvh, t & ((1 << a.cache.log2_page) - 1));
+        return cache.row(page, which, kvh, t & ((1 << cache.log2_page) - 1));
     }
 };
 
 // ---- restoring keys ---------------------------------------------------------------------
-// Four warps, BN / 4 tokens each (each with a power of two of its own), eight at a time:
-// lane = token % 8 + 8 j with j the quarter of the stored row.  A group's eight elements
-// are one chunk of the operand.
+// Four warps, BN / 4 tokens each, eight at a time: lane = token % 8 + 8 j with j the
+// quarter of the stored row.  A group's eight elements are one chunk of the operand.
 // A key s * c has up to 18 significant bits: its fp16 and the exact rest, which the
 // fused multiply-add gives, are two operands behind one another.
 template <int D, int BITS, int BN>
@@ -292,15 +371,14 @@ struct KeyTile {
     static constexpr int ITER = BN / 32, KW = F::kGroups * BITS / 4, SW = F::kGroups / 2;
     uint32_t w[ITER][KW], s[ITER][SW];
 
-    template <class Rows>
-    __device__ __forceinline__ void load(const Rows &rows, int t0, int warp, int lane) {
+    __device__ __forceinline__ void load(const TokenRows &rows, int t0, int warp, int lane) {
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             const int t = t0 + warp * (BN / 4) + 8 * i + (lane & 7);
             const int64_t r = rows.seen(t) ? rows.row(t, 0) : -1;
             if (r >= 0) {
-                load_global<KW>(w[i], rows.a.cache.codes + r * F::kRow + (lane >> 3) * KW * 4);
-                load_global<SW>(s[i], rows.a.cache.scales + r * F::kGroups);
+                load_global<KW>(w[i], rows.cache.codes + r * F::kRow + (lane >> 3) * KW * 4);
+                load_global<SW>(s[i], rows.cache.scales + r * F::kGroups);
             } else {
 #pragma unroll
                 for (int k = 0; k < KW; ++k) w[i][k] = 0u;
@@ -315,13 +393,7 @@ struct KeyTile {
         for (int i = 0; i < ITER; ++i)
 #pragma unroll
             for (int k = 0; k < SW; ++k) m = __vmaxu2(m, s[i][k]);
-        return max(m & 0xFFFFu, m >> 16) > kScale255;
-    }
-    __device__ __forceinline__ void scale_down() {  // to 2^-8
-#pragma unroll
-        for (int i = 0; i < ITER; ++i)
-#pragma unroll
-            for (int k = 0; k < SW; ++k) s[i][k] = h2_bits(__hmul2(as_h2(s[i][k]), __float2half2_rn(0.00390625f)));
+        return max(m & 0xFFFFu, m >> 16) > Big<BITS>::kBig;
     }
     __device__ __forceinline__ void store(uint8_t *stage, int warp, int lane) const {
 #pragma unroll
@@ -351,6 +423,27 @@ struct KeyTile {
             }
         }
     }
+    // Takes the large tokens down; returns a bit each of the warp's.  (A call, on a copy.)
+    struct Scales {
+        uint32_t s[ITER][SW];
+    };
+    __device__ __noinline__ static uint32_t tame(Scales &x, int lane) {
+        uint32_t big = 0u;
+#pragma unroll 1
+        for (int i = 0; i < ITER; ++i)
+            if (Big<BITS>::some(x.s[i])) {
+                Big<BITS>::down(x.s[i]);
+                big |= 1u << (8 * i + (lane & 7));
+            }
+        return __reduce_or_sync(0xffffffffu, big);
+    }
+    __device__ __forceinline__ uint32_t tame(int lane) {
+        Scales x;
+        memcpy(x.s, s, sizeof s);
+        const uint32_t big = tame(x, lane);
+        memcpy(s, x.s, sizeof s);
+        return big;
+    }
 };
 
 // ---- restoring values, transposed --------------------------------------------------------
@@ -377,8 +470,7 @@ struct ValueTile {
         p.part = SPLIT == 2 ? warp >> 1 : 0;
         return p;
     }
-    template <class Rows>
-    __device__ __forceinline__ void load(const Rows &rows, int t0, const Place &p) {
+    __device__ __forceinline__ void load(const TokenRows &rows, int t0, const Place &p) {
         const int t = t0 + 8 * p.chunk;
         const int64_t r = rows.some_seen(t) ? rows.row(t, 1) : -1;
         const bool all = rows.all_seen(t);
@@ -386,14 +478,13 @@ struct ValueTile {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (r >= 0 && (all || rows.seen(t + i))) {
-                load_global<VW>(w[i], rows.a.cache.codes + (r + i) * F::kRow + (p.r * SPLIT + p.part) * VW * 4);
-                load_global<SW>(s[i], rows.a.cache.scales + (r + i) * F::kGroups + p.part * SW * 2);
-                if constexpr (SPLIT == 2) {
-                    // one exponent serves a token's whole row
-                    uint32_t o[SW];
-                    load_global<SW>(o, rows.a.cache.scales + (r + i) * F::kGroups + (1 - p.part) * SW * 2);
+                load_global<VW>(w[i], rows.cache.codes + (r + i) * F::kRow + (p.r * SPLIT + p.part) * VW * 4);
+                uint32_t row[SPLIT * SW];
+                load_global<SPLIT * SW>(row, rows.cache.scales + (r + i) * F::kGroups);
 #pragma unroll
-                    for (int k = 0; k < SW; ++k) other = __vmaxu2(other, o[k]);
+                for (int k = 0; k < SW; ++k) {
+                    s[i][k] = p.part ? row[(SPLIT - 1) * SW + k] : row[k];
+                    if constexpr (SPLIT == 2) other = __vmaxu2(other, p.part ? row[k] : row[SW + k]);
                 }
             } else {
 #pragma unroll
@@ -409,32 +500,7 @@ struct ValueTile {
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int k = 0; k < SW; ++k) m = __vmaxu2(m, s[i][k]);
-        return max(m & 0xFFFFu, m >> 16) > kScale255;
-    }
-    // The slow way: scales at 2^-8, NaN scales taken out and their groups noted.
-    __device__ __forceinline__ bool tame(uint8_t *nan_groups, const Place &p) {
-        bool any = false;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t groups = 0u;
-#pragma unroll
-            for (int k = 0; k < SW; ++k) {
-                uint32_t lo = s[i][k] & 0xFFFFu, hi = s[i][k] >> 16;
-                if ((lo & 0x7FFFu) > 0x7C00u) {
-                    lo = 0u;
-                    groups |= 1u << (2 * k);
-                }
-                if ((hi & 0x7FFFu) > 0x7C00u) {
-                    hi = 0u;
-                    groups |= 2u << (2 * k);
-                }
-                s[i][k] = h2_bits(__hmul2(as_h2(lo | hi << 16), __float2half2_rn(0.00390625f)));
-            }
-            any |= groups != 0u;
-            // every run of a row notes the same groups; the parts of a row their own
-            if (p.r == 0) nan_groups[(p.part * BN) + 8 * p.chunk + i] = static_cast<uint8_t>(groups << (p.part * 2 * SW));
-        }
-        return any;
+        return max(m & 0xFFFFu, m >> 16) > Big<BITS>::kBig;
     }
     __device__ __forceinline__ void store(uint8_t *stage, const Place &p) const {
         uint8_t *base = stage + (p.chunk >> 3) * (D * 128);
@@ -471,6 +537,39 @@ struct ValueTile {
             put(d, even);
             put(d + 1, odd);
         }
+    }
+    // The slow way: NaN scales are taken out and their groups noted, large tokens taken down.
+    // Returns a bit each of the warp's 32 tokens that are, and in the high word whether
+    // there was a NaN.
+    __device__ __forceinline__ uint64_t tame(const TokenRows &rows, int t0, uint8_t *nan_groups, const Place &p) {
+        uint32_t all = 0u, big = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t groups = 0u;
+#pragma unroll
+            for (int k = 0; k < SW; ++k) {
+                const uint32_t nan = __vcmpgtu2(s[i][k] & 0x7FFF7FFFu, 0x7C007C00u);
+                groups |= (nan & 1u) << (2 * k) | (nan >> 16 & 1u) << (2 * k + 1);
+                s[i][k] &= ~nan;
+            }
+            all |= groups;
+            bool down = Big<BITS>::some(s[i]);
+            if constexpr (SPLIT == 2) {  // one power serves a token's whole row
+                uint32_t o[SW] = {};
+                const int t = t0 + 8 * p.chunk + i;
+                const int64_t r = rows.seen(t) ? rows.row(t, 1) : -1;
+                if (r >= 0) load_global<SW>(o, rows.cache.scales + r * F::kGroups + (1 - p.part) * SW * 2);
+                down |= Big<BITS>::some(o);
+            }
+            if (down) {
+                Big<BITS>::down(s[i]);
+                big |= 1u << (8 * (p.chunk & 3) + i);
+            }
+            // every run of a row notes the same groups; the parts of a row their own
+            if (p.r == 0) nan_groups[p.part * BN + 8 * p.chunk + i] = static_cast<uint8_t>(groups << (p.part * 2 * SW));
+        }
+        big = __reduce_or_sync(0xffffffffu, big);
+        return static_cast<uint64_t>(__any_sync(0xffffffffu, all != 0u)) << 32 | big;
     }
 };
 
@@ -630,54 +729,42 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
                 if (!wide_wait_warp(sh, &sh.s_full[b], S::phase(c))) return false;
                 tc_fence_after();
                 const uint32_t sbase = tmem + lanes + b * BN;
-                const uint32_t kflags = sh.key_flags[n & 7];
-                // the factor of columns 32i + 16h ..
-                const auto factor_of = [&](int i, int h) {
-                    return kflags >> (8 * ((32 * i + 16 * h) / (BN / 4))) & 1u ? factor * 256.0f : factor;
-                };
                 const bool masked = t0 + BN - 1 > it.lo_pos ||
                                     (a.window && t0 <= it.hi - 1 - a.window && t0 + BN > a.sinks);
                 // bit j: the row does not see token t0 + 32i + j
-                const auto hidden = [&](int i) {
-                    const int t = t0 + 32 * i;
-                    return ~below(pos + 1 - t) | (below(lo - t) & ~below(a.sinks - t));
-                };
+                const auto hidden = [&](int i) { return hidden_tokens(pos, lo, a.sinks, t0 + 32 * i); };
                 // (the values' flags are there once their stage is)
                 if (!wide_wait_warp(sh, &sh.v_full[vstage], S::round(n))) return false;
                 const uint32_t vflags = sh.val_flags[vstage];
+                if ((sh.key_flags[n & 7] | vflags) & 0x01010101u) {
+                    const float large = large_logits<BN, Big<BITS>::kDown>(sbase, sh.key_big[n & 7], sh.val_big[vstage],
+                                                                           factor, pos, lo, a.sinks, t0);
+                    sh.large[threadIdx.x] = large;
+                    if (large > m && m != -INFINITY) m = -FLT_MAX;  // the first chunk seen takes a new reference
+                }
 #pragma unroll 1
                 for (int i = 0; i < BN / 32; ++i) {
                     uint32_t v[32];
                     tmem_load32(v, sbase + 32 * i);
-                    float fk[2] = {factor, factor};
-                    if (kflags) {
-                        fk[0] = factor_of(i, 0);
-                        fk[1] = factor_of(i, 1);
-                    }
                     const uint32_t mask = masked ? hidden(i) : 0u;
-                    const bool ve = vflags >> (8 * i) & 1u;  // chunk i: warp i (and i + 2) restored it
                     tmem_wait_load(v);
                     if (masked) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (mask >> j & 1u) v[j] = 0xFF800000u;
                     }
-                    float most[2];
+                    float most = __uint_as_float(v[0]);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        most[h] = __uint_as_float(v[16 * h]);
-#pragma unroll
-                        for (int j = 1; j < 15; j += 2)
-                            most[h] = max3(most[h], __uint_as_float(v[16 * h + j]), __uint_as_float(v[16 * h + j + 1]));
-                        most[h] = fmaxf(most[h], __uint_as_float(v[16 * h + 15]));
-                    }
-                    const float top = fmaxf(most[0] * fk[0], most[1] * fk[1]);
+                    for (int j = 1; j < 31; j += 2)
+                        most = max3(most, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                    const float top = fmaxf(most, __uint_as_float(v[31])) * factor;
                     if (__any_sync(0xffffffffu, top > m)) {
                         // References are whole numbers, so a rescale is exact: of O, and of
                         // this tile's weights already stored.
                         float scale = 1.0f;
                         if (top > m) {
-                            const float nref = ceilf(top) + (kWideSlack - kWideRoom);
+                            const float least = vflags & 0x01010101u ? fmaxf(top, sh.large[threadIdx.x]) : top;
+                            const float nref = ceilf(least) + (kWideSlack - kWideRoom);
                             if (m != -INFINITY) scale = exp2_approx(ref - nref);
                             ref = nref;
                             m = nref + kWideRoom;
@@ -685,22 +772,23 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
                         }
                         if (!rescale(k > k0, i, scale, sbase)) return false;
                     }
-                    const float shift = (ve ? 8.0f : 0.0f) - ref;
+                    const float shift = -ref;
                     uint32_t y[16];
                     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         float p0, p1;
-                        fma2(p0, p1, __uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), fk[j / 8], shift);
+                        fma2(p0, p1, __uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), factor, shift);
                         p0 = exp2_approx(p0);
                         p1 = exp2_approx(p1);
                         add_pairs(sum[0], sum[1], p0, p1);
                         y[j] = h2_bits(__floats2half2_rn(p0, p1));
                     }
                     tmem_store16(sbase + 16 * i, y);  // over columns already read
-                    l = fmaf(sum[0] + sum[1], ve ? 0.00390625f : 1.0f, l);
+                    l += sum[0] + sum[1];
                 }
-                if (vflags & 0x02020202u) {
+                if (vflags) {
+                    if (vflags & 0x01010101u) large_weights<BN, Big<BITS>::kDown>(sbase, sh.val_big[vstage]);
                     for (int w = 0; w < 4; ++w) {
                         if (!(vflags >> (8 * w) & 2u)) continue;
                         const int first = BN == 64 ? 32 * (w & 1) : 32 * w, part_of = BN == 64 ? BN * (w >> 1) : 0;
@@ -756,17 +844,24 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
         const int w = warp - 4 * QT;
         uint32_t n = 0;
         each_run([&](const Item<L> &it, int head, int k0, int k1, float *) {
-            const TokenRows<D, BITS, L> rows{a, it, head};
+            const TokenRows rows(a, it, head);
             KeyTile<D, BITS, BN> tile;
             tile.load(rows, it.token(k0), w, lane);
             for (int k = k0; k < k1; ++k, ++n) {
                 const uint32_t s = S::key_stage(n), par = S::key_round(n);
                 // the products that read this stage before are over
                 if (!wide_wait_warp(sh, &sh.k_free[s], par ^ 1)) return false;
-                const bool small = __any_sync(0xffffffffu, tile.special());
-                if (small) tile.scale_down();
-                if (lane == 0) reinterpret_cast<uint8_t *>(&sh.key_flags[n & 7])[w] = small ? 1 : 0;
+                uint32_t big = 0u;
+                if (__any_sync(0xffffffffu, tile.special()))
+                    big = tile.tame(lane);
                 tile.store(ks + s * S::kKeyStage, w, lane);
+                if (lane == 0) {
+                    reinterpret_cast<uint8_t *>(&sh.key_flags[n & 7])[w] = big ? 1 : 0;
+                    if constexpr (BN == 128)
+                        sh.key_big[n & 7][w] = big;
+                    else
+                        reinterpret_cast<uint16_t *>(sh.key_big[n & 7])[w] = static_cast<uint16_t>(big);
+                }
                 fence_async_shared();
                 mbar_arrive(&sh.k_full[s]);
                 // the next tile's bytes come while this one is used
@@ -780,17 +875,21 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
         const auto place = ValueTile<D, BITS, BN>::place(w, lane);
         uint32_t n = 0;
         each_run([&](const Item<L> &it, int head, int k0, int k1, float *) {
-            const TokenRows<D, BITS, L> rows{a, it, head};
+            const TokenRows rows(a, it, head);
             ValueTile<D, BITS, BN> tile;
             tile.load(rows, it.token(k0), place);
             for (int k = k0; k < k1; ++k, ++n) {
                 const uint32_t s = S::stage(n), par = S::round(n);
                 if (!wide_wait_warp(sh, &sh.v_free[s], par ^ 1)) return false;
-                const bool slow = __any_sync(0xffffffffu, tile.special());
-                bool nan = false;
-                if (slow) nan = __any_sync(0xffffffffu, tile.tame(nan_groups[s], place));
-                if (lane == 0) reinterpret_cast<uint8_t *>(&sh.val_flags[s])[w] = (slow ? 1 : 0) | (nan ? 2 : 0);
+                uint64_t met = 0u;
+                if (__any_sync(0xffffffffu, tile.special()))
+                    met = tile.tame(rows, it.token(k), nan_groups[s], place);
                 tile.store(vs + s * S::kStage, place);
+                if (lane == 0) {
+                    const uint32_t big = static_cast<uint32_t>(met);
+                    sh.val_big[s][w] = big;  // (of 64 tokens, twice)
+                    reinterpret_cast<uint8_t *>(&sh.val_flags[s])[w] = (big ? 1 : 0) | (met >> 32 ? 2 : 0);
+                }
                 fence_async_shared();
                 mbar_arrive(&sh.v_full[s]);
                 if (k + 1 < k1) tile.load(rows, it.token(k + 1), place);

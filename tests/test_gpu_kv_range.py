@@ -12,6 +12,10 @@ largest of the row's, |v| the values' sizes, u = 2^-11 half a step of fp16:
     counts 2^10 at least.  The weight and the product are off by 2^-35 M a unit of code
     each, the scale by 2^-25 2^e w.  More columns: the largest weight W counts 2^10 at
     least, so a weight is off by 2^-35 W;
+  * more than 64 columns: a token with a scale above 65504 / Q (Q the largest code) counts
+    at 2^-3 of its size in 4 bits, 2^-7 in 8, and its weight that much more.  Its scales
+    are off by 2^-25 of that, half a step of subnormal fp16, a unit of code, and the
+    largest weight W is that of w * 2^3 (2^7) for it;
   * the fp32 sums: an instruction adds 17 numbers, each cut to the largest one's 24 bits.
     Up to 304 instructions follow one another here (4000 tokens, 16 an instruction, shared
     by the warps of several CTAs): 300 * 17 * 2^-24 * sum w |v| is far above them all;
@@ -38,7 +42,7 @@ pytestmark = pytest.mark.gpu
 EPS = torch.finfo(torch.bfloat16).eps / 2
 U = torch.finfo(torch.float16).eps / 2
 DOWN = {4: 3, 8: 7}
-TOP = {4: 65504 / 7, 8: 65504 / 127}
+TOP = {4: 9352.0, 8: 515.5}  # the largest scales of which Q is inside fp16
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -167,7 +171,7 @@ def test_values_of_any_size(bits, Hq, Hkv, D, n_q, size):
 
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("Hq,Hkv,D", SHAPES)
-@pytest.mark.parametrize("n_q,extra", [(3, 0), (9, 4096)])
+@pytest.mark.parametrize("n_q,extra", [(3, 0), (9, 4096), (50, 0), (50, 4096)])
 def test_a_huge_token_changes_no_other(bits, Hq, Hkv, D, n_q, extra):
     """A value and a key of 2e5 beside ones of a thousandth: queries that do not see
     them have the same bits as without them, the others are as exact as ever."""
@@ -196,7 +200,7 @@ def test_a_huge_token_changes_no_other(bits, Hq, Hkv, D, n_q, extra):
 
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("Hq,Hkv,D", SHAPES)
-@pytest.mark.parametrize("n_q", [1])
+@pytest.mark.parametrize("n_q", [1, 50])
 def test_huge_values_with_weight(bits, Hq, Hkv, D, n_q):
     """Several huge tokens of which each may dominate, NaN beside them in another group."""
     L = 400
