@@ -599,14 +599,21 @@ int kv_cache_read(const uint8_t *codes, const rn_f16 *scales, int format, int Hk
  * query sees a token are not used.  Requirements: Hq a multiple of Hkv; T * Hq,
  * B * Hq, max_q_len * Hq and max_pages * page_size < 2^31; scale finite,
  * window and sinks >= 0; scale * |q| and every logit below 2^100.
- * Arithmetic: a logit is an fp32 sum of exact products of query and key; a
- * softmax weight and its product with a value scale (where max_q_len * Hq / Hkv is
- * above 64: the weight and the value, or as before for sequences of few queries
- * that such a call launches apart) are each rounded to fp16, 2^-11 relative, before
- * fp32 sums.  A NaN reaches the outputs whose formula holds it
- * and no others.  The results do not depend on timing: the same call gives the
- * same bits.  Errors as kv_cache_write; a workspace that is too small is
- * RN_ERR_ARG. */
+ * Arithmetic, with max_q_len * Hq / Hkv up to 64 (and for sequences of few queries that
+ * a larger call launches apart): a logit is an fp32 sum of exact products of query and
+ * stored code, whose offset comes off the sum.  A softmax weight w, and its product with a
+ * value's scale, are each rounded to fp16: by 2^-11 of it at most, or if that is more by
+ * 2^-35 of the largest w * S of the row's tokens, S a token's largest value scale in
+ * the head (2^-15 at least); scales below 2^-13 S by 2^-24 S.
+ * Above 64: the products are of query and key, and exact.  A weight and a value are each
+ * rounded to fp16: by 2^-11 of it at most, the weight if that is more by 2^-35 of the
+ * row's largest.  A token with a scale above 9352 (4 bits) or 515.5 (8 bits) counts at 2^-3
+ * or 2^-7 of its size and its weight that much more; its scales are rounded by 2^-22 (2^-18).
+ * In both, elements of a query head below 2^-24 of its largest are rounded by 2^-34 of it
+ * at most.  A token that a query does not see changes nothing for it.
+ * A NaN reaches the outputs whose formula holds it and no others.  The results do not
+ * depend on timing: the same call gives the same bits.  Errors as kv_cache_write; a
+ * workspace that is too small is RN_ERR_ARG. */
 int kv_attention_fwd(const rn_bf16 *q, int64_t q_stride, const uint8_t *codes,
                      const rn_f16 *scales, int format, int Hq, int Hkv, int D,
                      int page_size, int64_t num_pages, const int32_t *page_table,

@@ -7,6 +7,7 @@
 // tcgen05.mma with the columns as the 128 rows of the accumulator:
 //   S = Q K'^T + Q K''^T   Q, K' and K'' in shared memory, S in tensor memory,
 //   O += P V'              P in tensor memory (over its S), V' in shared memory.
+// P and V' are fp16, the tensor cores' rate being half in tf32 and tensor memory full.
 // V' is the cached value s * c rounded once to fp16, K' the same of the key and K''
 // the exact rest, so the logits (and lse) have no rounding but that of fp32 sums.
 // Queries as in kv_attention.cu.  A token with a scale so large that s * c would leave
@@ -36,8 +37,11 @@
 
 namespace rn {
 
-constexpr float kWideRoom = 6.0f;   // weights (times 2^kDown of a large token) stay below 2^6
-constexpr float kWideSlack = 4.0f;  // powers of two a weight may grow before a rescale
+// Weights (times 2^kDown of a large token) stay below 2^kWideRoom.  They are fp16, and a new
+// reference leaves them kWideSlack powers of two to grow before a rescale: the largest is
+// 2^10 at least, so 2^-24 of it is a normal number.
+constexpr float kWideRoom = 15.0f;
+constexpr float kWideSlack = 4.0f;
 constexpr long long kWideLimit = 4000000000ll;  // clocks a wait may take, about two seconds
 
 // QT query tiles of 128 columns at a time: two share the restored tiles and take
@@ -289,6 +293,24 @@ __device__ __noinline__ void large_weights(uint32_t sbase, const uint32_t *val_b
         }
         tmem_store16(sbase + 16 * i, x);
     }
+}
+
+// Brings stored weights, 32 of each of the tile's first `chunks` quarters, down by a power of
+// two: in two steps, as it may be too small for fp16 where what it leaves of a weight is not.
+__device__ __forceinline__ void scale_weights(uint32_t sbase, int chunks, float scale) {
+    const uint32_t half = (127u - (__float_as_uint(scale) >> 23)) >> 1;
+    const __half2 first = __float2half2_rn(__uint_as_float((127u - half) << 23));
+    const __half2 second = __float2half2_rn(scale * __uint_as_float((127u + half) << 23));
+    tmem_wait_store();
+#pragma unroll 1
+    for (int i = 0; i < 16 * chunks; i += 16) {
+        uint32_t x[16];
+        tmem_load16(x, sbase + i);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = h2_bits(__hmul2(__hmul2(as_h2(x[j]), first), second));
+        tmem_store16(sbase + i, x);
+    }
+    tmem_wait_store();
 }
 
 struct WideShared {
@@ -702,23 +724,17 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
             const int lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
             // Multiplies O and the weights of the tile's first `chunks` quarters by scale.
             const auto rescale = [&](bool sums, int chunks, float scale, uint32_t sbase) {
-                if (sums) {
-                    if (!wide_wait_warp(sh, &sh.pv_done[S::buf(qt, c - 1)], S::phase(c - 1))) return false;
-                    tc_fence_after();
-                }
-                tmem_wait_store();
-                const __half2 hs = __float2half2_rn(scale);
+                if (chunks) scale_weights(sbase, chunks, scale);
+                if (!sums) return true;
+                if (!wide_wait_warp(sh, &sh.pv_done[S::buf(qt, c - 1)], S::phase(c - 1))) return false;
+                tc_fence_after();
 #pragma unroll 1
-                for (int i = 0; i < chunks + (sums ? D / 16 : 0); ++i) {
-                    const bool weight = i < chunks;
-                    const uint32_t at = weight ? sbase + 16 * i : obase + 16 * (i - chunks);
+                for (int i = 0; i < D; i += 16) {
                     uint32_t x[16];
-                    tmem_load16(x, at);
+                    tmem_load16(x, obase + i);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        x[j] = weight ? h2_bits(__hmul2(as_h2(x[j]), hs))
-                                      : __float_as_uint(__uint_as_float(x[j]) * scale);
-                    tmem_store16(at, x);
+                    for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * scale);
+                    tmem_store16(obase + i, x);
                 }
                 tmem_wait_store();
                 return true;
