@@ -623,8 +623,9 @@ int kv_attention_fwd(const rn_bf16 *q, int64_t q_stride, const uint8_t *codes,
                      void *workspace, int64_t workspace_bytes, rn_stream_t stream);
 
 /* Bytes of workspace a kv_attention_fwd call of these sizes needs on the
- * current device (a negative RN_ERR_* code for sizes it refuses).  Host-only
- * query: launches nothing. */
+ * current device (a negative RN_ERR_* code for sizes it refuses).  It does not
+ * decrease in B, Hq or max_q_len: a workspace for the largest call of a program
+ * serves them all.  Host-only query: launches nothing. */
 int64_t kv_attention_workspace_bytes(int format, int64_t B, int Hq, int Hkv, int D,
                                      int64_t max_q_len);
 

@@ -958,13 +958,17 @@ static int attn_launch(KvAttnArgs &a, cudaStream_t st) {
     return join_launch<D, typename S::L>(a, st);
 }
 
-// Workspace of a call, whichever launches it takes.
+// Workspace of a call, whichever launches it takes; one for max_q_len queries also serves
+// calls of fewer, whose kernels may have more CTAs: the most of all up to as many columns.
 static int64_t attn_bytes(int sm_count, int format, int64_t B, int group, int D, int64_t max_q_len) {
-    const int64_t all = attn_plan(sm_count, format, B, group, D, max_q_len).bytes;
-    const int64_t few = attn_few(D, group, max_q_len);
-    if (few == 0) return all;
-    const int64_t part = attn_plan(sm_count, format, B, group, D, few).bytes;
-    return part > all ? part : all;
+    const int64_t columns = max_q_len * group;
+    int64_t most = 0;
+    for (const int64_t c : {static_cast<int64_t>(8), static_cast<int64_t>(16), static_cast<int64_t>(64),
+                            static_cast<int64_t>(128), columns}) {
+        const int64_t bytes = attn_plan(sm_count, format, B, 1, D, c < columns ? c : columns).bytes;
+        most = bytes > most ? bytes : most;
+    }
+    return most;
 }
 
 // Whether sequences of few queries get a launch of their own, before the others': where

@@ -90,3 +90,46 @@ def test_results_the_caller_still_reads_are_not_written_again(which, kind):
     torch.cuda.synchronize()
     for x, y, z in zip(copies, want, again):
         assert torch.equal(x, y) and not torch.equal(z, y)
+
+
+@pytest.mark.parametrize("format", [binding.RN_KV_INT4, binding.RN_KV_INT8])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_workspaces_never_shrink_as_calls_grow(format, D):
+    query = binding.load().kv_attention_workspace_bytes
+    Hkv = 2
+    for group in (1, 2, 3, 4, 5, 8, 16, 20, 70, 130):
+        last = 0
+        for n in [*range(0, 140), 255, 256, 257, 5000]:
+            now = query(format, 3, group * Hkv, Hkv, D, n)
+            assert now >= last, (group, n)
+            last = now
+    for n in (1, 2, 7, 20, 100):
+        last = 0
+        for group in range(1, 200):
+            now = query(format, 3, group * Hkv, Hkv, D, n)
+            assert now >= last, (group, n)
+            last = now
+        assert query(format, 500, 8, Hkv, D, n) >= query(format, 3, 8, Hkv, D, n)
+
+
+@pytest.mark.parametrize("format", [binding.RN_KV_INT4, binding.RN_KV_INT8])
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 32, 8), (128, 32, 8), (256, 16, 4)])
+def test_one_workspace_for_calls_of_up_to_its_sizes(format, D, Hq, Hkv):
+    """A server's workspace for its longest draft, used by shorter ones."""
+    B, P, L, longest = 3, 64, 2048, 40
+    cache = plain_cache(B * L // P, Hkv, D, P, format)
+    table = torch.arange(B * L // P, dtype=torch.int32, device="cuda").view(B, -1)
+    lens = torch.tensor([L, 900, 77], dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(1)
+    ws = {n: binding.kv_attention_workspace(cache, B, Hq, max_q_len=n) for n in (16, longest)}
+    for n in (1, 2, 3, 4, 5, 16, 17, 32, 33, longest):
+        q = torch.randn(B * n, Hq, D, generator=g).bfloat16().cuda()
+        cu = torch.arange(B + 1, device="cuda") * n
+        want = binding.kv_attention_fwd(q, cache, table, lens, Hq, cu_q=cu, max_q_len=n)
+        for most, w in ws.items():
+            if n <= most:
+                w.fill_(0xFF)
+                got = binding.kv_attention_fwd(q, cache, table, lens, Hq, cu_q=cu, max_q_len=n,
+                                               workspace=w)
+                assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert binding.device_status() == 0
