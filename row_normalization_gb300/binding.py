@@ -775,7 +775,7 @@ def _workspace_bytes(cache: KVCache, B: int, Hq: int, max_q_len: int) -> int:
 
 def kv_attention_fwd(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
                      kv_lens: torch.Tensor, Hq: int, *, cu_q: torch.Tensor | None = None,
-                     max_q_len: int = 1, scale: float | None = None, window: int = 0,
+                     max_q_len: int | None = None, scale: float | None = None, window: int = 0,
                      sinks: int = 0, out: torch.Tensor | None = None,
                      lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                      stream=None):
@@ -788,11 +788,16 @@ def kv_attention_fwd(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
     page_table  int32 [B, max_pages];  kv_lens int32 [B]: tokens in the cache
     cu_q        int64 [B + 1]: sequence b's queries are rows cu_q[b] ..
                 cu_q[b+1] - 1; None: one query for each sequence
-    max_q_len   the largest number of queries of a sequence
+    max_q_len   the largest number of queries of a sequence; to be given with cu_q (queries
+                beyond it would stay unwritten), 1 without
     scale       softmax scale, default D ** -0.5
 
     Returns (out [T, Hq, D] bf16, lse [T, Hq] fp32, natural logarithms).  Rows
     outside every sequence are left as they were."""
+    if max_q_len is None:
+        if cu_q is not None:
+            raise ValueError("with cu_q, max_q_len has to be given")
+        max_q_len = 1
     dev = _kv_device(cache)
     D = cache.head_dim
     if not isinstance(q, torch.Tensor) or q.get_device() != dev:
