@@ -563,8 +563,8 @@ int kv_cache_write(const rn_bf16 *qkv, const int64_t *slots, int64_t T, int Hq,
  *   page_table [B, max_pages] int32; cu_lens [B + 1] int64, nondecreasing;
  *   starts [B] int32, or NULL for all zero.
  * Rows outside [cu_lens[0], cu_lens[B]) are left as they were.  A token behind
- * the table's end or on a page outside [0, num_pages) reads as zeros and
- * raises RN_STATUS_BAD_INDEX.  k and v must not overlap each other or the
+ * the table's end or on a page outside [0, num_pages) reads as zeros, one whose
+ * row is outside [0, total) is not written: each raises RN_STATUS_BAD_INDEX.  k and v must not overlap each other or the
  * cache.  total * Hkv < 2^31.  Errors as kv_cache_write; k == v is RN_ERR_ARG. */
 int kv_cache_read(const uint8_t *codes, const rn_f16 *scales, int format, int Hkv,
                   int D, int page_size, int64_t num_pages,

@@ -310,6 +310,9 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvReadArgs a)
     const uint32_t part = blockIdx.x * (kKvThreads / kRowLanes) + threadIdx.x / kRowLanes;
     const uint32_t i = part / a.parts;
     const int h0 = static_cast<int>(part - i * a.parts) * kHeads;
+    // offsets that name rows the results do not have
+    if (part == 0 && l == 0 && (a.cu_lens[0] < 0 || a.cu_lens[a.B] > static_cast<int64_t>(a.rows)))
+        atomicOr(&g_kv_cache_status, RN_STATUS_BAD_INDEX);
     const int64_t b = i < a.rows ? sequence_of_row(a.cu_lens, a.B, i) : -1;
     // lanes without a row take part in the warp's shuffles only
     if (__all_sync(0xffffffffu, b < 0)) return;

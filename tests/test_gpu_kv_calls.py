@@ -133,3 +133,22 @@ def test_one_workspace_for_calls_of_up_to_its_sizes(format, D, Hq, Hkv):
                                                workspace=w)
                 assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert binding.device_status() == 0
+
+
+@pytest.mark.parametrize("cu,total,bad", [([0, 40, 60], 60, False), ([5, 40, 60], 64, False),
+                                          ([0, 40, 60], 59, True), ([0, 40, 60], 7, True),
+                                          ([-3, 40, 60], 60, True), ([0, 0, 0], 4, False),
+                                          ([100, 140, 160], 60, True)])
+def test_reads_that_have_more_rows_than_their_results_say_so(cu, total, bad):
+    cache = plain_cache(8, 3, 64, 16, binding.RN_KV_INT8)
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+    k, v = (torch.full((total, 3, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    binding.kv_cache_read(cache, table, torch.tensor(cu).cuda(), total, k=k, v=v)
+    assert binding.device_status() == (binding.RN_STATUS_BAD_INDEX if bad else 0)
+    want, _ = binding.kv_cache_read(cache, table, torch.tensor([0, 64, 128]).cuda(), 128)
+    for row in range(total):
+        b = 0 if row < cu[1] else 1
+        if cu[0] <= row < cu[2]:
+            assert torch.equal(k[row], want[64 * b + row - cu[b]])
+        else:
+            assert (k[row] == 7).all() and (v[row] == 7).all()
