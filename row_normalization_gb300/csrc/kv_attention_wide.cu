@@ -786,6 +786,7 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
                             m = nref + kWideRoom;
                             l *= scale;
                         }
+                        __syncwarp();  // (tensor memory is for whole warps)
                         if (!rescale(k > k0, i, scale, sbase)) return false;
                     }
                     const float shift = -ref;
@@ -829,22 +830,22 @@ __global__ void __launch_bounds__(WideShape<D, BITS, QT>::kThreads, 1) kv_attent
                 tmem_load32(x, obase + 32 * i);
                 tmem_wait_load(x);
                 const float unit = nan_mask >> i & 1u ? __uint_as_float(0x7FC00000u) : scale;
-                if (!live) continue;
                 float y[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(x[j]) * unit;
-                if (part) {
+                if (live && part) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 4)
                         *reinterpret_cast<float4 *>(part + col * D + 32 * i + j) =
                             make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-                } else {
+                } else if (live) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 8)
                         st16(a.out + out_row * D + 32 * i + j,
                              make_uint4(pack_bf2(y[j], y[j + 1]), pack_bf2(y[j + 2], y[j + 3]),
                                         pack_bf2(y[j + 4], y[j + 5]), pack_bf2(y[j + 6], y[j + 7])));
                 }
+                __syncwarp();  // (the next load is the whole warp's)
             }
             if (live && part) {
                 part[NQ * D + col] = m == -INFINITY ? -INFINITY : ref;
