@@ -54,7 +54,7 @@ constexpr float kTop = 15.0f;        // weights stay below 2^kTop
 constexpr float kSlack = 4.0f;       // powers of two a weight may grow before a rescale
 // Units without work in front of each (query tile, head): its queries, first page and
 // copies, and the joining of its warps.  64 ragged sequences of 8 heads (540k tokens):
-// 175 us with none, 158 with 8, 128 with 16, 132 with 32; 4 long ones 124-126 throughout.
+// 145 us with none, 129 with 8, 124 with 16, 130 with 32; 4 long ones 116-118 throughout.
 constexpr int kLead = 16 * 32;  // in tokens
 constexpr int kMinTokens = 32 * kAttnWarps;  // a CTA's run is no shorter
 
@@ -63,8 +63,9 @@ template <int D, int BITS, int NT>
 struct AttnShape {
     using F = KvFormat<D, BITS>;
     static constexpr int NQ = 8 * NT;
-    // tokens a warp takes at once: 16 where 32 would leave room for one CTA an SM (17
-    // sequences, drafts of 3 to 5 tokens, heads of 256 in 8 bits: 47 against 57 us)
+    // tokens a warp takes at once: 16 where 32 would leave room for one CTA an SM (heads of
+    // 256 in 8 bits: 17 sequences, drafts of 3 to 5 tokens 51 against 61 us; 64 sequences,
+    // one token each 63 against 66)
     static constexpr int kTile = D == 256 && BITS == 8 ? 16 : 32;
     using L = LineShape<NQ, kTile, kLead / kTile, kMinTokens / kTile>;
     static constexpr int MT = D / 16;                 // 16-row tiles of the value product
@@ -76,9 +77,9 @@ struct AttnShape {
     // the operands, which then serve several instructions)
     static constexpr bool kKeySums = NT == 1;
     // CTAs an SM is to hold: by registers (O alone is MT * NT * 4 a thread), fewer with
-    // deeper rings in 8 bits, where the bytes bound (heads of 128, 64 sequences: 185 us
-    // with two, 230 with three; heads of 64, 96 sequences: 104 with three, 115 with four;
-    // in 4 bits 112 with three, 119 with two), and by shared memory for two stages
+    // deeper rings in 8 bits, where the bytes bound (heads of 128, 64 sequences: 184 us
+    // with two, 190 with three; heads of 64, 96 sequences: 90 with three, 91 with four; in
+    // 4 bits 124 with three, 137 with two), and by shared memory for two stages
     static constexpr int kQuery = NQ * D * 2;  // the queries, as operand registers
     static constexpr int kRoom = 224 * 1024;
     static constexpr int stages_at(int ctas) { return ctas < 1 ? 0 : (kRoom / ctas - 2048 - kQuery) / (kAttnWarps * kStage); }
@@ -872,8 +873,8 @@ int kv_attention_status(unsigned int *out, int clear) {
 
 // More columns than this go to the kernel that takes 128 of them at a time (16 sequences
 // of 3000 to 8000 tokens, 8 heads; this kernel against that one, us: heads of 128 in 4
-// bits, 64 columns 124 / 145, 128 columns 223 / 153; heads of 64 in 8 bits 71 / 101 and
-// 125 / 105; heads of 256 in 4 bits 250 / 321 and 478 / 336).
+// bits, 64 columns 132 / 157, 128 columns 243 / 166; heads of 64 in 8 bits 76 / 107 and
+// 139 / 111; heads of 256 in 4 bits 256 / 324 and 493 / 337).
 static bool wide(int64_t columns) { return columns > 64; }
 
 // Columns of a query tile, in eights: the smallest that holds all queries of a
@@ -919,7 +920,9 @@ static AttnPlan attn_plan(int sm_count, int format, int64_t B, int group, int D,
 }
 
 // Up to how many queries a sequence may go to a launch of its own: eight columns, or one
-// token; 0 where max_q_len's kernel is the same, or takes 16 columns and is as good.
+// token; 0 where max_q_len's kernel is the same, or takes 16 columns (single tokens pay
+// for that: 64 of them over 4000 to 16000 tokens, 4 bits, 211 us where max_q_len is 4, 152
+// where it is 1).
 static int64_t attn_few(int D, int group, int64_t max_q_len) {
     const int64_t few = group < 8 ? 8 / group : 1, columns = few * group, most = max_q_len * group;
     if (wide(columns) || max_q_len <= few) return 0;
@@ -929,8 +932,8 @@ static int64_t attn_few(int D, int group, int64_t max_q_len) {
 // Whether each (query tile, head) gets a CTA of its own: no line, no joining.  Where no
 // CTA can meet more than 1024 tokens, or 2048 and there are heads to fill the GPU (one
 // token a sequence, 4 bits, 8 heads of 128, us on the line / directly: 4 sequences of up
-// to 700 tokens 10.1 / 7.3, 256 of up to 900 59 / 50; of 300 to 1900 tokens 16
-// sequences 15.8 / 17.4, 64 of them 30.1 / 29.1; of 1000 to 4000, 16: 24 / 33).
+// to 700 tokens 10.3 / 7.8, 256 of up to 900 55 / 50; of 300 to 1900 tokens 16
+// sequences 15.8 / 18.2, 64 of them 30.6 / 30.4; of 1000 to 4000, 16: 25 / 36).
 static bool attn_direct(const KvAttnArgs &a, int columns) {
     const int64_t most = attn_most_tokens(a, columns), busy = attn_busy_heads(a, columns);
     if (a.heads > 2 * busy || a.heads > INT32_MAX) return false;  // a grid of CTAs without work
@@ -975,8 +978,8 @@ static int64_t attn_bytes(int sm_count, int format, int64_t B, int group, int D,
 // there are at most half as many queries as max_q_len allows (some sequences then have
 // far fewer than others), and sequences enough to pay for the second launch.  One chunk
 // of n queries among sequences of one (32 and 8 heads of 128 in 4 bits, contexts of up
-// to 2000 tokens, us in one / in two): 64 sequences, n 4 49 / 61, 12 88 / 72, 60 226 / 95,
-// 500 284 / 107; 16, n 12 32 / 46, 60 71 / 63, 500 113 / 81; 4, n 60 37 / 51, 500 76 / 76.
+// to 2000 tokens, us in one / in two): 64 sequences, n 12 85 / 69, 60 185 / 94, 500 294 /
+// 109; 16, n 12 33 / 44, 60 77 / 64, 500 121 / 82; 4, n 60 39 / 51, 500 78 / 76.
 static bool attn_mixed(const KvAttnArgs &a, int64_t few, int sm_count) {
     if (few == 0 || !a.cu_q || 2 * a.T > a.B * a.max_q_len) return false;
     const int64_t heads = (a.T < a.B ? a.T : a.B) * a.cache.Hkv;  // that may have a query
@@ -1008,7 +1011,7 @@ static int kv_attention_check(int format, int64_t B, int Hq, int Hkv, int D, int
     if (rc != RN_OK) return rc;
     if (Hq < 1 || Hq > 65535 || Hq % Hkv != 0) return RN_ERR_SHAPE;
     if (B < 0 || B > INT32_MAX / Hq || max_q_len < 0 || max_q_len > INT32_MAX / Hq) return RN_ERR_SHAPE;
-    // one block of the second kernel for each sequence and query tile
+    // make_item counts (sequence, query tile)s in 31 bits, tiles of eight columns at least
     if (B > 0 && (max_q_len * (Hq / Hkv) + 7) / 8 > INT32_MAX / B) return RN_ERR_SHAPE;
     return RN_OK;
 }

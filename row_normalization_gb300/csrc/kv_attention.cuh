@@ -60,6 +60,8 @@ struct LineShape {
     static constexpr int NQ = NQ_, TILE = TILE_, LEAD = LEAD_, MIN = MIN_;
 };
 
+// 2^x to 2^-22 of it, and zero below 2^-126: the weights are rounded to 2^-11 behind it,
+// and the factors that join sums are as good as the sums.
 __device__ __forceinline__ float exp2_approx(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -456,7 +458,8 @@ inline int64_t attn_most_tokens(const KvAttnArgs &a, int columns) {
 
 // About how many (query tile, kv head)s have work: by the queries there are, not those that
 // max_q_len allows for.  (The second launch of a mixed call counts on few sequences: of 16
-// one with 60 queries over 2000 tokens took 50 us with a CTA for each head, 32 on the line.)
+// one with 60 queries over 2000 tokens took 50 us with a CTA for each head, 32 on the line,
+// when this was chosen.)
 inline int64_t attn_busy_heads(const KvAttnArgs &a, int columns) {
     const int64_t busy = (a.T * a.group / columns + (a.min_q > 1 ? 1 : a.B)) * a.cache.Hkv;
     return busy < a.heads ? busy : a.heads;

@@ -20,12 +20,16 @@
 // of one run beside the softmax of the other.
 //
 // What bounds it: 64 queries over 131072 tokens of 8 heads of 128 in 4 bits (two query
-// tiles) take 284 us, 484 TFLOP/s: 10300 clocks a tile of 256 columns by 128 tokens,
+// tiles) take 247 us, 556 TFLOP/s: 9000 clocks a tile of 256 columns by 128 tokens,
 // of which the products need 3000 and the exponentials (16 a clock and SM) 2000.  No
-// unit is full (tensor cores about a quarter, issue slots a third): with a form
+// unit is full (tensor cores about a third, issue slots a third): with an earlier form
 // without K'' that took 8700 clocks, leaving out the restoring gave 7000, three
 // quarters of the softmax 8300, most of the products 7100, all of these 2900.  What
-// is left is each role's latency and the handing over between them.
+// is left is each role's latency, the handing over between them, and registers: with two
+// query tiles 17 warps are allotted as 20, 96 registers a thread, and up to 540 bytes a
+// thread are spilled and reloaded (with one tile 13 warps have 128, and a tenth of that).
+// How much code lies between the roles' loops shows as well: forms that differ in nothing
+// that runs differ by 10%.
 //
 // Shared memory operands are K-major with the 128-byte exchange of 16-byte chunks
 // (chunk ^ row % 8 in rows of 128 bytes): 64 elements a row, blocks of 64 elements
@@ -51,8 +55,9 @@ template <int D, int BITS, int QT>
 struct WideShape {
     using F = KvFormat<D, BITS>;
     // Tokens of a tile.  (D 128 with two query tiles: tiles of 64 would leave tensor
-    // memory for two S each, but what a tile costs beside its tokens outweighs that: 64
-    // queries over 131072 tokens of 8 heads 289 against 257 us.)
+    // memory for two S each, but what a tile costs beside its tokens outweighs that: in an
+    // earlier form, without K'', 64 queries over 131072 tokens of 8 heads 289 against 257
+    // us.)
     static constexpr int BN = D == 256 ? 64 : 128;
     static constexpr int kBufs = QT * (2 * BN + D) <= 512 ? 2 : 1;  // S of a query tile
     static constexpr int kStages = 2;                                              // of values
@@ -71,6 +76,7 @@ struct WideShape {
     // tensor memory columns: the S buffers, then O
     static constexpr uint32_t kO = QT * kBufs * BN;
     static_assert(kO + QT * D <= 512 && kUsed <= 226 * 1024, "tensor and shared memory");
+    static_assert(QT * kBufs <= 2 && kKeyStages <= 2 && kStages <= 2, "WideShared has barriers for two of each");
     // S buffer and barrier phase of a query tile's c-th tile of tokens
     __device__ static __forceinline__ uint32_t buf(uint32_t qt, uint32_t c) { return qt * kBufs + c % kBufs; }
     __device__ static __forceinline__ uint32_t phase(uint32_t c) { return c / kBufs & 1; }
@@ -993,8 +999,8 @@ static int wide_launch_of(KvAttnArgs &a, cudaStream_t st) {
     // A CTA for each (query tile, head), without line and joining, where there are few
     // tiles of tokens, or heads to fill the GPU with them, or so many that the last round
     // does not matter (chunks of a quarter of their context, 8 heads of 128, us on the
-    // line / directly: contexts of 600, 1 sequence 32 / 29, 32 of them 163 / 141; 2000, 1
-    // sequence 50 / 56, 8 of them 224 / 208; 3000, 16 of them 718 / 679).
+    // line / directly: contexts of 600, 1 sequence 32 / 33, 32 of them 204 / 175; 2000, 1
+    // sequence 62 / 72, 8 of them 298 / 272; 3000, 16 of them 1089 / 1030).
     const int64_t most = attn_most_tokens(a, S::NQ), busy = attn_busy_heads(a, S::NQ);
     a.direct = a.heads <= 2 * busy && a.heads <= INT32_MAX &&  // few CTAs without work
                (most <= 640 || (most <= 2048 && 5 * busy >= 3 * static_cast<int64_t>(a.grid)) ||

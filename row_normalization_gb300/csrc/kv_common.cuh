@@ -28,8 +28,8 @@ struct KvFormat {
 };
 
 // The scale of a group that held a NaN or an infinity: every element reads as
-// NaN.  With the sign bit set it is the smallest 16-bit integer but one, so a
-// signed integer maximum over scales passes it by.
+// NaN.  As a signed 16-bit integer it is -1, so a signed maximum over scales passes
+// it by.
 constexpr uint16_t kKvNanScale = 0xFFFFu;
 
 // Where the cache's parts lie.  Pages are [2, Hkv, P, row]: head h of page p
