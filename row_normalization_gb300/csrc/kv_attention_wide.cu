@@ -26,7 +26,7 @@
 // without K'' that took 8700 clocks, leaving out the restoring gave 7000, three
 // quarters of the softmax 8300, most of the products 7100, all of these 2900.  What
 // is left is each role's latency, the handing over between them, and registers: with two
-// query tiles 17 warps are allotted as 20, 96 registers a thread, and up to 540 bytes a
+// query tiles 17 warps are allotted as 20, 96 registers a thread, and up to 550 bytes a
 // thread are spilled and reloaded (with one tile 13 warps have 128, and a tenth of that).
 // How much code lies between the roles' loops shows as well: forms that differ in nothing
 // that runs differ by 10%.
