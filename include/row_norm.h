@@ -29,6 +29,13 @@
  *                     what follows the fused Q/K step in serving: a paged
  *                     key/value cache in 8 or 4 bits, and causal attention
  *                     (whole, or a sliding window with sinks) over it.
+ *   qk_norm_rope_axes_fwd, qk_norm_rope_axes_bwd
+ *                     the fused Q/K step with rotary positions of several axes
+ *                     (time, height, width), and its gradient.
+ *   token_logprobs_fwd, token_logprobs_bwd
+ *                     rows of logits normalised: log probabilities of given
+ *                     tokens, log-sum-exp, entropy and the largest
+ *                     alternatives, and their gradient.
  *   add_rmsnorm_fwd   h = x + residual (written out) and y = rmsnorm(h), one
  *                     kernel: the norm / residual-add chain fused ("TorchInductor:
  *                     from ATen IR to Triton kernel", sections 14.3 and 14.27).
@@ -96,10 +103,12 @@ enum {
 enum {
     RN_STATUS_WAIT_TIMEOUT = 1u,  /* a pipeline wait ran out; that launch's
                                      output is incomplete                     */
-    RN_STATUS_BAD_POSITION = 2u,  /* qk_norm_rope_fwd_checked met a position
+    RN_STATUS_BAD_POSITION = 2u,  /* qk_norm_rope_fwd_checked or
+                                     qk_norm_rope_axes_* met a position
                                      outside [0, max_pos)                     */
     RN_STATUS_BAD_INDEX = 4u      /* a key/value cache call met a slot, page,
-                                     token or length outside its tensors      */
+                                     token or length outside its tensors, or
+                                     token_logprobs_* a token outside its row */
 };
 
 /* Static description of a code.  Never NULL. */
@@ -230,7 +239,7 @@ int add_rmsnorm_fwd_sched(const rn_bf16 *x, const rn_bf16 *residual,
 /* ------------------------------------------------------------------------ */
 
 /* Element formats and operations of row_norm_fwd_ex. */
-enum { RN_DTYPE_BF16 = 0, RN_DTYPE_F16 = 1 };
+enum { RN_DTYPE_BF16 = 0, RN_DTYPE_F16 = 1, RN_DTYPE_F32 = 2 /* logits only */ };
 enum {
     RN_OP_RMSNORM = 0,      /* rmsnorm_fwd:     x, w            -> y      */
     RN_OP_L2NORM = 1,       /* l2norm_fwd:      x               -> y      */
@@ -632,6 +641,128 @@ int kv_attention_fwd(const rn_bf16 *q, int64_t q_stride, const uint8_t *codes,
  * serves them all.  Host-only query: launches nothing. */
 int64_t kv_attention_workspace_bytes(int format, int64_t B, int Hq, int Hkv, int D,
                                      int64_t max_q_len);
+
+/* ------------------------------------------------------------------------ */
+/* Fused Q/K RMSNorm + rotary positions with several axes, and its gradient   */
+/* ------------------------------------------------------------------------ */
+
+/* qk_norm_rope_fwd_ex for tokens that stand in more than one direction (time,
+ * height, width): pair i of a head turns by the position of axis pair_axis[i],
+ *   p_i = positions[pair_axis[i] * pos_stride + t],
+ *   c = cos_sin[p_i, i],  s = cos_sin[p_i, r/2 + i],  r = rotary_dim,
+ * and everything else is as there: n = x rstd w over the whole head, pairs
+ * (i, i + r/2) or (2i, 2i + 1) by rope_style, dimensions from r on only
+ * normalised, one rounding at the store.  (Frequencies that begin anew on each
+ * axis are columns of the caller's table.)
+ *
+ *   dtype       RN_DTYPE_BF16 or RN_DTYPE_F16: qkv, wq, wk and out.
+ *   qkv         [T, >= (Hq + Hkv) D], rows qkv_stride elements apart: query
+ *               heads, then key heads; what follows in a row is not touched.
+ *   out         the same for the results, rows out_stride apart; qkv itself
+ *               with the same stride (in place), or memory that qkv's heads do
+ *               not overlap.
+ *   cos_sin     [max_pos, r], fp32, or bf16 with table_bf16 = 1; max_pos >= 1.
+ *   positions   int64, axis a's at positions + a * pos_stride (0: one row for
+ *               all axes); always checked: a token with a position outside
+ *               [0, max_pos) on an axis that turns some pair is not written
+ *               and raises RN_STATUS_BAD_POSITION in the status word.
+ *   pair_axis   HOST array of r / 2 axes, each below num_axes (1 to 4); read
+ *               before the call returns.
+ *   Requirements: those of qk_norm_rope_fwd on sizes; strides a multiple of 8
+ *   and at least (Hq + Hkv) D (T <= 1: unused), pos_stride 0 or at least T.
+ * Errors: RN_ERR_NULL, RN_ERR_ALIGN, RN_ERR_SHAPE, RN_ERR_ARG, RN_ERR_DEVICE,
+ * RN_ERR_LAUNCH. */
+int qk_norm_rope_axes_fwd(int dtype, const void *qkv, int64_t qkv_stride, const void *wq,
+                          const void *wk, const void *cos_sin, int table_bf16, int64_t max_pos,
+                          const int64_t *positions, int64_t pos_stride,
+                          const uint8_t *pair_axis, int num_axes, int64_t T, int Hq, int Hkv,
+                          int D, int rotary_dim, float eps, int rope_style, void *out,
+                          int64_t out_stride, rn_stream_t stream);
+
+/* Its gradient.  With R the rotation, g = R^T dout, n^ = x rstd, u = g w:
+ *   dx = rstd (u - n^ mean(u n^)),  dw = sum over tokens and heads of g n^.
+ *   dout        gradient of the forward call's results, laid out as they are,
+ *               rows dout_stride apart.
+ *   qkv ..      the forward call's arguments, qkv as it was BEFORE that call.
+ *   dx          gradient of qkv's query and key heads, rows dx_stride apart;
+ *               may be dout or qkv itself with the same stride, else it overlaps
+ *               neither.  (In place in a packed gradient the value heads stay
+ *               what they are: their own gradient.)
+ *   dwq, dwk    [D] fp32, or NULL: not wanted; accumulate = 1 adds to what they
+ *               hold, 0 overwrites it (also where there is no token).
+ *   workspace   qk_norm_rope_axes_workspace_bytes(D) or more bytes of DEVICE
+ *               memory, 16-byte aligned; needs no clearing; calls that run one
+ *               after another may share it, calls whose kernels may run at the
+ *               same time need one each.
+ * A token that the forward call did not write gets no dx and adds nothing to dw.
+ * The sums are fp32 in an order that the sizes alone give: the same call gives
+ * the same bits.  Errors as the forward call; a workspace that is too small,
+ * or dwq == dwk, is RN_ERR_ARG. */
+int qk_norm_rope_axes_bwd(int dtype, const void *dout, int64_t dout_stride, const void *qkv,
+                          int64_t qkv_stride, const void *wq, const void *wk,
+                          const void *cos_sin, int table_bf16, int64_t max_pos,
+                          const int64_t *positions, int64_t pos_stride,
+                          const uint8_t *pair_axis, int num_axes, int64_t T, int Hq, int Hkv,
+                          int D, int rotary_dim, float eps, int rope_style, void *dx,
+                          int64_t dx_stride, float *dwq, float *dwk, int accumulate,
+                          void *workspace, int64_t workspace_bytes, rn_stream_t stream);
+
+/* Bytes of workspace qk_norm_rope_axes_bwd needs on the current device for heads
+ * of D (a negative RN_ERR_* code otherwise).  Host-only query. */
+int64_t qk_norm_rope_axes_workspace_bytes(int D);
+
+/* ------------------------------------------------------------------------ */
+/* Log probabilities of given tokens                                          */
+/* ------------------------------------------------------------------------ */
+
+/* Rows of logits x [T, V], rows `stride` elements apart, V from 1 to 2^31 - 65,
+ * T < 2^28, in bf16, fp16 or fp32 (dtype; RN_DTYPE_F32 exists for these two
+ * calls only); scale > 0 (1 / temperature), s = scale x:
+ *   lse[t]      = ln sum_v exp(s_v)
+ *   logprobs[t] = s_target - lse        targets [T] int64
+ *   entropy[t]  = -sum_v p_v ln p_v,    p_v = exp(s_v - lse)
+ *   top_logprobs, top_ids [T, top_k]    the top_k largest s_v - lse and their
+ *               columns, in descending order, the lowest column first among
+ *               equal logits; top_k from 0 to 32 and at most V.
+ * fp32 throughout (fp32 sums; 1 - p keeps its precision where a token is nearly
+ * sure).  Any of logprobs (and targets), lse and entropy may be NULL.
+ * Logits need only their elements' alignment, and V and stride may be odd.
+ *   target < 0     ignored: logprobs 0.
+ *   target >= V    logprobs NaN, and RN_STATUS_BAD_INDEX in the status word.
+ *   -infinity      a banned token: probability 0, nothing to the entropy.  A row
+ *                  of nothing else: lse and log probabilities -infinity, entropy 0.
+ *   +infinity      lse +infinity, log probabilities -infinity (of +infinity NaN),
+ *                  entropy NaN.
+ *   NaN            every result of its row NaN; it ranks above every number.
+ * The results do not depend on timing.  Errors: RN_ERR_NULL, RN_ERR_ALIGN,
+ * RN_ERR_SHAPE, RN_ERR_ARG (dtype, scale), RN_ERR_DEVICE, RN_ERR_LAUNCH. */
+int token_logprobs_fwd(int dtype, const void *logits, int64_t stride, const int64_t *targets,
+                       int64_t T, int64_t V, float scale, int top_k, float *logprobs,
+                       float *lse, float *entropy, float *top_logprobs, int64_t *top_ids,
+                       rn_stream_t stream);
+
+/* The gradient by the logits of what comes back for logprobs, entropy and lse
+ * (the top log probabilities have none):
+ *   dlogits_v = scale (dlogprobs (1[v = target] - p_v)
+ *                      - dentropy p_v (s_v - lse + entropy) + dlse p_v)
+ *   logprobs, lse, entropy   [T] fp32, the forward call's; logprobs is read only
+ *               with dlogprobs, entropy only with dentropy.
+ *   dlogprobs, dentropy, dlse   fp32, element t at [t * its stride] (0: one
+ *               value for all rows); each may be NULL (zero).
+ *   dlogits     [T, V] in dtype, rows dlogits_stride apart; logits itself with
+ *               the same stride, or memory that does not overlap it.
+ * An ignored target's dlogprobs counts as 0; with a target >= V the row is NaN
+ * and RN_STATUS_BAD_INDEX is raised.  Banned tokens, and rows of nothing else,
+ * get 0; a row whose lse is NaN or +infinity gets NaN.  A row's accesses are 16
+ * bytes wide where logits and dlogits lie alike within 16 bytes, and an element
+ * wide in dlogits otherwise.  T * ceil(V / 4096) below 2^31.  Errors as the
+ * forward call. */
+int token_logprobs_bwd(int dtype, const void *logits, int64_t stride, const int64_t *targets,
+                       const float *logprobs, const float *lse, const float *entropy,
+                       const float *dlogprobs, int64_t dlogprobs_stride, const float *dentropy,
+                       int64_t dentropy_stride, const float *dlse, int64_t dlse_stride,
+                       int64_t T, int64_t V, float scale, void *dlogits,
+                       int64_t dlogits_stride, rn_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Status word                                                                */

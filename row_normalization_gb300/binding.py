@@ -12,6 +12,7 @@ import ctypes
 import math
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -50,6 +51,7 @@ RN_ROPE_GPTJ = 1
 
 RN_DTYPE_BF16 = 0
 RN_DTYPE_F16 = 1
+RN_DTYPE_F32 = 2  # rows of logits only
 
 RN_OP_RMSNORM = 0
 RN_OP_L2NORM = 1
@@ -64,6 +66,7 @@ RN_WORKSPACE_BYTES = 256
 RN_NOALLOC_SCRATCH_BYTES = 256  # the fixed scratch array of rmsnorm_fwd_noalloc
 
 _ROW_DTYPES = {torch.bfloat16: RN_DTYPE_BF16, torch.float16: RN_DTYPE_F16}
+_LOGIT_DTYPES = {**_ROW_DTYPES, torch.float32: RN_DTYPE_F32}
 
 
 class RowNormError(RuntimeError):
@@ -168,6 +171,18 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.kv_attention_fwd.restype = i32
         L.kv_attention_workspace_bytes.argtypes = [i32, i64, i32, i32, i32, i64]
         L.kv_attention_workspace_bytes.restype = i64
+        axes_in = [vp, i64, vp, vp, vp, i32, i64, vp, i64, vp, i32, i64, i32, i32, i32, i32, f32, i32]
+        L.qk_norm_rope_axes_fwd.argtypes = [i32, *axes_in, vp, i64, vp]
+        L.qk_norm_rope_axes_fwd.restype = i32
+        L.qk_norm_rope_axes_bwd.argtypes = [i32, vp, i64, *axes_in, vp, i64, vp, vp, i32, vp, i64, vp]
+        L.qk_norm_rope_axes_bwd.restype = i32
+        L.qk_norm_rope_axes_workspace_bytes.argtypes = [i32]
+        L.qk_norm_rope_axes_workspace_bytes.restype = i64
+        L.token_logprobs_fwd.argtypes = [i32, vp, i64, vp, i64, i64, f32, i32, vp, vp, vp, vp, vp, vp]
+        L.token_logprobs_fwd.restype = i32
+        L.token_logprobs_bwd.argtypes = [i32, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, vp, i64, i64,
+                                         i64, f32, vp, i64, vp]
+        L.token_logprobs_bwd.restype = i32
         L.rn_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), i32]
         L.rn_device_status.restype = i32
         _lib = L
@@ -705,7 +720,7 @@ def _new(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tenso
 
 
 def _kv_call(dev: int, name: str, *args, stream) -> None:
-    """Calls a key/value cache entry point with the tensors' device current."""
+    """Calls an entry point with the device of its tensors current."""
     L = _lib if _lib is not None else load()
     if dev == torch.cuda.current_device():
         s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
@@ -833,6 +848,265 @@ def kv_attention_fwd(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
              D ** -0.5 if scale is None else scale, window, sinks, op, sp, workspace.data_ptr(),
              workspace.nbytes, stream=stream)
     return out, lse
+
+
+# ---- rotary positions with several axes, and the gradient of the Q/K step ----------
+
+class RopeAxes:
+    """Which axis' position turns each pair of a head: axes[i] (0 to 3) for pair i
+    of rotary_dim / 2.  Checked once, here."""
+    __slots__ = ("axes", "num_axes", "_pair_axis")
+
+    def __init__(self, axes):
+        self.axes = tuple(int(a) for a in axes)
+        if not self.axes or min(self.axes) < 0 or max(self.axes) > 3:
+            raise ValueError("axes must name an axis from 0 to 3 for each pair")
+        self.num_axes = max(self.axes) + 1
+        self._pair_axis = (ctypes.c_uint8 * len(self.axes))(*self.axes)
+
+    def __len__(self) -> int:
+        return len(self.axes)
+
+    def __repr__(self):
+        return f"RopeAxes({list(self.axes)})"
+
+
+def rope_axes(sections, *, interleaved: bool = False) -> RopeAxes:
+    """The axes of sections[a] pairs for each axis a: one section after another, or
+    interleaved: axis a >= 1 takes every len(sections)-th pair from pair a on, axis
+    0 what is left."""
+    sections = [int(n) for n in sections]
+    A, pairs = len(sections), sum(sections)
+    if not 1 <= A <= 4 or min(sections) < 0 or pairs == 0:
+        raise ValueError("sections must give 1 to 4 axes their numbers of pairs")
+    if not interleaved:
+        return RopeAxes([a for a, n in enumerate(sections) for _ in range(n)])
+    axes = [0] * pairs
+    for a in range(1, A):
+        if sections[a] and a + A * (sections[a] - 1) >= pairs:
+            raise ValueError(f"axis {a}: {sections[a]} pairs do not fit every {A}th of {pairs}")
+        for i in range(sections[a]):
+            axes[a + A * i] = a
+    return RopeAxes(axes)
+
+
+def _rows2d(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int, T: int, width: int):
+    """(address, row stride) of a [T, >= width] tensor with contiguous rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the same CUDA device as the other tensors")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != T or shape[1] < width or (t.numel() and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{T}, >= {width}] with contiguous rows")
+    return t.data_ptr(), t.stride(0) if T > 1 else shape[1]
+
+
+def _cuda_device(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _axes_call(qkv, wq, wk, cos_sin, positions, axes, Hq, Hkv, D, rotary_dim, eps, rope_style):
+    """(device, dtype, T, width, the arguments both calls share from qkv on)."""
+    dev = _cuda_device(qkv, "qkv")
+    dt = qkv.dtype
+    if dt not in _ROW_DTYPES:
+        raise TypeError(f"qkv must be torch.bfloat16 or torch.float16, got {dt}")
+    if qkv.dim() != 2:
+        raise ValueError("qkv must be [T, >= (Hq + Hkv) * D]")
+    T, width = qkv.shape[0], (Hq + Hkv) * D
+    xp, xs = _rows2d(qkv, "qkv", dt, dev, T, width)
+    wqp = _on(dev, wq, "wq", dt, D)
+    wkp = _on(dev, wk, "wk", dt, D)
+    table_dt = torch.bfloat16 if cos_sin.dtype is torch.bfloat16 else torch.float32
+    cp = _on(dev, cos_sin, "cos_sin", table_dt)
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != rotary_dim:
+        raise ValueError("cos_sin must be [max_pos, rotary_dim]")
+    if not isinstance(axes, RopeAxes):
+        axes = RopeAxes(axes)
+    if 2 * len(axes) != rotary_dim:
+        raise ValueError(f"axes must name the axis of each of the {rotary_dim // 2} pairs")
+    if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int64 or \
+            positions.get_device() != dev:
+        raise ValueError("positions must be an int64 tensor on qkv's device")
+    ps = positions.shape
+    if len(ps) != 2 or ps[0] < axes.num_axes or ps[1] != T or (T > 1 and positions.stride(1) != 1):
+        raise ValueError(f"positions must be [>= {axes.num_axes}, {T}] with contiguous rows")
+    return dev, dt, T, width, (
+        xp, xs, wqp, wkp, cp, int(table_dt is torch.bfloat16), cos_sin.shape[0],
+        positions.data_ptr(), positions.stride(0) if axes.num_axes > 1 else 0, axes._pair_axis,
+        axes.num_axes, T, Hq, Hkv, D, rotary_dim, eps, rope_style)
+
+
+def qk_norm_rope_axes_fwd(qkv: torch.Tensor, wq: torch.Tensor, wk: torch.Tensor,
+                          cos_sin: torch.Tensor, positions: torch.Tensor, axes, Hq: int, Hkv: int,
+                          D: int, rotary_dim: int, eps: float, *, rope_style: int = RN_ROPE_NEOX,
+                          out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Per-head RMSNorm of the query and key heads of qkv [T, >= (Hq + Hkv) * D]
+    (bf16 or fp16, rows may be strided), then rotary positions with several axes:
+    pair i turns by positions[axes[i], t].
+
+    cos_sin    [max_pos, rotary_dim] fp32 or bf16 (rope_cos_sin_table)
+    positions  int64 [axes, T], always checked: a token outside the table is left
+               unwritten and raises RN_STATUS_BAD_POSITION in device_status()
+    axes       RopeAxes (rope_axes((16, 24, 24))), or the axis of each pair
+
+    In place, or into out [T, >= (Hq + Hkv) * D], whose other columns stay as they
+    were.  Returns what was written."""
+    dev, dt, T, width, args = _axes_call(qkv, wq, wk, cos_sin, positions, axes, Hq, Hkv, D,
+                                         rotary_dim, eps, rope_style)
+    if out is None:
+        out = qkv
+    op, ostride = _rows2d(out, "out", dt, dev, T, width)
+    _kv_call(dev, "qk_norm_rope_axes_fwd", _ROW_DTYPES[dt], *args, op, ostride, stream=stream)
+    return out
+
+
+def qk_norm_rope_axes_workspace(D: int, device=None) -> torch.Tensor:
+    """A workspace for qk_norm_rope_axes_bwd with heads of D.  Calls that run one
+    after another can share one; calls that may run at the same time need one each."""
+    with torch.cuda.device(device):
+        return _new(_axes_workspace_bytes(D), torch.uint8,
+                    torch.device("cuda", torch.cuda.current_device()), None)
+
+
+def _axes_workspace_bytes(D: int) -> int:
+    n = int(load().qk_norm_rope_axes_workspace_bytes(D))
+    if n < 0:
+        raise RowNormError("qk_norm_rope_axes_workspace_bytes", n)
+    return n
+
+
+def qk_norm_rope_axes_bwd(dout: torch.Tensor, qkv: torch.Tensor, wq: torch.Tensor,
+                          wk: torch.Tensor, cos_sin: torch.Tensor, positions: torch.Tensor, axes,
+                          Hq: int, Hkv: int, D: int, rotary_dim: int, eps: float, *,
+                          rope_style: int = RN_ROPE_NEOX, dx: torch.Tensor | None = None,
+                          dwq: torch.Tensor | None = None, dwk: torch.Tensor | None = None,
+                          accumulate: bool = False, workspace: torch.Tensor | None = None,
+                          stream=None):
+    """The gradient of qk_norm_rope_axes_fwd (with one axis: of qk_norm_rope_fwd).
+
+    dout       gradient of the results, [T, >= (Hq + Hkv) * D] in qkv's dtype
+    qkv        as it was before the forward call (which works in place unless it
+               is given an out)
+    dx         gradient of qkv's query and key heads; default: in place in dout,
+               whose value heads then stay what they are
+    dwq, dwk   fp32 [D], new ones by default; accumulate=True adds to those given
+
+    Returns (dx, dwq, dwk)."""
+    dev, dt, T, width, args = _axes_call(qkv, wq, wk, cos_sin, positions, axes, Hq, Hkv, D,
+                                         rotary_dim, eps, rope_style)
+    gp, gs = _rows2d(dout, "dout", dt, dev, T, width)
+    if dx is None:
+        dx = dout
+    dp, ds = _rows2d(dx, "dx", dt, dev, T, width)
+    if accumulate and (dwq is None or dwk is None):
+        raise ValueError("accumulate adds to dwq and dwk, which have to be given")
+    dwq, qp = _result(dev, dwq, "dwq", torch.float32, (D,), qkv.device, stream)
+    dwk, kp = _result(dev, dwk, "dwk", torch.float32, (D,), qkv.device, stream)
+    if workspace is None:
+        with torch.cuda.device(dev):
+            n = _axes_workspace_bytes(D)
+        workspace = _new(n, torch.uint8, qkv.device, stream)
+    elif not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError("workspace must be a contiguous tensor on qkv's device")
+    _kv_call(dev, "qk_norm_rope_axes_bwd", _ROW_DTYPES[dt], gp, gs, *args, dp, ds, qp, kp,
+             int(accumulate), workspace.data_ptr(), workspace.nbytes, stream=stream)
+    return dx, dwq, dwk
+
+
+# ---- log probabilities of given tokens ------------------------------------------------
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs_fwd returns; top_* are None without top_k."""
+    logprobs: torch.Tensor
+    lse: torch.Tensor
+    entropy: torch.Tensor
+    top_logprobs: torch.Tensor | None = None
+    top_ids: torch.Tensor | None = None
+
+
+def _logits(logits: torch.Tensor):
+    """(device, dtype code, T, V, address, row stride) of [T, V] logits."""
+    dev = _cuda_device(logits, "logits")
+    code = _LOGIT_DTYPES.get(logits.dtype)
+    if code is None:
+        raise TypeError(f"logits must be bfloat16, float16 or float32, got {logits.dtype}")
+    if logits.dim() != 2 or logits.shape[1] < 1:
+        raise ValueError("logits must be [T, V]")
+    T, V = logits.shape
+    p, s = _rows2d(logits, "logits", logits.dtype, dev, T, V)
+    return dev, code, T, V, p, s
+
+
+def token_logprobs_fwd(logits: torch.Tensor, targets: torch.Tensor, *, scale: float = 1.0,
+                       top_k: int = 0, logprobs: torch.Tensor | None = None,
+                       lse: torch.Tensor | None = None, entropy: torch.Tensor | None = None,
+                       top_logprobs: torch.Tensor | None = None,
+                       top_ids: torch.Tensor | None = None, stream=None) -> TokenLogprobs:
+    """Log probabilities of the tokens targets [T] (int64; negative: ignored, 0)
+    under softmax(scale * logits), with log-sum-exp, entropy and the top_k (up to
+    32) largest alternatives with their columns, ties to the lowest.
+
+    logits [T, V] in bf16, fp16 or fp32; rows may be strided, -infinity bans a
+    token.  Returns TokenLogprobs(logprobs, lse, entropy [T] fp32, top_logprobs
+    [T, top_k] fp32, top_ids [T, top_k] int64)."""
+    dev, code, T, V, xp, xs = _logits(logits)
+    tp = _on(dev, targets, "targets", torch.int64, T)
+    d, f32 = logits.device, torch.float32
+    logprobs, pp = _result(dev, logprobs, "logprobs", f32, (T,), d, stream)
+    lse, lp = _result(dev, lse, "lse", f32, (T,), d, stream)
+    entropy, ep = _result(dev, entropy, "entropy", f32, (T,), d, stream)
+    kp = ip = None
+    if top_k > 0:
+        top_logprobs, kp = _result(dev, top_logprobs, "top_logprobs", f32, (T, top_k), d, stream)
+        top_ids, ip = _result(dev, top_ids, "top_ids", torch.int64, (T, top_k), d, stream)
+    elif top_logprobs is not None or top_ids is not None:
+        raise ValueError("top_logprobs and top_ids go with a top_k")
+    _kv_call(dev, "token_logprobs_fwd", code, xp, xs, tp, T, V, scale, top_k, pp, lp, ep, kp, ip,
+             stream=stream)
+    return TokenLogprobs(logprobs, lse, entropy, top_logprobs, top_ids)
+
+
+def _row_values(dev: int, t: torch.Tensor | None, name: str, T: int):
+    """(address, stride) of fp32 [T] values, which may be one value expanded."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a float32 tensor on the logits' device")
+    if t.dim() != 1 or t.shape[0] != T:
+        raise ValueError(f"{name} must have {T} elements")
+    return t.data_ptr(), t.stride(0)
+
+
+def token_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor, forward: TokenLogprobs,
+                       dlogprobs: torch.Tensor | None = None,
+                       dentropy: torch.Tensor | None = None, dlse: torch.Tensor | None = None, *,
+                       scale: float = 1.0, dlogits: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """The gradient by the logits of what comes back for logprobs, entropy and lse
+    ([T] fp32 each, or None; an expanded scalar will do), given the forward call's
+    arguments and results.  dlogits may be logits itself.  Returns dlogits."""
+    dev, code, T, V, xp, xs = _logits(logits)
+    tp = _on(dev, targets, "targets", torch.int64, T)
+    pp = _on(dev, forward.logprobs, "forward.logprobs", torch.float32, T)
+    lp = _on(dev, forward.lse, "forward.lse", torch.float32, T)
+    ep = _on(dev, forward.entropy, "forward.entropy", torch.float32, T)
+    given = [v for name, t in (("dlogprobs", dlogprobs), ("dentropy", dentropy), ("dlse", dlse))
+             for v in _row_values(dev, t, name, T)]
+    if dlogits is None:
+        dlogits = _new((T, V), logits.dtype, logits.device, stream)
+    dp, ds = _rows2d(dlogits, "dlogits", logits.dtype, dev, T, V)
+    _kv_call(dev, "token_logprobs_bwd", code, xp, xs, tp, pp, lp, ep, *given, T, V, scale, dp, ds,
+             stream=stream)
+    return dlogits
 
 
 def rmsnorm_select_schedule(M: int, N: int, *, workspace: bool = False) -> int:

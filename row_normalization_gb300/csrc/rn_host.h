@@ -64,6 +64,10 @@ int kv_cache_status(unsigned int *out, int clear);
 int kv_attention_status(unsigned int *out, int clear);
 int kv_attention_wide_status(unsigned int *out, int clear);
 
+// And for the several-axes Q/K step and the log probabilities.
+int qk_axes_status(unsigned int *out, int clear);
+int logprobs_status(unsigned int *out, int clear);
+
 // One row-normalization call, independent of the element format.
 enum RowOp { ROW_RMS = 0, ROW_L2 = 1, ROW_ADD_RMS = 2, ROW_LN = 3 };
 
