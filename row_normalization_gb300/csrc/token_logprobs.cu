@@ -6,17 +6,23 @@
 //   gradient   p_v = e^(s_v - lse),
 //   dx_v = scale (dlogp (1[v = target] - p_v) - dH p_v (s_v - lse + H) + dlse p_v)
 //
-// Forward: one pass over a row, every thread with a running maximum and sums relative to
-// it, joined over the block and, where rows are few, over a cluster of blocks that share a
-// row.  The pass does nothing for the top k but keep each thread's maximum: the k-th
-// largest of those bounds the k-th largest value from below, and only the threads at or
-// above it, k of them but for ties, can hold one of the k; what they read is looked at
-// once more (it is still in L2).  The gradient is one pass without any sum.
+// Forward: one pass over a row, every thread with a running maximum and sums relative to a
+// reference, joined over the block and, where rows are few, over a cluster of blocks that
+// share a row.  The pass does nothing for the top k but note each thread's largest values of
+// runs of its elements: the k-th largest of 32 groups of threads' bounds the k-th largest
+// element from below, and only runs that reach it, little more than k of them but for ties,
+// can hold one of the k; they are looked at once more (they are still in L2).  The gradient
+// is one pass without any sum.
 //
-// What bounds them: HBM; the forward pass needs an exponential for every logit, 16 a clock
-// and SM, where HBM delivers 11.8 logits of 16 bits.
+// What bounds the forward pass: HBM, with the issue slots not far behind.  A logit of 16 bits
+// takes 6.8 instructions (one exponential, half each of a maximum, a clamp and three fused
+// operations, one to widen it), which at HBM's 11.2 logits a clock and SM fill 60% of them; the
+// special function unit is at 45%.  2048 rows of 131072 in bf16: 86.8 us without
+// alternatives, 6.19 TB/s, 93.6 with 8, 102 with 20 (joining a row takes a block about 2 us).
 #include <cooperative_groups.h>
 #include <float.h>
+
+#include <type_traits>
 
 #include "rn_common.cuh"
 #include "rn_host.h"
@@ -28,33 +34,47 @@ namespace cg = cooperative_groups;
 static __device__ unsigned int g_logprobs_status = 0u;
 
 // ---- element formats ----------------------------------------------------------------
-// A row is read in granules of 16 bytes.  kLowBit: the lowest bit in which the ordered
-// keys (below) of two values of the format can differ.
+// A row is read in granules of 16 bytes.
 
 struct Row16Bf {
     using E = Bf16;
     using T = uint16_t;
-    static constexpr int kElems = 8, kLowBit = 16;
+    static constexpr int kElems = 8;
+    static constexpr uint32_t kNone = 0xFF80FF80u;  // a word of -infinity
     __device__ static __forceinline__ float one(T v) { return bf_lo(v); }
-    __device__ static __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    __device__ static __forceinline__ uint32_t below2(float x) {  // two of the next value not above x
+        return 0x10001u * __bfloat16_as_ushort(__float2bfloat16_rd(x));
+    }
+    __device__ static __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
         __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+        return *reinterpret_cast<uint32_t *>(&r);
+    }
+    __device__ static __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
         return *reinterpret_cast<uint32_t *>(&r);
     }
 };
 struct Row16Half {
     using E = F16;
     using T = uint16_t;
-    static constexpr int kElems = 8, kLowBit = 13;
+    static constexpr int kElems = 8;
+    static constexpr uint32_t kNone = 0xFC00FC00u;
     __device__ static __forceinline__ float one(T v) { return F16::lo(v); }
-    __device__ static __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    __device__ static __forceinline__ uint32_t below2(float x) { return 0x10001u * __half_as_ushort(__float2half_rd(x)); }
+    __device__ static __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
         __half2 r = __hmax2_nan(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+        return *reinterpret_cast<uint32_t *>(&r);
+    }
+    __device__ static __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        __half2 r = __hmax2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
         return *reinterpret_cast<uint32_t *>(&r);
     }
 };
 struct Row32 {
     using E = void;
     using T = float;
-    static constexpr int kElems = 4, kLowBit = 0;
+    static constexpr int kElems = 4;
+    static constexpr uint32_t kNone = 0xFF800000u;
     __device__ static __forceinline__ float one(T v) { return v; }
 };
 
@@ -92,17 +112,36 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// The largest of a granule; NaN where it holds one.
-template <class F>
-__device__ __forceinline__ float largest(const uint4 &u) {
+// The largest of some granules; NaN where they hold one.
+template <class F, int N>
+__device__ __forceinline__ float largest(const uint4 (&u)[N]) {
     if constexpr (F::kElems == 8) {
-        const uint32_t w = F::max2(F::max2(u.x, u.y), F::max2(u.z, u.w));
+        uint32_t w = F::max2_nan(F::max2_nan(u[0].x, u[0].y), F::max2_nan(u[0].z, u[0].w));
+#pragma unroll
+        for (int i = 1; i < N; ++i)
+            w = F::max2_nan(w, F::max2_nan(F::max2_nan(u[i].x, u[i].y), F::max2_nan(u[i].z, u[i].w)));
         return max_nan(F::E::lo(w), F::E::hi(w));
     } else {
-        return max_nan(max_nan(__uint_as_float(u.x), __uint_as_float(u.y)),
-                       max_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            m = max_nan(m, max_nan(max_nan(__uint_as_float(u[i].x), __uint_as_float(u[i].y)),
+                                   max_nan(__uint_as_float(u[i].z), __uint_as_float(u[i].w))));
+        return m;
     }
 }
+
+// Two fp32 values; an operation on both is one instruction.
+struct Pair {
+    float2 v;
+    __device__ __forceinline__ static Pair of(float x, float y) { return {make_float2(x, y)}; }
+    __device__ __forceinline__ float2 split() const { return v; }
+    __device__ __forceinline__ float sum() const { return v.x + v.y; }
+    __device__ __forceinline__ Pair operator*(Pair b) const { return {__fmul2_rn(v, b.v)}; }
+    __device__ __forceinline__ Pair operator+(Pair b) const { return {__fadd2_rn(v, b.v)}; }
+    // this * b + c
+    __device__ __forceinline__ Pair fma(Pair b, Pair c) const { return {__ffma2_rn(v, b.v, c.v)}; }
+};
 
 // 32 bits that are ordered as the values are, NaN above all; never 0, so 0 is "none".
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -129,52 +168,72 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // ---- a row --------------------------------------------------------------------------------
 // Granules of a row lie on 16-byte boundaries; its first and last may begin before or end
 // behind it, and only the elements that are the row's are read then.
+// Elements i .. of a row that are in [0, V), as a granule.  (A call: it would be in many places.)
+template <class F>
+__device__ __noinline__ uint4 end_of_row(const typename F::T *x, int i, int V) {
+    uint32_t w[4] = {F::kNone, F::kNone, F::kNone, F::kNone};
+#pragma unroll
+    for (int e = 0; e < F::kElems; ++e)
+        if (i + e >= 0 && i + e < V) {
+            if constexpr (F::kElems == 8)
+                w[e / 2] = __byte_perm(w[e / 2], x[i + e], e & 1 ? 0x5410 : 0x3254);
+            else
+                w[e] = __float_as_uint(x[i + e]);
+        }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 template <class F>
 struct Row {
     const typename F::T *x;
-    int64_t V;
-    int off;           // elements of the first granule in front of the row
-    int64_t granules;
+    int V;
+    int off;       // elements of the first granule in front of the row
+    int granules;
 
-    __device__ __forceinline__ Row(const void *logits, int64_t stride, int64_t t, int64_t V_) : V(V_) {
+    __device__ __forceinline__ Row(const void *logits, int64_t stride, int64_t t, int64_t V_) : V(static_cast<int>(V_)) {
         x = static_cast<const typename F::T *>(logits) + t * stride;
         off = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(typename F::T));
         granules = (off + V + F::kElems - 1) / F::kElems;
     }
     // index of a granule's first element (that of the first may be negative)
-    __device__ __forceinline__ int64_t index(int64_t g) const { return g * F::kElems - off; }
-    __device__ __forceinline__ bool whole(int64_t g) const {
-        const int64_t i = index(g);
-        return i >= 0 && i + F::kElems <= V;
+    __device__ __forceinline__ int index(int g) const { return g * F::kElems - off; }
+    __device__ __forceinline__ bool whole(int g) const {
+        const int i = index(g);
+        return i >= 0 && i <= V - F::kElems;
     }
-    __device__ __forceinline__ uint4 load(int64_t g) const { return *reinterpret_cast<const uint4 *>(x + index(g)); }
-    // A granule's elements, -infinity where it has none; a bit for each that there is.
-    __device__ __forceinline__ uint32_t fetch(int64_t g, float (&v)[F::kElems]) const {
-        const int64_t i = index(g);
-        if (whole(g)) {
-            widen<F>(load(g), v);
-            return (1u << F::kElems) - 1u;
-        }
-        uint32_t there = 0u;
-#pragma unroll
-        for (int e = 0; e < F::kElems; ++e) {
-            const bool in = i + e >= 0 && i + e < V;
-            v[e] = in ? F::one(x[i + e]) : -INFINITY;
-            there |= in ? 1u << e : 0u;
-        }
-        return there;
+    __device__ __forceinline__ uint4 load(int g) const { return *reinterpret_cast<const uint4 *>(x + index(g)); }
+    // A granule, -infinity where it has no element.
+    __device__ __forceinline__ uint4 fetch(int g) const { return whole(g) ? load(g) : end_of_row<F>(x, index(g), V); }
+    // A bit for each element that a granule has.
+    __device__ __forceinline__ uint32_t there(int g) const {
+        const int i = index(g), lo = i < 0 ? -i : 0, hi = V - i < F::kElems ? V - i : F::kElems;
+        return (1u << hi) - (1u << lo);
     }
 };
 
+// Element e of a granule.
+template <class F>
+__device__ __forceinline__ float element(const uint4 &u, int e) {
+    const int word = F::kElems == 8 ? e >> 1 : e;
+    const uint32_t w = word & 2 ? (word & 1 ? u.w : u.z) : (word & 1 ? u.y : u.x);
+    if constexpr (F::kElems == 8)
+        return e & 1 ? F::E::hi(w) : F::E::lo(w);
+    else
+        return __uint_as_float(w);
+}
+
 // ---- forward ------------------------------------------------------------------------------
 
-constexpr int kRowThreads = 512;
-constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kRowBatch = 4;      // granules a thread has under way
+constexpr int kStages = 2;        // batches that a thread has under way or is taking
+constexpr int kRowBatch = 4;    // granules that a thread has under way, and takes together
 constexpr int kMostTop = 32;      // alternatives
+constexpr int resident_blocks(int threads) { return threads == 256 ? 4 : 896 / threads; }  // of an SM, by registers
 constexpr int kMostCluster = 8;   // blocks of a row
-constexpr int kFewThreads = 64;   // threads whose granules are looked at again one by one
-constexpr int kList = 1024;       // entries of the list
+constexpr int kList = 190;        // entries of the list
+constexpr int kItems = 128;       // runs of batches that are looked at again
+// The most runs of batches whose largest values a thread notes: as shared memory allows.
+template <class F, int NT>
+constexpr int kRuns = (NT == 64 ? 32 : 16) * F::kElems / 8;
 
 struct LogprobsArgs {
     const void *logits;
@@ -188,153 +247,268 @@ struct LogprobsArgs {
     int64_t *top_ids;
 };
 
-// A thread's running sums: m the largest so far, z = sum 2^t and s = sum 2^t t over its
-// elements, t = (x - m) scale log2 e.  t stops at -200, where 2^t is zero: a product with
-// the -infinity of a banned token would be NaN.  (A NaN leaves z and s as they are, and m
-// says so; with m infinite all t stop there.)
-struct Running {
-    float m, z, s;
-
-    __device__ __forceinline__ void raise(float to, float scale) {
-        to = max_nan(to, m);  // (a NaN stays)
-        const float t = fmaxf((m - to) * scale, -200.0f), f = exp2_fast(t);
-        s = f * fmaf(t, z, s);
-        z *= f;
-        m = to;
-    }
-    __device__ __forceinline__ void add(float x, float scale) {
-        const float t = fmaxf((x - m) * scale, -200.0f), e = exp2_fast(t);
-        z += e;
-        s = fmaf(e, t, s);
-    }
-};
-
-struct RowShared {
-    uint32_t keys[kRowWarps];
-    float z[kRowWarps], s[kRowWarps];
-    int owner;           // the lowest thread whose maximum is the block's
-    float owner_z;
-    // what the cluster's first block reads: the block's maximum, R and the sum of e t
-    uint32_t max_key;
-    float rest, sum_t;
-    int cand[kFewThreads];
-    int cands;
-    int listed;          // entries wanted in the list (it holds kList)
-    int counts[kRowWarps];
-    uint64_t best[kRowWarps];
-    uint64_t top[kMostTop];   // the block's largest, in order; 0 behind the last
-    uint64_t list[kList];
-};
+// A thread's running sums: top the largest so far, z = sum 2^t and s = sum 2^t t over its
+// elements, t = c x - r with c = scale log2 e.  The reference r, a power of two that the
+// sums are multiples of, is any number near c top: so its rounding does not count, and it
+// stays until the largest passes it by kRoom; nearly always the first batch's does.
+constexpr float kRoom = 8.0f;
+// t stops where 2^t is zero, at -200 or so: a product with the -infinity of a banned token
+// would be NaN.  In 16 bits that is done two elements an instruction, on x, with the
+// format's next value below; where there is none the thread's sums wait (shallow) for a
+// second pass over its elements.  In 32 bits it is done on t.
+constexpr float kDeep = 200.0f;
+// References beyond this stand too far from c top for a power of two: the second pass, too.
+constexpr float kFar = 0x1p20f;
 
 template <class F>
-__device__ __forceinline__ void push(RowShared &sh, const Row<F> &row, int64_t g, uint32_t least, bool above) {
-    float v[F::kElems];
-    const uint32_t there = row.fetch(g, v);
-#pragma unroll
-    for (int e = 0; e < F::kElems; ++e) {
-        const uint32_t key = ordered(v[e]);
-        if ((there >> e & 1u) && (above ? key > least : key >= least)) {
-            const int at = atomicAdd(&sh.listed, 1);
-            if (at < kList) sh.list[at] = entry(key, row.index(g) + e);
+struct Running {
+    float top, r;
+    float limit;      // the largest x that the reference serves
+    uint32_t least;   // two of the least x that are told apart
+    Pair z, s;
+    bool shallow;     // there is no such x
+
+    // (The sums of what comes before the first finite x do not matter.)
+    __device__ __forceinline__ Running()
+        : top(-INFINITY), r(0.0f), limit(-INFINITY), least(0u), z(Pair::of(0.0f, 0.0f)), s(z), shallow(false) {}
+
+    // (An infinity or NaN decides the row, and no sum matters.)
+    __device__ __forceinline__ void refer(float to, float c) {
+        if (!(fabsf(to) < INFINITY)) return;
+        const float now = c * to;
+        if (limit == -INFINITY) {
+            z = s = Pair::of(0.0f, 0.0f);
+        } else {
+            const float t = fmaxf(r - now, -kDeep), f = exp2_fast(t);
+            const Pair ff = Pair::of(f, f);
+            s = ff * Pair::of(t, t).fma(z, s);
+            z = ff * z;
         }
+        r = now;
+        limit = to + kRoom / c;
+        if constexpr (F::kElems == 8) {
+            least = F::below2(__fsub_rd(to, kDeep / c));
+            shallow |= !(F::E::lo(least) > -INFINITY);
+        }
+        shallow |= !(fabsf(now) <= kFar);
+    }
+    __device__ __forceinline__ void add(Pair t) {
+        const float2 x = t.split();
+        const Pair e = Pair::of(exp2_fast(x.x), exp2_fast(x.y));
+        z = z + e;
+        s = e.fma(t, s);
+    }
+    // Adds N granules, the largest of them `most`.
+    template <int N>
+    __device__ __forceinline__ void take(const uint4 (&u)[N], float most, float c) {
+        top = max_nan(top, most);
+        if (!(most <= limit)) refer(most, c);
+        const Pair cc = Pair::of(c, c), rr = Pair::of(-r, -r);
+        if constexpr (F::kElems == 8) {
+            const auto word = [&](uint32_t w) {
+                w = F::max2(w, least);
+                add(Pair::of(F::E::lo(w), F::E::hi(w)).fma(cc, rr));
+            };
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                word(u[i].x);
+                word(u[i].y);
+                word(u[i].z);
+                word(u[i].w);
+            }
+        } else {
+            const auto two = [&](uint32_t a, uint32_t b) {
+                const float2 t = Pair::of(__uint_as_float(a), __uint_as_float(b)).fma(cc, rr).split();
+                add(Pair::of(fmaxf(t.x, -kDeep), fmaxf(t.y, -kDeep)));
+            };
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                two(u[i].x, u[i].y);
+                two(u[i].z, u[i].w);
+            }
+        }
+    }
+};
+
+// A block's share of a row: granules g0 .. g1 - 1, of which w0 .. w1 - 1 lie in the row as a
+// whole.  Thread i takes w0 + i, w0 + i + NT, ..; thread 0 the row's first granule as well
+// if that is the block's and not whole, thread 1 the last.
+struct Share {
+    int g0, w0, w1, g1;
+
+    template <class F>
+    __device__ __forceinline__ Share(const Row<F> &row, int first, int end)
+        : g0(first), w0(first < end && !row.whole(first) ? first + 1 : first), w1(end), g1(end) {
+        if (w0 < end && !row.whole(end - 1)) --w1;
+    }
+    // what block `rank` of `blocks` has of a row
+    template <class F>
+    __device__ __forceinline__ static Share of(const Row<F> &row, int rank, int blocks) {
+        const int per = (row.granules + blocks - 1) / blocks;
+        const int64_t start = static_cast<int64_t>(per) * rank;
+        const int g0 = start < row.granules ? static_cast<int>(start) : row.granules;
+        return Share(row, g0, row.granules - g0 > per ? g0 + per : row.granules);
+    }
+    // the end of the row that a thread takes, or -1
+    __device__ __forceinline__ int end_of(int tid) const {
+        return tid == 0 && g0 < w0 ? g0 : (tid == 1 && w1 < g1 ? w1 : -1);
+    }
+};
+
+// The sums of a thread's elements once more, by `top`, their largest, with t stopped by itself.
+template <class F, int NT>
+__device__ __noinline__ float2 sums_again(const void *x, int64_t V, float top, Share share, float c) {
+    const Row<F> row(x, 0, 0, V);
+    float z = 0.0f, s = 0.0f;
+    const auto take = [&](int g) {
+        const uint4 u = row.fetch(g);
+#pragma unroll 1
+        for (int e = 0; e < F::kElems; ++e) {
+            const float t = fmaxf((element<F>(u, e) - top) * c, -kDeep), p = exp2_fast(t);
+            z += p;
+            s = fmaf(p, t, s);
+        }
+    };
+    if (fabsf(top) < INFINITY) {
+        for (int g = share.w0 + threadIdx.x; g < share.w1; g += NT) take(g);
+        if (share.end_of(threadIdx.x) >= 0) take(share.end_of(threadIdx.x));
+    }
+    return make_float2(z, s);
+}
+
+// What one block of a row knows of it: its largest key (0: no element), what the sum of
+// 2^t has beside one of the largest, and the sum of 2^t t, t by that largest.
+struct RowPart {
+    uint32_t key;
+    float rest, sum_t;
+};
+
+// What a cluster's first block is told by all of them, of one row and the next.
+struct ClusterShared {
+    RowPart parts[2][kMostCluster];
+    uint64_t tops[2][kMostCluster][kMostTop];
+};
+struct NoCluster {};
+
+template <class F, int NT, bool CLUSTER>
+struct RowShared {
+    uint4 stage[kStages][kRowBatch][NT];        // batches under way, each thread's own
+    alignas(16) uint64_t list[kList + 2];
+    alignas(16) uint32_t groups[NT / 32][32];
+    uint64_t best[NT / 32];
+    uint64_t top[kMostTop];                     // the block's largest, in order; 0 behind the last
+    uint32_t keys[NT];
+    float z[NT / 32], s[NT / 32];
+    float owner_z, owner_s;
+    int listed;                                 // entries wanted in the list (it holds kList)
+    int items;                                  // runs wanted in `item` (it holds kItems)
+    int counts[NT / 32];
+    float ends[2];                              // the largest of the row's ends
+    int item[kItems];                           // thread and run
+    typename F::T slots[kRuns<F, NT>][NT];            // by run of batches and thread: its largest
+    std::conditional_t<CLUSTER, ClusterShared, NoCluster> cluster;
+};
+
+// Lists the elements of a granule that are no less than `least` (above: that are larger).
+// (By floats, a NaN is listed whatever `least` is, and it ranks first.)
+template <class F, class S>
+__device__ __forceinline__ void push(S &sh, const Row<F> &row, int g, uint32_t least, bool above) {
+    const uint4 u = row.fetch(g);
+    float v[F::kElems];
+    widen<F>(u, v);
+    uint32_t hit = row.there(g);
+    const float low = value_of(least);
+#pragma unroll
+    for (int e = 0; e < F::kElems; ++e)
+        if (above ? v[e] <= low : v[e] < low) hit &= ~(1u << e);
+    if (hit == 0u) return;
+    int at = atomicAdd(&sh.listed, __popc(hit));
+#pragma unroll 1
+    for (; hit; hit &= hit - 1, ++at) {
+        const int e = __ffs(hit) - 1;
+        if (at < kList) sh.list[at] = entry(ordered(element<F>(u, e)), row.index(g) + e);
     }
 }
 
-// The block's k largest of granules [g0, g1), thread i having read g0 + i, g0 + i +
-// kRowThreads, ..; `key` its largest's, 0 where it read none.  Leaves them in sh.top.
-template <class F>
-__device__ void block_top(RowShared &sh, const Row<F> &row, int64_t g0, int64_t g1, uint32_t key, int k) {
+// The granules of the threads of `lanes` of this warp, by the warp together.
+template <class F, int NT, class S>
+__device__ __forceinline__ void push_threads(S &sh, const Row<F> &row, const Share &share, uint32_t lanes,
+                                             uint32_t least, bool above) {
+    const int lane = threadIdx.x & 31, first = threadIdx.x - lane;
+    while (lanes) {
+        const int who = first + __ffs(lanes) - 1;
+        lanes &= lanes - 1;
+        for (int g = share.w0 + who + lane * NT; g < share.w1; g += 32 * NT) push<F>(sh, row, g, least, above);
+        if (lane == 0 && share.end_of(who) >= 0) push<F>(sh, row, share.end_of(who), least, above);
+    }
+}
+
+// Many elements equal `least`, or the list is full: lists those above it and, where these
+// are fewer than k, equal ones in the order of their indices.  For all threads; sh.listed is
+// what the list then needs to hold.
+template <class F, int NT, class S>
+__device__ __noinline__ void list_many(S &sh, const Row<F> &row, const Share &share, uint32_t key,
+                                       uint32_t least, int k) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // least: the largest key that k threads reach (0: fewer than k read anything)
-    uint32_t least = 0u;
-    int reach = 0;
-    for (int bit = 31; bit >= F::kLowBit; --bit) {
-        // (below a negative value's lowest bit that differs its key is all ones)
-        const uint32_t mid = least | 1u << bit;
-        const int n = __syncthreads_count(key >= mid);
-        if (n >= k) {
-            least = mid;
-            reach = n;
-        }
-    }
-    if (least == 0u) reach = __syncthreads_count(key != 0u);
-    if (tid == 0) sh.cands = sh.listed = 0;
-    if (tid < kMostTop) sh.top[tid] = 0u;
     __syncthreads();
-    // the least key of a value: the bits below kLowBit say nothing
-    const uint32_t wanted = least == 0u ? 1u : least;
-    const bool few = reach <= kFewThreads;
-    // few threads reach it: theirs at least that large.  Else many values equal it: those
-    // above it, of fewer than k threads, and then equal ones in the order of their indices.
-    constexpr uint32_t kRest = (1u << F::kLowBit) - 1u;
-    const bool mine = few ? key >= wanted : key > (least | kRest);
-    if (mine) {
-        const int at = atomicAdd(&sh.cands, 1);
-        sh.cand[at] = tid;
-    }
+    if (tid == 0) sh.listed = 0;
     __syncthreads();
-    for (int i = warp; i < sh.cands; i += kRowWarps)
-        for (int64_t g = g0 + sh.cand[i] + static_cast<int64_t>(lane) * kRowThreads; g < g1; g += 32ll * kRowThreads)
-            push<F>(sh, row, g, few ? wanted : (least | kRest), !few);
+    push_threads<F, NT>(sh, row, share, __ballot_sync(0xffffffffu, key > least), least, true);
     __syncthreads();
-    if (!few && sh.listed < k) {
-        int have = sh.listed;
-        for (int64_t base = g0; base < g1 && have < k; base += kRowThreads) {
+    int have = sh.listed;
+    __syncthreads();
+    if (have >= k) return;
+    for (int base = share.g0; base < share.g1 && have < k; base += NT) {
+        uint32_t equal = 0u;
+        if (base + tid < share.g1) {
             float v[F::kElems];
-            uint32_t equal = 0u;
-            if (base + tid < g1) {
-                const uint32_t there = row.fetch(base + tid, v);
-#pragma unroll
-                for (int e = 0; e < F::kElems; ++e)
-                    if ((there >> e & 1u) && (ordered(v[e]) | kRest) == (least | kRest)) equal |= 1u << e;
-            }
-            int before = __popc(equal);
-            const int n = before;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int w = __shfl_up_sync(0xffffffffu, before, o);
-                if (lane >= o) before += w;
-            }
-            if (lane == 31) sh.counts[warp] = before;
-            __syncthreads();
-            int total = 0;
-            before += have - n;
-#pragma unroll
-            for (int w = 0; w < kRowWarps; ++w) {
-                if (w < warp) before += sh.counts[w];
-                total += sh.counts[w];
-            }
+            widen<F>(row.fetch(base + tid), v);
+            const uint32_t there = row.there(base + tid);
 #pragma unroll
             for (int e = 0; e < F::kElems; ++e)
-                if (equal >> e & 1u) {
-                    if (before < k) sh.list[before] = entry(ordered(v[e]), row.index(base + tid) + e);
-                    ++before;
-                }
-            have += total;
-            __syncthreads();
+                if ((there >> e & 1u) && ordered(v[e]) == least) equal |= 1u << e;
         }
-        if (tid == 0) sh.listed = have < k ? have : k;
+        int before = __popc(equal);
+        const int n = before;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += w;
+        }
+        if (lane == 31) sh.counts[warp] = before;
+        __syncthreads();
+        int total = 0;
+        before += have - n;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            if (w < warp) before += sh.counts[w];
+            total += sh.counts[w];
+        }
+#pragma unroll
+        for (int e = 0; e < F::kElems; ++e)
+            if (equal >> e & 1u) {
+                if (before < k) sh.list[before] = entry(least, row.index(base + tid) + e);
+                ++before;
+            }
+        have += total;
         __syncthreads();
     }
-    const int n = sh.listed;
-    if (n <= kList) {
-        for (int i = tid; i < n; i += kRowThreads) {
-            const uint64_t me = sh.list[i];
-            int rank = 0;
-            for (int j = 0; j < n; ++j) rank += sh.list[j] > me ? 1 : 0;
-            if (rank < k) sh.top[rank] = me;
-        }
-        __syncthreads();
-        return;
-    }
-    // more than the list holds, all in few threads' granules: the largest below the last,
-    // k times
+    if (tid == 0) sh.listed = have < k ? have : k;
+    __syncthreads();
+}
+
+// More elements above some value than the list holds, all in few threads' granules: k
+// times the largest below the last.  For all threads.
+template <class F, int NT, class S>
+__device__ __noinline__ void top_by_rounds(S &sh, const Row<F> &row, const Share &share, int k) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t last = ~0ull;
     for (int r = 0; r < k; ++r) {
         uint64_t best = 0u;
-        for (int64_t g = g0 + tid; g < g1; g += kRowThreads) {
+        for (int g = share.g0 + tid; g < share.g1; g += NT) {
             float v[F::kElems];
-            const uint32_t there = row.fetch(g, v);
+            widen<F>(row.fetch(g), v);
+            const uint32_t there = row.there(g);
 #pragma unroll
             for (int e = 0; e < F::kElems; ++e) {
                 const uint64_t c = there >> e & 1u ? entry(ordered(v[e]), row.index(g) + e) : 0u;
@@ -348,7 +522,7 @@ __device__ void block_top(RowShared &sh, const Row<F> &row, int64_t g0, int64_t 
         }
         if (lane == 0) sh.best[warp] = best;
         __syncthreads();
-        for (int w = 0; w < kRowWarps; ++w)
+        for (int w = 0; w < NT / 32; ++w)
             if (sh.best[w] > best) best = sh.best[w];
         if (tid == 0) sh.top[r] = best;
         last = best;
@@ -356,94 +530,101 @@ __device__ void block_top(RowShared &sh, const Row<F> &row, int64_t g0, int64_t 
     }
 }
 
-template <class F, bool CLUSTER>
-__global__ void __launch_bounds__(kRowThreads, 2) logprobs_fwd_kernel(const __grid_constant__ LogprobsArgs a) {
-    __shared__ RowShared sh;
-    pdl_trigger();
-    pdl_wait();
+// Entries of a list of n, an even number, that are larger than e.
+__device__ __forceinline__ int larger(const uint64_t *list, int n, uint64_t e) {
+    int r = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; j += 2) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(list + j);
+        r += (v.x > e ? 1 : 0) + (v.y > e ? 1 : 0);
+    }
+    return r;
+}
+
+// Entries of each of n descending lists that are larger than e, in all.
+__device__ __forceinline__ int larger(const uint64_t (&lists)[kMostCluster][kMostTop], int n, uint64_t e) {
+    int at[kMostCluster];
+#pragma unroll
+    for (int o = 0; o < kMostCluster; ++o) at[o] = 0;
+#pragma unroll 1
+    for (int step = kMostTop / 2; step > 0; step >>= 1)
+#pragma unroll
+        for (int o = 0; o < kMostCluster; ++o)
+            at[o] += lists[o][at[o] + step - 1] > e ? step : 0;
+    int r = 0;
+#pragma unroll
+    for (int o = 0; o < kMostCluster; ++o)
+        if (o < n) r += at[o] + (lists[o][at[o]] > e ? 1 : 0);
+    return r;
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Notes a thread's largest of each run of batches: 1 << shift of them, so that there are
+// kRuns at most.
+template <class F, int NT>
+struct Runs {
+    int shift, batch;
+    float top;  // of the run under way
+
+    __device__ __forceinline__ explicit Runs(int batches) : shift(0), batch(0), top(-INFINITY) {
+        while ((batches + (1 << shift) - 1) >> shift > kRuns<F, NT>) ++shift;
+    }
+    template <class S>
+    __device__ __forceinline__ void note(S &sh, float most) {
+        top = max_nan(top, most);
+        store_one<F>(&sh.slots[batch >> shift][threadIdx.x], top);
+        ++batch;
+        if ((batch & ((1 << shift) - 1)) == 0) top = -INFINITY;
+    }
+    // of a thread that noted all its batches
+    __device__ __forceinline__ int count() const { return (batch + (1 << shift) - 1) >> shift; }
+};
+
+// Joins what the block's threads found; returns it in warp 0.  With k > 0 the block's largest
+// are in sh.top behind the next barrier.
+template <class F, int NT, class S>
+__device__ __forceinline__ RowPart join_threads(S &sh, const Row<F> &row, const Share &share,
+                                                Running<F> &run, const Runs<F, NT> &runs, int k, float c) {
+    constexpr int WARPS = NT / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = CLUSTER ? static_cast<int>(blockIdx.x % a.blocks) : 0;
-    const int64_t t = CLUSTER ? blockIdx.x / a.blocks : blockIdx.x;
-    const Row<F> row(a.logits, a.stride, t, a.V);
-    int64_t g0 = 0, g1 = row.granules;
-    if (CLUSTER) {
-        const int64_t per = (row.granules + a.blocks - 1) / a.blocks;
-        g0 = per * rank < g1 ? per * rank : g1;
-        g1 = g0 + per < g1 ? g0 + per : g1;
+    // the block's maximum, and the lowest thread that has it
+    const uint32_t key = share.w0 + tid < share.w1 || share.end_of(tid) >= 0 ? ordered(run.top) : 0u;
+    sh.keys[tid] = key;
+    if (__syncthreads_or(run.shallow)) {
+        const float2 zs = sums_again<F, NT>(row.x, row.V, run.top, share, c);
+        run.z = Pair::of(zs.x, 0.0f);
+        run.s = Pair::of(zs.y, 0.0f);
+        run.shallow = true;
     }
-    // the given token's logit comes while the row is read
-    int64_t target = -1;
-    float given = 0.0f;
-    if (rank == 0 && tid == 0 && a.targets) {
-        target = a.targets[t];
-        if (target >= 0 && target < a.V) given = F::one(row.x[target]);
-    }
-
-    Running run = {-INFINITY, 0.0f, 0.0f};
-    const float c = a.scale_log2;
-    // granules that lie in the row as a whole
-    const int64_t w1 = g1 > g0 && row.whole(g1 - 1) ? g1 : g1 - 1;
-    int64_t g = g0 + tid;
-    if (g < g1 && g == 0 && !row.whole(0)) g += kRowThreads;
-    for (; g + (kRowBatch - 1) * kRowThreads < w1; g += kRowBatch * kRowThreads) {
-        uint4 u[kRowBatch];
+    // one of 32 groups of threads a lane, in every warp alike
+    uint32_t group_key = 0u;
+    int group_owner = 0;
 #pragma unroll
-        for (int b = 0; b < kRowBatch; ++b) u[b] = row.load(g + b * kRowThreads);
-        float m = largest<F>(u[0]);
-#pragma unroll
-        for (int b = 1; b < kRowBatch; ++b) m = max_nan(m, largest<F>(u[b]));
-        if (!(m <= run.m)) run.raise(m, c);
-#pragma unroll
-        for (int b = 0; b < kRowBatch; ++b) {
-            float v[F::kElems];
-            widen<F>(u[b], v);
-#pragma unroll
-            for (int e = 0; e < F::kElems; ++e) run.add(v[e], c);
+    for (int w = 0; w < WARPS; ++w) {
+        const uint32_t v = sh.keys[w * 32 + lane];
+        if (v > group_key) {
+            group_key = v;
+            group_owner = w * 32 + lane;
         }
     }
-    for (; g < w1; g += kRowThreads) {
-        const uint4 u = row.load(g);
-        const float m = largest<F>(u);
-        if (!(m <= run.m)) run.raise(m, c);
-        float v[F::kElems];
-        widen<F>(u, v);
-#pragma unroll
-        for (int e = 0; e < F::kElems; ++e) run.add(v[e], c);
-    }
-    // the row's ends, by the threads whose turn it would be
-    const auto part = [&](int64_t at) {
-        float v[F::kElems];
-        row.fetch(at, v);
-        for (int e = 0; e < F::kElems; ++e) {
-            if (!(v[e] <= run.m)) run.raise(v[e], c);
-            run.add(v[e], c);
-        }
-    };
-    if (g1 > g0) {
-        if (g0 == 0 && tid == 0 && !row.whole(0)) part(0);
-        const int64_t last = g1 - 1;
-        if (last != 0 && !row.whole(last) && (last - g0) % kRowThreads == tid) part(last);
-    }
-
-    // the block's maximum and sums
-    const uint32_t key = g0 + tid < g1 ? ordered(run.m) : 0u;
-    const uint32_t warp_key = __reduce_max_sync(0xffffffffu, key);
-    if (lane == 0) sh.keys[warp] = warp_key;
-    if (tid == 0) sh.owner = kRowThreads;
-    __syncthreads();
-    uint32_t top_key = 0u;
-#pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) top_key = max(top_key, sh.keys[w]);
-    // a thread with the maximum counts apart: its sum is 1 and what may be little beside it
-    if (key == top_key && key != 0u) atomicMin(&sh.owner, tid);
-    __syncthreads();
+    const uint32_t top_key = __reduce_max_sync(0xffffffffu, group_key);
+    const int owner = static_cast<int>(
+        __reduce_min_sync(0xffffffffu, group_key == top_key && top_key != 0u ? static_cast<uint32_t>(group_owner) : NT));
     const float m = top_key == 0u ? -INFINITY : value_of(top_key);
     {
-        const float shift = fmaxf((run.m - m) * c, -200.0f), f = exp2_fast(shift);
-        float z = f * run.z, s = f * fmaf(shift, run.z, run.s);
-        if (tid == sh.owner) {
+        // t by the block's maximum: as the reference stands to it, or the thread's own
+        const float up = run.shallow ? (run.top - m) * c : -fmaf(m, c, -run.r);
+        const float shift = fmaxf(up, -kDeep), f = exp2_fast(shift);
+        float z = run.z.sum(), s = f * fmaf(shift, z, run.s.sum());
+        z *= f;
+        if (run.top == -INFINITY) z = s = 0.0f;
+        // its sum is 1 and what may be little beside it
+        if (tid == owner) {
             sh.owner_z = z;
-            z = 0.0f;
+            sh.owner_s = s;
+            z = s = 0.0f;
         }
         z = warp_sum(z);
         s = warp_sum(s);
@@ -452,114 +633,321 @@ __global__ void __launch_bounds__(kRowThreads, 2) logprobs_fwd_kernel(const __gr
             sh.s[warp] = s;
         }
     }
+    // The k-th largest of the groups' largest: k elements are no less.  Threads whose
+    // largest is no less hold them all: about as many threads.  (The five bits below are
+    // the lane's, so that no two are equal; 1 where fewer groups than k have an element.)
+    uint32_t least = 1u;
+    if (k > 0) {
+        const uint32_t mine = (group_key & ~31u) | (31u - lane);
+        sh.groups[warp][lane] = mine;
+        __syncwarp();
+        int above = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(&sh.groups[warp][4 * j]);
+            above += (v.x > mine ? 1 : 0) + (v.y > mine ? 1 : 0) + (v.z > mine ? 1 : 0) + (v.w > mine ? 1 : 0);
+        }
+        const uint32_t kth =
+            __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, above == k - 1)) - 1) & ~31u;
+        if (kth != 0u) least = kth;
+        // their runs that hold them: one at least for each such thread
+        if (key >= least) {
+            const float low = value_of(least);
+            const auto look = [&](float top, int r) {
+                if (top < low) return;  // (a NaN is looked at)
+                const int at = atomicAdd(&sh.items, 1);
+                if (at < kItems) sh.item[at] = tid * (kRuns<F, NT> + 1) + r;
+            };
+#pragma unroll 1
+            for (int r = 0; r < runs.count(); ++r) look(F::one(sh.slots[r][tid]), r);
+            if (share.end_of(tid) >= 0) look(sh.ends[tid], kRuns<F, NT>);
+        }
+    }
     __syncthreads();
-    float rest = 0.0f, sum_t = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) {
-        rest += sh.z[w];
-        sum_t += sh.s[w];
-    }
-    if (sh.owner < kRowThreads) {
-        if (rest + sh.owner_z >= 2.0f) {
-            rest += sh.owner_z - 1.0f;
-        } else if (warp == 0) {
-            // one token holds more than half of the sum: the owner's others once more, alone
-            float r = 0.0f;
-            for (int64_t at = g0 + sh.owner + static_cast<int64_t>(lane) * kRowThreads; at < g1;
-                 at += 32ll * kRowThreads) {
-                float v[F::kElems];
-                row.fetch(at, v);
-#pragma unroll
-                for (int e = 0; e < F::kElems; ++e)
-                    if (v[e] < m) r += exp2_fast(fmaxf((v[e] - m) * c, -200.0f));
+    if (k > 0) {
+        const int items = sh.items;
+        if (items <= kItems) {
+            constexpr int kLog2Batch = kRowBatch == 4 ? 2 : (kRowBatch == 2 ? 1 : 0);
+            const int log2_per = kLog2Batch + runs.shift;  // granules of a run
+#pragma unroll 1
+            for (int i = tid; i < items << log2_per; i += NT) {
+                const int what = sh.item[i >> log2_per], who = what / (kRuns<F, NT> + 1), r = what % (kRuns<F, NT> + 1);
+                const int j = i & ((1 << log2_per) - 1);
+                int g = share.w0 + who + ((r << log2_per) + j) * NT;
+                if (r == kRuns<F, NT>) g = j == 0 ? share.end_of(who) : share.w1;
+                if (g < share.w1 || (r == kRuns<F, NT> && j == 0)) push<F>(sh, row, g, least, false);
             }
-            rest += warp_sum(r);
+            __syncthreads();
+        }
+        if (items > kItems || sh.listed > kList) list_many<F, NT>(sh, row, share, key, least, k);
+        const int n = sh.listed;
+        if (n <= kList) {
+            if (tid == 0) sh.list[n] = 0u;
+            __syncthreads();
+#pragma unroll 1
+            for (int i = tid; i < n; i += NT) {
+                const uint64_t me = sh.list[i];
+                const int r = larger(sh.list, (n + 1) & ~1, me);
+                if (r < k) sh.top[r] = me;
+            }
+        } else {
+            top_by_rounds<F, NT>(sh, row, share, k);
         }
     }
-    // (warp 0's are complete)
-    if (tid == 0) {
-        sh.max_key = top_key;
-        sh.rest = rest;
-        sh.sum_t = sum_t;
+    RowPart all = {top_key, 0.0f, 0.0f};
+    if (warp != 0) return all;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        all.rest += sh.z[w];
+        all.sum_t += sh.s[w];
     }
+    if (owner >= NT) return all;
+    const float oz = sh.owner_z;
+    if (all.rest + oz >= 2.0f) {
+        all.rest += oz - 1.0f;
+        all.sum_t += sh.owner_s;
+        return all;
+    }
+    // one token holds more than half of the sum: its thread's others once more, alone
+    float r = 0.0f, q = 0.0f;
+    const auto others = [&](int g) {
+        float v[F::kElems];
+        widen<F>(row.fetch(g), v);
+#pragma unroll
+        for (int e = 0; e < F::kElems; ++e)
+            if (v[e] < m) {
+                const float x = fmaxf((v[e] - m) * c, -kDeep), p = exp2_fast(x);
+                r += p;
+                q = fmaf(p, x, q);
+            }
+    };
+    // (one body: the last turn of lane 0 is the row's end)
+    const int end = lane == 0 ? share.end_of(owner) : -1;
+    bool more = true;
+#pragma unroll 1
+    for (int g = share.w0 + owner + lane * NT; more; g += 32 * NT) {
+        more = g < share.w1;
+        if (!more) g = end;
+        if (g >= 0) others(g);
+    }
+    all.rest += warp_sum(r);
+    all.sum_t += warp_sum(q);
+    return all;
+}
 
-    if (a.k > 0) block_top<F>(sh, row, g0, g1, key, a.k);
+// A row's results, by warp 0.
+template <class S>
+__device__ __forceinline__ void store_row(const LogprobsArgs &a, const S &sh, const RowPart &all, int64_t t,
+                                          int64_t target, float given) {
+    const int lane = threadIdx.x & 31;
+    const float nan = __uint_as_float(0x7FFFFFFFu);
+    const float most = value_of(all.key), ln_z = log1pf(all.rest);
+    const bool plain = fabsf(most) < INFINITY;
+    const auto logp = [&](float x) {
+        if (plain) return (x - most) * a.scale - ln_z;
+        if (most == -INFINITY) return -INFINITY;
+        return x < INFINITY && most == INFINITY ? -INFINITY : nan;
+    };
+    if (lane == 0) {
+        const float none = most == -INFINITY ? 0.0f : nan;
+        if (a.lse) a.lse[t] = plain ? fmaf(most, a.scale, ln_z) : most;
+        if (a.entropy) a.entropy[t] = plain ? fmaf(-0.6931471805599453f, all.sum_t / (1.0f + all.rest), ln_z) : none;
+        if (a.logprobs) {
+            float v = 0.0f;
+            if (target >= a.V) {
+                atomicOr(&g_logprobs_status, RN_STATUS_BAD_INDEX);
+                v = nan;
+            } else if (target >= 0) {
+                v = logp(given);
+            }
+            a.logprobs[t] = v;
+        }
+    }
+    if (lane < a.k) {
+        const uint64_t e = sh.top[lane];
+        a.top_logprobs[t * a.k + lane] = logp(value_of(static_cast<uint32_t>(e >> 32)));
+        a.top_ids[t * a.k + lane] = 0xFFFFFFFFu - static_cast<uint32_t>(e);
+    }
+}
 
-    float row_m = m, row_rest = rest, row_t = sum_t;
-    if constexpr (CLUSTER) {
-        auto cluster = cg::this_cluster();
-        cluster.sync();
-        if (rank == 0) {
-            // joins the blocks' sums in their order
+// The row's ends, by their threads.
+template <class F, class S>
+__device__ __forceinline__ void take_end(S &sh, const Row<F> &row, const Share &share, Running<F> &run,
+                                         float c) {
+    const int end = share.end_of(threadIdx.x);
+    if (end < 0) return;
+    const uint4 u[1] = {row.fetch(end)};
+    const float most = largest<F>(u);
+    run.take(u, most, c);
+    sh.ends[threadIdx.x] = most;
+}
+
+// ---- the stream of batches ------------------------------------------------------------
+
+__device__ __forceinline__ void copy_async16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// A block's share of its rows (t, t + step, ..) as one stream of batches.  Each thread
+// copies its own granules to its own places in shared memory, kStages - 1 batches ahead of
+// the one it takes, so that nothing waits for another thread, and the next row comes in
+// while a row is joined.
+template <class F, int NT, class S>
+struct Stream {
+    const LogprobsArgs &a;
+    S &sh;
+    const void *at;      // this thread's first granule of the batch to be copied next
+    int left;            // granules of the share from the block's first of that batch on
+    int rank;
+    uint32_t head;       // stage of the batch to be copied next
+    int64_t t, step;
+
+    __device__ __forceinline__ Stream(const LogprobsArgs &a_, S &sh_, int rank_, int64_t t_, int64_t step_)
+        : a(a_), sh(sh_), rank(rank_), head(0), t(t_), step(step_) {
+        begin();
+    }
+    __device__ __forceinline__ void begin() {
+        const Row<F> row(a.logits, a.stride, t, a.V);
+        const Share share = Share::of(row, rank, a.blocks);
+        at = row.x + row.index(share.w0 + threadIdx.x);
+        left = share.w1 - share.w0;
+    }
+    // Copies a batch, if there is one; the group counts anyway.  (A share without a whole
+    // granule is a batch of nothing.)
+    __device__ __forceinline__ void copy() {
+        if (t < a.T) {
+            const uint8_t *from = static_cast<const uint8_t *>(at);
+            uint4 *to = &sh.stage[head][0][threadIdx.x];
+            if (left >= kRowBatch * NT) {
+#pragma unroll
+                for (int b = 0; b < kRowBatch; ++b) copy_async16(to + b * NT, from + b * NT * 16);
+            } else {
+#pragma unroll
+                for (int b = 0; b < kRowBatch; ++b)
+                    if (b * NT + static_cast<int>(threadIdx.x) < left) copy_async16(to + b * NT, from + b * NT * 16);
+            }
+            left -= kRowBatch * NT;
+            at = from + kRowBatch * NT * 16;
+            if (left <= 0) {
+                t += step;
+                if (t < a.T) begin();
+            }
+        }
+        copy_commit();
+        head = head + 1 == kStages ? 0 : head + 1;
+    }
+};
+
+template <class F, int NT, bool CLUSTER>
+__global__ void __launch_bounds__(NT, resident_blocks(NT)) logprobs_fwd_kernel(const __grid_constant__ LogprobsArgs a) {
+    extern __shared__ __align__(16) uint8_t row_shared[];
+    using S = RowShared<F, NT, CLUSTER>;
+    S &sh = *reinterpret_cast<S *>(row_shared);
+    pdl_trigger();
+    if constexpr (CLUSTER) cluster_arrive();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = CLUSTER ? static_cast<int>(blockIdx.x % a.blocks) : 0;
+    const int64_t first = CLUSTER ? blockIdx.x / a.blocks : blockIdx.x;
+    const int64_t step = CLUSTER ? gridDim.x / a.blocks : gridDim.x;
+    Stream<F, NT, S> stream(a, sh, rank, first, step);
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) stream.copy();
+    if (tid == 0) sh.listed = sh.items = 0;
+    if (tid < kMostTop) sh.top[tid] = 0u;
+    const float c = a.scale_log2;
+    uint32_t tail = 0;  // stage of the batch to be taken next
+    int turn = 0;       // of the two places for what the cluster knows
+
+    for (int64_t t = first; t < a.T; t += step, turn ^= 1) {
+        const Row<F> row(a.logits, a.stride, t, a.V);
+        const Share share = Share::of(row, rank, a.blocks);
+        // the given token's logit comes while the row is read
+        int64_t target = -1;
+        float given = 0.0f;
+        if (rank == 0 && tid == 0 && a.targets) {
+            target = a.targets[t];
+            if (target >= 0 && target < a.V) given = F::one(row.x[target]);
+        }
+        Running<F> run;
+        Runs<F, NT> runs((share.w1 - share.w0 + kRowBatch * NT - 1) / (kRowBatch * NT));
+        take_end(sh, row, share, run, c);
+        int g = share.w0;
+        do {
+            copy_wait<kStages - 2>();
+            uint4 u[kRowBatch];
+            const uint4 *from = &sh.stage[tail][0][tid];
+            if (g + kRowBatch * NT <= share.w1) {
+#pragma unroll
+                for (int b = 0; b < kRowBatch; ++b) u[b] = ld_shared16(from + b * NT);
+            } else {
+#pragma unroll
+                for (int b = 0; b < kRowBatch; ++b) {
+                    u[b] = make_uint4(F::kNone, F::kNone, F::kNone, F::kNone);
+                    if (g + b * NT + tid < share.w1) u[b] = ld_shared16(from + b * NT);
+                }
+            }
+            tail = tail + 1 == kStages ? 0 : tail + 1;
+            stream.copy();  // (to the stage that the batch before came from)
+            const float most = largest<F>(u);
+            run.take(u, most, c);
+            if (a.k > 0) runs.note(sh, most);
+            g += kRowBatch * NT;
+        } while (g < share.w1);
+        RowPart all = join_threads<F, NT>(sh, row, share, run, runs, a.k, c);
+        __syncthreads();
+        if constexpr (CLUSTER) {
+            // Everything goes to the first block, which joins it in the blocks' order.  The
+            // barrier's phases: all have begun; then for each row: all have told, and the
+            // first block has joined the row before, so the one behind may take its place.
+            if (rank != 0 || t == first) cluster_wait();
+            ClusterShared *to = cg::this_cluster().map_shared_rank(&sh.cluster, 0);
+            if (tid == 0) to->parts[turn][rank] = all;
+            if (tid < kMostTop && a.k > 0) to->tops[turn][rank][tid] = sh.top[tid];
+            cluster_arrive();
+            if (rank != 0) {
+                if (tid < kMostTop) sh.top[tid] = 0u;
+                if (tid == 0) sh.listed = sh.items = 0;
+                continue;
+            }
+            cluster_wait();
             const int n = a.blocks;
-            uint32_t most = 0u;
-            for (int b = 0; b < n; ++b) most = max(most, *cluster.map_shared_rank(&sh.max_key, b));
-            row_m = value_of(most);
-            row_rest = row_t = 0.0f;
-            bool found = false;
-            for (int b = 0; b < n; ++b) {
-                const uint32_t bk = *cluster.map_shared_rank(&sh.max_key, b);
-                if (bk == 0u) continue;
-                const float br = *cluster.map_shared_rank(&sh.rest, b), bt = *cluster.map_shared_rank(&sh.sum_t, b);
-                const float shift = fmaxf((value_of(bk) - row_m) * c, -200.0f), f = exp2_fast(shift);
-                row_t += f * fmaf(shift, 1.0f + br, bt);
-                if (bk == most && !found) {
-                    found = true;
-                    row_rest += br;
-                } else {
-                    row_rest += f * (1.0f + br);
+            if (a.k > 0)
+#pragma unroll 1
+                for (int i = tid; i < n * kMostTop; i += NT) {
+                    const uint64_t me = sh.cluster.tops[turn][i / kMostTop][i % kMostTop];
+                    if (me == 0u) continue;
+                    const int r = larger(sh.cluster.tops[turn], n, me);
+                    if (r < a.k) sh.top[r] = me;
                 }
-            }
-            if (a.k > 0) {
-                // ranks the blocks' entries; equal ones are no entries
-                uint64_t me = 0u;
-                if (tid < n * kMostTop) me = *cluster.map_shared_rank(&sh.top[tid % kMostTop], tid / kMostTop);
-                if (tid < n * kMostTop) sh.list[tid] = me;
-                __syncthreads();
-                int r = 0;
-                if (me != 0u)
-                    for (int j = 0; j < n * kMostTop; ++j) r += sh.list[j] > me ? 1 : 0;
-                __syncthreads();
-                if (me != 0u && r < a.k) sh.list[kList - kMostTop + r] = me;
-                __syncthreads();
-                if (tid < a.k) sh.top[tid] = sh.list[kList - kMostTop + tid];
-                __syncthreads();
+            __syncthreads();
+            if (warp == 0) {
+                const RowPart p = lane < n ? sh.cluster.parts[turn][lane] : RowPart{0u, 0.0f, 0.0f};
+                const uint32_t most = __reduce_max_sync(0xffffffffu, p.key);
+                const int holder = __ffs(__ballot_sync(0xffffffffu, p.key == most)) - 1;
+                float z = 0.0f, s = 0.0f;
+                if (p.key != 0u) {
+                    const float shift = fmaxf((value_of(p.key) - value_of(most)) * c, -kDeep), f = exp2_fast(shift);
+                    s = f * fmaf(shift, 1.0f + p.rest, p.sum_t);
+                    z = lane == holder ? p.rest : f * (1.0f + p.rest);
+                }
+                all = {most, warp_sum(z), warp_sum(s)};
             }
         }
-        cluster.sync();  // the others' shared memory is read until here
-        if (rank != 0) return;
-    }
-    // rank 0, every thread of it with the row's maximum and warp 0 with its sums
-    const bool plain = row_m > -INFINITY && row_m < INFINITY;
-    if (warp == 0) {
-        const float z = 1.0f + row_rest, ln_z = log1pf(row_rest);
-        const float none = row_m == -INFINITY ? 0.0f : __uint_as_float(0x7FFFFFFFu);
-        const float entropy = plain ? fmaf(-0.6931471805599453f, row_t / z, ln_z) : none;
-        const auto logp = [&](float x) {
-            if (plain) return (x - row_m) * a.scale - ln_z;
-            if (row_m == -INFINITY) return -INFINITY;
-            return x == INFINITY || !(row_m == row_m) ? __uint_as_float(0x7FFFFFFFu) : x - row_m;
-        };
-        if (lane == 0) {
-            if (a.lse) a.lse[t] = plain ? fmaf(row_m, a.scale, ln_z) : row_m;
-            if (a.entropy) a.entropy[t] = entropy;
-            if (a.logprobs) {
-                float v = 0.0f;
-                if (target >= a.V) {
-                    atomicOr(&g_logprobs_status, RN_STATUS_BAD_INDEX);
-                    v = __uint_as_float(0x7FFFFFFFu);
-                } else if (target >= 0) {
-                    v = logp(given);
-                }
-                a.logprobs[t] = v;
-            }
-        }
-        if (lane < a.k) {
-            const uint64_t e = sh.top[lane];
-            a.top_logprobs[t * a.k + lane] = logp(value_of(static_cast<uint32_t>(e >> 32)));
-            a.top_ids[t * a.k + lane] = 0xFFFFFFFFu - static_cast<uint32_t>(e);
+        if (warp == 0) {
+            store_row(a, sh, all, t, target, given);
+            // for the next row; the others come to them behind its first barrier
+            __syncwarp();
+            sh.top[tid] = 0u;
+            if (tid == 0) sh.listed = sh.items = 0;
         }
     }
+    if (CLUSTER && rank != 0) cluster_wait();
 }
 
 // ---- gradient --------------------------------------------------------------------------------
@@ -637,12 +1025,8 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_bwd_kernel(const __grid
         if (g >= row.granules) return;
         const int64_t i = row.index(g);
         float v[F::kElems];
-        uint32_t there = (1u << F::kElems) - 1u;
         const bool whole = row.whole(g);
-        if (whole)
-            widen<F>(u[b], v);
-        else
-            there = row.fetch(g, v);
+        widen<F>(whole ? u[b] : row.fetch(g), v);
 #pragma unroll
         for (int e = 0; e < F::kElems; ++e) v[e] = grad(v[e]);
         if (target >= i && target < i + F::kElems) {
@@ -656,7 +1040,7 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_bwd_kernel(const __grid
         } else {
 #pragma unroll
             for (int e = 0; e < F::kElems; ++e)
-                if (there >> e & 1u) store_one<F>(out + i + e, v[e]);
+                if (row.there(g) >> e & 1u) store_one<F>(out + i + e, v[e]);
         }
     }
 }
@@ -665,19 +1049,61 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_bwd_kernel(const __grid
 
 static int elem_bytes(int dtype) { return dtype == RN_DTYPE_F32 ? 4 : 2; }
 
-// Blocks that share a row: more where rows are too few to fill the GPU.
-static int row_blocks(int64_t T, int64_t V, int dtype, int sm_count) {
-    int n = 1;
-    const int64_t granules = V * elem_bytes(dtype) / 16;
-    while (n < kMostCluster && T * n < 4 * static_cast<int64_t>(sm_count) && granules / (2 * n) >= kRowThreads) n *= 2;
-    return n;
+// Threads of a block, and blocks that share a row.
+struct RowShape {
+    int threads, blocks;
+};
+// The layout that an estimate prefers.  An SM takes its blocks' shares of rows in rounds of
+// as many as it holds; a round takes what HBM needs for the SM's shares in it (44.6 KB a us),
+// longer where there are less than 26 warps to take them in, and 3 us in which the last rows
+// are joined, 4.5 where clusters join.  So many rows are best in rounds that are nearly full,
+// few rows on many blocks each.  (Alternatives 8, bf16, 131072 columns, us as 256 threads x 1
+// block / 128 x 1 / 64 x 1 / 128 x 2 / 256 x 8: 1 row 12.3 / - / - / 12.4 / 6.8; 500 rows 28.7 /
+// 37.9 / 51 / 28.5 / -; 1000 57 / 47.9 / 66 / 55; 2048 109 / 94 / 89 / 107; 3000 140 / 136 /
+// 159 / 156.)
+static RowShape row_shape(int64_t T, int64_t V, int dtype, int sm_count) {
+    const double kb = static_cast<double>(V) * elem_bytes(dtype) / 1024;
+    RowShape best = {256, 1};
+    double least = 0;
+    for (int threads = 256; threads >= 64; threads /= 2)
+        for (int blocks = 1; blocks <= kMostCluster; blocks *= 2) {
+            if (blocks > 1 && kb * 64 < 2.0 * threads * blocks) break;  // two granules a thread at least
+            const double each = static_cast<double>(T) * blocks / sm_count;
+            const double rounds = ceil(each / resident_blocks(threads)), at_once = ceil(each / rounds);
+            const double warps = at_once * threads / 32;
+            const double us = rounds * (at_once * kb / blocks / 44.6 * (warps < 26 ? 26 / warps : 1.0) +
+                                        (blocks > 1 ? 4.5 : 3.0));
+            if (least == 0 || us < least) {
+                least = us;
+                best = {threads, blocks};
+            }
+        }
+    return best;
 }
 
-template <class F, bool CLUSTER>
-static int launch_fwd(const LogprobsArgs &a, cudaStream_t st) {
+template <class F, int NT, bool CLUSTER>
+static int launch_fwd(const LogprobsArgs &a, const DeviceInfo &dev, cudaStream_t st) {
+    static std::atomic<int> resident[kMaxDevices];  // blocks that an SM holds
+    const auto kernel = logprobs_fwd_kernel<F, NT, CLUSTER>;
+    constexpr int smem = sizeof(RowShared<F, NT, CLUSTER>);
+    const int idx = current_device_index();
+    if (idx < 0 || idx >= kMaxDevices) return RN_ERR_DEVICE;
+    int fit = resident[idx].load(std::memory_order_acquire);
+    if (fit == 0) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, NT, smem) != cudaSuccess || fit < 1) {
+            cudaGetLastError();
+            return RN_ERR_DEVICE;
+        }
+        resident[idx].store(fit, std::memory_order_release);
+    }
+    // as many rows at once as the GPU holds
+    int64_t rows = static_cast<int64_t>(dev.sm_count) * fit / a.blocks;
+    if (rows > a.T) rows = a.T;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.T * a.blocks));
-    cfg.blockDim = dim3(kRowThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * a.blocks));
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -687,7 +1113,7 @@ static int launch_fwd(const LogprobsArgs &a, cudaStream_t st) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CLUSTER ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, logprobs_fwd_kernel<F, CLUSTER>, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
         cudaGetLastError();
         return RN_ERR_LAUNCH;
     }
@@ -695,8 +1121,14 @@ static int launch_fwd(const LogprobsArgs &a, cudaStream_t st) {
 }
 
 template <class F>
-static int run_fwd(const LogprobsArgs &a, cudaStream_t st) {
-    return a.blocks > 1 ? launch_fwd<F, true>(a, st) : launch_fwd<F, false>(a, st);
+static int run_fwd(LogprobsArgs &a, int dtype, const DeviceInfo &dev, cudaStream_t st) {
+    const RowShape s = row_shape(a.T, a.V, dtype, dev.sm_count);
+    a.blocks = s.blocks;
+    if (s.threads == 64)
+        return a.blocks > 1 ? launch_fwd<F, 64, true>(a, dev, st) : launch_fwd<F, 64, false>(a, dev, st);
+    if (s.threads == 128)
+        return a.blocks > 1 ? launch_fwd<F, 128, true>(a, dev, st) : launch_fwd<F, 128, false>(a, dev, st);
+    return a.blocks > 1 ? launch_fwd<F, 256, true>(a, dev, st) : launch_fwd<F, 256, false>(a, dev, st);
 }
 
 template <class F>
@@ -759,16 +1191,15 @@ int token_logprobs_fwd(int dtype, const void *logits, int64_t stride, const int6
     a.scale = scale;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.k = top_k;
-    a.blocks = rn::row_blocks(T, V, dtype, dev->sm_count);
     a.logprobs = logprobs;
     a.lse = lse;
     a.entropy = entropy;
     a.top_logprobs = top_logprobs;
     a.top_ids = top_ids;
     const auto st = reinterpret_cast<cudaStream_t>(stream);
-    if (dtype == RN_DTYPE_F32) return rn::run_fwd<rn::Row32>(a, st);
-    if (dtype == RN_DTYPE_F16) return rn::run_fwd<rn::Row16Half>(a, st);
-    return rn::run_fwd<rn::Row16Bf>(a, st);
+    if (dtype == RN_DTYPE_F32) return rn::run_fwd<rn::Row32>(a, dtype, *dev, st);
+    if (dtype == RN_DTYPE_F16) return rn::run_fwd<rn::Row16Half>(a, dtype, *dev, st);
+    return rn::run_fwd<rn::Row16Bf>(a, dtype, *dev, st);
 }
 
 int token_logprobs_bwd(int dtype, const void *logits, int64_t stride, const int64_t *targets, const float *logprobs,

@@ -136,8 +136,10 @@ def logprobs(x, targets, scale, k):
 def logprobs_grad(x, targets, given, lse, entropy, dp, dh, dl, scale):
     """(gradient, slack) by the formula, with the forward results as they are given.
 
-    s - lse = l is off by U |l|, p = e^l by (3 |l| + 4) U, c0 - c1 l by 6 U of its parts."""
+    s - lse = l is off by U |l|, p = e^l by (3 |l| + 4) U, c0 - c1 l by 6 U of its parts.  A
+    given token's l is its log probability as it is given, where that gets a gradient."""
     T, V = x.shape
+    targets = targets if dp is not None else torch.full_like(targets, -1)
     zero = torch.zeros(T, dtype=torch.float64, device=x.device)
     given, lse, entropy, dp, dh, dl = (zero if v is None else v.double()
                                        for v in (given, lse, entropy, dp, dh, dl))
