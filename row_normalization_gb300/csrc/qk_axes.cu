@@ -15,9 +15,18 @@
 // shuffle of its packed words.  Neighbouring pairs lie in one lane anyway.
 //
 // A group of lanes takes one token and walks over a part of its heads, so a lane turns by
-// the same angles throughout: cosines and sines are fetched once for each (token, part).
-// Parts hold query heads or key heads only: one weight in registers, and in the gradient
-// one set of 16 sums of dw a lane.
+// the same angles throughout: cosines and sines are fetched once for each (token, part), and
+// the weights multiplied into them in the forward pass.  Parts hold query heads or key heads
+// only: one weight in registers, and in the gradient one set of 16 sums of dw a lane.
+// Every lane copies its own elements ahead into its own places in shared memory.  That beats
+// loads into registers (16384 tokens of 40 heads of 128, us): forward 65.3 -> 55.2, of which the
+// bytes need 50.8; gradient 99.5 -> 81.1, of 75.5.  Three stages are enough for the forward pass:
+// 24 warps an SM with two heads of 1 KB under way each; eight stages took 56.9 there and 18.9
+// against 16.5 at 4096 tokens, as a warp begins later.
+//
+// What is left: a quarter of the gradient at 4096 tokens (27.9 us, floor 18.9) is its second
+// launch, beginning and end; axes that change within four pairs cost 4 to 20% (heads of 256 that
+// turn a half of 128 by three interleaved axes: 57.9 us forward, 96.3 gradient, floors as above).
 #include "rn_common.cuh"
 #include "rn_host.h"
 
@@ -48,6 +57,7 @@ struct QkAxesArgs {
     uint8_t used;           // axes that turn some pair, a bit each
     bool table_bf16;
     int q_parts, k_parts;   // parts of a token's query and key heads
+    int part_heads;         // heads of a part, but for the last
     // gradient: blocks 0 .. q_blocks - 1 take the query parts, the others the key parts,
     // and each leaves its sums of dw in row blockIdx.x of partial [blocks, D]
     int q_blocks;
@@ -63,13 +73,32 @@ struct AxesLane {
     static constexpr int kPartner = R / 16;  // and, in neox pairs, how far its partner's lane is
 };
 
+// A token's positions on the axes that turn some pair; false where one is outside the table.
+struct Positions {
+    int at[kMaxAxes];
+    bool ok;
+
+    __device__ __forceinline__ void load(const QkAxesArgs &a, int64_t t, bool live) {
+        ok = live;
+#pragma unroll
+        for (int i = 0; i < kMaxAxes; ++i) {
+            at[i] = 0;
+            if (live && (a.used >> i & 1)) {
+                const int64_t p = __ldg(a.pos + i * a.pos_stride + t);
+                const bool in = static_cast<uint64_t>(p) < static_cast<uint64_t>(a.max_pos);
+                ok &= in;
+                at[i] = in ? static_cast<int>(p) : 0;  // keeps every address in range; nothing is stored
+            }
+        }
+    }
+};
+
 // c[0..3], s[0..3]: cosines and sines of four pairs from p on, of a token at `pos`.
 template <int R>
-__device__ __forceinline__ void load_angles(const QkAxesArgs &a, const int64_t (&pos)[kMaxAxes], int p, float *c,
-                                            float *s) {
+__device__ __forceinline__ void load_angles(const QkAxesArgs &a, const Positions &pos, int p, float *c, float *s) {
     const uint32_t code = a.pair_axis[p >> 4] >> (2 * (p & 15)) & 0xFFu;
-    const auto at = [&](uint32_t axis) {
-        return axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
+    const auto at = [&](uint32_t axis) -> int64_t {
+        return axis == 0 ? pos.at[0] : axis == 1 ? pos.at[1] : axis == 2 ? pos.at[2] : pos.at[3];
     };
     const int64_t row = at(code & 3u) * R + p;
     if (code == (code & 3u) * 0x55u) {  // one axis: one run of the table each
@@ -103,24 +132,11 @@ __device__ __forceinline__ void load_angles(const QkAxesArgs &a, const int64_t (
     }
 }
 
-// The angles of a lane's elements (see turn()) for the token at t; false where one of its
-// positions is outside the table.
+// The angles of a lane's elements (see Turn) for a token at pos.
 template <int D, int R, int STYLE>
-__device__ __forceinline__ bool lane_angles(const QkAxesArgs &a, int64_t t, int sub, float (&c)[8], float (&s)[8]) {
+__device__ __forceinline__ void lane_angles(const QkAxesArgs &a, const Positions &pos, int sub, float (&c)[8],
+                                            float (&s)[8]) {
     using L = AxesLane<D, R, STYLE>;
-    int64_t pos[kMaxAxes];
-    bool ok = true;
-#pragma unroll
-    for (int i = 0; i < kMaxAxes; ++i) {
-        pos[i] = 0;
-        if (a.used >> i & 1) {
-            pos[i] = __ldg(a.pos + i * a.pos_stride + t);
-            if (static_cast<uint64_t>(pos[i]) >= static_cast<uint64_t>(a.max_pos)) {
-                ok = false;
-                pos[i] = 0;  // keeps every address in range; nothing is stored
-            }
-        }
-    }
     if constexpr (L::kWhole && STYLE == RN_ROPE_NEOX) {
         load_angles<R>(a, pos, sub * 8, c, s);
         load_angles<R>(a, pos, sub * 8 + 4, c + 4, s + 4);
@@ -139,265 +155,374 @@ __device__ __forceinline__ bool lane_angles(const QkAxesArgs &a, int64_t t, int 
     } else {
         if (sub < L::kRotary) load_angles<R>(a, pos, sub * 4, c, s);
     }
-    return ok;
 }
 
-// Turns a lane's elements lo, hi: by R, or with `back` by R^T.  `other`: the partner
-// lane's first chunk where it is another's (neox pairs, R < D).
-template <int D, int R, int STYLE>
-__device__ __forceinline__ void turn(float (&lo)[8], float (&hi)[8], const float (&other)[8], const float (&c)[8],
-                                     const float (&s)[8], int sub, bool back) {
-    using L = AxesLane<D, R, STYLE>;
-    const auto pair = [&](float &x, float &y, float co, float si) {
-        const float b = back ? -si : si;
-        const float u = x * co - y * b, v = y * co + x * b;
-        x = u;
-        y = v;
-    };
-    if constexpr (L::kWhole && STYLE == RN_ROPE_NEOX) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) pair(lo[e], hi[e], c[e], s[e]);
-    } else if constexpr (STYLE == RN_ROPE_NEOX) {
-        if (sub < L::kRotary)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) lo[e] = lo[e] * c[e] + other[e] * (back ? -s[e] : s[e]);
-    } else if (L::kWhole || sub < L::kRotary) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pair(lo[2 * i], lo[2 * i + 1], c[i], s[i]);
-        if constexpr (L::kWhole)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) pair(hi[2 * i], hi[2 * i + 1], c[4 + i], s[4 + i]);
-    }
-}
+// ---- a lane's elements -------------------------------------------------------------------
 
+// Eight elements as they are stored, and as four fp32 pairs of neighbours.
 template <class E>
-__device__ __forceinline__ void widen(const uint4 &u, float (&x)[8]) {
-    x[0] = E::lo(u.x); x[1] = E::hi(u.x); x[2] = E::lo(u.y); x[3] = E::hi(u.y);
-    x[4] = E::lo(u.z); x[5] = E::hi(u.z); x[6] = E::lo(u.w); x[7] = E::hi(u.w);
+__device__ __forceinline__ void widen(const uint4 &u, Pair (&x)[4]) {
+    x[0] = Pair::of(E::lo(u.x), E::hi(u.x));
+    x[1] = Pair::of(E::lo(u.y), E::hi(u.y));
+    x[2] = Pair::of(E::lo(u.z), E::hi(u.z));
+    x[3] = Pair::of(E::lo(u.w), E::hi(u.w));
 }
 template <class E>
-__device__ __forceinline__ uint4 narrow(const float (&x)[8]) {
-    return make_uint4(E::pack(x[0], x[1]), E::pack(x[2], x[3]), E::pack(x[4], x[5]), E::pack(x[6], x[7]));
+__device__ __forceinline__ uint4 narrow(const Pair (&x)[4]) {
+    return make_uint4(E::pack(x[0].v.x, x[0].v.y), E::pack(x[1].v.x, x[1].v.y), E::pack(x[2].v.x, x[2].v.y),
+                      E::pack(x[3].v.x, x[3].v.y));
 }
 template <class E>
 __device__ __forceinline__ float square_sum(const uint4 &u, float acc) {
     return E::sq_acc(E::sq_acc(E::sq_acc(E::sq_acc(acc, u.x), u.y), u.z), u.w);
 }
-__device__ __forceinline__ uint4 shuffle_xor(const uint4 &u, int lanes) {
-    return make_uint4(__shfl_xor_sync(0xffffffffu, u.x, lanes), __shfl_xor_sync(0xffffffffu, u.y, lanes),
-                      __shfl_xor_sync(0xffffffffu, u.z, lanes), __shfl_xor_sync(0xffffffffu, u.w, lanes));
-}
 
-// The partner lane's chunk; lanes beyond the rotary ones take part and use nothing.
+// The partner lane's chunk; zeros for a lane that does not turn.  (All lanes take part.)
 template <int D, int R, int STYLE>
-__device__ __forceinline__ uint4 partner(const uint4 &u) {
+__device__ __forceinline__ uint4 partner(const uint4 &u, int sub) {
     using L = AxesLane<D, R, STYLE>;
-    if constexpr (!L::kWhole && STYLE == RN_ROPE_NEOX) return shuffle_xor(u, L::kPartner);
-    return u;
+    if constexpr (L::kWhole || STYLE != RN_ROPE_NEOX) return u;
+    const uint4 v = make_uint4(
+        __shfl_xor_sync(0xffffffffu, u.x, L::kPartner), __shfl_xor_sync(0xffffffffu, u.y, L::kPartner),
+        __shfl_xor_sync(0xffffffffu, u.z, L::kPartner), __shfl_xor_sync(0xffffffffu, u.w, L::kPartner));
+    return sub < L::kRotary ? v : make_uint4(0u, 0u, 0u, 0u);
 }
 
-constexpr int kAxesThreads = 256;
-constexpr int kAxesWarps = kAxesThreads / 32;
-
-// Heads h0 .. h1 - 1 of part `part` of n equal parts of `heads` heads.
-__device__ __forceinline__ void part_heads(int part, int n, int heads, int &h0, int &h1) {
-    h0 = static_cast<int>(static_cast<int64_t>(part) * heads / n);
-    h1 = static_cast<int>(static_cast<int64_t>(part + 1) * heads / n);
-}
-
-constexpr int kFwdAhead = 4;  // heads whose loads are under way together
-
-template <int D, int R, int STYLE, class E>
-__global__ void __launch_bounds__(kAxesThreads) qk_axes_fwd_kernel(const __grid_constant__ QkAxesArgs a) {
+// What a lane multiplies its elements by: with x = lo, hi and o the partner's chunk,
+//   neox, whole head:  lo' = lo a - hi b,  hi' = hi c + lo d   (pairs of neighbours at a time)
+//   neox, a part:      lo' = lo a + o b,   hi' = hi c
+//   neighbours:        of each pair (x, y) of a chunk: x' = x a.x - y a.y,  y' = y b.x + x b.y;
+//                      a, b for lo, c, d for hi (which only weighs where it does not turn)
+// The weights are in them: R w for the forward pass.
+template <int D, int R, int STYLE>
+struct Turn {
     using L = AxesLane<D, R, STYLE>;
-    pdl_trigger();
-    pdl_wait();
-    const int lane = threadIdx.x & 31, sub = lane % L::LPH;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kAxesWarps + (threadIdx.x >> 5);
-    const int parts = a.q_parts + a.k_parts;
-    const int64_t t = unit / parts * L::TOKENS + lane / L::LPH;
-    const int part = static_cast<int>(unit % parts);
-    if (unit / parts * L::TOKENS >= a.T) return;  // a whole warp
-    const bool live = t < a.T;
-    const bool is_q = part < a.q_parts;
-    int h0, h1;
-    if (is_q) {
-        part_heads(part, a.q_parts, a.Hq, h0, h1);
-    } else {
-        part_heads(part - a.q_parts, a.k_parts, a.Hkv, h0, h1);
-        h0 += a.Hq;
-        h1 += a.Hq;
-    }
-    const uint16_t *row = a.x + t * a.x_stride + sub * 8;
-    uint16_t *out = a.y + t * a.y_stride + sub * 8;
-    constexpr int HI = D / 2;
-    uint4 lo[kFwdAhead], hi[kFwdAhead];
-    const auto fetch = [&](int h) {
+    Pair a[4], b[4], c[4], d[4];
+
+    // co, si as lane_angles gives them; wl, wh: weights; wo: the partner's
+    __device__ __forceinline__ void set(const float (&co)[8], const float (&si)[8], const Pair (&wl)[4],
+                                        const Pair (&wh)[4], const Pair (&wo)[4], int sub) {
 #pragma unroll
-        for (int u = 0; u < kFwdAhead; ++u) {
-            lo[u] = hi[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (live && h + u < h1) {
-                lo[u] = *reinterpret_cast<const uint4 *>(row + static_cast<int64_t>(h + u) * D);
-                hi[u] = *reinterpret_cast<const uint4 *>(row + static_cast<int64_t>(h + u) * D + HI);
+        for (int i = 0; i < 4; ++i) {
+            const Pair cc = Pair::of(co[2 * i], co[2 * i + 1]), ss = Pair::of(si[2 * i], si[2 * i + 1]);
+            if constexpr (STYLE == RN_ROPE_NEOX && L::kWhole) {
+                a[i] = wl[i] * cc;
+                b[i] = -(wh[i] * ss);
+                c[i] = wh[i] * cc;
+                d[i] = wl[i] * ss;
+            } else if constexpr (STYLE == RN_ROPE_NEOX) {
+                a[i] = sub < L::kRotary ? wl[i] * cc : wl[i];
+                b[i] = wo[i] * ss;
+                c[i] = wh[i];
+            } else {
+                const bool turns = L::kWhole || sub < L::kRotary;
+                const float x = turns ? co[i] : 1.0f, y = turns ? si[i] : 0.0f;
+                a[i] = Pair::of(wl[i].v.x * x, -wl[i].v.y * y);
+                b[i] = Pair::of(wl[i].v.y * x, wl[i].v.x * y);
+                const float p = L::kWhole ? co[4 + i] : 1.0f, q = L::kWhole ? si[4 + i] : 0.0f;
+                c[i] = Pair::of(wh[i].v.x * p, -wh[i].v.y * q);
+                d[i] = Pair::of(wh[i].v.y * p, wh[i].v.x * q);
             }
         }
-    };
-    fetch(h0);
-    // the heads' loads do not wait for the position and its angles
-    const uint16_t *w = (is_q ? a.wq : a.wk) + sub * 8;
-    const uint4 wl = ld_ro16(w), wh = ld_ro16(w + HI);
-    const uint4 wp = partner<D, R, STYLE>(wl);
-    float c[8], s[8];
-    bool ok = false;
-    if (live) {
-        ok = lane_angles<D, R, STYLE>(a, t, sub, c, s);
-        if (!ok && sub == 0) atomicOr(&g_qk_axes_status, RN_STATUS_BAD_POSITION);
     }
-    for (int h = h0; h < h1; h += kFwdAhead) {
-        if (h != h0) fetch(h);
-        float rstd[kFwdAhead];
+    __device__ __forceinline__ void apply(Pair (&lo)[4], Pair (&hi)[4], const Pair (&o)[4], int sub) const {
 #pragma unroll
-        for (int u = 0; u < kFwdAhead; ++u) rstd[u] = square_sum<E>(hi[u], square_sum<E>(lo[u], 0.0f));
-#pragma unroll
-        for (int u = 0; u < kFwdAhead; ++u)
-            rstd[u] = __frsqrt_rn(group_sum<L::LPH>(rstd[u]) / static_cast<float>(D) + a.eps);
-#pragma unroll
-        for (int u = 0; u < kFwdAhead; ++u) {
-            const uint4 po = partner<D, R, STYLE>(lo[u]);
-            if (!ok || h + u >= h1) continue;  // (a group of lanes alike; nothing below crosses lanes)
-            float x[8], y[8], o[8], wv[8];
-            const auto weigh = [&](const uint4 &v, const uint4 &weight, float (&to)[8]) {
-                widen<E>(v, to);
-                widen<E>(weight, wv);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) to[e] = to[e] * rstd[u] * wv[e];
-            };
-            weigh(lo[u], wl, x);
-            weigh(hi[u], wh, y);
-            if constexpr (!L::kWhole && STYLE == RN_ROPE_NEOX) weigh(po, wp, o);
-            turn<D, R, STYLE>(x, y, o, c, s, sub, false);
-            st16(out + static_cast<int64_t>(h + u) * D, narrow<E>(x));
-            st16(out + static_cast<int64_t>(h + u) * D + HI, narrow<E>(y));
+        for (int i = 0; i < 4; ++i) {
+            const Pair x = lo[i], y = hi[i];
+            if constexpr (STYLE == RN_ROPE_NEOX && L::kWhole) {
+                lo[i] = x.fma(a[i], y * b[i]);
+                hi[i] = y.fma(c[i], x * d[i]);
+            } else if constexpr (STYLE == RN_ROPE_NEOX) {
+                lo[i] = x.fma(a[i], o[i] * b[i]);
+                hi[i] = y * c[i];
+            } else {
+                // (a lane that does not turn: a product with zero would make an infinity NaN)
+                const float2 v = x.v, w = y.v;
+                const bool turns = L::kWhole || sub < L::kRotary;
+                lo[i] = Pair::of(fmaf(v.x, a[i].v.x, turns ? v.y * a[i].v.y : 0.0f),
+                                 fmaf(v.y, b[i].v.x, turns ? v.x * b[i].v.y : 0.0f));
+                hi[i] = L::kWhole ? Pair::of(fmaf(w.x, c[i].v.x, w.y * c[i].v.y), fmaf(w.y, d[i].v.x, w.x * d[i].v.y))
+                                  : Pair::of(w.x * c[i].v.x, w.y * d[i].v.x);
+            }
         }
+    }
+};
+
+// ---- the stream of heads -----------------------------------------------------------------
+
+// A unit is a part of the heads of a warp's tokens: part_heads query heads or key heads, or
+// what is left of them.  A warp takes its units one after another as one stream of heads,
+// each lane with its own elements, copied to its own places in shared memory some heads
+// ahead: nothing waits for another lane, and the next unit comes in while one ends.  This is
+// a place in the stream.
+template <int TOKENS>
+struct HeadPlace {
+    int64_t t;            // the lanes' token
+    int64_t quad, quads;  // of how many groups of TOKENS tokens
+    int part, parts;      // parts first .. first + parts - 1 of a token's q_parts + k_parts
+    int quad_step, part_step;
+    int h, h1;            // the head, and the unit's end
+    bool is_q, live;
+
+    // Place `unit` of every `step`-th.
+    __device__ __forceinline__ HeadPlace(const QkAxesArgs &a, int first, int parts_, uint32_t unit, uint32_t step)
+        : quads((a.T + TOKENS - 1) / TOKENS), parts(first + parts_) {
+        const uint32_t n = parts_;
+        quad = unit / n;
+        part = first + static_cast<int>(unit - static_cast<uint32_t>(quad) * n);
+        quad_step = static_cast<int>(step / n);
+        part_step = static_cast<int>(step - quad_step * n);
+        enter(a);
+    }
+    __device__ __forceinline__ bool inside() const { return quad < quads; }
+    __device__ __forceinline__ void enter(const QkAxesArgs &a) {
+        t = quad * TOKENS + (threadIdx.x & 31) / (32 / TOKENS);
+        live = t < a.T;  // (also where there is no such unit)
+        is_q = part < a.q_parts;
+        h = (is_q ? part : part - a.q_parts) * a.part_heads;
+        h1 = min(h + a.part_heads, is_q ? a.Hq : a.Hkv);
+        if (!is_q) {
+            h += a.Hq;
+            h1 += a.Hq;
+        }
+    }
+    __device__ __forceinline__ void next_unit(const QkAxesArgs &a, int first) {
+        quad += quad_step;
+        part += part_step;
+        if (part >= parts) {
+            part -= parts - first;
+            ++quad;
+        }
+        enter(a);
+    }
+    // On to the next head; true where a unit ends.
+    __device__ __forceinline__ bool next(const QkAxesArgs &a, int first) {
+        if (++h < h1) return false;
+        next_unit(a, first);
+        return true;
+    }
+};
+
+// ---- forward ---------------------------------------------------------------------------
+
+constexpr int kFwdThreads = 256;
+constexpr int kFwdWarps = kFwdThreads / 32;
+constexpr int kFwdBlocks = 3;   // blocks of an SM
+constexpr int kFwdStages = 3;   // heads that a warp has under way or is taking
+
+template <int D, int R, int STYLE, class E>
+__global__ void __launch_bounds__(kFwdThreads, kFwdBlocks)
+    qk_axes_fwd_kernel(const __grid_constant__ QkAxesArgs a) {
+    using L = AxesLane<D, R, STYLE>;
+    constexpr int HI = D / 2;
+    extern __shared__ __align__(16) uint4 heads_in[];
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L::LPH;
+    HeadPlace<L::TOKENS> now(a, 0, a.q_parts + a.k_parts, blockIdx.x * kFwdWarps + warp, gridDim.x * kFwdWarps);
+    HeadPlace<L::TOKENS> ahead = now;
+    uint4 *in = heads_in + warp * (kFwdStages * 64) + lane;
+    uint32_t head = 0, tail = 0;  // stages of the head to be copied next, and to be taken next
+    const auto copy = [&] {
+        if (ahead.live) {
+            const uint16_t *x = a.x + ahead.t * a.x_stride + static_cast<int64_t>(ahead.h) * D + sub * 8;
+            copy_async16(in + head * 64, x);
+            copy_async16(in + head * 64 + 32, x + HI);
+        }
+        copy_commit();
+        head = head + 1 == kFwdStages ? 0 : head + 1;
+        ahead.next(a, 0);
+    };
+    Positions pos;
+    pos.load(a, now.t, now.live);
+#pragma unroll 1
+    for (int i = 0; i < kFwdStages - 1; ++i) copy();
+
+    while (now.inside()) {
+        Turn<D, R, STYLE> turn;
+        const bool ok = pos.ok;
+        if (now.live && !ok && sub == 0) atomicOr(&g_qk_axes_status, RN_STATUS_BAD_POSITION);
+        {
+            const uint16_t *w = (now.is_q ? a.wq : a.wk) + sub * 8;
+            const uint4 ul = ld_ro16(w), uh = ld_ro16(w + HI);
+            Pair wl[4], wh[4], wo[4];
+            float c[8] = {}, s[8] = {};
+            if (ok) lane_angles<D, R, STYLE>(a, pos, sub, c, s);
+            widen<E>(ul, wl);
+            widen<E>(uh, wh);
+            widen<E>(partner<D, R, STYLE>(ul, sub), wo);
+            turn.set(c, s, wl, wh, wo, sub);
+        }
+        {
+            HeadPlace<L::TOKENS> then = now;  // the next unit's positions come meanwhile
+            then.next_unit(a, 0);
+            pos.load(a, then.t, then.live);
+        }
+        bool end;
+        do {
+            copy_wait<kFwdStages - 2>();
+            const uint4 lo = ld_shared16(in + tail * 64), hi = ld_shared16(in + tail * 64 + 32);
+            tail = tail + 1 == kFwdStages ? 0 : tail + 1;
+            copy();  // (to the stage that the head before came from)
+            const float rstd = __frsqrt_rn(
+                group_sum<L::LPH>(square_sum<E>(hi, square_sum<E>(lo, 0.0f))) / static_cast<float>(D) + a.eps);
+            const uint4 po = partner<D, R, STYLE>(lo, sub);
+            if (ok) {
+                Pair x[4], y[4], o[4];
+                widen<E>(lo, x);
+                widen<E>(hi, y);
+                widen<E>(po, o);
+                const Pair r = Pair::both(rstd);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = x[i] * r;
+                    y[i] = y[i] * r;
+                    if constexpr (!L::kWhole && STYLE == RN_ROPE_NEOX) o[i] = o[i] * r;
+                }
+                turn.apply(x, y, o, sub);
+                uint16_t *out = a.y + now.t * a.y_stride + static_cast<int64_t>(now.h) * D + sub * 8;
+                st16(out, narrow<E>(x));
+                st16(out + HI, narrow<E>(y));
+            }
+            end = now.next(a, 0);
+        } while (!end);
     }
 }
 
-constexpr int kBwdAhead = 2;
+// ---- gradient ----------------------------------------------------------------------------
+
+constexpr int kBwdThreads = 256;
+constexpr int kBwdWarps = kBwdThreads / 32;
+constexpr int kBwdBlocks = 2;  // blocks of an SM
+constexpr int kBwdStages = 3;  // heads that a warp has under way or is taking
 
 template <int D, int R, int STYLE, class E>
-__global__ void __launch_bounds__(kAxesThreads, 2) qk_axes_bwd_kernel(const __grid_constant__ QkAxesArgs a) {
+__global__ void __launch_bounds__(kBwdThreads, kBwdBlocks)
+    qk_axes_bwd_kernel(const __grid_constant__ QkAxesArgs a) {
     using L = AxesLane<D, R, STYLE>;
-    constexpr int GROUPS = kAxesWarps * L::TOKENS;  // groups of lanes of the block
-    __shared__ float sums[GROUPS][D];
+    constexpr int HI = D / 2;
+    constexpr int GROUPS = kBwdWarps * L::TOKENS;  // groups of lanes of the block
+    static_assert(GROUPS * D * 4 <= kBwdWarps * kBwdStages * 2048, "the sums take the place of the stages");
+    extern __shared__ __align__(16) uint4 heads_in[];
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31, sub = lane % L::LPH;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L::LPH;
+    // query heads or key heads alone
     const bool is_q = static_cast<int>(blockIdx.x) < a.q_blocks;
     const int block = is_q ? blockIdx.x : blockIdx.x - a.q_blocks;
     const int blocks = is_q ? a.q_blocks : gridDim.x - a.q_blocks;
-    const int parts = is_q ? a.q_parts : a.k_parts, heads = is_q ? a.Hq : a.Hkv, first = is_q ? 0 : a.Hq;
-    const int64_t units = (a.T + L::TOKENS - 1) / L::TOKENS * parts;
-    constexpr int HI = D / 2;
-    const uint16_t *w = (is_q ? a.wq : a.wk) + sub * 8;
-    const uint4 wl = ld_ro16(w), wh = ld_ro16(w + HI);
-    float dl[8], dh[8];  // sums of g n^
-#pragma unroll
-    for (int e = 0; e < 8; ++e) dl[e] = dh[e] = 0.0f;
+    const int first = is_q ? 0 : a.q_parts;
+    HeadPlace<L::TOKENS> now(a, first, is_q ? a.q_parts : a.k_parts, block * kBwdWarps + warp, blocks * kBwdWarps);
+    HeadPlace<L::TOKENS> ahead = now;
+    uint4 *in = heads_in + warp * (kBwdStages * 128) + lane;
+    uint32_t head = 0, tail = 0;  // stages of the head to be copied next, and to be taken next
+    const auto copy = [&] {
+        if (ahead.live) {
+            uint4 *to = in + head * 128;
+            const int64_t at = static_cast<int64_t>(ahead.h) * D + sub * 8;
+            const uint16_t *x = a.x + ahead.t * a.x_stride + at, *g = a.dout + ahead.t * a.dout_stride + at;
+            copy_async16(to, x);
+            copy_async16(to + 32, x + HI);
+            copy_async16(to + 64, g);
+            copy_async16(to + 96, g + HI);
+        }
+        copy_commit();
+        head = head + 1 == kBwdStages ? 0 : head + 1;
+        ahead.next(a, first);
+    };
+    Positions pos;
+    pos.load(a, now.t, now.live);
+#pragma unroll 1
+    for (int i = 0; i < kBwdStages - 1; ++i) copy();
 
-    for (int64_t unit = static_cast<int64_t>(block) * kAxesWarps + (threadIdx.x >> 5); unit < units;
-         unit += static_cast<int64_t>(blocks) * kAxesWarps) {
-        const int64_t t = unit / parts * L::TOKENS + lane / L::LPH;
-        const bool live = t < a.T;
-        int h0, h1;
-        part_heads(static_cast<int>(unit % parts), parts, heads, h0, h1);
-        h0 += first;
-        h1 += first;
-        const uint16_t *row = a.x + t * a.x_stride + sub * 8;
-        const uint16_t *grad = a.dout + t * a.dout_stride + sub * 8;
-        uint16_t *out = a.y + t * a.y_stride + sub * 8;
-        uint4 xl[kBwdAhead], xh[kBwdAhead], gl[kBwdAhead], gh[kBwdAhead];
-        const auto fetch = [&](int h) {
+    const uint16_t *w = (is_q ? a.wq : a.wk) + sub * 8;
+    Pair wl[4], wh[4], dl[4], dh[4];  // weights; sums of g n^
+    widen<E>(ld_ro16(w), wl);
+    widen<E>(ld_ro16(w + HI), wh);
 #pragma unroll
-            for (int u = 0; u < kBwdAhead; ++u) {
-                xl[u] = xh[u] = gl[u] = gh[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (live && h + u < h1) {
-                    const int64_t at = static_cast<int64_t>(h + u) * D;
-                    xl[u] = *reinterpret_cast<const uint4 *>(row + at);
-                    xh[u] = *reinterpret_cast<const uint4 *>(row + at + HI);
-                    gl[u] = *reinterpret_cast<const uint4 *>(grad + at);
-                    gh[u] = *reinterpret_cast<const uint4 *>(grad + at + HI);
-                }
-            }
-        };
-        fetch(h0);
-        float c[8], s[8];
-        bool ok = false;
-        if (live) {
-            ok = lane_angles<D, R, STYLE>(a, t, sub, c, s);
-            if (!ok && sub == 0) atomicOr(&g_qk_axes_status, RN_STATUS_BAD_POSITION);
+    for (int i = 0; i < 4; ++i) dl[i] = dh[i] = Pair::both(0.0f);
+
+    while (now.inside()) {
+        // R^T: the angles with the other sign, and no weights
+        Turn<D, R, STYLE> back;
+        const bool ok = pos.ok;
+        if (now.live && !ok && sub == 0) atomicOr(&g_qk_axes_status, RN_STATUS_BAD_POSITION);
+        {
+            float c[8] = {}, s[8] = {};
+            if (ok) lane_angles<D, R, STYLE>(a, pos, sub, c, s);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] = -s[i];
+            const Pair one[4] = {Pair::both(1.0f), Pair::both(1.0f), Pair::both(1.0f), Pair::both(1.0f)};
+            back.set(c, s, one, one, one, sub);
         }
-        for (int h = h0; h < h1; h += kBwdAhead) {
-            if (h != h0) fetch(h);
-            float rstd[kBwdAhead];
-#pragma unroll
-            for (int u = 0; u < kBwdAhead; ++u) rstd[u] = square_sum<E>(xh[u], square_sum<E>(xl[u], 0.0f));
-#pragma unroll
-            for (int u = 0; u < kBwdAhead; ++u)
-                rstd[u] = __frsqrt_rn(group_sum<L::LPH>(rstd[u]) / static_cast<float>(D) + a.eps);
-#pragma unroll
-            for (int u = 0; u < kBwdAhead; ++u) {
-                float x[8], y[8], p[8], q[8], o[8], wv[8];
-                const uint4 po = partner<D, R, STYLE>(gl[u]);
-                widen<E>(gl[u], p);
-                widen<E>(gh[u], q);
-                widen<E>(po, o);
-                turn<D, R, STYLE>(p, q, o, c, s, sub, true);
-                widen<E>(xl[u], x);
-                widen<E>(xh[u], y);
-                const bool use = ok && h + u < h1;
-                float dot = 0.0f;
-                // n^ = x rstd, dw += g n^, u = g w, dot = sum u n^
-                widen<E>(wl, wv);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[e] *= rstd[u];
-                    if (use) dl[e] = fmaf(p[e], x[e], dl[e]);
-                    p[e] *= wv[e];
-                    dot = fmaf(p[e], x[e], dot);
-                }
-                widen<E>(wh, wv);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    y[e] *= rstd[u];
-                    if (use) dh[e] = fmaf(q[e], y[e], dh[e]);
-                    q[e] *= wv[e];
-                    dot = fmaf(q[e], y[e], dot);
-                }
-                dot = group_sum<L::LPH>(dot) / static_cast<float>(D);
-                if (!use) continue;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    p[e] = rstd[u] * fmaf(-x[e], dot, p[e]);
-                    q[e] = rstd[u] * fmaf(-y[e], dot, q[e]);
-                }
-                st16(out + static_cast<int64_t>(h + u) * D, narrow<E>(p));
-                st16(out + static_cast<int64_t>(h + u) * D + HI, narrow<E>(q));
-            }
+        {
+            HeadPlace<L::TOKENS> then = now;  // the next unit's positions come meanwhile
+            then.next_unit(a, first);
+            pos.load(a, then.t, then.live);
         }
+        bool end;
+        do {
+            copy_wait<kBwdStages - 2>();
+            const uint4 *from = in + tail * 128;
+            const uint4 ul = ld_shared16(from), uh = ld_shared16(from + 32);
+            const uint4 vl = ld_shared16(from + 64), vh = ld_shared16(from + 96);
+            tail = tail + 1 == kBwdStages ? 0 : tail + 1;
+            copy();  // (to the stage that the head before came from)
+            const float rstd = __frsqrt_rn(
+                group_sum<L::LPH>(square_sum<E>(uh, square_sum<E>(ul, 0.0f))) / static_cast<float>(D) + a.eps);
+            Pair x[4], y[4], p[4], q[4], o[4];
+            widen<E>(vl, p);
+            widen<E>(vh, q);
+            widen<E>(partner<D, R, STYLE>(vl, sub), o);
+            back.apply(p, q, o, sub);
+            widen<E>(ul, x);
+            widen<E>(uh, y);
+            const Pair r = Pair::both(rstd);
+            Pair dots = Pair::both(0.0f);
+            // n^ = x rstd, dw += g n^, u = g w, dot = sum u n^
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = x[i] * r;
+                y[i] = y[i] * r;
+                if (ok) {
+                    dl[i] = p[i].fma(x[i], dl[i]);
+                    dh[i] = q[i].fma(y[i], dh[i]);
+                }
+                p[i] = p[i] * wl[i];
+                q[i] = q[i] * wh[i];
+                dots = p[i].fma(x[i], dots);
+                dots = q[i].fma(y[i], dots);
+            }
+            const Pair dot = Pair::both(-group_sum<L::LPH>(dots.sum()) / static_cast<float>(D));
+            if (ok) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    p[i] = r * x[i].fma(dot, p[i]);
+                    q[i] = r * y[i].fma(dot, q[i]);
+                }
+                uint16_t *out = a.y + now.t * a.y_stride + static_cast<int64_t>(now.h) * D + sub * 8;
+                st16(out, narrow<E>(p));
+                st16(out + HI, narrow<E>(q));
+            }
+            end = now.next(a, first);
+        } while (!end);
     }
+    copy_wait<0>();
+    __syncthreads();
 
     // the block's sums of dw, its groups in their order
-    const int group = (threadIdx.x >> 5) * L::TOKENS + lane / L::LPH;
+    float *sums = reinterpret_cast<float *>(heads_in);
+    float *mine = sums + (warp * L::TOKENS + lane / L::LPH) * D + sub * 8;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        sums[group][sub * 8 + e] = dl[e];
-        sums[group][HI + sub * 8 + e] = dh[e];
+    for (int i = 0; i < 4; ++i) {
+        *reinterpret_cast<float2 *>(mine + 2 * i) = dl[i].v;
+        *reinterpret_cast<float2 *>(mine + HI + 2 * i) = dh[i].v;
     }
     __syncthreads();
-    for (int d = threadIdx.x; d < D; d += kAxesThreads) {
+    for (int d = threadIdx.x; d < D; d += kBwdThreads) {
         float v = 0.0f;
 #pragma unroll 8
-        for (int g = 0; g < GROUPS; ++g) v += sums[g][d];
+        for (int g = 0; g < GROUPS; ++g) v += sums[g * D + d];
         a.partial[static_cast<int64_t>(blockIdx.x) * D + d] = v;
     }
 }
@@ -406,30 +531,27 @@ __global__ void __launch_bounds__(kAxesThreads, 2) qk_axes_bwd_kernel(const __gr
 constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(32 * kSumWarps) qk_axes_sum_kernel(const float *partial, int q_blocks, int blocks,
                                                                      int D, float *dwq, float *dwk, int accumulate) {
-    __shared__ float sums[kSumWarps][32];
+    __shared__ float sums[kSumWarps][33];
     pdl_trigger();
-    pdl_wait();
     float *dw = blockIdx.y == 0 ? dwq : dwk;
     if (!dw) return;
+    pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int d = blockIdx.x * 32 + lane;
     const int b0 = blockIdx.y == 0 ? 0 : q_blocks, b1 = blockIdx.y == 0 ? q_blocks : blocks;
     float v = 0.0f;
 #pragma unroll 8
-    for (int b = b0 + warp; b < b1; b += kSumWarps) v += partial[static_cast<int64_t>(b) * D + d];
+    for (int b = b0 + warp; b < b1; b += kSumWarps) v += partial[static_cast<int64_t>(b) * D + blockIdx.x * 32 + lane];
     sums[warp][lane] = v;
     __syncthreads();
-    if (warp == 0) {
-        v = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kSumWarps; ++k) v += sums[k][lane];
+    v = warp_sum(sums[lane][warp]);  // dimension `warp` of the block's
+    if (lane == 0) {
+        const int d = blockIdx.x * 32 + warp;
         dw[d] = accumulate ? dw[d] + v : v;
     }
 }
 
 // ---- host -------------------------------------------------------------------------------
 
-constexpr int kBwdBlocks = 4;  // blocks an SM, at most
 
 static int64_t bwd_workspace(int sm_count, int D) {
     return static_cast<int64_t>(sm_count) * kBwdBlocks * D * 4;
@@ -438,41 +560,82 @@ static int64_t bwd_workspace(int sm_count, int D) {
 // Parts that `heads` heads are cut into so that a part has up to `most` of them.
 static int parts_of(int heads, int most) { return (heads + most - 1) / most; }
 
-// Heads of a part: eight, or fewer where tokens are too few to fill the GPU's warps.
-static int part_size(int64_t warps_of_tokens, int heads, int64_t want) {
-    for (int n = 8; n > 1; n /= 2)
-        if (warps_of_tokens * parts_of(heads, n) >= want) return n;
-    return 1;
+// Heads of a part, at most: of 1, 2, 4 .. 32 what lets the last of `warps` warps end first, where
+// to enter a unit costs a warp about as much as `enter` heads.
+static int part_size(int64_t quads, int Hq, int Hkv, int64_t warps, int enter) {
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int n = 1; n <= 32; n *= 2) {
+        const int64_t units = quads * (parts_of(Hq, n) + parts_of(Hkv, n));
+        const int64_t cost = (units + warps - 1) / warps * (n + enter);
+        if (cost < least) {
+            least = cost;
+            best = n;
+        }
+    }
+    return best;
+}
+
+// A kernel with more than 48 KB of shared memory has to be told once on each device.
+template <class Kernel>
+static int allow_shared(Kernel kernel, int bytes, std::atomic<int> (&done)[kMaxDevices]) {
+    const int idx = current_device_index();
+    if (idx < 0 || idx >= kMaxDevices) return RN_ERR_DEVICE;
+    if (done[idx].load(std::memory_order_acquire)) return RN_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return RN_ERR_DEVICE;
+    }
+    done[idx].store(1, std::memory_order_release);
+    return RN_OK;
 }
 
 template <int D, int R, int STYLE, class E>
 static int qk_axes_launch(QkAxesArgs &a, bool backward, float *dwq, float *dwk, int accumulate, const DeviceInfo &dev,
                           cudaStream_t st) {
     using L = AxesLane<D, R, STYLE>;
+    static std::atomic<int> fwd_done[kMaxDevices], bwd_done[kMaxDevices];
     const int64_t quads = (a.T + L::TOKENS - 1) / L::TOKENS;
-    const int n = part_size(quads, a.Hq + a.Hkv, static_cast<int64_t>(dev.sm_count) * 16);
+    // four pairs of one axis are one load of the table each way, of several eight
+    int mixed = 0;
+    for (int p = 0; p < R / 2; p += 4) {
+        const uint32_t code = a.pair_axis[p >> 4] >> (2 * (p & 15)) & 0xFFu;
+        if (code != (code & 3u) * 0x55u) mixed = 3;
+    }
+    const int n = backward ? part_size(quads, a.Hq, a.Hkv, static_cast<int64_t>(dev.sm_count) * kBwdBlocks * kBwdWarps,
+                                       1 + mixed)
+                           : part_size(quads, a.Hq, a.Hkv, static_cast<int64_t>(dev.sm_count) * kFwdBlocks * kFwdWarps,
+                                       3 + mixed);
+    a.part_heads = n;
     a.q_parts = parts_of(a.Hq, n);
     a.k_parts = parts_of(a.Hkv, n);
-    const int64_t units = quads * (a.q_parts + a.k_parts);
-    if (!backward) {
-        const int64_t blocks = (units + kAxesWarps - 1) / kAxesWarps;
-        return launch_pdl(qk_axes_fwd_kernel<D, R, STYLE, E>, dim3(static_cast<unsigned>(blocks)), dim3(kAxesThreads),
-                          0, st, a);
-    }
-    const int64_t most = static_cast<int64_t>(dev.sm_count) * 2;
-    const auto blocks_of = [&](int64_t u, int64_t cap) {
-        const int64_t b = (u + kAxesWarps - 1) / kAxesWarps;
+    const auto blocks_of = [&](int64_t units, int warps, int64_t cap) {
+        const int64_t b = (units + warps - 1) / warps;
         return static_cast<int>(b < cap ? b : cap);
     };
-    // shares of the grid by their heads
-    int64_t q_cap = most * a.Hq / (a.Hq + a.Hkv);
+    if (!backward) {
+        constexpr int smem = kFwdWarps * kFwdStages * 1024;
+        const int rc = allow_shared(qk_axes_fwd_kernel<D, R, STYLE, E>, smem, fwd_done);
+        if (rc != RN_OK) return rc;
+        const int blocks = blocks_of(quads * (a.q_parts + a.k_parts), kFwdWarps,
+                                     static_cast<int64_t>(dev.sm_count) * kFwdBlocks);
+        return launch_pdl(qk_axes_fwd_kernel<D, R, STYLE, E>, dim3(static_cast<unsigned>(blocks)), dim3(kFwdThreads),
+                          smem, st, a);
+    }
+    constexpr int smem = kBwdWarps * kBwdStages * 2048;
+    int rc = allow_shared(qk_axes_bwd_kernel<D, R, STYLE, E>, smem, bwd_done);
+    if (rc != RN_OK) return rc;
+    const int64_t most = static_cast<int64_t>(dev.sm_count) * kBwdBlocks;
+    // shares of the grid by the heads, and the units that they are taken in
+    const int64_t q_cost = a.Hq + a.q_parts, k_cost = a.Hkv + a.k_parts;
+    int64_t q_cap = (most * q_cost + (q_cost + k_cost) / 2) / (q_cost + k_cost);
     if (q_cap < 1) q_cap = 1;
     if (q_cap > most - 1) q_cap = most - 1;
-    a.q_blocks = blocks_of(quads * a.q_parts, a.Hkv ? q_cap : most);
-    const int k_blocks = blocks_of(quads * a.k_parts, a.Hq ? most - q_cap : most);
+    a.q_blocks = blocks_of(quads * a.q_parts, kBwdWarps, a.Hkv ? q_cap : most);
+    const int k_blocks = blocks_of(quads * a.k_parts, kBwdWarps, a.Hq ? most - q_cap : most);
     const int blocks = a.q_blocks + k_blocks;
-    const int rc = launch_pdl(qk_axes_bwd_kernel<D, R, STYLE, E>, dim3(static_cast<unsigned>(blocks)),
-                              dim3(kAxesThreads), 0, st, a);
+    rc = launch_pdl(qk_axes_bwd_kernel<D, R, STYLE, E>, dim3(static_cast<unsigned>(blocks)), dim3(kBwdThreads), smem,
+                    st, a);
     if (rc != RN_OK || (!dwq && !dwk)) return rc;
     return launch_pdl(qk_axes_sum_kernel, dim3(D / 32, 2), dim3(32 * kSumWarps), 0, st,
                       static_cast<const float *>(a.partial), a.q_blocks, blocks, D, dwq, dwk, accumulate);
@@ -510,7 +673,7 @@ static int qk_axes_run(QkAxesArgs &a, const QkAxesCall &k, rn_stream_t stream) {
     if (k.num_axes < 1 || k.num_axes > kMaxAxes) return RN_ERR_SHAPE;
     const int64_t H = static_cast<int64_t>(a.Hq) + a.Hkv;
     if (H > INT32_MAX || (H > 0 && a.T > INT32_MAX / H)) return RN_ERR_SHAPE;
-    if (a.max_pos < 1) return RN_ERR_SHAPE;
+    if (a.max_pos < 1 || a.max_pos > INT32_MAX) return RN_ERR_SHAPE;
     const int64_t width = H * D;
     const auto bad_stride = [&](int64_t stride) { return width > 0 && a.T > 1 && (stride < width || stride % 8 != 0); };
     if (bad_stride(a.x_stride) || bad_stride(a.y_stride) || (k.backward && bad_stride(a.dout_stride)))

@@ -164,6 +164,38 @@ __device__ __forceinline__ void st16(void *p, uint4 v) {
     *reinterpret_cast<uint4 *>(p) = v;
 }
 
+// ---- packed fp32 ---------------------------------------------------------------
+
+// Two fp32 values; an operation on both is one instruction.
+struct Pair {
+    float2 v;
+    __device__ __forceinline__ static Pair of(float x, float y) { return {make_float2(x, y)}; }
+    __device__ __forceinline__ static Pair both(float x) { return {make_float2(x, x)}; }
+    __device__ __forceinline__ float2 split() const { return v; }
+    __device__ __forceinline__ float sum() const { return v.x + v.y; }
+    __device__ __forceinline__ Pair operator-() const { return {make_float2(-v.x, -v.y)}; }
+    __device__ __forceinline__ Pair operator*(Pair b) const { return {__fmul2_rn(v, b.v)}; }
+    __device__ __forceinline__ Pair operator+(Pair b) const { return {__fadd2_rn(v, b.v)}; }
+    // this * b + c
+    __device__ __forceinline__ Pair fma(Pair b, Pair c) const { return {__ffma2_rn(v, b.v, c.v)}; }
+};
+
+// ---- asynchronous copies by thread ------------------------------------------------
+// 16 bytes from global to shared memory; a thread's copies count in groups, and copy_wait
+// returns when all but its last LEFT groups are there (for itself).
+
+__device__ __forceinline__ void copy_async16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+                 "l"(from)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
 // ---- reductions ---------------------------------------------------------------
 
 __device__ __forceinline__ float warp_sum(float v) {

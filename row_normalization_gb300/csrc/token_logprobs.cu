@@ -131,18 +131,6 @@ __device__ __forceinline__ float largest(const uint4 (&u)[N]) {
     }
 }
 
-// Two fp32 values; an operation on both is one instruction.
-struct Pair {
-    float2 v;
-    __device__ __forceinline__ static Pair of(float x, float y) { return {make_float2(x, y)}; }
-    __device__ __forceinline__ float2 split() const { return v; }
-    __device__ __forceinline__ float sum() const { return v.x + v.y; }
-    __device__ __forceinline__ Pair operator*(Pair b) const { return {__fmul2_rn(v, b.v)}; }
-    __device__ __forceinline__ Pair operator+(Pair b) const { return {__fadd2_rn(v, b.v)}; }
-    // this * b + c
-    __device__ __forceinline__ Pair fma(Pair b, Pair c) const { return {__ffma2_rn(v, b.v, c.v)}; }
-};
-
 // 32 bits that are ordered as the values are, NaN above all; never 0, so 0 is "none".
 __device__ __forceinline__ uint32_t ordered(float x) {
     if (x != x) return 0xFFFFFFFFu;
@@ -783,15 +771,6 @@ __device__ __forceinline__ void take_end(S &sh, const Row<F> &row, const Share &
 }
 
 // ---- the stream of batches ------------------------------------------------------------
-
-__device__ __forceinline__ void copy_async16(void *to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
-}
 
 // A block's share of its rows (t, t + step, ..) as one stream of batches.  Each thread
 // copies its own granules to its own places in shared memory, kStages - 1 batches ahead of
