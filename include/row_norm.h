@@ -753,10 +753,9 @@ int token_logprobs_fwd(int dtype, const void *logits, int64_t stride, const int6
  *               the same stride, or memory that does not overlap it.
  * An ignored target's dlogprobs counts as 0; with a target >= V the row is NaN
  * and RN_STATUS_BAD_INDEX is raised.  Banned tokens, and rows of nothing else,
- * get 0; a row whose lse is NaN or +infinity gets NaN.  A row's accesses are 16
- * bytes wide where logits and dlogits lie alike within 16 bytes, and an element
- * wide in dlogits otherwise.  T * ceil(V / 4096) below 2^31.  Errors as the
- * forward call. */
+ * get 0; a row whose lse is NaN or +infinity gets NaN.  T * ceil(V / 4096) below
+ * 2^31 (with V + 8 for V where rows of dlogits begin off 16-byte boundaries).
+ * Errors as the forward call. */
 int token_logprobs_bwd(int dtype, const void *logits, int64_t stride, const int64_t *targets,
                        const float *logprobs, const float *lse, const float *entropy,
                        const float *dlogprobs, int64_t dlogprobs_stride, const float *dentropy,

@@ -943,26 +943,65 @@ struct LogprobsGradArgs {
     void *dlogits;
     int64_t dstride;
     int64_t chunks;  // blocks of a row
+    int share;       // granules of a block
 };
 
 constexpr int kGradThreads = 256;
 constexpr int kGradBatch = 4;  // granules of a thread
 
+// The granule of elements i .. of a row, wherever they lie: two aligned ones, shifted.
+template <class F>
+__device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, uint32_t bytes) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t s[6], q[5];
+#pragma unroll
+    for (int j = 0; j < 6; ++j) s[j] = bytes & 8u ? w[j + 2] : w[j];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) q[j] = bytes & 4u ? s[j + 1] : s[j];
+    const uint32_t bits = (bytes & 2u) * 8u;
+    return make_uint4(__funnelshift_r(q[0], q[1], bits), __funnelshift_r(q[1], q[2], bits),
+                      __funnelshift_r(q[2], q[3], bits), __funnelshift_r(q[3], q[4], bits));
+}
+
+// A block takes a share of a row, by the granules of dlogits; logits may lie otherwise
+// within 16 bytes.  HBM bounds it: 4096 rows of 131072 in bf16, 2.15 GB, take 302 us (7.1 TB/s,
+// 1.05 of the copy's rate); 309 with loads and stores that keep their lines, 387 with two
+// granules a thread, 351 with scalar fp32 and shares that leave each row's last block a rest.
+// 2048 rows of 50021: 64 us (floor 60); 79 where dlogits lies otherwise than logits (235 with
+// stores of one element).
 template <class F>
 __global__ void __launch_bounds__(kGradThreads) logprobs_bwd_kernel(const __grid_constant__ LogprobsGradArgs a) {
     pdl_trigger();
     pdl_wait();
-    const int64_t t = blockIdx.x / a.chunks, chunk = blockIdx.x - t * a.chunks;
-    const Row<F> row(a.logits, a.stride, t, a.V);
-    typename F::T *out = static_cast<typename F::T *>(a.dlogits) + t * a.dstride;
-    const bool aligned = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row.x)) & 15u) == 0;
-    const int64_t first = chunk * (kGradThreads * kGradBatch) + threadIdx.x;
+    const int64_t t = blockIdx.x / a.chunks;
+    const int chunk = static_cast<int>(blockIdx.x - t * a.chunks);
+    const Row<F> out(a.dlogits, a.dstride, t, a.V);
+    const typename F::T *x = static_cast<const typename F::T *>(a.logits) + t * a.stride;
+    typename F::T *y = const_cast<typename F::T *>(out.x);
+    const int first = chunk * a.share + threadIdx.x;
+    const int end = min(out.granules, (chunk + 1) * a.share);
+    // granules g of which logits' 16 bytes (32 where they lie otherwise) are all the row's
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x + out.index(0))) & 15u;
+    const int before = static_cast<int>(off / sizeof(typename F::T));
+    const auto inside = [&](int g) {
+        const int i = out.index(g) - before;
+        return i >= 0 && i <= a.V - (off ? 2 : 1) * F::kElems;
+    };
     uint4 u[kGradBatch];
 #pragma unroll
     for (int b = 0; b < kGradBatch; ++b) {
-        const int64_t g = first + b * kGradThreads;
+        const int g = first + b * kGradThreads;
         u[b] = make_uint4(0u, 0u, 0u, 0u);
-        if (g < row.granules && row.whole(g)) u[b] = row.load(g);
+        if (g >= end) continue;
+        const int i = out.index(g);
+        if (!inside(g)) {
+            u[b] = end_of_row<F>(x, i, static_cast<int>(a.V));
+        } else if (off == 0u) {
+            u[b] = ld_stream16(x + i);
+        } else {
+            const uint4 *p = reinterpret_cast<const uint4 *>(x + (i - before));
+            u[b] = shifted<F>(p[0], p[1], off);
+        }
     }
     const float lse = a.lse[t];
     const float h = a.entropy ? a.entropy[t] : 0.0f;
@@ -994,32 +1033,38 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_bwd_kernel(const __grid
         const float l = fmaxf(lt, -150.0f);
         return a.scale * (expf(l) * (dl - dh * (l + h)) - expm1f(l) * dp);
     };
-    const auto grad = [&](float x) {
-        const float l = fmaxf(fmaf(x, a.scale, -lse), -150.0f);
-        return exp2_fast(l * 1.4426950408889634f) * fmaf(-c1, l, c0);
+    const Pair scale = Pair::both(a.scale), ref = Pair::both(-lse), log2e = Pair::both(1.4426950408889634f);
+    const Pair k0 = Pair::both(c0), k1 = Pair::both(-c1);
+    const auto grad = [&](float &p, float &q) {
+        const float2 l = Pair::of(p, q).fma(scale, ref).v;
+        const Pair m = Pair::of(fmaxf(l.x, -150.0f), fmaxf(l.y, -150.0f));
+        const float2 e = (m * log2e).v;
+        const float2 r = (Pair::of(exp2_fast(e.x), exp2_fast(e.y)) * m.fma(k1, k0)).v;
+        p = r.x;
+        q = r.y;
     };
 #pragma unroll
     for (int b = 0; b < kGradBatch; ++b) {
-        const int64_t g = first + b * kGradThreads;
-        if (g >= row.granules) return;
-        const int64_t i = row.index(g);
+        const int g = first + b * kGradThreads;
+        if (g >= end) return;
+        const int i = out.index(g);
         float v[F::kElems];
-        const bool whole = row.whole(g);
-        widen<F>(whole ? u[b] : row.fetch(g), v);
+        widen<F>(u[b], v);
 #pragma unroll
-        for (int e = 0; e < F::kElems; ++e) v[e] = grad(v[e]);
+        for (int e = 0; e < F::kElems; e += 2) grad(v[e], v[e + 1]);
         if (target >= i && target < i + F::kElems) {
             const float gt = given();
 #pragma unroll
             for (int e = 0; e < F::kElems; ++e)
                 if (target == i + e) v[e] = gt;
         }
-        if (whole && aligned) {
-            st16(out + i, narrow<F>(v));
+        if (out.whole(g)) {
+            __stcs(reinterpret_cast<uint4 *>(y + i), narrow<F>(v));
         } else {
+            const uint32_t there = out.there(g);
 #pragma unroll
             for (int e = 0; e < F::kElems; ++e)
-                if (row.there(g) >> e & 1u) store_one<F>(out + i + e, v[e]);
+                if (there >> e & 1u) store_one<F>(y + i + e, v[e]);
         }
     }
 }
@@ -1200,9 +1245,12 @@ int token_logprobs_bwd(int dtype, const void *logits, int64_t stride, const int6
     const int64_t elems = 16 / bytes, per = static_cast<int64_t>(rn::kGradThreads) * rn::kGradBatch;
     rn::LogprobsGradArgs a = {};
     // (a row that begins inside a granule may touch one more)
-    const bool inside = rn::misaligned(logits, 16) || (T > 1 && stride * bytes % 16 != 0);
-    a.chunks = ((V + elems - 1) / elems + (inside ? 1 : 0) + per - 1) / per;
+    const bool inside = rn::misaligned(dlogits, 16) || (T > 1 && dlogits_stride * bytes % 16 != 0);
+    const int64_t granules = (V + elems - 1) / elems + (inside ? 1 : 0);
+    a.chunks = (granules + per - 1) / per;
     if (a.chunks > INT32_MAX / T) return RN_ERR_SHAPE;
+    // equal shares, in whole warps' rounds
+    a.share = static_cast<int>(((granules + a.chunks - 1) / a.chunks + 31) / 32 * 32);
     a.logits = logits;
     a.stride = stride;
     a.targets = targets;
