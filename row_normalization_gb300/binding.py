@@ -700,7 +700,8 @@ def _result(dev: int, t: torch.Tensor | None, name: str, dtype: torch.dtype, sha
     """(t, its address): the caller's tensor, checked, or a new one."""
     if t is not None:
         return t, _on(dev, t, name, dtype, math.prod(shape))
-    t = _new(shape, dtype, device, stream)
+    t = torch.empty(shape, dtype=dtype, device=device) if stream is None else \
+        _new(shape, dtype, device, stream)
     return t, t.data_ptr()
 
 
@@ -898,10 +899,10 @@ def _rows2d(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int, T: int, wi
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the same CUDA device as the other tensors")
-    shape = t.shape
-    if len(shape) != 2 or shape[0] != T or shape[1] < width or (t.numel() and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != T or shape[1] < width or (stride[1] != 1 and t.numel()):
         raise ValueError(f"{name} must be [{T}, >= {width}] with contiguous rows")
-    return t.data_ptr(), t.stride(0) if T > 1 else shape[1]
+    return t.data_ptr(), stride[0] if T > 1 else shape[1]
 
 
 def _cuda_device(t: torch.Tensor, name: str) -> int:

@@ -796,6 +796,16 @@ struct Stream {
         at = row.x + row.index(share.w0 + threadIdx.x);
         left = share.w1 - share.w0;
     }
+    // Copies a batch that is whole and not its share's last.
+    __device__ __forceinline__ void copy_whole() {
+        const uint8_t *from = static_cast<const uint8_t *>(at);
+        uint4 *to = &sh.stage[head][0][threadIdx.x];
+#pragma unroll
+        for (int b = 0; b < kRowBatch; ++b) copy_async16(to + b * NT, from + b * NT * 16);
+        at = from + kRowBatch * NT * 16;
+        copy_commit();
+        head = head + 1 == kStages ? 0 : head + 1;
+    }
     // Copies a batch, if there is one; the group counts anyway.  (A share without a whole
     // granule is a batch of nothing.)
     __device__ __forceinline__ void copy() {
@@ -857,6 +867,24 @@ __global__ void __launch_bounds__(NT, resident_blocks(NT)) logprobs_fwd_kernel(c
         Runs<F, NT> runs((share.w1 - share.w0 + kRowBatch * NT - 1) / (kRowBatch * NT));
         take_end(sh, row, share, run, c);
         int g = share.w0;
+        const auto taken = [&](const uint4 (&u)[kRowBatch]) {
+            const float most = largest<F>(u);
+            run.take(u, most, c);
+            if (a.k > 0) runs.note(sh, most);
+            g += kRowBatch * NT;
+        };
+        // while this batch and that to be copied are whole, and more of the share follows
+        for (int n = (share.w1 - share.w0 - 1) / (kRowBatch * NT) - (kStages - 1); n > 0; --n) {
+            copy_wait<kStages - 2>();
+            uint4 u[kRowBatch];
+            const uint4 *from = &sh.stage[tail][0][tid];
+#pragma unroll
+            for (int b = 0; b < kRowBatch; ++b) u[b] = ld_shared16(from + b * NT);
+            tail = tail + 1 == kStages ? 0 : tail + 1;
+            stream.copy_whole();
+            stream.left -= kRowBatch * NT;
+            taken(u);
+        }
         do {
             copy_wait<kStages - 2>();
             uint4 u[kRowBatch];
@@ -873,10 +901,7 @@ __global__ void __launch_bounds__(NT, resident_blocks(NT)) logprobs_fwd_kernel(c
             }
             tail = tail + 1 == kStages ? 0 : tail + 1;
             stream.copy();  // (to the stage that the batch before came from)
-            const float most = largest<F>(u);
-            run.take(u, most, c);
-            if (a.k > 0) runs.note(sh, most);
-            g += kRowBatch * NT;
+            taken(u);
         } while (g < share.w1);
         RowPart all = join_threads<F, NT>(sh, row, share, run, runs, a.k, c);
         __syncthreads();
