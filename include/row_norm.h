@@ -661,7 +661,8 @@ int64_t kv_attention_workspace_bytes(int format, int64_t B, int Hq, int Hkv, int
  *   out         the same for the results, rows out_stride apart; qkv itself
  *               with the same stride (in place), or memory that qkv's heads do
  *               not overlap.
- *   cos_sin     [max_pos, r], fp32, or bf16 with table_bf16 = 1; max_pos >= 1.
+ *   cos_sin     [max_pos, r], fp32, or bf16 with table_bf16 = 1; max_pos from 1 to
+ *               2^31 - 1.
  *   positions   int64, axis a's at positions + a * pos_stride (0: one row for
  *               all axes); always checked: a token with a position outside
  *               [0, max_pos) on an axis that turns some pair is not written
@@ -751,6 +752,8 @@ int token_logprobs_fwd(int dtype, const void *logits, int64_t stride, const int6
  *               value for all rows); each may be NULL (zero).
  *   dlogits     [T, V] in dtype, rows dlogits_stride apart; logits itself with
  *               the same stride, or memory that does not overlap it.
+ * s - lse is taken in fp32, so p is off by 2^-24 |lse| of itself (not that of the
+ * given token, which goes by logprobs).
  * An ignored target's dlogprobs counts as 0; with a target >= V the row is NaN
  * and RN_STATUS_BAD_INDEX is raised.  Banned tokens, and rows of nothing else,
  * get 0; a row whose lse is NaN or +infinity gets NaN.  T * ceil(V / 4096) below

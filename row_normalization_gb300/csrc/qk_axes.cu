@@ -672,7 +672,7 @@ static int qk_axes_run(QkAxesArgs &a, const QkAxesCall &k, rn_stream_t stream) {
     if (r != D && r != D / 2 && r != D / 4) return RN_ERR_SHAPE;
     if (k.num_axes < 1 || k.num_axes > kMaxAxes) return RN_ERR_SHAPE;
     const int64_t H = static_cast<int64_t>(a.Hq) + a.Hkv;
-    if (H > INT32_MAX || (H > 0 && a.T > INT32_MAX / H)) return RN_ERR_SHAPE;
+    if (H > INT32_MAX - 64 || (H > 0 && a.T > INT32_MAX / H)) return RN_ERR_SHAPE;
     if (a.max_pos < 1 || a.max_pos > INT32_MAX) return RN_ERR_SHAPE;
     const int64_t width = H * D;
     const auto bad_stride = [&](int64_t stride) { return width > 0 && a.T > 1 && (stride < width || stride % 8 != 0); };

@@ -154,8 +154,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 // ---- a row --------------------------------------------------------------------------------
-// Granules of a row lie on 16-byte boundaries; its first and last may begin before or end
-// behind it, and only the elements that are the row's are read then.
+
 // Elements i .. of a row that are in [0, V), as a granule.  (A call: it would be in many places.)
 template <class F>
 __device__ __noinline__ uint4 end_of_row(const typename F::T *x, int i, int V) {
@@ -171,6 +170,8 @@ __device__ __noinline__ uint4 end_of_row(const typename F::T *x, int i, int V) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Granules of a row lie on 16-byte boundaries; its first and last may begin before or end
+// behind it, and only the elements that are the row's are read then.
 template <class F>
 struct Row {
     const typename F::T *x;
@@ -213,7 +214,7 @@ __device__ __forceinline__ float element(const uint4 &u, int e) {
 // ---- forward ------------------------------------------------------------------------------
 
 constexpr int kStages = 2;        // batches that a thread has under way or is taking
-constexpr int kRowBatch = 4;    // granules that a thread has under way, and takes together
+constexpr int kRowBatch = 4;      // granules of a batch
 constexpr int kMostTop = 32;      // alternatives
 constexpr int resident_blocks(int threads) { return threads == 256 ? 4 : 896 / threads; }  // of an SM, by registers
 constexpr int kMostCluster = 8;   // blocks of a row
@@ -236,9 +237,9 @@ struct LogprobsArgs {
 };
 
 // A thread's running sums: top the largest so far, z = sum 2^t and s = sum 2^t t over its
-// elements, t = c x - r with c = scale log2 e.  The reference r, a power of two that the
-// sums are multiples of, is any number near c top: so its rounding does not count, and it
-// stays until the largest passes it by kRoom; nearly always the first batch's does.
+// elements, t = c x - r with c = scale log2 e and a reference r near c top.  Which number r is
+// does not matter (nor its rounding), and it stays until c top passes it by kRoom: nearly
+// always the first batch's largest does for the whole row.
 constexpr float kRoom = 8.0f;
 // t stops where 2^t is zero, at -200 or so: a product with the -infinity of a banned token
 // would be NaN.  In 16 bits that is done two elements an instruction, on x, with the
@@ -252,9 +253,9 @@ template <class F>
 struct Running {
     float top, r;
     float limit;      // the largest x that the reference serves
-    uint32_t least;   // two of the least x that are told apart
+    uint32_t least;   // 16 bits: two of an x whose 2^t is zero; smaller ones count as it
     Pair z, s;
-    bool shallow;     // there is no such x
+    bool shallow;     // there is no such x, or r is too far from c top
 
     // (The sums of what comes before the first finite x do not matter.)
     __device__ __forceinline__ Running()
@@ -621,9 +622,10 @@ __device__ __forceinline__ RowPart join_threads(S &sh, const Row<F> &row, const 
             sh.s[warp] = s;
         }
     }
-    // The k-th largest of the groups' largest: k elements are no less.  Threads whose
-    // largest is no less hold them all: about as many threads.  (The five bits below are
-    // the lane's, so that no two are equal; 1 where fewer groups than k have an element.)
+    // The least of k groups' largest, those that rank first: k elements are no less.  Threads
+    // whose largest is no less hold them all: about as many threads.  (1 where fewer groups
+    // than k have an element; in the rank the lane stands in the last five bits, so that no
+    // two are equal.)
     uint32_t least = 1u;
     if (k > 0) {
         const uint32_t mine = (group_key & ~31u) | (31u - lane);
@@ -635,14 +637,13 @@ __device__ __forceinline__ RowPart join_threads(S &sh, const Row<F> &row, const 
             const uint4 v = *reinterpret_cast<const uint4 *>(&sh.groups[warp][4 * j]);
             above += (v.x > mine ? 1 : 0) + (v.y > mine ? 1 : 0) + (v.z > mine ? 1 : 0) + (v.w > mine ? 1 : 0);
         }
-        const uint32_t kth =
-            __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, above == k - 1)) - 1) & ~31u;
-        if (kth != 0u) least = kth;
+        least = max(1u, __reduce_min_sync(0xffffffffu, above < k ? group_key : 0xFFFFFFFFu));
         // their runs that hold them: one at least for each such thread
         if (key >= least) {
             const float low = value_of(least);
             const auto look = [&](float top, int r) {
-                if (top < low) return;  // (a NaN is looked at)
+                // (a NaN is looked at; where too many are, their number does not matter)
+                if (top < low || *const_cast<volatile int *>(&sh.items) > kItems) return;
                 const int at = atomicAdd(&sh.items, 1);
                 if (at < kItems) sh.item[at] = tid * (kRuns<F, NT> + 1) + r;
             };

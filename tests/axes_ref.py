@@ -76,8 +76,8 @@ def qk_axes_grad(dout, qkv, wq, wk, table, positions, axes, Hq, Hkv, D, r, eps, 
 
     g is off by 3 U of its products, u = g w by 4, n^ by 14, the mean of u n^ by
     4 + 14 + 20 + 1 of the mean of its sizes; the difference and rstd add 12 + 2: 64 U.
-    A lane's sum of g n^ has 40 terms at most in these tests, a block's 64 lanes' sums, and
-    the blocks' come as 19 and 32: with 18 U a term 200 U of the sum of sizes."""
+    A lane's sum of g n^ has 60 terms at most in these tests, a block's 64 lanes' sums, and
+    the blocks' come as 10 and 5: with 18 U a term 200 U of the sum of sizes."""
     x, w = heads_of(qkv, Hq, Hkv, D), weights_of(wq, wk, Hq, Hkv)
     do = heads_of(dout, Hq, Hkv, D)
     c, s = angles(table, positions, axes, r)

@@ -47,7 +47,7 @@ def bwd(lib, dtype=0, qkv=P, xs=1024, wq=P, wk=P, table=P, bf16=0, max_pos=100, 
     ({"bf16": 2}, RN_ERR_ARG),
     ({"T": -1}, RN_ERR_SHAPE), ({"Hq": -1}, RN_ERR_SHAPE), ({"Hkv": -1}, RN_ERR_SHAPE),
     ({"D": 96}, RN_ERR_SHAPE), ({"r": 96}, RN_ERR_SHAPE), ({"D": 512, "r": 512}, RN_ERR_SHAPE),
-    ({"n": 0}, RN_ERR_SHAPE), ({"n": 5}, RN_ERR_SHAPE), ({"max_pos": 0}, RN_ERR_SHAPE),
+    ({"n": 0}, RN_ERR_SHAPE), ({"n": 5}, RN_ERR_SHAPE), ({"max_pos": 0}, RN_ERR_SHAPE), ({"max_pos": 1 << 31}, RN_ERR_SHAPE),
     ({"T": 1 << 29, "xs": 1024}, RN_ERR_SHAPE), ({"Hq": (1 << 31) - 1, "Hkv": 1}, RN_ERR_SHAPE),
     ({"xs": 760}, RN_ERR_SHAPE), ({"xs": 1028}, RN_ERR_SHAPE), ({"os": 0}, RN_ERR_SHAPE),
     ({"os": 1025}, RN_ERR_SHAPE), ({"ps": 3}, RN_ERR_SHAPE), ({"ps": -64}, RN_ERR_SHAPE),

@@ -266,6 +266,60 @@ def test_a_nan_reaches_its_head_and_the_sums_alone():
     assert bad[4, 1].all() and int(bad.sum()) == 128 and dwq.isnan().all() and dwk.isfinite().all()
 
 
+def test_the_gradient_in_place_of_qkv():
+    st = inputs(333, 8, 2, 128, 128, pad=8)
+    sizes = (8, 2, 128, 128, 1e-6)
+    want, dwq, dwk = backward(st, sizes, dx=torch.empty(333, 1280, dtype=BF, device="cuda"))
+    values = st["qkv"][:, 1280:].clone()
+    got = backward(st, sizes, dx=st["qkv"])
+    assert got[0] is st["qkv"] and torch.equal(st["qkv"][:, :1280], want) and torch.equal(st["qkv"][:, 1280:], values)
+    assert torch.equal(got[1], dwq) and torch.equal(got[2], dwk)
+
+
+@pytest.mark.parametrize("kind", ["eights", "interleaved"])
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(9000, 16, 2, 128), (20000, 8, 1, 64), (5000, 10, 5, 256)])
+def test_units_that_follow_one_another(T, Hq, Hkv, D, kind):
+    """More units than warps: a warp's stream of heads goes from one into the next."""
+    st = inputs(T, Hq, Hkv, D, D // 2, kind)
+    st["positions"][1, T // 2] = -1
+    sizes = (Hq, Hkv, D, D // 2, 1e-6)
+    good = torch.arange(T, device="cuda") != T // 2
+    st2 = {k: (v[good] if k in ("qkv", "dout") else v[:, good] if k == "positions" else v) for k, v in st.items()}
+    n = (Hq + Hkv) * D
+    want, slack = want_forward(st2, sizes, RN_ROPE_NEOX)
+    out = torch.full((T, n), 5.0, dtype=BF, device="cuda")
+    forward(st, sizes, out=out)
+    assert (out[T // 2] == 5).all()
+    assert_near(out[good].view(want.shape), want, slack, "results")
+    del want, slack
+    grads, slacks = want_backward(st2, sizes, RN_ROPE_NEOX)
+    out.fill_(5.0)
+    _, dwq, dwk = backward(st, sizes, dx=out)
+    assert (out[T // 2] == 5).all()
+    assert_near(out[good].view(grads[0].shape), grads[0], slacks[0], "dx")
+    assert_near(dwq, grads[1], slacks[1], "dwq")
+    assert_near(dwk, grads[2], slacks[2], "dwk")
+    assert binding.device_status() == RN_STATUS_BAD_POSITION
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own workspace."""
+    sizes = (8, 2, 128, 128, 1e-6)
+    sts = [inputs(3000, 8, 2, 128, 128, seed=s) for s in (1, 2)]
+    outs = [torch.empty(3000, 1280, dtype=BF, device="cuda") for _ in sts]
+    want = [[x.clone() for x in backward(st, sizes, dx=o)] for st, o in zip(sts, outs)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    spaces = [binding.qk_norm_rope_axes_workspace(128) for _ in sts]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = [backward(st, sizes, dx=o, workspace=w, stream=s)
+               for st, o, w, s in zip(sts, outs, spaces, streams)]
+        torch.cuda.synchronize()
+        for w, g in zip(want, got):
+            for p, q in zip(w, g):
+                assert torch.equal(p, q)
+
+
 @pytest.mark.parametrize("which", ["forward", "backward"])
 def test_captured_and_replayed(which):
     """Graphs of a call and its plain run give the same bits, on new inputs as well."""

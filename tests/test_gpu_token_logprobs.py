@@ -109,38 +109,52 @@ def test_few_values_and_signed_zeros(T, dtype):
     assert torch.equal(got.top_ids, first)
 
 
-@pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("T", [1, 1300])
-def test_large_logits_that_one_thread_meets(T, dtype):
-    """More candidates than the list holds, in the columns that a single thread of the
-    block reads (every 512th group of 16 bytes), in all orders."""
+# rows, and the threads of a block that such rows of about 100000 logits are given
+LAYOUTS = [(1, 256), (20, 256), (1000, 128), (2048, 64)]
+
+
+def concentrated(T, threads, dtype):
+    """[T, V] and its view by the groups of 16 bytes that a block's threads take in turn."""
     per = 128 // torch.finfo(dtype).bits
-    V = per * 512 * 200 if T == 1 else per * 512 * 170
-    x = torch.zeros(T, V, dtype=dtype, device="cuda")
-    g = torch.Generator(device="cuda").manual_seed(4)
-    big = x.view(T, -1, 512, per)
-    big[:, :, 3] = (torch.rand(T, big.shape[1], per, generator=g, device="cuda") * 8 + 1).to(dtype)
-    targets = torch.randint(0, V, (T,), generator=g, device="cuda")
-    check(x[:2], targets[:2], 32, what="one thread")
-    if T > 2:
-        check(x, targets, 32, what="one thread", grad=False)
+    x = torch.zeros(T, per * threads * (40960 // threads // per), dtype=dtype, device="cuda")
+    return x, x.view(T, -1, threads, per), torch.Generator(device="cuda").manual_seed(4)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("T", [1, 1300])
-def test_many_equal_and_a_few_threads_with_more(T, dtype):
+@pytest.mark.parametrize("T,threads", LAYOUTS)
+def test_large_logits_that_one_thread_meets(T, threads, dtype):
+    """More candidates than the list holds, in the columns that a single thread of the
+    block reads, in all orders."""
+    x, view, g = concentrated(T, threads, dtype)
+    view[:, :, 3] = (torch.rand(T, view.shape[1], view.shape[3], generator=g, device="cuda") * 8 + 1).to(dtype)
+    targets = torch.randint(0, x.shape[1], (T,), generator=g, device="cuda")
+    check(x, targets, 32, what="one thread", grad=T < 100)
+    check(x, targets, 1, what="one thread, one alternative", grad=False)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,threads", LAYOUTS)
+def test_many_equal_and_a_few_threads_with_more(T, threads, dtype):
     """Fewer threads than k above a value that many threads share, some with many columns
     above it, and one with more than the list holds."""
-    per = 128 // torch.finfo(dtype).bits
-    V = per * 512 * 160
-    x = torch.full((T, V), -1.0, dtype=dtype, device="cuda")
-    view = x.view(T, -1, 512, per)
-    view[:, ::9, 100, 2] = 2.0
+    x, view, _ = concentrated(T, threads, dtype)
+    x.fill_(-1.0)
+    view[:, ::9, 50, 2] = 2.0
     view[:, 5, 7, 0] = 3.0
     targets = torch.full((T,), 5, device="cuda")
     check(x, targets, 32, what="many equal", grad=False)
     view[:, :, 9] = 0.5
     check(x, targets, 32, what="many equal, a full list", grad=False)
+    x[:, ::2] = -INF
+    check(x, targets.fill_(1), 32, what="many equal, half banned", grad=False)
+
+
+@pytest.mark.parametrize("k", [1, 31, 32])
+@pytest.mark.parametrize("T,V", [(1, 131072), (1000, 32000), (2048, 32000), (3000, 5000)])
+def test_more_runs_reach_than_are_listed(T, V, k):
+    """Values that fall along the row, so that every thread's first are near the largest."""
+    x = (-torch.arange(V, device="cuda") / 64).bfloat16().repeat(T, 1)
+    check(x, torch.full((T,), V // 2, device="cuda"), k, what="falling slowly", grad=False)
 
 
 @pytest.mark.parametrize("rising", [True, False])
@@ -320,6 +334,35 @@ def test_rows_beyond_32_bits():
     d = binding.token_logprobs_bwd(x, targets, got, dlogprobs=torch.ones(1, device="cuda"), dlogits=x)
     assert abs(float(d[0, V - 1]) - (1 - math.exp(-1.0) / z)) <= 2.0 ** -6
     assert float(d[0, 77]) < 0
+
+
+def test_two_calls_at_once():
+    """Calls on two streams share nothing."""
+    a, ta = logits(1500, 30000, BF, 20)
+    b, tb = logits(900, 50001, HALF, 21)
+    want = [binding.token_logprobs_fwd(a, ta, top_k=5), binding.token_logprobs_fwd(b, tb, top_k=20)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = [binding.token_logprobs_fwd(x, t, top_k=k, stream=s)
+               for (x, t, k), s in zip(((a, ta, 5), (b, tb, 20)), streams)]
+        torch.cuda.synchronize()
+        for w, g in zip(want, got):
+            for p, q in zip(w, g):
+                assert torch.equal(p, q)
+
+
+def test_scales_whose_powers_leave_the_format():
+    """Temperatures so high that no fp16 or bf16 logit is out of reach of the largest, and so
+    low that all but the largest are."""
+    for dtype in DTYPES:
+        x, targets = logits(5, 9000, dtype, 22)
+        for scale in (1e-30, 1e-6, 1e-3, 0.003, 300.0, 1e20):
+            check(x, targets, 7, scale, f"scale {scale}", grad=scale < 1e3)
+        x[:, ::3] = -INF
+        targets = targets // 3 * 3 + 1
+        for scale in (1e-30, 1e-3, 300.0):
+            check(x, targets, 7, scale, f"banned, scale {scale}")
 
 
 def test_same_bits_again_and_beside_other_work():
