@@ -213,16 +213,19 @@ __device__ __forceinline__ float element(const uint4 &u, int e) {
 
 // ---- forward ------------------------------------------------------------------------------
 
-constexpr int kStages = 2;        // batches that a thread has under way or is taking
+// Batches that a thread has under way or is taking: as shared memory allows.
+template <int NT>
+constexpr int kStages = NT == 128 ? 3 : 2;
 constexpr int kRowBatch = 4;      // granules of a batch
 constexpr int kMostTop = 32;      // alternatives
-constexpr int resident_blocks(int threads) { return threads == 256 ? 4 : 896 / threads; }  // of an SM, by registers
+// Blocks of an SM, by registers: 72 a thread in blocks of 64 and 128, 64 in the others.
+constexpr int resident_blocks(int threads) { return (threads == 64 || threads == 128 ? 896 : 1024) / threads; }
 constexpr int kMostCluster = 8;   // blocks of a row
 constexpr int kList = 190;        // entries of the list
 constexpr int kItems = 128;       // runs of batches that are looked at again
 // The most runs of batches whose largest values a thread notes: as shared memory allows.
 template <class F, int NT>
-constexpr int kRuns = (NT == 64 ? 32 : 16) * F::kElems / 8;
+constexpr int kRuns = (NT == 64 ? 32 : NT == 128 ? 8 : 16) * F::kElems / 8;
 
 struct LogprobsArgs {
     const void *logits;
@@ -381,7 +384,7 @@ struct NoCluster {};
 
 template <class F, int NT, bool CLUSTER>
 struct RowShared {
-    uint4 stage[kStages][kRowBatch][NT];        // batches under way, each thread's own
+    uint4 stage[kStages<NT>][kRowBatch][NT];    // batches under way, each thread's own
     alignas(16) uint64_t list[kList + 2];
     alignas(16) uint32_t groups[NT / 32][32];
     uint64_t best[NT / 32];
@@ -394,7 +397,7 @@ struct RowShared {
     int counts[NT / 32];
     float ends[2];                              // the largest of the row's ends
     int item[kItems];                           // thread and run
-    typename F::T slots[kRuns<F, NT>][NT];            // by run of batches and thread: its largest
+    typename F::T slots[kRuns<F, NT>][NT];      // by run of batches and thread: its largest
     std::conditional_t<CLUSTER, ClusterShared, NoCluster> cluster;
 };
 
@@ -805,7 +808,7 @@ struct Stream {
         for (int b = 0; b < kRowBatch; ++b) copy_async16(to + b * NT, from + b * NT * 16);
         at = from + kRowBatch * NT * 16;
         copy_commit();
-        head = head + 1 == kStages ? 0 : head + 1;
+        head = head + 1 == kStages<NT> ? 0 : head + 1;
     }
     // Copies a batch, if there is one; the group counts anyway.  (A share without a whole
     // granule is a batch of nothing.)
@@ -829,7 +832,7 @@ struct Stream {
             }
         }
         copy_commit();
-        head = head + 1 == kStages ? 0 : head + 1;
+        head = head + 1 == kStages<NT> ? 0 : head + 1;
     }
 };
 
@@ -847,7 +850,7 @@ __global__ void __launch_bounds__(NT, resident_blocks(NT)) logprobs_fwd_kernel(c
     const int64_t step = CLUSTER ? gridDim.x / a.blocks : gridDim.x;
     Stream<F, NT, S> stream(a, sh, rank, first, step);
 #pragma unroll 1
-    for (int i = 0; i < kStages - 1; ++i) stream.copy();
+    for (int i = 0; i < kStages<NT> - 1; ++i) stream.copy();
     if (tid == 0) sh.listed = sh.items = 0;
     if (tid < kMostTop) sh.top[tid] = 0u;
     const float c = a.scale_log2;
@@ -875,19 +878,19 @@ __global__ void __launch_bounds__(NT, resident_blocks(NT)) logprobs_fwd_kernel(c
             g += kRowBatch * NT;
         };
         // while this batch and that to be copied are whole, and more of the share follows
-        for (int n = (share.w1 - share.w0 - 1) / (kRowBatch * NT) - (kStages - 1); n > 0; --n) {
-            copy_wait<kStages - 2>();
+        for (int n = (share.w1 - share.w0 - 1) / (kRowBatch * NT) - (kStages<NT> - 1); n > 0; --n) {
+            copy_wait<kStages<NT> - 2>();
             uint4 u[kRowBatch];
             const uint4 *from = &sh.stage[tail][0][tid];
 #pragma unroll
             for (int b = 0; b < kRowBatch; ++b) u[b] = ld_shared16(from + b * NT);
-            tail = tail + 1 == kStages ? 0 : tail + 1;
+            tail = tail + 1 == kStages<NT> ? 0 : tail + 1;
             stream.copy_whole();
             stream.left -= kRowBatch * NT;
             taken(u);
         }
         do {
-            copy_wait<kStages - 2>();
+            copy_wait<kStages<NT> - 2>();
             uint4 u[kRowBatch];
             const uint4 *from = &sh.stage[tail][0][tid];
             if (g + kRowBatch * NT <= share.w1) {
@@ -900,7 +903,7 @@ __global__ void __launch_bounds__(NT, resident_blocks(NT)) logprobs_fwd_kernel(c
                     if (g + b * NT + tid < share.w1) u[b] = ld_shared16(from + b * NT);
                 }
             }
-            tail = tail + 1 == kStages ? 0 : tail + 1;
+            tail = tail + 1 == kStages<NT> ? 0 : tail + 1;
             stream.copy();  // (to the stage that the batch before came from)
             taken(u);
         } while (g < share.w1);
@@ -1105,24 +1108,30 @@ struct RowShape {
 };
 // The layout that an estimate prefers.  An SM takes its blocks' shares of rows in rounds of
 // as many as it holds; a round takes what HBM needs for the SM's shares in it (44.6 KB a us),
-// longer where there are less than 26 warps to take them in, and 3 us in which the last rows
-// are joined, 4.5 where clusters join.  So many rows are best in rounds that are nearly full,
-// few rows on many blocks each.  (Alternatives 8, bf16, 131072 columns, us as 256 threads x 1
-// block / 128 x 1 / 64 x 1 / 128 x 2 / 256 x 8: 1 row 12.3 / - / - / 12.4 / 6.8; 500 rows 28.7 /
-// 37.9 / 51 / 28.5 / -; 1000 57 / 47.9 / 66 / 55; 2048 109 / 94 / 89 / 107; 3000 140 / 136 /
-// 159 / 156.)
+// longer where there are less than 26 warps to take them in, and some us in which the last
+// rows are joined: more in larger blocks and in clusters.  So many rows are best in rounds
+// that are nearly full, few rows on many blocks each.  Over 100 pairs of T and V in three
+// formats it chose layouts that took 3% longer than the best of them on average, 29% at most.
+// (8 alternatives, bf16, 131072 columns, us as 256 threads x 1 block / 128 x 1 / 96 x 1 / 64 x 1 /
+// 128 x 2 / 256 x 8: 1 row 12 / - / - / - / 10.1 / 6.8; 500 rows 27.9 / 33.6 / 36.7 / - / 37.6; 1000 55.5 /
+// 46.6 / 59.1 / - / 59.5; 1500 82.1 / 82.4 / 67.1 / 74.5 / 81.2; 2048 108 / 91.9 / - / 90.4 / 109; 3000 138 /
+// 134 / 130 / 159 / 149.)
 static RowShape row_shape(int64_t T, int64_t V, int dtype, int sm_count) {
     const double kb = static_cast<double>(V) * elem_bytes(dtype) / 1024;
     RowShape best = {256, 1};
     double least = 0;
-    for (int threads = 256; threads >= 64; threads /= 2)
+    for (int threads : {512, 320, 256, 192, 128, 96, 64})
         for (int blocks = 1; blocks <= kMostCluster; blocks *= 2) {
-            if (blocks > 1 && kb * 64 < 2.0 * threads * blocks) break;  // two granules a thread at least
+            // clusters of blocks of 64, 128 or 256; two granules a thread at least
+            const bool paired = threads == 64 || threads == 128 || threads == 256;
+            if (blocks > 1 && (!paired || kb * 64 < 2.0 * threads * blocks)) break;
+            // (their shared memory counts, too)
+            const int resident = blocks == 1 ? resident_blocks(threads) : threads == 64 ? 11 : threads == 128 ? 6 : 4;
             const double each = static_cast<double>(T) * blocks / sm_count;
-            const double rounds = ceil(each / resident_blocks(threads)), at_once = ceil(each / rounds);
+            const double rounds = ceil(each / resident), at_once = ceil(each / rounds);
             const double warps = at_once * threads / 32;
-            const double us = rounds * (at_once * kb / blocks / 44.6 * (warps < 26 ? 26 / warps : 1.0) +
-                                        (blocks > 1 ? 4.5 : 3.0));
+            const double us = rounds * (at_once * kb / blocks / 44.6 * (warps < 26 ? 26 / warps : 1.0) + 2.5 +
+                                        threads / 256.0 + (blocks > 1 ? 3.0 : 0.0));
             if (least == 0 || us < least) {
                 least = us;
                 best = {threads, blocks};
@@ -1174,11 +1183,15 @@ template <class F>
 static int run_fwd(LogprobsArgs &a, int dtype, const DeviceInfo &dev, cudaStream_t st) {
     const RowShape s = row_shape(a.T, a.V, dtype, dev.sm_count);
     a.blocks = s.blocks;
-    if (s.threads == 64)
-        return a.blocks > 1 ? launch_fwd<F, 64, true>(a, dev, st) : launch_fwd<F, 64, false>(a, dev, st);
-    if (s.threads == 128)
-        return a.blocks > 1 ? launch_fwd<F, 128, true>(a, dev, st) : launch_fwd<F, 128, false>(a, dev, st);
-    return a.blocks > 1 ? launch_fwd<F, 256, true>(a, dev, st) : launch_fwd<F, 256, false>(a, dev, st);
+    switch (s.threads) {
+        case 512: return launch_fwd<F, 512, false>(a, dev, st);
+        case 320: return launch_fwd<F, 320, false>(a, dev, st);
+        case 192: return launch_fwd<F, 192, false>(a, dev, st);
+        case 96: return launch_fwd<F, 96, false>(a, dev, st);
+        case 64: return a.blocks > 1 ? launch_fwd<F, 64, true>(a, dev, st) : launch_fwd<F, 64, false>(a, dev, st);
+        case 128: return a.blocks > 1 ? launch_fwd<F, 128, true>(a, dev, st) : launch_fwd<F, 128, false>(a, dev, st);
+        default: return a.blocks > 1 ? launch_fwd<F, 256, true>(a, dev, st) : launch_fwd<F, 256, false>(a, dev, st);
+    }
 }
 
 template <class F>

@@ -72,11 +72,14 @@ def test_sizes_and_alignments(V, dtype, T, offset, pad):
     check(x, targets, min(V, 20), what=f"V {V}")
 
 
-@pytest.mark.parametrize("T,V", [(17, 131072), (64, 32768), (300, 9001), (700, 4096), (1300, 20001), (2000, 1000)])
+@pytest.mark.parametrize("T,V", [(17, 131072), (64, 32768), (128, 131072), (200, 40003), (200, 131072), (300, 9001),
+                                 (333, 50000), (500, 30011), (700, 4096), (1000, 7777), (1300, 20001), (2000, 1000),
+                                 (3000, 2000), (5000, 515)])
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_row_counts(T, V, dtype):
-    """Rows shared by clusters of every size, and rows of one block."""
-    x, targets = logits(T, V, dtype, 1)
+    """Rows shared by clusters of every size, rows of blocks of every size, and blocks that
+    take several rows one after another."""
+    x, targets = logits(T, V, dtype, 1, pad=V % 8)
     check(x, targets, 8, what=f"T {T} V {V}")
 
 
@@ -109,14 +112,15 @@ def test_few_values_and_signed_zeros(T, dtype):
     assert torch.equal(got.top_ids, first)
 
 
-# rows, and the threads of a block that such rows of about 100000 logits are given
-LAYOUTS = [(1, 256), (20, 256), (1000, 128), (2048, 64)]
+# rows, and the threads of a block that so many rows of concentrated()'s length are given
+LAYOUTS = [(1, 256), (20, 256), (150, 512), (333, 320), (700, 192), (1000, 128), (1500, 96), (2048, 64)]
 
 
 def concentrated(T, threads, dtype):
-    """[T, V] and its view by the groups of 16 bytes that a block's threads take in turn."""
+    """[T, V] and its view by the groups of 16 bytes that a block's threads take in turn, 48
+    each (so that one thread may have more candidates than are listed)."""
     per = 128 // torch.finfo(dtype).bits
-    x = torch.zeros(T, per * threads * (40960 // threads // per), dtype=dtype, device="cuda")
+    x = torch.zeros(T, per * threads * 48, dtype=dtype, device="cuda")
     return x, x.view(T, -1, threads, per), torch.Generator(device="cuda").manual_seed(4)
 
 
