@@ -20,13 +20,13 @@
 // only: one weight in registers, and in the gradient one set of 16 sums of dw a lane.
 // Every lane copies its own elements ahead into its own places in shared memory.  That beats
 // loads into registers (16384 tokens of 40 heads of 128, us): forward 65.3 -> 55.2, of which the
-// bytes need 50.8; gradient 99.5 -> 81.1, of 75.5.  Three stages are enough for the forward pass:
+// bytes need 50.8; gradient 99.5 -> 80.9, of 75.5.  Three stages are enough for the forward pass:
 // 24 warps an SM with two heads of 1 KB under way each; eight stages took 56.9 there and 18.9
 // against 16.5 at 4096 tokens, as a warp begins later.
 //
 // What is left: a quarter of the gradient at 4096 tokens (27.9 us, floor 18.9) is its second
 // launch, beginning and end; axes that change within four pairs cost 4 to 20% (heads of 256 that
-// turn a half of 128 by three interleaved axes: 57.9 us forward, 96.3 gradient, floors as above).
+// turn a half of 128 by three interleaved axes: 57.9 us forward, 96.9 gradient, floors as above).
 #include "rn_common.cuh"
 #include "rn_host.h"
 

@@ -15,10 +15,10 @@
 // is one pass without any sum.
 //
 // What bounds the forward pass: HBM, with the issue slots not far behind.  A logit of 16 bits
-// takes 6.8 instructions (one exponential, half each of a maximum, a clamp and three fused
-// operations, one to widen it), which at HBM's 11.2 logits a clock and SM fill 60% of them; the
-// special function unit is at 45%.  2048 rows of 131072 in bf16: 86.8 us without
-// alternatives, 6.19 TB/s, 93.6 with 8, 102 with 20 (joining a row takes a block about 2 us).
+// takes 6.3 instructions (one exponential, half each of a maximum, a clamp and three fused
+// operations, one to widen it); with 8 alternatives the issue slots are 54% full at 1024 rows of
+// 131072, the special function unit 30%.  2048 rows of 131072 in bf16: 85.3 us without
+// alternatives, 6.30 TB/s, 92.3 with 8, 101 with 20 (joining a row takes a block about 2 us).
 #include <cooperative_groups.h>
 #include <float.h>
 
@@ -996,7 +996,7 @@ __device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, uint32_
 // within 16 bytes.  HBM bounds it: 4096 rows of 131072 in bf16, 2.15 GB, take 302 us (7.1 TB/s,
 // 1.05 of the copy's rate); 309 with loads and stores that keep their lines, 387 with two
 // granules a thread, 351 with scalar fp32 and shares that leave each row's last block a rest.
-// 2048 rows of 50021: 64 us (floor 60); 79 where dlogits lies otherwise than logits (235 with
+// 2048 rows of 50021: 62 us (floor 60); 79 where dlogits lies otherwise than logits (235 with
 // stores of one element).
 template <class F>
 __global__ void __launch_bounds__(kGradThreads) logprobs_bwd_kernel(const __grid_constant__ LogprobsGradArgs a) {
