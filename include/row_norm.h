@@ -698,7 +698,8 @@ int qk_norm_rope_axes_fwd(int dtype, const void *qkv, int64_t qkv_stride, const 
  * A token that the forward call did not write gets no dx and adds nothing to dw.
  * The sums are fp32 in an order that the sizes alone give: the same call gives
  * the same bits.  Errors as the forward call; a workspace that is too small,
- * or dwq == dwk, is RN_ERR_ARG. */
+ * or dwq == dwk, is RN_ERR_ARG, and so is, in both, an output that begins where
+ * an input does with other strides. */
 int qk_norm_rope_axes_bwd(int dtype, const void *dout, int64_t dout_stride, const void *qkv,
                           int64_t qkv_stride, const void *wq, const void *wk,
                           const void *cos_sin, int table_bf16, int64_t max_pos,
@@ -758,7 +759,7 @@ int token_logprobs_fwd(int dtype, const void *logits, int64_t stride, const int6
  * and RN_STATUS_BAD_INDEX is raised.  Banned tokens, and rows of nothing else,
  * get 0; a row whose lse is NaN or +infinity gets NaN.  T * ceil(V / 4096) below
  * 2^31 (with V + 8 for V where rows of dlogits begin off 16-byte boundaries).
- * Errors as the forward call. */
+ * Errors as the forward call; dlogits == logits with another stride is RN_ERR_ARG. */
 int token_logprobs_bwd(int dtype, const void *logits, int64_t stride, const int64_t *targets,
                        const float *logprobs, const float *lse, const float *entropy,
                        const float *dlogprobs, int64_t dlogprobs_stride, const float *dentropy,

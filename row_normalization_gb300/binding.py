@@ -900,7 +900,7 @@ def _rows2d(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int, T: int, wi
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the same CUDA device as the other tensors")
     shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or shape[0] != T or shape[1] < width or (stride[1] != 1 and t.numel()):
+    if len(shape) != 2 or shape[0] != T or shape[1] < width or (stride[1] != 1 and shape[1] > 1 and T):
         raise ValueError(f"{name} must be [{T}, >= {width}] with contiguous rows")
     return t.data_ptr(), stride[0] if T > 1 else shape[1]
 

@@ -699,6 +699,10 @@ static int qk_axes_run(QkAxesArgs &a, const QkAxesCall &k, rn_stream_t stream) {
         ((reinterpret_cast<uintptr_t>(k.dwq) | reinterpret_cast<uintptr_t>(k.dwk)) & 3u))
         return RN_ERR_ALIGN;
     if (k.backward && k.dwq && k.dwq == k.dwk) return RN_ERR_ARG;
+    // in place is row by row
+    if (a.T > 1 && !empty &&
+        ((a.y == a.x && a.y_stride != a.x_stride) || (k.backward && a.y == a.dout && a.y_stride != a.dout_stride)))
+        return RN_ERR_ARG;
     const DeviceInfo *dev = current_device_info();
     if (!dev) return RN_ERR_DEVICE;
     const auto st = reinterpret_cast<cudaStream_t>(stream);

@@ -1281,6 +1281,7 @@ int token_logprobs_bwd(int dtype, const void *logits, int64_t stride, const int6
         rn::misaligned(logprobs, 4) || rn::misaligned(lse, 4) || rn::misaligned(entropy, 4) ||
         rn::misaligned(dlogprobs, 4) || rn::misaligned(dentropy, 4) || rn::misaligned(dlse, 4))
         return RN_ERR_ALIGN;
+    if (T > 1 && dlogits == logits && dlogits_stride != stride) return RN_ERR_ARG;  // in place is row by row
     const int64_t elems = 16 / bytes, per = static_cast<int64_t>(rn::kGradThreads) * rn::kGradBatch;
     rn::LogprobsGradArgs a = {};
     // (a row that begins inside a granule may touch one more)

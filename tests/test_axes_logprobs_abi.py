@@ -57,6 +57,7 @@ def bwd(lib, dtype=0, qkv=P, xs=1024, wq=P, wk=P, table=P, bf16=0, max_pos=100, 
     ({"pos": None}, RN_ERR_NULL),
     ({"qkv": P + 8}, RN_ERR_ALIGN), ({"out": P + 2}, RN_ERR_ALIGN), ({"wk": P + 8}, RN_ERR_ALIGN),
     ({"table": P + 4}, RN_ERR_ALIGN), ({"pos": P + 4}, RN_ERR_ALIGN),
+    ({"os": 1032}, RN_ERR_ARG),  # in place with other strides
 ])
 def test_axes_arguments(lib, call, kw, expect):
     assert call(lib, **kw) == expect
@@ -71,7 +72,7 @@ def test_axes_calls_without_work(lib):
 @pytest.mark.parametrize("kw,expect", [
     ({"gs": 760}, RN_ERR_SHAPE), ({"dout": None}, RN_ERR_NULL), ({"ws": None}, RN_ERR_NULL),
     ({"dout": P + 8}, RN_ERR_ALIGN), ({"ws": P + 8}, RN_ERR_ALIGN), ({"dwq": P + 2}, RN_ERR_ALIGN),
-    ({"dwk": P}, RN_ERR_ARG), ({"acc": 2}, RN_ERR_ARG),
+    ({"dwk": P}, RN_ERR_ARG), ({"acc": 2}, RN_ERR_ARG), ({"gs": 1032}, RN_ERR_ARG),
 ])
 def test_axes_gradient_arguments(lib, kw, expect):
     assert bwd(lib, **kw) == expect
@@ -120,6 +121,7 @@ def test_logprobs_top_arguments(lib, kw, expect):
     ({"dp": P + 2}, RN_ERR_ALIGN), ({"dh": P + 2}, RN_ERR_ALIGN), ({"dl": P + 2}, RN_ERR_ALIGN),
     ({"dps": -1}, RN_ERR_SHAPE), ({"dhs": -1}, RN_ERR_SHAPE), ({"dls": -1}, RN_ERR_SHAPE),
     ({"T": 1 << 20, "V": 1 << 27, "stride": 1 << 27, "os": 1 << 27}, RN_ERR_SHAPE),
+    ({"os": 1008}, RN_ERR_ARG),  # in place with another stride
 ])
 def test_logprobs_gradient_arguments(lib, kw, expect):
     assert rows_grad(lib, **kw) == expect

@@ -425,6 +425,13 @@ def test_on_another_stream_with_results_made_for_it():
             assert torch.equal(a, b)
 
 
+def test_one_column_of_any_stride():
+    x = torch.randn(1, 5, device="cuda", dtype=F32).t()  # [5, 1]
+    assert x.stride() == (1, 5)
+    got = check(x, torch.zeros(5, dtype=torch.int64, device="cuda"), k=1, what="one column")
+    assert (got.logprobs == 0).all() and (got.entropy == 0).all() and (got.top_ids == 0).all()
+
+
 def test_no_rows():
     x = torch.empty(0, 100, dtype=BF, device="cuda")
     t = torch.empty(0, dtype=torch.int64, device="cuda")
