@@ -225,7 +225,7 @@ constexpr int kList = 190;        // entries of the list
 constexpr int kItems = 128;       // runs of batches that are looked at again
 // The most runs of batches whose largest values a thread notes: as shared memory allows.
 template <class F, int NT>
-constexpr int kRuns = (NT == 64 ? 32 : NT == 128 ? 8 : 16) * F::kElems / 8;
+constexpr int kRuns = (NT == 64 ? 32 : NT == 128 ? 8 : 16) * F::kElems / 8;  // up to 32: bits of a word
 
 struct LogprobsArgs {
     const void *logits;
@@ -641,18 +641,22 @@ __device__ __forceinline__ RowPart join_threads(S &sh, const Row<F> &row, const 
             above += (v.x > mine ? 1 : 0) + (v.y > mine ? 1 : 0) + (v.z > mine ? 1 : 0) + (v.w > mine ? 1 : 0);
         }
         least = max(1u, __reduce_min_sync(0xffffffffu, above < k ? group_key : 0xFFFFFFFFu));
-        // their runs that hold them: one at least for each such thread
+        // Their runs that hold them: one at least for each such thread (a NaN is looked at).
+        // (Four at a time: one after another it took 7000 clocks while others read, of 32 runs.)
         if (key >= least) {
             const float low = value_of(least);
-            const auto look = [&](float top, int r) {
-                // (a NaN is looked at; where too many are, their number does not matter)
-                if (top < low || *const_cast<volatile int *>(&sh.items) > kItems) return;
-                const int at = atomicAdd(&sh.items, 1);
-                if (at < kItems) sh.item[at] = tid * (kRuns<F, NT> + 1) + r;
-            };
+            uint32_t hit = 0u;
 #pragma unroll 1
-            for (int r = 0; r < runs.count(); ++r) look(F::one(sh.slots[r][tid]), r);
-            if (share.end_of(tid) >= 0) look(sh.ends[tid], kRuns<F, NT>);
+            for (int r0 = 0; r0 < runs.count(); r0 += 4)  // (there is place for a multiple of 4)
+#pragma unroll
+                for (int r = r0; r < r0 + 4; ++r) hit |= F::one(sh.slots[r][tid]) < low ? 0u : 1u << r;
+            hit &= (1u << (runs.count() - 1) << 1) - 1u;
+            const bool end = share.end_of(tid) >= 0 && !(sh.ends[tid] < low);
+            int at = atomicAdd(&sh.items, __popc(hit) + (end ? 1 : 0));
+#pragma unroll 1
+            for (; hit; hit &= hit - 1, ++at)
+                if (at < kItems) sh.item[at] = (__ffs(hit) - 1) << 10 | tid;
+            if (end && at < kItems) sh.item[at] = kRuns<F, NT> << 10 | tid;
         }
     }
     __syncthreads();
@@ -661,13 +665,18 @@ __device__ __forceinline__ RowPart join_threads(S &sh, const Row<F> &row, const 
         if (items <= kItems) {
             constexpr int kLog2Batch = kRowBatch == 4 ? 2 : (kRowBatch == 2 ? 1 : 0);
             const int log2_per = kLog2Batch + runs.shift;  // granules of a run
-#pragma unroll 1
-            for (int i = tid; i < items << log2_per; i += NT) {
-                const int what = sh.item[i >> log2_per], who = what / (kRuns<F, NT> + 1), r = what % (kRuns<F, NT> + 1);
+            const int n = items << log2_per;
+            const auto granule = [&](int i) {  // or -1
+                const int what = sh.item[i >> log2_per], who = what & 1023, r = what >> 10;
                 const int j = i & ((1 << log2_per) - 1);
-                int g = share.w0 + who + ((r << log2_per) + j) * NT;
-                if (r == kRuns<F, NT>) g = j == 0 ? share.end_of(who) : share.w1;
-                if (g < share.w1 || (r == kRuns<F, NT> && j == 0)) push<F>(sh, row, g, least, false);
+                if (r == kRuns<F, NT>) return j == 0 ? share.end_of(who) : -1;
+                const int g = share.w0 + who + ((r << log2_per) + j) * NT;
+                return g < share.w1 ? g : -1;
+            };
+#pragma unroll 1
+            for (int i = tid; i < n; i += NT) {
+                const int g = granule(i);
+                if (g >= 0) push<F>(sh, row, g, least, false);
             }
             __syncthreads();
         }
