@@ -1116,36 +1116,38 @@ struct RowShape {
     int threads, blocks;
 };
 // The layout that an estimate prefers.  An SM takes its blocks' shares of rows in rounds of
-// as many as it holds; a round takes what HBM needs for the SM's shares in it (44.6 KB a us),
-// longer where there are less than 26 warps to take them in, and some us in which the last
-// rows are joined: more in larger blocks and in clusters.  So many rows are best in rounds
-// that are nearly full, few rows on many blocks each.  Over 100 pairs of T and V in three
-// formats it chose layouts that took 3% longer than the best of them on average, 29% at most.
-// (8 alternatives, bf16, 131072 columns, us as 256 threads x 1 block / 128 x 1 / 96 x 1 / 64 x 1 /
-// 128 x 2 / 256 x 8: 1 row 12 / - / - / - / 10.1 / 6.8; 500 rows 27.9 / 33.6 / 36.7 / - / 37.6; 1000 55.5 /
-// 46.6 / 59.1 / - / 59.5; 1500 82.1 / 82.4 / 67.1 / 74.5 / 81.2; 2048 108 / 91.9 / - / 90.4 / 109; 3000 138 /
-// 134 / 130 / 159 / 149.)
+// as many as it holds.  A round takes what HBM needs for the SM's shares in it (44.6 KB a us),
+// what a block needs to take in its own (3.2 KB a us for each warp), and some us in which rows
+// are joined; clusters do not fill all SMs alike.  So many rows are best in rounds that are
+// nearly full, few rows on many blocks each.  Over 159 pairs of T and V in three formats it
+// chose layouts that took 2.7% longer than the best of them on average, 23% at most.
+// (8 alternatives, bf16, 131072 columns, us as 512 threads x 1 block / 256 x 1 / 128 x 1 / 96 x 1 /
+// 64 x 1 / 128 x 4 / 256 x 8: 64 rows 12.9 / 15.8 / 16.8 / - / - / 11.2 / 11.1; 152 12.1 / 15.6 / 16.1 / - / - / 14.7 / -;
+// 500 30.8 / 26.4 / 32.1; 1000 59.0 / 52.5 / 45.7 / 56.7; 1500 75.4 / 78.3 / 80.1 / 66.3 / 71.6; 2048 104 / 104 /
+// 91.7 / - / 87.1; 3000 147 / 131 / 132 / 128 / 153.)
 static RowShape row_shape(int64_t T, int64_t V, int dtype, int sm_count) {
     const double kb = static_cast<double>(V) * elem_bytes(dtype) / 1024;
     RowShape best = {256, 1};
     double least = 0;
-    for (int threads : {512, 320, 256, 192, 128, 96, 64})
+    for (int threads : {512, 320, 256, 192, 128, 96, 64}) {
+        double join = 3.5 + threads / 150.0;
         for (int blocks = 1; blocks <= kMostCluster; blocks *= 2) {
             // clusters of blocks of 64, 128 or 256; two granules a thread at least
             const bool paired = threads == 64 || threads == 128 || threads == 256;
             if (blocks > 1 && (!paired || kb * 64 < 2.0 * threads * blocks)) break;
+            join += blocks == 1 ? 0.0 : blocks == 2 ? 2.5 : 0.25;
             // (their shared memory counts, too)
             const int resident = blocks == 1 ? resident_blocks(threads) : threads == 64 ? 11 : threads == 128 ? 6 : 4;
             const double each = static_cast<double>(T) * blocks / sm_count;
             const double rounds = ceil(each / resident), at_once = ceil(each / rounds);
-            const double warps = at_once * threads / 32;
-            const double us = rounds * (at_once * kb / blocks / 44.6 * (warps < 26 ? 26 / warps : 1.0) + 2.5 +
-                                        threads / 256.0 + (blocks > 1 ? 3.0 : 0.0));
+            const double us =
+                rounds * (kb / blocks * (at_once / 44.6 + 10.0 / threads) * (blocks > 1 ? 1.5 : 1.0) + join);
             if (least == 0 || us < least) {
                 least = us;
                 best = {threads, blocks};
             }
         }
+    }
     return best;
 }
 
