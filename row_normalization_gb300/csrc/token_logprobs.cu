@@ -1136,8 +1136,9 @@ static RowShape row_shape(int64_t T, int64_t V, int dtype, int sm_count) {
             const bool paired = threads == 64 || threads == 128 || threads == 256;
             if (blocks > 1 && (!paired || kb * 64 < 2.0 * threads * blocks)) break;
             join += blocks == 1 ? 0.0 : blocks == 2 ? 2.5 : 0.25;
-            // (their shared memory counts, too)
-            const int resident = blocks == 1 ? resident_blocks(threads) : threads == 64 ? 11 : threads == 128 ? 6 : 4;
+            // (their shared memory counts, too, and not every place suits a cluster: 76 rows of 131072
+            // in clusters of 8 x 256, 4 blocks an SM, take 14.9 us, in blocks of 512 10.6)
+            const double resident = blocks == 1 ? resident_blocks(threads) : threads == 64 ? 10.5 : threads == 128 ? 5.7 : 3.8;
             const double each = static_cast<double>(T) * blocks / sm_count;
             const double rounds = ceil(each / resident), at_once = ceil(each / rounds);
             const double us =
