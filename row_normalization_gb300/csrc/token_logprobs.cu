@@ -16,9 +16,10 @@
 //
 // What bounds the forward pass: HBM, with the issue slots not far behind.  A logit of 16 bits
 // takes 6.3 instructions (one exponential, half each of a maximum, a clamp and three fused
-// operations, one to widen it); with 8 alternatives the issue slots are 54% full at 1024 rows of
-// 131072, the special function unit 30%.  2048 rows of 131072 in bf16: 85.3 us without
-// alternatives, 6.30 TB/s, 92.3 with 8, 101 with 20 (joining a row takes a block about 2 us).
+// operations, one to widen it); with 8 alternatives the issue slots are 55% full at 1024 rows of
+// 131072, the special function unit 30%.  2048 rows of 131072 in bf16: 85.5 us without
+// alternatives, 6.28 TB/s, 89.4 with 8, 96.9 with 20 (to join a row takes a block, beside others
+// that read, about 3500 clocks, 10000 and 16000).
 #include <cooperative_groups.h>
 #include <float.h>
 
