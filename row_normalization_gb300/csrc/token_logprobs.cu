@@ -710,8 +710,11 @@ __device__ __forceinline__ RowPart join_threads(S &sh, const Row<F> &row, const 
         all.sum_t += sh.owner_s;
         return all;
     }
-    // one token holds more than half of the sum: its thread's others once more, alone
+    // One token holds more than half of the sum, or two that are equal share it (each counts as
+    // 2^t 2^-t with both powers rounded, so two may come to less than 2): the thread's others
+    // once more, alone.  All but one of those equal to the largest count 1.
     float r = 0.0f, q = 0.0f;
+    int equal = 0;
     const auto others = [&](int g) {
         float v[F::kElems];
         widen<F>(row.fetch(g), v);
@@ -721,6 +724,8 @@ __device__ __forceinline__ RowPart join_threads(S &sh, const Row<F> &row, const 
                 const float x = fmaxf((v[e] - m) * c, -kDeep), p = exp2_fast(x);
                 r += p;
                 q = fmaf(p, x, q);
+            } else if (v[e] == m) {
+                ++equal;
             }
     };
     // (one body: the last turn of lane 0 is the row's end)
@@ -732,7 +737,7 @@ __device__ __forceinline__ RowPart join_threads(S &sh, const Row<F> &row, const 
         if (!more) g = end;
         if (g >= 0) others(g);
     }
-    all.rest += warp_sum(r);
+    all.rest += warp_sum(r) + static_cast<float>(__reduce_add_sync(0xffffffffu, equal) - 1);
     all.sum_t += warp_sum(q);
     return all;
 }
