@@ -754,10 +754,16 @@ int token_logprobs_fwd(int dtype, const void *logits, int64_t stride, const int6
  *   dlogits     [T, V] in dtype, rows dlogits_stride apart; logits itself with
  *               the same stride, or memory that does not overlap it.
  * s - lse is taken in fp32, so p is off by 2^-24 |lse| of itself (not that of the
- * given token, which goes by logprobs).
+ * given token, which goes by logprobs), and is 1 at most where |lse| is beyond
+ * 2^20.  A row of nothing but the format's lowest value is such a row: its p say
+ * nothing but that (mask with -infinity where gradients count).  The entropy's
+ * gradient by a token that is nearly sure and not the given one is off by
+ * 2^-24 |lse| of scale dentropy, however small it is.
  * An ignored target's dlogprobs counts as 0; with a target >= V the row is NaN
- * and RN_STATUS_BAD_INDEX is raised.  Banned tokens, and rows of nothing else,
- * get 0; a row whose lse is NaN or +infinity gets NaN.  T * ceil(V / 4096) below
+ * and RN_STATUS_BAD_INDEX is raised.  Banned tokens, and rows whose lse is
+ * -infinity, get 0; a row whose lse is NaN or +infinity gets NaN.  (An s beyond
+ * fp32 counts as infinite in both calls' lse; logprobs and entropy go by
+ * differences of logits and do not mind.)  T * ceil(V / 4096) below
  * 2^31 (with V + 8 for V where rows of dlogits begin off 16-byte boundaries).
  * Errors as the forward call; dlogits == logits with another stride is RN_ERR_ARG. */
 int token_logprobs_bwd(int dtype, const void *logits, int64_t stride, const int64_t *targets,

@@ -992,6 +992,10 @@ struct LogprobsGradArgs {
 
 constexpr int kGradThreads = 256;
 constexpr int kGradBatch = 4;  // granules of a thread
+// Beyond this the rounding of lse may put scale x - lse far above zero: 1e30 above in a row of
+// nothing but bf16's or fp32's lowest value, and the power would be infinite.  There scale x is
+// rounded before lse is taken off: no rounded s is above the rounded lse, so p is 1 at most.
+constexpr float kFarLse = 0x1p20f;
 
 // The granule of elements i .. of a row, wherever they lie: two aligned ones, shifted.
 template <class F>
@@ -1011,10 +1015,11 @@ __device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, uint32_
 // within 16 bytes.  HBM bounds it: 4096 rows of 131072 in bf16, 2.15 GB, take 302 us (7.1 TB/s,
 // 1.05 of the copy's rate); 309 with loads and stores that keep their lines, 387 with two
 // granules a thread, 351 with scalar fp32 and shares that leave each row's last block a rest.
-// 2048 rows of 50021: 62 us (floor 60); 79 where dlogits lies otherwise than logits (235 with
-// stores of one element).
+// 2048 rows of 50021: 63 us (floor 60); 79 where dlogits lies otherwise than logits (235 with
+// stores of one element).  Six blocks an SM: with the way for a far lse the compiler takes 46
+// registers, five blocks, and the three take 307, 65 and 81.
 template <class F>
-__global__ void __launch_bounds__(kGradThreads) logprobs_bwd_kernel(const __grid_constant__ LogprobsGradArgs a) {
+__global__ void __launch_bounds__(kGradThreads, 6) logprobs_bwd_kernel(const __grid_constant__ LogprobsGradArgs a) {
     pdl_trigger();
     pdl_wait();
     const int64_t t = blockIdx.x / a.chunks;
@@ -1077,40 +1082,49 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_bwd_kernel(const __grid
         const float l = fmaxf(lt, -150.0f);
         return a.scale * (expf(l) * (dl - dh * (l + h)) - expm1f(l) * dp);
     };
-    const Pair scale = Pair::both(a.scale), ref = Pair::both(-lse), log2e = Pair::both(1.4426950408889634f);
+    const Pair scale = Pair::both(a.scale), log2e = Pair::both(1.4426950408889634f);
     const Pair k0 = Pair::both(c0), k1 = Pair::both(-c1);
-    const auto grad = [&](float &p, float &q) {
-        const float2 l = Pair::of(p, q).fma(scale, ref).v;
+    const auto grad = [&](float &p, float &q, Pair ref, auto far) {
+        float2 l = Pair::of(p, q).fma(scale, ref).v;
+        if constexpr (far.value)  // (scalar operations: a packed product and sum may become one)
+            l = make_float2(__fadd_rn(__fmul_rn(p, a.scale), ref.v.x), __fadd_rn(__fmul_rn(q, a.scale), ref.v.y));
         const Pair m = Pair::of(fmaxf(l.x, -150.0f), fmaxf(l.y, -150.0f));
         const float2 e = (m * log2e).v;
         const float2 r = (Pair::of(exp2_fast(e.x), exp2_fast(e.y)) * m.fma(k1, k0)).v;
         p = r.x;
         q = r.y;
     };
+    // (both ways whole: a choice within the loop takes registers of the usual one)
+    const auto store = [&](Pair ref, auto far) {
 #pragma unroll
-    for (int b = 0; b < kGradBatch; ++b) {
-        const int g = first + b * kGradThreads;
-        if (g >= end) return;
-        const int i = out.index(g);
-        float v[F::kElems];
-        widen<F>(u[b], v);
+        for (int b = 0; b < kGradBatch; ++b) {
+            const int g = first + b * kGradThreads;
+            if (g >= end) return;
+            const int i = out.index(g);
+            float v[F::kElems];
+            widen<F>(u[b], v);
 #pragma unroll
-        for (int e = 0; e < F::kElems; e += 2) grad(v[e], v[e + 1]);
-        if (target >= i && target < i + F::kElems) {
-            const float gt = given();
+            for (int e = 0; e < F::kElems; e += 2) grad(v[e], v[e + 1], ref, far);
+            if (target >= i && target < i + F::kElems) {
+                const float gt = given();
 #pragma unroll
-            for (int e = 0; e < F::kElems; ++e)
-                if (target == i + e) v[e] = gt;
+                for (int e = 0; e < F::kElems; ++e)
+                    if (target == i + e) v[e] = gt;
+            }
+            if (out.whole(g)) {
+                __stcs(reinterpret_cast<uint4 *>(y + i), narrow<F>(v));
+            } else {
+                const uint32_t there = out.there(g);
+#pragma unroll
+                for (int e = 0; e < F::kElems; ++e)
+                    if (there >> e & 1u) store_one<F>(y + i + e, v[e]);
+            }
         }
-        if (out.whole(g)) {
-            __stcs(reinterpret_cast<uint4 *>(y + i), narrow<F>(v));
-        } else {
-            const uint32_t there = out.there(g);
-#pragma unroll
-            for (int e = 0; e < F::kElems; ++e)
-                if (there >> e & 1u) store_one<F>(y + i + e, v[e]);
-        }
-    }
+    };
+    if (!(fabsf(lse) > kFarLse))
+        store(Pair::both(-lse), std::false_type());
+    else  // (-infinity: all tokens are banned, or too far down for fp32, and p is 0)
+        store(Pair::both(lse == -INFINITY ? lse : -lse), std::true_type());
 }
 
 // ---- host ---------------------------------------------------------------------------------------
