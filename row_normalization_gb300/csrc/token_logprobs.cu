@@ -1017,7 +1017,7 @@ __device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, uint32_
 // granules a thread, 351 with scalar fp32 and shares that leave each row's last block a rest.
 // 2048 rows of 50021: 63 us (floor 60); 79 where dlogits lies otherwise than logits (235 with
 // stores of one element).  Six blocks an SM: with the way for a far lse the compiler takes 46
-// registers, five blocks, and the three take 307, 65 and 81.
+// registers, five blocks, and 4096 rows of 131072 take 307, 2048 of 50021 65.
 template <class F>
 __global__ void __launch_bounds__(kGradThreads, 6) logprobs_bwd_kernel(const __grid_constant__ LogprobsGradArgs a) {
     pdl_trigger();
@@ -1151,14 +1151,12 @@ static RowShape row_shape(int64_t T, int64_t V, int dtype, int sm_count) {
     double least = 0;
     for (int threads : {512, 320, 256, 192, 128, 96, 64}) {
         double join = 3.5 + threads / 150.0;
-        for (int blocks = 1; blocks <= kMostCluster; blocks *= 2) {
-            // clusters of blocks of 64, 128 or 256; two granules a thread at least
-            const bool paired = threads == 64 || threads == 128 || threads == 256;
-            if (blocks > 1 && (!paired || kb * 64 < 2.0 * threads * blocks)) break;
-            join += blocks == 1 ? 0.0 : blocks == 2 ? 2.5 : 0.25;
-            // (their shared memory counts, too, and not every place suits a cluster: 76 rows of 131072
-            // in clusters of 8 x 256, 4 blocks an SM, take 14.9 us, in blocks of 512 10.6)
-            const double resident = blocks == 1 ? resident_blocks(threads) : threads == 64 ? 10.5 : threads == 128 ? 5.7 : 3.8;
+        for (int blocks : {1, 4, kMostCluster}) {
+            // clusters of blocks of 128 or 256; two granules a thread at least
+            if (blocks > 1 && ((threads != 128 && threads != 256) || kb * 64 < 2.0 * threads * blocks)) break;
+            join += blocks == 1 ? 0.0 : blocks == 4 ? 2.75 : 0.25;
+            // (their shared memory counts, too, and not every place suits a cluster)
+            const double resident = blocks == 1 ? resident_blocks(threads) : threads == 128 ? 5.7 : 3.8;
             const double each = static_cast<double>(T) * blocks / sm_count;
             const double rounds = ceil(each / resident), at_once = ceil(each / rounds);
             const double us =
@@ -1220,7 +1218,7 @@ static int run_fwd(LogprobsArgs &a, int dtype, const DeviceInfo &dev, cudaStream
         case 320: return launch_fwd<F, 320, false>(a, dev, st);
         case 192: return launch_fwd<F, 192, false>(a, dev, st);
         case 96: return launch_fwd<F, 96, false>(a, dev, st);
-        case 64: return a.blocks > 1 ? launch_fwd<F, 64, true>(a, dev, st) : launch_fwd<F, 64, false>(a, dev, st);
+        case 64: return launch_fwd<F, 64, false>(a, dev, st);
         case 128: return a.blocks > 1 ? launch_fwd<F, 128, true>(a, dev, st) : launch_fwd<F, 128, false>(a, dev, st);
         default: return a.blocks > 1 ? launch_fwd<F, 256, true>(a, dev, st) : launch_fwd<F, 256, false>(a, dev, st);
     }
