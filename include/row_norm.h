@@ -743,6 +743,12 @@ int token_logprobs_fwd(int dtype, const void *logits, int64_t stride, const int6
                        float *lse, float *entropy, float *top_logprobs, int64_t *top_ids,
                        rn_stream_t stream);
 
+/* The layout that token_logprobs_fwd gives T >= 1 rows of V logits on the current
+ * device: *threads of a block, and *blocks that share a row (1, or a cluster).
+ * Errors as the call's (RN_ERR_NULL without a place for either).  Host-only query:
+ * launches nothing. */
+int token_logprobs_select_layout(int dtype, int64_t T, int64_t V, int *threads, int *blocks);
+
 /* The gradient by the logits of what comes back for logprobs, entropy and lse
  * (the top log probabilities have none):
  *   dlogits_v = scale (dlogprobs (1[v = target] - p_v)

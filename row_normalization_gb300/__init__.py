@@ -22,4 +22,5 @@ from .binding import (  # noqa: F401
     qk_norm_rope_axes_workspace, qk_norm_rope_fwd, qk_norm_rope_fwd_checked, qk_norm_rope_fwd_ex,
     qk_norm_rope_select_schedule, rmsnorm_fwd, rmsnorm_select_schedule, rope_axes,
     rope_cos_sin_table,
-    row_norm_select_schedule, token_logprobs_bwd, token_logprobs_fwd, version)
+    row_norm_select_schedule, token_logprobs_bwd, token_logprobs_fwd,
+    token_logprobs_select_layout, version)

@@ -180,6 +180,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.qk_norm_rope_axes_workspace_bytes.restype = i64
         L.token_logprobs_fwd.argtypes = [i32, vp, i64, vp, i64, i64, f32, i32, vp, vp, vp, vp, vp, vp]
         L.token_logprobs_fwd.restype = i32
+        L.token_logprobs_select_layout.argtypes = [i32, i64, i64, ctypes.POINTER(i32), ctypes.POINTER(i32)]
+        L.token_logprobs_select_layout.restype = i32
         L.token_logprobs_bwd.argtypes = [i32, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, vp, i64, i64,
                                          i64, f32, vp, i64, vp]
         L.token_logprobs_bwd.restype = i32
@@ -1074,6 +1076,19 @@ def token_logprobs_fwd(logits: torch.Tensor, targets: torch.Tensor, *, scale: fl
     _kv_call(dev, "token_logprobs_fwd", code, xp, xs, tp, T, V, scale, top_k, pp, lp, ep, kp, ip,
              stream=stream)
     return TokenLogprobs(logprobs, lse, entropy, top_logprobs, top_ids)
+
+
+def token_logprobs_select_layout(dtype: torch.dtype, T: int, V: int) -> tuple[int, int]:
+    """(threads of a block, blocks that share a row) that token_logprobs_fwd gives T
+    rows of V logits of dtype on the current device."""
+    if dtype not in _LOGIT_DTYPES:
+        raise TypeError(f"logits must be bfloat16, float16 or float32, got {dtype}")
+    threads, blocks = ctypes.c_int(), ctypes.c_int()
+    rc = int(load().token_logprobs_select_layout(_LOGIT_DTYPES[dtype], int(T), int(V),
+                                                 ctypes.byref(threads), ctypes.byref(blocks)))
+    if rc != RN_OK:
+        raise RowNormError("token_logprobs_select_layout", rc)
+    return threads.value, blocks.value
 
 
 def _row_values(dev: int, t: torch.Tensor | None, name: str, T: int):

@@ -1295,6 +1295,19 @@ int token_logprobs_fwd(int dtype, const void *logits, int64_t stride, const int6
     return rn::run_fwd<rn::Row16Bf>(a, dtype, *dev, st);
 }
 
+int token_logprobs_select_layout(int dtype, int64_t T, int64_t V, int *threads, int *blocks) {
+    const int rc = rn::check_rows(dtype, V, T, V, 1.0f);
+    if (rc != RN_OK) return rc;
+    if (T < 1) return RN_ERR_SHAPE;
+    if (!threads || !blocks) return RN_ERR_NULL;
+    const rn::DeviceInfo *dev = rn::current_device_info();
+    if (!dev) return RN_ERR_DEVICE;
+    const rn::RowShape s = rn::row_shape(T, V, dtype, dev->sm_count);
+    *threads = s.threads;
+    *blocks = s.blocks;
+    return RN_OK;
+}
+
 int token_logprobs_bwd(int dtype, const void *logits, int64_t stride, const int64_t *targets, const float *logprobs,
                        const float *lse, const float *entropy, const float *dlogprobs, int64_t dlogprobs_stride,
                        const float *dentropy, int64_t dentropy_stride, const float *dlse, int64_t dlse_stride,
