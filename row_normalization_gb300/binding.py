@@ -684,7 +684,7 @@ def _on(dev: int, t: torch.Tensor, name: str, dtype: torch.dtype, numel: int | N
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or \
             not t.is_contiguous():
         _need(t, name, dtype)
-        raise ValueError(f"{name} must be on the cache's device")
+        raise ValueError(f"{name} must be on the same CUDA device as the other tensors")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
     return t.data_ptr()
