@@ -705,16 +705,14 @@ __device__ __forceinline__ RowPart join_threads(S &sh, const Row<F> &row, const 
     }
     if (owner >= NT) return all;
     const float oz = sh.owner_z;
-    if (all.rest + oz >= 2.0f) {
+    // (one token is 1 off by 2^-21 at most, two that are equal are 2 off by that: 1.5 tells them apart)
+    if (all.rest + oz >= 1.5f) {
         all.rest += oz - 1.0f;
         all.sum_t += sh.owner_s;
         return all;
     }
-    // One token holds more than half of the sum, or two that are equal share it (each counts as
-    // 2^t 2^-t with both powers rounded, so two may come to less than 2): the thread's others
-    // once more, alone.  All but one of those equal to the largest count 1.
+    // one token holds more than two thirds of the sum: its thread's others once more, alone
     float r = 0.0f, q = 0.0f;
-    int equal = 0;
     const auto others = [&](int g) {
         float v[F::kElems];
         widen<F>(row.fetch(g), v);
@@ -724,8 +722,6 @@ __device__ __forceinline__ RowPart join_threads(S &sh, const Row<F> &row, const 
                 const float x = fmaxf((v[e] - m) * c, -kDeep), p = exp2_fast(x);
                 r += p;
                 q = fmaf(p, x, q);
-            } else if (v[e] == m) {
-                ++equal;
             }
     };
     // (one body: the last turn of lane 0 is the row's end)
@@ -737,7 +733,7 @@ __device__ __forceinline__ RowPart join_threads(S &sh, const Row<F> &row, const 
         if (!more) g = end;
         if (g >= 0) others(g);
     }
-    all.rest += warp_sum(r) + static_cast<float>(__reduce_add_sync(0xffffffffu, equal) - 1);
+    all.rest += warp_sum(r);
     all.sum_t += warp_sum(q);
     return all;
 }
