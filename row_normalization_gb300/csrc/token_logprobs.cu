@@ -1012,10 +1012,10 @@ __device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, uint32_
 // 1.05 of the copy's rate); 309 with loads and stores that keep their lines, 387 with two
 // granules a thread, 351 with scalar fp32 and shares that leave each row's last block a rest.
 // 2048 rows of 50021: 63 us (floor 60); 79 where dlogits lies otherwise than logits (235 with
-// stores of one element).  Six blocks an SM: with the way for a far lse the compiler takes 46
-// registers, five blocks, and 4096 rows of 131072 take 307, 2048 of 50021 65.
+// stores of one element).  40 registers a thread are six blocks an SM; with 46, five, the two
+// take 307 and 65.
 template <class F>
-__global__ void __launch_bounds__(kGradThreads, 6) logprobs_bwd_kernel(const __grid_constant__ LogprobsGradArgs a) {
+__global__ void __launch_bounds__(kGradThreads) logprobs_bwd_kernel(const __grid_constant__ LogprobsGradArgs a) {
     pdl_trigger();
     pdl_wait();
     const int64_t t = blockIdx.x / a.chunks;
@@ -1050,31 +1050,31 @@ __global__ void __launch_bounds__(kGradThreads, 6) logprobs_bwd_kernel(const __g
     }
     const float lse = a.lse[t];
     const float h = a.entropy ? a.entropy[t] : 0.0f;
-    const float dh = a.dentropy ? a.dentropy[t * a.dentropy_stride] : 0.0f;
-    const float dl = a.dlse ? a.dlse[t * a.dlse_stride] : 0.0f;
-    int64_t target = -1;
+    float dh = a.dentropy ? a.dentropy[t * a.dentropy_stride] : 0.0f;
+    float dl = a.dlse ? a.dlse[t * a.dlse_stride] : 0.0f;
+    int64_t wanted = -1;
     float dp = 0.0f, lt = 0.0f;
     if (a.dlogprobs) {
-        target = a.targets[t];
-        if (target >= 0) {
+        wanted = a.targets[t];
+        if (wanted >= 0) {
             dp = a.dlogprobs[t * a.dlogprobs_stride];
             lt = a.logprobs[t];
         }
     }
-    // dx = p (c0 - c1 (s - lse)); s - lse stops at -150, where p is zero and a product with
-    // the -infinity of a banned token would be NaN
-    float c0 = a.scale * (dl - dp - dh * h);
-    const float c1 = a.scale * dh;
     const float nan = __uint_as_float(0x7FFFFFFFu);
-    if (!(lse < INFINITY)) c0 = nan;  // NaN or +infinity
-    if (target >= a.V) {
-        c0 = nan;
+    if (lse == -INFINITY) dp = dh = dl = 0.0f;  // all tokens are banned, or too far down for fp32
+    if (!(lse < INFINITY)) dp = nan;            // NaN or +infinity
+    // (-1: none of the row's)
+    const int target = wanted < a.V ? static_cast<int>(wanted < 0 ? -1 : wanted) : -1;
+    if (wanted >= a.V) {
+        dp = nan;
         if (chunk == 0 && threadIdx.x == 0) atomicOr(&g_logprobs_status, RN_STATUS_BAD_INDEX);
     }
+    // dx = p (c0 - c1 (s - lse)); s - lse stops at -150, where p is zero and a product with
+    // the -infinity of a banned token would be NaN
+    const float c0 = a.scale * (dl - dp - dh * h), c1 = a.scale * dh;
     // of the given token, by its own log probability: 1 - p where p is nearly 1
     const auto given = [&] {
-        if (!(lse < INFINITY)) return nan;
-        if (lse == -INFINITY) return 0.0f;
         const float l = fmaxf(lt, -150.0f);
         return a.scale * (expf(l) * (dl - dh * (l + h)) - expm1f(l) * dp);
     };
@@ -1101,7 +1101,7 @@ __global__ void __launch_bounds__(kGradThreads, 6) logprobs_bwd_kernel(const __g
             widen<F>(u[b], v);
 #pragma unroll
             for (int e = 0; e < F::kElems; e += 2) grad(v[e], v[e + 1], ref, far);
-            if (target >= i && target < i + F::kElems) {
+            if (target >= 0 && static_cast<uint32_t>(target - i) < F::kElems) {
                 const float gt = given();
 #pragma unroll
                 for (int e = 0; e < F::kElems; ++e)
@@ -1119,7 +1119,7 @@ __global__ void __launch_bounds__(kGradThreads, 6) logprobs_bwd_kernel(const __g
     };
     if (!(fabsf(lse) > kFarLse))
         store(Pair::both(-lse), std::false_type());
-    else  // (-infinity: all tokens are banned, or too far down for fp32, and p is 0)
+    else  // (-infinity: p is 0)
         store(Pair::both(lse == -INFINITY ? lse : -lse), std::true_type());
 }
 
