@@ -726,8 +726,12 @@ int64_t qk_norm_rope_axes_workspace_bytes(int D);
  *   top_logprobs, top_ids [T, top_k]    the top_k largest s_v - lse and their
  *               columns, in descending order, the lowest column first among
  *               equal logits; top_k from 0 to 32 and at most V.
- * fp32 throughout (fp32 sums; 1 - p keeps its precision where a token is nearly
- * sure).  Any of logprobs (and targets), lse and entropy may be NULL.
+ * fp32 throughout (1 - p keeps its precision where a token is nearly sure).  The
+ * sums are fp32, too: a thread adds up to V / 128 terms one after another, so lse,
+ * log probabilities and entropy would be off by V 2^-31 if every rounding went one
+ * way (2^-14 at 131072 columns), and are by far less at such sizes; rows of 2^31
+ * columns, 2^19 terms a thread, are taken, but their lse is good to 2^-5 alone.
+ * Any of logprobs (and targets), lse and entropy may be NULL.
  * Logits need only their elements' alignment, and V and stride may be odd.
  *   target < 0     ignored: logprobs 0.
  *   target >= V    logprobs NaN, and RN_STATUS_BAD_INDEX in the status word.

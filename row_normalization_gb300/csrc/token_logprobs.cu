@@ -17,9 +17,9 @@
 // What bounds the forward pass: HBM, with the issue slots not far behind.  A logit of 16 bits
 // takes 6.3 instructions (one exponential, half each of a maximum, a clamp and three fused
 // operations, one to widen it); with 8 alternatives the issue slots are 55% full at 1024 rows of
-// 131072, the special function unit 30%.  2048 rows of 131072 in bf16: 85.5 us without
-// alternatives, 6.28 TB/s, 89.4 with 8, 96.9 with 20 (to join a row takes a block, beside others
-// that read, about 3500 clocks, 10000 and 16000).
+// 131072, the special function unit 30%.  2048 rows of 131072 normal logits in bf16: 83.5 us
+// without alternatives, 6.43 TB/s, 86.9 with 8, 94.6 with 20 (to join a row takes a block, beside
+// others that read, about 3500 clocks, 10000 and 16000).
 #include <cooperative_groups.h>
 #include <float.h>
 
@@ -1009,7 +1009,7 @@ __device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, uint32_
 
 // A block takes a share of a row, by the granules of dlogits; logits may lie otherwise
 // within 16 bytes.  HBM bounds it: 4096 rows of 131072 in bf16, 2.15 GB, take 302 us (7.1 TB/s,
-// 1.05 of the copy's rate); 309 with loads and stores that keep their lines, 387 with two
+// 1.05 of the copy's rate) launch after launch, 319 a single call (0.99); 309 with loads and stores that keep their lines, 387 with two
 // granules a thread, 351 with scalar fp32 and shares that leave each row's last block a rest.
 // 2048 rows of 50021: 63 us (floor 60); 79 where dlogits lies otherwise than logits (235 with
 // stores of one element).  40 registers a thread are six blocks an SM; with 46, five, the two
@@ -1135,12 +1135,16 @@ struct RowShape {
 // as many as it holds.  A round takes what HBM needs for the SM's shares in it (44.6 KB a us),
 // what a block needs to take in its own (3.2 KB a us for each warp), and some us in which rows
 // are joined; clusters do not fill all SMs alike.  So many rows are best in rounds that are
-// nearly full, few rows on many blocks each.  Over 159 pairs of T and V in three formats it
-// chose layouts that took 2.7% longer than the best of them on average, 23% at most.
+// nearly full, few rows on many blocks each.  Over the 159 pairs of T and V in three formats that
+// it was fitted to it chose layouts that took 2.8% longer than the best of them on average, 23% at
+// most; over 217 others 4.9%, and 37% (100 fp16 rows of 50021 without alternatives: 8.9 us in
+// blocks of 320, 6.5 in clusters of 8 x 128).  It does not know how many alternatives a join
+// looks for: without any, clusters are better further up than it says.
 // (8 alternatives, bf16, 131072 columns, us as 512 threads x 1 block / 256 x 1 / 128 x 1 / 96 x 1 /
-// 64 x 1 / 128 x 4 / 256 x 8: 64 rows 12.9 / 15.8 / 16.8 / - / - / 11.2 / 11.1; 152 12.1 / 15.6 / 16.1 / - / - / 14.7 / -;
-// 500 30.8 / 26.4 / 32.1; 1000 59.0 / 52.5 / 45.7 / 56.7; 1500 75.4 / 78.3 / 80.1 / 66.3 / 71.6; 2048 104 / 104 /
-// 91.7 / - / 87.1; 3000 147 / 131 / 132 / 128 / 153.)
+// 64 x 1 / 128 x 4 / 128 x 8 / 256 x 8; * what it chooses.  64 rows 12.1 / 14.8 / 15.2 / 29.7 / 38.5 / 11.1 /
+// 11.6 / 10.9*; 76 10.8 / 15.0 / 15.4 / 29.8 / 38.6 / 11.7 / 11.8* / 14.9; 152 12.1* / 15.7 / 16.1 / 29.0 / 37.0 / 14.7 /
+// 20.7 / 28.7; 500 30.8 / 26.6* / 32.8 / 35.9 / 44.7; 1000 59.0 / 52.6 / 46.7* / 57.9 / 63.4; 1500 75.5 / 78.6 / 80.1 /
+// 65.9* / 72.7; 2048 104 / 104 / 91.2 / 115 / 86.9*; 3000 146 / 132 / 133 / 129* / 155.)
 static RowShape row_shape(int64_t T, int64_t V, int dtype, int sm_count) {
     const double kb = static_cast<double>(V) * elem_bytes(dtype) / 1024;
     RowShape best = {256, 1};
